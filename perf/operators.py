@@ -177,7 +177,7 @@ def prepare(case, seed):
         s["scale"] = 1.0 / math.sqrt(c["d"])
         if own:
             import wfst_beam_search_gb300 as W
-            s["W"], s["ws"] = W, W.attend_workspace(c["lanes"], c["hkv"], DEV)
+            s["W"], s["ws"] = W, W.attend_workspace(DEV)
     else:
         # a peaked head over a broad tail, as trained models answer
         x = normal(c["lanes"], c["vocab"], scale=2.0, dtype=torch.float32)
