@@ -49,6 +49,7 @@ extern "C" {
 /* ---- log-prob element types ------------------------------------------ */
 #define WFST_F32 0
 #define WFST_F16 1 /* widened exactly to fp32 inside (§11 "fp16") */
+#define WFST_BF16 2 /* second-pass operators only */
 
 /* ---- per-lane overflow bits (meta[3*b + 2]; §7 "Overflow bits") ------- */
 #define WFST_OVF_ARENA 4     /* winners log or lattice arena full            */
@@ -414,6 +415,134 @@ int wfst_blank_skip(const void* log_probs, int32_t dtype, int64_t stride_b, int6
                     int32_t vocab_size, int32_t blank_id, float threshold, const int32_t* lens,
                     int32_t B, int32_t T, void* out, int32_t* out_lens, int32_t* frame_map,
                     void* stream);
+
+/* ---- second pass -------------------------------------------------------
+ * The operators of one step of a small language model that reads the
+ * first-pass words and answers one token per lane (the page has no
+ * counterpart): products with 4-bit weights, the heads' norm and rotation
+ * with the write into the paged cache, attention of the new token over that
+ * cache, and the draw of the next token.  Shared by all of them:
+ *   - every array is device memory of one device (host pointers are refused);
+ *     nothing is allocated and nothing is copied to the host: the kernels are
+ *     enqueued on `stream`, on the arrays' own device, and the call returns
+ *     without waiting;
+ *   - `dtype` is WFST_F16 or WFST_BF16 for weights, activations and the
+ *     cache, and also WFST_F32 for logits; sums, softmax statistics and norms
+ *     are held in fp32 or wider and rounded once at the end;
+ *   - strides count elements; the innermost axis has unit stride;
+ *   - results do not depend on the order in which CTAs run.
+ */
+
+/*
+ * A matrix w[n, k] = scales[n, k / group] * (codes[n, k] - zeros[n, k /
+ * group]) with codes 0..15, laid out once for wfst_matvec_quant.  codes:
+ * [n, k/2] bytes, the even k in the lower half of a byte.  scales and zeros:
+ * [n, k / group], 16-bit values of the type that wfst_matvec_quant is given;
+ * zeros NULL stands for 8 everywhere.  group is 32, 64, 128 or 256 and
+ * divides k; n >= 1.  packed: 16-byte aligned, wfst_quant_size's bytes (its
+ * `zeros` says whether there are zero points).  Errors: INVALID_ARG, CUDA.
+ */
+int wfst_quant_size(int32_t n, int32_t k, int32_t group, int32_t zeros, int64_t* bytes);
+int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros, int32_t n, int32_t k,
+                    int32_t group, void* packed, void* stream);
+
+/*
+ * y[r, n] = bias[n] + sum over k of x[r, k] * w[n, k], for rows r of x
+ * [rows, k] (16-byte aligned, stride_x a multiple of 8) and a packed matrix.
+ * bias [n] may be NULL.  rows = 0 does nothing.  Errors: INVALID_ARG, CUDA.
+ */
+int wfst_matvec_quant(const void* packed, int32_t n, int32_t k, int32_t group, int32_t zeros, int32_t dtype,
+                      const void* x, int64_t stride_x, int32_t rows, const void* bias, void* y,
+                      int64_t stride_y, void* stream);
+
+/*
+ * The new tokens' heads: each head of q and k is divided by the root of its
+ * mean square (plus eps), multiplied by the gain, and its first `rot`
+ * elements are turned by the token's position; q goes to q_out, k and v to
+ * the cache rows of the tokens' slots.  Pairs are (i, i + rot/2), or (2i,
+ * 2i + 1) when interleaved; table [contexts, rot] fp32 holds a position's
+ * rot/2 cosines, then its rot/2 sines (contiguous rows).  A slot is page *
+ * page_size + place; a negative slot, or one past the pool, keeps nothing
+ * of that token's k and v.  A position outside the table turns its head's
+ * `rot` elements into NaN.  Slots of one call must differ.  q_out may be q.
+ * Gains may be NULL (one).  head_dim: 64, 128 or 256; rot: a multiple of 16,
+ * up to head_dim (0: no turn).  q, k, v, gains, q_out and the cache are
+ * 16-byte aligned, their strides multiples of 8.  tokens = 0 does nothing.
+ * Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  const void *q, *k, *v;            /* [tokens, heads, head_dim] */
+  const void *q_gain, *k_gain;      /* [head_dim] or NULL */
+  const int32_t *positions, *slots; /* [tokens] */
+  const float* table;
+  void *q_out, *k_pages, *v_pages;  /* pages: [num_pages, page_size, kv_heads, head_dim] in any stride order */
+  int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2]; /* token, head */
+  int64_t k_page_stride[3], v_page_stride[3];                   /* page, place, head */
+  int32_t dtype, tokens, q_heads, kv_heads, head_dim, rot, interleaved, contexts, num_pages, page_size;
+  float eps;
+} wfst_rotate_args;
+int wfst_norm_rotate(const wfst_rotate_args* args, void* stream);
+
+/*
+ * Attention of one new token per lane over its paged cache.  Lane b's cache
+ * has lengths[b] tokens, the new one among them (its k and v are already in
+ * the cache); token j lies in page table[b, j / page_size] at place j %
+ * page_size.  Without a window all of them are seen; with window > 0 the last
+ * `window` ones and the first `sinks` ones.  Entries of the table whose
+ * tokens are not seen are never read; a token whose entry is outside [0,
+ * num_pages) counts as not seen, and lengths are clamped to [0, table_width *
+ * page_size].  q_heads is a multiple of kv_heads: query head h reads
+ * key-value head h / (q_heads / kv_heads).  o = softmax(scale * q k^T) v;
+ * lse (may be NULL) receives the log of the sum of exponentials.  A lane that
+ * sees nothing has o = 0 and lse = -inf.  head_dim: 64, 128 or 256.  q, the
+ * pages and the workspace are 16-byte aligned, strides of q and the pages
+ * multiples of 8.
+ * workspace: wfst_attend_size's bytes, zeros before its first use; calls that
+ * use the same one must follow each other on a stream, and each leaves it
+ * ready for the next.  lanes = 0 does nothing.  Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  const void *q, *k_pages, *v_pages; /* q: [lanes, q_heads, head_dim] */
+  const int32_t *table, *lengths;    /* [lanes, table_width], [lanes] */
+  void* o;                           /* [lanes, q_heads, head_dim] */
+  float* lse;                        /* [lanes, q_heads] */
+  void* workspace;
+  int64_t q_stride[2], o_stride[2], lse_stride, table_stride;
+  int64_t k_page_stride[3], v_page_stride[3]; /* page, place, head */
+  int32_t dtype, lanes, q_heads, kv_heads, head_dim, table_width, num_pages, page_size, window, sinks;
+  float scale;
+} wfst_attend_args;
+int wfst_attend_size(int64_t* bytes);
+int wfst_attend_paged(const wfst_attend_args* args, void* stream);
+
+/*
+ * One token per lane from its logits [lanes, vocab] and a uniform number in
+ * [0, 1).  With weights exp((x - max x) / temperature), the tokens kept are
+ * the first top_k in order of descending logit (equal ones by ascending
+ * index; 0: all), of those the shortest prefix whose weight reaches top_p of
+ * theirs (1: all), and of those the ones whose weight is at least min_p of
+ * the largest.  The token is the first index whose cumulative kept weight
+ * exceeds uniform times their total; logprobs receives the log of its share
+ * of that total, kept the number of tokens kept.  temperature = 0 takes the
+ * first largest logit.  Weights are summed as whole multiples of 2^-43 of the
+ * largest one, so results do not depend on any order.  -inf and NaN logits
+ * weigh nothing; a lane with no other logit gets token -1, logprob -inf and
+ * kept 0; +inf logits share all the weight.  The four settings apply to every
+ * lane, or per lane where the array beside them is not NULL.  vocab <= 2^20.
+ * Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  const void* logits;
+  const float *uniform, *temperature_v, *top_p_v, *min_p_v; /* [lanes] */
+  const int32_t* top_k_v;
+  int32_t* tokens;  /* [lanes] */
+  float* logprobs;  /* [lanes] */
+  int32_t* kept;    /* [lanes] */
+  int64_t stride;   /* between lanes of logits */
+  int32_t dtype, lanes, vocab, top_k;
+  float temperature, top_p, min_p;
+} wfst_sample_args;
+int wfst_sample_tokens(const wfst_sample_args* args, void* stream);
 
 const char* wfst_last_error(void);
 

@@ -1,0 +1,212 @@
+"""Attention of one new token over a paged cache against the formula in 64
+bits.
+
+Tolerance: o is rounded once (u of it); in front of that, scores are fp32 sums
+of d products, off by at most (d + 8) * 2^-23 of the terms' size (for a score:
+scale * sum |q k|, here called r), which changes a weight by that much,
+relative; the weights add up in fp32 in any split.  So o is off by at most
+u |o| + (2 r (d + 8) + n / 8 + 64) 2^-23 sum p |v|, and the 16-bit halves of P
+leave 2^-16 (bf16: two times 8 bits) of sum p |v| at most."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+UNIT = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def W():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import wfst_beam_search_gb300 as W
+    W.load()
+    return W
+
+
+@pytest.fixture(scope="module")
+def ws(W):
+    return W.attend_workspace("cuda")
+
+
+def visible(n, window, sinks):
+    start = max(0, n - window) if window else 0
+    return list(range(min(sinks, start) if window else 0)) + list(range(start, n))
+
+
+def make(seed, lens, hq, hkv, d, page, dtype, window=0, sinks=0, spread=1.5):
+    """Inputs whose pages lie anywhere; what no lane sees is NaN, pages and table entries alike."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    width = max(1, -(-max(lens) // page)) + 1
+    table = torch.full((len(lens), width), -7, dtype=torch.int32)
+    ids = [(b, i) for b, n in enumerate(lens) for i in sorted({j // page for j in visible(n, window, sinks)})]
+    order = torch.randperm(len(ids) + 2, generator=g, device="cuda").cpu()[: len(ids)]
+    shape = (len(ids) + 2, page, hkv, d)
+    kc, vc = (torch.full(shape, math.nan, device="cuda", dtype=dtype) for _ in range(2))
+    for (b, i), o in zip(ids, order.tolist()):
+        table[b, i] = o
+    table = table.cuda()
+    for b, n in enumerate(lens):
+        j = torch.tensor(visible(n, window, sinks), dtype=torch.long, device="cuda")
+        if len(j):
+            at = (table[b][j // page].long(), j % page)
+            kc[at] = torch.randn(len(j), hkv, d, generator=g, device="cuda").to(dtype)
+            vc[at] = torch.randn(len(j), hkv, d, generator=g, device="cuda").to(dtype)
+    q = (torch.randn(len(lens), hq, d, generator=g, device="cuda") * spread).to(dtype)
+    return q, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def check(o, lse, q, kc, vc, table, lens, scale, window=0, sinks=0, seen=None):
+    page, hkv, d = kc.shape[1:]
+    share = q.shape[1] // hkv
+    for b, n in enumerate(lens.tolist()):
+        j = torch.tensor(seen[b] if seen else visible(n, window, sinks), dtype=torch.long, device="cuda")
+        if not len(j):
+            assert bool((o[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+            continue
+        at = (table[b][j // page].long(), j % page)
+        k, v = (c[at].double().repeat_interleave(share, 1) for c in (kc, vc))
+        x = torch.einsum("hd,jhd->hj", q[b].double(), k) * scale
+        r = (torch.einsum("hd,jhd->hj", q[b].double().abs(), k.abs()) * abs(scale)).amax(1)
+        p = torch.softmax(x, 1)
+        ref, size = torch.einsum("hj,jhd->hd", p, v), torch.einsum("hj,jhd->hd", p, v.abs())
+        fp = (2 * r * (d + 8) + len(j) / 8 + 64)[:, None] * 2.0 ** -23
+        bound = UNIT[o.dtype] * ref.abs() + (fp + 2.0 ** -16) * size + 2.0 ** -24
+        assert bool(((o[b].double() - ref).abs() <= bound).all()), (b, n)
+        assert bool(((lse[b].double() - torch.logsumexp(x, 1)).abs() <= fp[:, 0]).all()), (b, n)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (6, 2), (8, 1), (18, 2), (16, 1), (40, 2)])
+def test_head_layouts(W, ws, hq, hkv, d, dtype):
+    a = make(hq * d, [1, 0, 17, 64, 65, 333], hq, hkv, d, 16, dtype)
+    check(*W.attend_paged(*a, workspace=ws, with_lse=True), *a, d ** -0.5)
+
+
+@pytest.mark.parametrize("page", [1, 7, 16, 64, 100])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 3), (63, 1), (64, 4), (200, 40), (5000, 4)])
+def test_lengths_pages_and_windows(W, ws, page, window, sinks):
+    lens = [0, 1, 2, 3, 4, 5, 15, 16, 31, 63, 64, 65, 67, 68, 69, 127, 128, 129, 200, 240, 241, 1000, 3001]
+    a = make(page + window, lens, 4, 2, 64, page, torch.bfloat16, window, sinks)
+    check(*W.attend_paged(*a, window=window, sinks=sinks, workspace=ws, with_lse=True), *a, 0.125, window, sinks)
+
+
+@pytest.mark.parametrize("lens", [[40000], [20000, 1, 30011], [1] * 700, [0] * 5, [0, 9000, 0, 0, 129], [130] * 331])
+def test_splits(W, ws, lens):
+    """One lane over all CTAs, lanes that share CTAs, more lanes than threads of one."""
+    a = make(len(lens), lens, 8, 2, 128, 32, torch.bfloat16)
+    check(*W.attend_paged(*a, workspace=ws, with_lse=True), *a, 128 ** -0.5)
+
+
+def test_large_scores_and_other_scale(W, ws):
+    """Weights that are nearly all on one key, and a negative scale."""
+    a = make(5, [700, 64, 33], 8, 4, 64, 16, torch.float16, spread=30.0)
+    check(*W.attend_paged(*a, workspace=ws, with_lse=True), *a, 0.125)
+    check(*W.attend_paged(*a, scale=-0.02, workspace=ws, with_lse=True), *a, -0.02)
+
+
+def test_missing_pages_and_long_lengths(W, ws):
+    """Tokens of pages outside the pool are not seen; a length past the table ends with it."""
+    lens = [100, 100, 64]
+    q, kc, vc, table, n = make(6, lens, 2, 1, 64, 16, torch.bfloat16)
+    table = table[:, :6].contiguous()            # 96 tokens
+    table[0, 2], table[1, 0], table[1, 5], table[2] = -1, kc.shape[0], 2 ** 31 - 1, -2 ** 31
+    seen = [[j for j in range(96) if j // 16 != 2], list(range(16, 80)), []]
+    big = torch.tensor([100, 2 ** 31 - 1, 64], dtype=torch.int32, device="cuda")
+    o, lse = W.attend_paged(q, kc, vc, table, big, workspace=ws, with_lse=True)
+    check(o, lse, q, kc, vc, table, n, 0.125, seen=seen)
+    n[:] = -5
+    o, lse = W.attend_paged(q, kc, vc, table, n, workspace=ws, with_lse=True)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_infinities_and_nan_in_seen_places(W, ws):
+    """What is seen counts as the formula says: a NaN spreads to its own lane
+    and heads alone, a key of weight zero (-inf score) weighs nothing."""
+    q, kc, vc, table, n = make(7, [50, 50], 4, 2, 64, 16, torch.float16)
+    clean = W.attend_paged(q, kc, vc, table, n, workspace=ws)
+    vc2 = vc.clone()
+    vc2[table[1, 1].long(), 3, 1, 5] = math.nan
+    o = W.attend_paged(q, kc, vc2, table, n, workspace=ws)
+    assert torch.equal(o[0], clean[0]) and torch.equal(o[1, :2], clean[1, :2])
+    assert bool(o[1, 2:, 5].isnan().all()) and int(o[1, 2:].isnan().sum()) == 2
+    q[:] = 1.0
+    kc2 = kc.clone()
+    kc2[table[0, 0].long(), 2] = -65504.0
+    kc2[table[0, 0].long(), 2, :, 0] = -math.inf
+    o, lse = W.attend_paged(q, kc2, vc, table, n, workspace=ws, with_lse=True)
+    seen = [[j for j in range(50) if j != 2], list(range(50))]
+    check(o, lse, q, kc2, vc, table, n, 0.125, seen=seen)
+
+
+def test_layouts_streams_and_repeats(W, ws):
+    """Heads before places, q and o as parts of wider tensors, a table with
+    longer rows, another stream with a workspace of its own; the same bits
+    every time."""
+    q, kc, vc, table, n = make(8, [5000, 300, 1, 77], 12, 4, 128, 16, torch.bfloat16)
+    kc, vc = (c.transpose(1, 2).contiguous().transpose(1, 2) for c in (kc, vc))
+    wide = torch.zeros(4, 20, 128, device="cuda", dtype=torch.bfloat16)
+    wide[:, 4:16] = q
+    q = wide[:, 4:16]
+    long = torch.zeros(4, table.shape[1] + 9, dtype=torch.int32, device="cuda")
+    long[:, : table.shape[1]] = table
+    table = long[:, : table.shape[1]]
+    room = torch.full((4, 14, 130), 3.0, device="cuda", dtype=torch.bfloat16)
+    out = room[:, 1:13, :128]
+    first, lse = W.attend_paged(q, kc, vc, table, n, workspace=ws, with_lse=True, out=out)
+    assert first is out
+    check(out, lse, q, kc, vc, table, n, 128 ** -0.5)
+    assert bool((room[:, 0] == 3).all()) and bool((room[:, 13] == 3).all()) and bool((room[..., 128:] == 3).all())
+    want = out.clone()
+    torch.cuda.synchronize()
+    side, ws2 = torch.cuda.Stream(), W.attend_workspace("cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        again = W.attend_paged(q, kc, vc, table, n, workspace=ws2, stream=side)
+        side.synchronize()
+        assert torch.equal(again, want)
+    assert torch.equal(W.attend_paged(q, kc, vc, table, n), want)      # a workspace made by the call
+
+
+def test_offsets_past_32_bits(W, ws):
+    """A pool of more than 2^31 elements, its last pages in use."""
+    hkv, d, page = 8, 128, 16
+    pages = 2 ** 31 // (hkv * d * page) + 50
+    pool = torch.empty(pages, page, hkv, d, device="cuda", dtype=torch.bfloat16)
+    q, kc, vc, table, n = make(9, [300], 8, hkv, d, page, torch.bfloat16)
+    used = table[0, :19].long()
+    for c in (kc, vc):
+        pool[pages - 40: pages - 21] = c[used]
+        table2 = table.clone()
+        table2[0, :19] = torch.arange(pages - 40, pages - 21, device="cuda")
+    o, lse = W.attend_paged(q, pool, pool, table2, n, workspace=ws, with_lse=True)
+    check(o, lse, q, pool, pool, table2, n, 128 ** -0.5)
+
+
+def test_no_lanes(W, ws):
+    q, kc, vc, table, n = make(10, [5], 4, 2, 64, 16, torch.float16)
+    assert W.attend_paged(q[:0], kc, vc, table[:0], n[:0], workspace=ws).shape == (0, 4, 64)
+
+
+def test_refusals(W, ws):
+    q, kc, vc, table, n = make(11, [40, 50], 4, 2, 64, 16, torch.float16)
+    ok = dict(q=q, k_pages=kc, v_pages=vc, page_table=table, lengths=n, workspace=ws)
+    W.attend_paged(**ok)
+    for error, change in [
+            (TypeError, dict(q=q.float())), (TypeError, dict(k_pages=kc.bfloat16())),
+            (TypeError, dict(lengths=n.long())), (TypeError, dict(page_table=table.long())),
+            (ValueError, dict(q=q.cpu())), (ValueError, dict(lengths=n[:1])), (ValueError, dict(v_pages=vc[:1])),
+            (ValueError, dict(page_table=table[:1])), (ValueError, dict(workspace=ws[:100])),
+            (ValueError, dict(page_table=table.t().contiguous().t())),
+            (ValueError, dict(q=torch.zeros(2, 64, 4, device="cuda").half().transpose(1, 2))),
+            (ValueError, dict(out=torch.zeros(2, 4, 65, device="cuda").half())),
+            (W.WfstError, dict(q=torch.zeros(2, 5, 64, device="cuda").half())),    # 5 heads over 2
+            (W.WfstError, dict(q=q[..., :32], k_pages=kc[..., :32], v_pages=vc[..., :32])),
+            (W.WfstError, dict(window=-1)), (W.WfstError, dict(sinks=-1)), (W.WfstError, dict(scale=math.nan))]:
+        with pytest.raises(error):
+            W.attend_paged(**{**ok, **change})

@@ -1,0 +1,91 @@
+"""What the second-pass operators refuse without a GPU: sizes and NULL
+pointers at the C entries, host tensors and wrong types in the binding."""
+import ctypes as C
+
+import pytest
+
+import wfst_beam_search_gb300 as W
+from wfst_beam_search_gb300 import _build
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return W.load()
+
+
+def test_sizes_of_a_packed_matrix(lib):
+    # 16 outputs by 64 k are 512 bytes of codes; a group's scales of a tile 32 bytes, with zero points 64
+    assert W.wfst_quant_size(16, 64, 64, 0) == 512 + 32
+    assert W.wfst_quant_size(17, 64, 64, 1) == 2 * (512 + 64)
+    assert W.wfst_quant_size(1, 32, 32, 0) == 512 + 2 * 32          # half a block is stored as a whole one
+    assert W.wfst_quant_size(100000, 65536, 128, 0) == 6250 * (1024 * 512 + 512 * 32)   # past 2^31 bytes
+    for n, k, group in ((0, 64, 64), (16, 0, 64), (16, 64, 16), (16, 96, 64), (16, 64, 0), (-1, 64, 64)):
+        with pytest.raises(W.WfstError) as e:
+            W.wfst_quant_size(n, k, group, 0)
+        assert e.value.code == -1
+    assert lib.wfst_quant_size(16, 64, 64, 0, None) == -1
+    assert lib.wfst_quant_pack(None, None, None, 16, 64, 64, None, None) == -1
+    assert b"NULL" in lib.wfst_last_error()
+    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, 1, None, None, 16, None) == -1
+    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F32, None, 64, 1, None, None, 16, None) == -1
+    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, -1, None, None, 16, None) == -1
+    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, 0, None, None, 16, None) == 0
+
+
+def test_null_blocks(lib):
+    for f in (lib.wfst_norm_rotate, lib.wfst_attend_paged, lib.wfst_sample_tokens):
+        assert f(None, None) == -1 and b"NULL" in lib.wfst_last_error()
+    assert lib.wfst_attend_size(None) == -1
+    assert W.wfst_attend_size() > 0 and W.wfst_attend_size() % 16 == 0
+
+
+def test_fields_are_checked_in_the_blocks(lib):
+    from wfst_beam_search_gb300 import _ops
+
+    def rotate(**kw):
+        f = dict(dtype=1, tokens=1, hq=1, hkv=1, d=64, rot=64, inter=0, contexts=1, pages=1, page=16, eps=1e-6)
+        f.update(kw)
+        return lib.wfst_norm_rotate(_ops._ROTATE(*([0] * 25), *f.values()), None), lib.wfst_last_error()
+
+    def attend(**kw):
+        f = dict(dtype=1, lanes=1, hq=2, hkv=1, d=64, width=1, pages=1, page=16, window=0, sinks=0, scale=1.0)
+        f.update(kw)
+        return lib.wfst_attend_paged(_ops._ATTEND(*([0] * 20), *f.values()), None), lib.wfst_last_error()
+
+    def sample(**kw):
+        f = dict(stride=10, dtype=0, lanes=1, vocab=10, top_k=0, temp=1.0, top_p=1.0, min_p=0.0)
+        f.update(kw)
+        return lib.wfst_sample_tokens(_ops._SAMPLE(*([0] * 9), *f.values()), None), lib.wfst_last_error()
+
+    assert rotate(tokens=0)[0] == 0 and attend(lanes=0)[0] == 0 and sample(lanes=0)[0] == 0
+    for call, word, change in [
+            (rotate, b"NULL", {}), (rotate, b"dtype", dict(dtype=0)), (rotate, b"head_dim", dict(d=80)),
+            (rotate, b"rot", dict(rot=8)), (rotate, b"rot", dict(rot=128)), (rotate, b"eps", dict(eps=float("nan"))),
+            (rotate, b"counts", dict(tokens=-1)),
+            (attend, b"NULL", {}), (attend, b"dtype", dict(dtype=0)), (attend, b"head_dim", dict(d=32)),
+            (attend, b"multiple", dict(hq=3, hkv=2)), (attend, b"page_size", dict(page=0)),
+            (attend, b"2^31", dict(page=1 << 20, width=1 << 12)), (attend, b"window", dict(window=-1)),
+            (attend, b"scale", dict(scale=float("nan"))),
+            (sample, b"NULL", {}), (sample, b"dtype", dict(dtype=3)), (sample, b"vocab", dict(vocab=0)),
+            (sample, b"vocab", dict(vocab=(1 << 20) + 1)), (sample, b"stride", dict(lanes=2, stride=9)),
+            (sample, b"temperature", dict(temp=-1.0)), (sample, b"top_k", dict(top_k=-1)),
+            (sample, b"top_p", dict(top_p=0.0)), (sample, b"min_p", dict(min_p=2.0))]:
+        rc, said = call(**change)
+        assert rc == -1 and word in said, (call.__name__, change, said)
+
+
+def test_host_tensors_are_refused():
+    h = torch.zeros(2, 64, dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    pages = torch.zeros(1, 16, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        W.pack_quant(torch.zeros(4, 32, dtype=torch.uint8), torch.ones(4, 1).half())
+    with pytest.raises(ValueError):
+        W.sample_tokens(torch.zeros(2, 10), torch.zeros(2))
+    with pytest.raises(ValueError):
+        W.attend_paged(h[:, None], pages, pages, i[:, None], i)
+    with pytest.raises(ValueError):
+        W.norm_rotate(h[:, None], h[:, None], h[:, None], i, torch.zeros(4, 64), None, None, pages, pages, i)

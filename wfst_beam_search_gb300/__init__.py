@@ -20,7 +20,7 @@ import numpy as np
 from . import _build
 
 WFST_OK = 0
-WFST_F32, WFST_F16 = 0, 1
+WFST_F32, WFST_F16, WFST_BF16 = 0, 1, 2
 OVF_ARENA, OVF_KEPT, OVF_PATH = 4, 16, 32
 REC_EPS, REC_FINAL, REC_REDIRECT = 1, 2, 4
 STAT_NAMES = ["frames", "arcs_expanded", "sum_n", "sum_D", "sum_a", "sum_m", "eps",
@@ -38,7 +38,9 @@ EXPORTED = ["wfst_graph_upload", "wfst_graph_info", "wfst_graph_free", "wfst_dec
             "wfst_decoder_free", "wfst_decode", "wfst_lattice_export", "wfst_stream_create",
             "wfst_stream_advance", "wfst_stream_finalize", "wfst_stream_release", "wfst_stats",
             "wfst_decode_static", "wfst_mem_stats", "wfst_blank_skip", "wfst_test_barrier_timeout",
-            "wfst_probe_random_gather", "wfst_last_error"]
+            "wfst_probe_random_gather", "wfst_quant_size", "wfst_quant_pack", "wfst_matvec_quant",
+            "wfst_norm_rotate", "wfst_attend_size", "wfst_attend_paged", "wfst_sample_tokens",
+            "wfst_last_error"]
 
 
 class WfstError(RuntimeError):
@@ -110,6 +112,12 @@ def load(build_if_missing: bool = False):
         L.wfst_test_barrier_timeout.argtypes = [P, i64]
         L.wfst_probe_random_gather.argtypes = [P, i64, i32, i32, i32, i32, P, P]
         L.wfst_blank_skip.argtypes = [P, i32, i64, i64, i32, i32, C.c_float, P, i32, i32, P, P, P, P]
+        L.wfst_quant_size.argtypes = [i32, i32, i32, i32, C.POINTER(i64)]
+        L.wfst_quant_pack.argtypes = [P, P, P, i32, i32, i32, P, P]
+        L.wfst_matvec_quant.argtypes = [P, i32, i32, i32, i32, i32, P, i64, i32, P, P, i64, P]
+        L.wfst_attend_size.argtypes = [C.POINTER(i64)]
+        for name in ("wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens"):
+            getattr(L, name).argtypes = [P, P]    # the argument block, the stream
         for name in EXPORTED:
             if name not in ("wfst_last_error", "wfst_graph_free", "wfst_decoder_free"):
                 getattr(L, name).restype = C.c_int
@@ -267,6 +275,55 @@ def blank_skip(lp, lens, threshold=0.98, blank_id=0, stream=None):
     wfst_blank_skip(ptr, dt, sb, st, V, int(blank_id), threshold, _ptr(lens_d), B, T, _ptr(out),
                     _ptr(out_lens), _ptr(fmap), _stream(s))
     return out, out_lens, fmap
+
+
+def wfst_quant_size(n, k, group, zeros):
+    out = C.c_int64()
+    _check(load().wfst_quant_size(n, k, group, int(bool(zeros)), C.byref(out)))
+    return out.value
+
+
+def wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, stream):
+    _check(load().wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, stream))
+
+
+def wfst_matvec_quant(packed_ptr, n, k, group, zeros, dtype, x_ptr, stride_x, rows, bias_ptr, y_ptr, stride_y,
+                      stream):
+    _check(load().wfst_matvec_quant(packed_ptr, n, k, group, zeros, dtype, x_ptr, stride_x, rows, bias_ptr, y_ptr,
+                                    stride_y, stream))
+
+
+def wfst_norm_rotate(args, stream):
+    """``args``: a wfst_rotate_args block (bytes or a pointer), as for the two calls below."""
+    _check(load().wfst_norm_rotate(args, stream))
+
+
+def wfst_attend_size():
+    out = C.c_int64()
+    _check(load().wfst_attend_size(C.byref(out)))
+    return out.value
+
+
+def wfst_attend_paged(args, stream):
+    _check(load().wfst_attend_paged(args, stream))
+
+
+def wfst_sample_tokens(args, stream):
+    _check(load().wfst_sample_tokens(args, stream))
+
+
+#: the second-pass operators on torch tensors (``_ops``), loaded on first use: the decoder itself needs no torch
+_OPS = ("QuantMatrix", "pack_quant", "matvec_quant", "norm_rotate", "attend_workspace", "attend_paged",
+        "sample_tokens")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import _ops
+        for n in _OPS:
+            globals()[n] = getattr(_ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 # ------------------------------------------------------------ convenience wrappers
