@@ -422,14 +422,18 @@ int wfst_blank_skip(const void* log_probs, int32_t dtype, int64_t stride_b, int6
  * counterpart): products with 4-bit weights, the heads' norm and rotation
  * with the write into the paged cache, attention of the new token over that
  * cache, and the draw of the next token.  Shared by all of them:
- *   - every array is device memory of one device (host pointers are refused);
- *     nothing is allocated and nothing is copied to the host: the kernels are
- *     enqueued on `stream`, on the arrays' own device, and the call returns
- *     without waiting;
+ *   - every array is device memory of one device; nothing is allocated and
+ *     nothing is copied to the host: the kernels are enqueued on `stream`, on
+ *     the arrays' own device, and the call returns without waiting;
+ *   - `device` is that device where the caller knows it, as a tensor library
+ *     does, and -1 where the call has to ask the driver about every pointer
+ *     (half a microsecond each): it then refuses host pointers and arrays of
+ *     different devices;
  *   - `dtype` is WFST_F16 or WFST_BF16 for weights, activations and the
  *     cache, and also WFST_F32 for logits; sums, softmax statistics and norms
  *     are held in fp32 or wider and rounded once at the end;
- *   - strides count elements; the innermost axis has unit stride;
+ *   - strides count elements; the innermost axis has unit stride, and a
+ *     stride along an axis of one entry is not read;
  *   - results do not depend on the order in which CTAs run.
  */
 
@@ -451,9 +455,13 @@ int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros,
  * [rows, k] (16-byte aligned, stride_x a multiple of 8) and a packed matrix.
  * bias [n] may be NULL.  rows = 0 does nothing.  Errors: INVALID_ARG, CUDA.
  */
-int wfst_matvec_quant(const void* packed, int32_t n, int32_t k, int32_t group, int32_t zeros, int32_t dtype,
-                      const void* x, int64_t stride_x, int32_t rows, const void* bias, void* y,
-                      int64_t stride_y, void* stream);
+typedef struct {
+  const void *packed, *x, *bias;
+  void* y;
+  int64_t stride_x, stride_y; /* between rows */
+  int32_t device, dtype, n, k, group, zeros, rows;
+} wfst_matvec_args;
+int wfst_matvec_quant(const wfst_matvec_args* args, void* stream);
 
 /*
  * The new tokens' heads: each head of q and k is divided by the root of its
@@ -478,7 +486,7 @@ typedef struct {
   void *q_out, *k_pages, *v_pages;  /* pages: [num_pages, page_size, kv_heads, head_dim] in any stride order */
   int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2]; /* token, head */
   int64_t k_page_stride[3], v_page_stride[3];                   /* page, place, head */
-  int32_t dtype, tokens, q_heads, kv_heads, head_dim, rot, interleaved, contexts, num_pages, page_size;
+  int32_t device, dtype, tokens, q_heads, kv_heads, head_dim, rot, interleaved, contexts, num_pages, page_size;
   float eps;
 } wfst_rotate_args;
 int wfst_norm_rotate(const wfst_rotate_args* args, void* stream);
@@ -509,7 +517,7 @@ typedef struct {
   void* workspace;
   int64_t q_stride[2], o_stride[2], lse_stride, table_stride;
   int64_t k_page_stride[3], v_page_stride[3]; /* page, place, head */
-  int32_t dtype, lanes, q_heads, kv_heads, head_dim, table_width, num_pages, page_size, window, sinks;
+  int32_t device, dtype, lanes, q_heads, kv_heads, head_dim, table_width, num_pages, page_size, window, sinks;
   float scale;
 } wfst_attend_args;
 int wfst_attend_size(int64_t* bytes);
@@ -539,7 +547,7 @@ typedef struct {
   float* logprobs;  /* [lanes] */
   int32_t* kept;    /* [lanes] */
   int64_t stride;   /* between lanes of logits */
-  int32_t dtype, lanes, vocab, top_k;
+  int32_t device, dtype, lanes, vocab, top_k;
   float temperature, top_p, min_p;
 } wfst_sample_args;
 int wfst_sample_tokens(const wfst_sample_args* args, void* stream);

@@ -134,7 +134,13 @@ def test_refusals(W):
         W.pack_quant(codes.int(), scales)
     with pytest.raises(ValueError):
         W.pack_quant(codes.cpu(), scales)
-    host = np.zeros(1 << 16, np.uint8)      # host memory at the C entry
+    from wfst_beam_search_gb300 import _ops
+    host = np.zeros(1 << 16, np.uint8)      # host memory at the C entry, which has to ask
     with pytest.raises(W.WfstError):
-        W.wfst_matvec_quant(w.ptr, 40, 128, 64, 0, W.WFST_F16, (host.ctypes.data + 15) & ~15, 128, 1, None,
-                            x.data_ptr(), 40, None)
+        W.wfst_matvec_quant(_ops._MATVEC(w.ptr, (host.ctypes.data + 15) & ~15, 0, x.data_ptr(), 128, 40, -1, W.WFST_F16,
+                                         40, 128, 64, 0, 1), None)
+    y = torch.empty(1, 40, device="cuda").half()      # and device memory
+    W.wfst_matvec_quant(_ops._MATVEC(w.ptr, x.data_ptr(), 0, y.data_ptr(), 128, 40, -1, W.WFST_F16, 40, 128, 64, 0, 1),
+                        None)
+    torch.cuda.synchronize()
+    assert torch.equal(y, W.matvec_quant(x, w)[:1])

@@ -29,14 +29,10 @@ def test_sizes_of_a_packed_matrix(lib):
     assert lib.wfst_quant_size(16, 64, 64, 0, None) == -1
     assert lib.wfst_quant_pack(None, None, None, 16, 64, 64, None, None) == -1
     assert b"NULL" in lib.wfst_last_error()
-    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, 1, None, None, 16, None) == -1
-    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F32, None, 64, 1, None, None, 16, None) == -1
-    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, -1, None, None, 16, None) == -1
-    assert lib.wfst_matvec_quant(None, 16, 64, 64, 0, W.WFST_F16, None, 64, 0, None, None, 16, None) == 0
 
 
 def test_null_blocks(lib):
-    for f in (lib.wfst_norm_rotate, lib.wfst_attend_paged, lib.wfst_sample_tokens):
+    for f in (lib.wfst_matvec_quant, lib.wfst_norm_rotate, lib.wfst_attend_paged, lib.wfst_sample_tokens):
         assert f(None, None) == -1 and b"NULL" in lib.wfst_last_error()
     assert lib.wfst_attend_size(None) == -1
     assert W.wfst_attend_size() > 0 and W.wfst_attend_size() % 16 == 0
@@ -45,23 +41,30 @@ def test_null_blocks(lib):
 def test_fields_are_checked_in_the_blocks(lib):
     from wfst_beam_search_gb300 import _ops
 
+    def matvec(**kw):
+        f = dict(sx=64, sy=16, device=-1, dtype=1, n=16, k=64, group=64, zeros=0, rows=1)
+        f.update(kw)
+        return lib.wfst_matvec_quant(_ops._MATVEC(*([0] * 4), *f.values()), None), lib.wfst_last_error()
+
     def rotate(**kw):
-        f = dict(dtype=1, tokens=1, hq=1, hkv=1, d=64, rot=64, inter=0, contexts=1, pages=1, page=16, eps=1e-6)
+        f = dict(device=-1, dtype=1, tokens=1, hq=1, hkv=1, d=64, rot=64, inter=0, contexts=1, pages=1, page=16, eps=1e-6)
         f.update(kw)
         return lib.wfst_norm_rotate(_ops._ROTATE(*([0] * 25), *f.values()), None), lib.wfst_last_error()
 
     def attend(**kw):
-        f = dict(dtype=1, lanes=1, hq=2, hkv=1, d=64, width=1, pages=1, page=16, window=0, sinks=0, scale=1.0)
+        f = dict(device=-1, dtype=1, lanes=1, hq=2, hkv=1, d=64, width=1, pages=1, page=16, window=0, sinks=0, scale=1.0)
         f.update(kw)
         return lib.wfst_attend_paged(_ops._ATTEND(*([0] * 20), *f.values()), None), lib.wfst_last_error()
 
     def sample(**kw):
-        f = dict(stride=10, dtype=0, lanes=1, vocab=10, top_k=0, temp=1.0, top_p=1.0, min_p=0.0)
+        f = dict(stride=10, device=-1, dtype=0, lanes=1, vocab=10, top_k=0, temp=1.0, top_p=1.0, min_p=0.0)
         f.update(kw)
         return lib.wfst_sample_tokens(_ops._SAMPLE(*([0] * 9), *f.values()), None), lib.wfst_last_error()
 
-    assert rotate(tokens=0)[0] == 0 and attend(lanes=0)[0] == 0 and sample(lanes=0)[0] == 0
+    assert matvec(rows=0)[0] == 0 and rotate(tokens=0)[0] == 0 and attend(lanes=0)[0] == 0 and sample(lanes=0)[0] == 0
     for call, word, change in [
+            (matvec, b"NULL", {}), (matvec, b"dtype", dict(dtype=0)), (matvec, b"rows", dict(rows=-1)),
+            (matvec, b"group", dict(group=16)), (matvec, b"multiple", dict(k=96)),
             (rotate, b"NULL", {}), (rotate, b"dtype", dict(dtype=0)), (rotate, b"head_dim", dict(d=80)),
             (rotate, b"rot", dict(rot=8)), (rotate, b"rot", dict(rot=128)), (rotate, b"eps", dict(eps=float("nan"))),
             (rotate, b"counts", dict(tokens=-1)),

@@ -114,9 +114,8 @@ def load(build_if_missing: bool = False):
         L.wfst_blank_skip.argtypes = [P, i32, i64, i64, i32, i32, C.c_float, P, i32, i32, P, P, P, P]
         L.wfst_quant_size.argtypes = [i32, i32, i32, i32, C.POINTER(i64)]
         L.wfst_quant_pack.argtypes = [P, P, P, i32, i32, i32, P, P]
-        L.wfst_matvec_quant.argtypes = [P, i32, i32, i32, i32, i32, P, i64, i32, P, P, i64, P]
         L.wfst_attend_size.argtypes = [C.POINTER(i64)]
-        for name in ("wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens"):
+        for name in ("wfst_matvec_quant", "wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens"):
             getattr(L, name).argtypes = [P, P]    # the argument block, the stream
         for name in EXPORTED:
             if name not in ("wfst_last_error", "wfst_graph_free", "wfst_decoder_free"):
@@ -287,14 +286,12 @@ def wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, s
     _check(load().wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, stream))
 
 
-def wfst_matvec_quant(packed_ptr, n, k, group, zeros, dtype, x_ptr, stride_x, rows, bias_ptr, y_ptr, stride_y,
-                      stream):
-    _check(load().wfst_matvec_quant(packed_ptr, n, k, group, zeros, dtype, x_ptr, stride_x, rows, bias_ptr, y_ptr,
-                                    stride_y, stream))
+def wfst_matvec_quant(args, stream):
+    """``args``: a wfst_matvec_args block (bytes or a pointer), as for the calls below."""
+    _check(load().wfst_matvec_quant(args, stream))
 
 
 def wfst_norm_rotate(args, stream):
-    """``args``: a wfst_rotate_args block (bytes or a pointer), as for the two calls below."""
     _check(load().wfst_norm_rotate(args, stream))
 
 

@@ -509,14 +509,16 @@ template <typename T, int D, int NT>
 cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
   auto* fn = attend_kernel<T, D, NT>;
   constexpr int smem = kSmem<D, NT>;
-  static int resident = 0;  // CTAs of a multiprocessor
-  if (!resident) {
+  static OpsOnce once;
+  static int resident = 1;  // CTAs of a multiprocessor
+  if (const int dev = ops_current(); !once(dev)) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int v = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps * 32, smem);
     if (e != cudaSuccess) return e;
     resident = v > 0 ? v : 1;
+    once.set(dev);
   }
   int64_t grid = (int64_t)resident * ops_sm_count();
   if (grid > kMaxGrid) grid = kMaxGrid;
@@ -573,23 +575,25 @@ extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
     return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: NULL argument");
   for (const void* p : {r->q, r->k_pages, r->v_pages, (const void*)r->workspace})
     if (!aligned(p, 16)) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: arrays must be 16-byte aligned");
-  for (int64_t s : {r->q_stride[0], r->q_stride[1], r->k_page_stride[0], r->k_page_stride[1], r->k_page_stride[2],
-                    r->v_page_stride[0], r->v_page_stride[1], r->v_page_stride[2]})
-    if (s % 8) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: strides must be multiples of 8 elements");
-  const int dev = ops_device({r->q, r->k_pages, r->v_pages, r->table, r->lengths, r->o, r->lse, r->workspace});
+  auto stride = [&](int64_t s, int64_t n) { return n > 1 ? s : 0; };
+  Args a;
+  a.sq_b = stride(r->q_stride[0], r->lanes), a.sq_h = stride(r->q_stride[1], r->q_heads);
+  a.ck_p = stride(r->k_page_stride[0], r->num_pages), a.ck_s = stride(r->k_page_stride[1], r->page_size);
+  a.cv_p = stride(r->v_page_stride[0], r->num_pages), a.cv_s = stride(r->v_page_stride[1], r->page_size);
+  a.ck_h = stride(r->k_page_stride[2], r->kv_heads), a.cv_h = stride(r->v_page_stride[2], r->kv_heads);
+  if ((a.sq_b | a.sq_h | a.ck_p | a.ck_s | a.ck_h | a.cv_p | a.cv_s | a.cv_h) & 7)
+    return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: strides must be multiples of 8 elements");
+  const int dev = ops_device(r->device, {r->q, r->k_pages, r->v_pages, r->table, r->lengths, r->o, r->lse, r->workspace});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: every array must be device memory of one device");
   OpsDevice guard(dev);
-  Args a;
+  if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "attend_paged: device");
   a.q = r->q, a.kc = r->k_pages, a.vc = r->v_pages;
   a.table = r->table, a.lens = r->lengths;
   a.o = r->o, a.lse = r->lse;
   a.counters = reinterpret_cast<uint32_t*>(r->workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(r->workspace) + kCounterBytes);
-  a.sq_b = r->q_stride[0], a.sq_h = r->q_stride[1];
   a.so_b = r->o_stride[0], a.so_h = r->o_stride[1], a.sl_b = r->lse_stride;
-  a.ck_p = r->k_page_stride[0], a.ck_s = r->k_page_stride[1], a.ck_h = r->k_page_stride[2];
-  a.cv_p = r->v_page_stride[0], a.cv_s = r->v_page_stride[1], a.cv_h = r->v_page_stride[2];
-  a.st_b = r->table_stride;
+  a.st_b = stride(r->table_stride, r->lanes);
   a.lanes = r->lanes, a.hkv = r->kv_heads, a.share = r->q_heads / r->kv_heads, a.runs = 1;
   a.width = r->table_width, a.page = r->page_size, a.num_pages = r->num_pages;
   a.window = r->window, a.sinks = r->window ? r->sinks : 0;

@@ -222,9 +222,11 @@ template <typename T, int NT, bool SUB, bool ZERO>
 cudaError_t launch(const Args& a, cudaStream_t st) {
   constexpr int smem = kWarps * NT * 8 * kMT * 16 * (int)sizeof(float);
   auto* fn = matvec_kernel<T, NT, SUB, ZERO>;
-  if (smem > 48 * 1024) {
+  static OpsOnce once;
+  if (const int dev = ops_current(); smem > 48 * 1024 && !once(dev)) {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    once.set(dev);
   }
   const dim3 grid((a.tiles + kMT - 1) / kMT, (a.rows + NT * 8 - 1) / (NT * 8));
   fn<<<grid, kWarps * 32, smem, st>>>(a);
@@ -295,9 +297,10 @@ extern "C" int wfst_quant_pack(const uint8_t* codes, const void* scales, const v
   if (!codes || !scales || !packed) return api_fail(WFST_ERR_INVALID_ARG, "quant_pack: NULL argument");
   if (const char* why = sizes(n, k, group, zeros != nullptr, &s)) return api_fail(WFST_ERR_INVALID_ARG, why);
   if (!aligned(packed, 16)) return api_fail(WFST_ERR_INVALID_ARG, "quant_pack: packed must be 16-byte aligned");
-  const int dev = ops_device({codes, scales, zeros, packed});
+  const int dev = ops_device(-1, {codes, scales, zeros, packed});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "quant_pack: every array must be device memory of one device");
   OpsDevice guard(dev);
+  if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "quant_pack: device");
   cudaStream_t st = (cudaStream_t)stream;
   const int grid = ops_sm_count() * 8;
   pack_codes<<<grid, 256, 0, st>>>(codes, n, k, s.blocks, s.code_bytes / 4, reinterpret_cast<uint32_t*>(packed));
@@ -310,40 +313,41 @@ extern "C" int wfst_quant_pack(const uint8_t* codes, const void* scales, const v
   return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "quant_pack: pack_scales launch");
 }
 
-extern "C" int wfst_matvec_quant(const void* packed, int32_t n, int32_t k, int32_t group, int32_t zeros, int32_t dtype,
-                                 const void* x, int64_t stride_x, int32_t rows, const void* bias, void* y,
-                                 int64_t stride_y, void* stream) {
+extern "C" int wfst_matvec_quant(const wfst_matvec_args* r, void* stream) {
   Sizes s;
-  if (const char* why = sizes(n, k, group, zeros != 0, &s)) return api_fail(WFST_ERR_INVALID_ARG, why);
-  if (rows < 0) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: rows must be >= 0");
-  if (dtype != WFST_F16 && dtype != WFST_BF16) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: bad dtype");
-  if (rows == 0) return WFST_OK;
-  if (!packed || !x || !y) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: NULL argument");
-  if (!aligned(packed, 16) || !aligned(x, 16) || stride_x % 8)
+  if (!r) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: NULL argument");
+  if (const char* why = sizes(r->n, r->k, r->group, r->zeros != 0, &s)) return api_fail(WFST_ERR_INVALID_ARG, why);
+  if (r->rows < 0) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: rows must be >= 0");
+  if (r->dtype != WFST_F16 && r->dtype != WFST_BF16) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: bad dtype");
+  if (r->rows == 0) return WFST_OK;
+  if (!r->packed || !r->x || !r->y) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: NULL argument");
+  if (!aligned(r->packed, 16) || !aligned(r->x, 16) || (r->rows > 1 && r->stride_x % 8))
     return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: packed and the rows of x must be 16-byte aligned");
-  if (rows > 1 && (stride_x < 0 || stride_y < n))
+  if (r->rows > 1 && (r->stride_x < 0 || r->stride_y < r->n))
     return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: stride_y must be >= n and stride_x >= 0");
-  if (rows > 65535 * 32) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: too many rows");
-  const int dev = ops_device({packed, x, bias, y});
+  if (r->rows > 65535 * 32) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: too many rows");
+  const int dev = ops_device(r->device, {r->packed, r->x, r->bias, r->y});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: every array must be device memory of one device");
   OpsDevice guard(dev);
+  if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "matvec_quant: device");
   Args a;
-  a.codes = reinterpret_cast<const uint4*>(packed);
-  a.scales = static_cast<const char*>(packed) + s.code_bytes;
-  a.x = x;
-  a.bias = bias;
-  a.y = y;
-  a.sx = stride_x;
-  a.sy = stride_y;
-  a.n = n;
-  a.k = k;
-  a.rows = rows;
+  a.codes = reinterpret_cast<const uint4*>(r->packed);
+  a.scales = static_cast<const char*>(r->packed) + s.code_bytes;
+  a.x = r->x;
+  a.bias = r->bias;
+  a.y = r->y;
+  a.sx = r->rows > 1 ? r->stride_x : 0;
+  a.sy = r->rows > 1 ? r->stride_y : 0;
+  a.n = r->n;
+  a.k = r->k;
+  a.rows = r->rows;
   a.tiles = (int32_t)s.tiles;
   a.blocks = (int32_t)s.blocks;
   a.groups_p = (int32_t)s.groups_p;
-  a.group = group;
+  a.group = r->group;
   cudaStream_t st = (cudaStream_t)stream;
+  const bool zeros = r->zeros != 0;
   const cudaError_t e =
-      dtype == WFST_F16 ? by_rows<__half>(a, zeros != 0, st) : by_rows<__nv_bfloat16>(a, zeros != 0, st);
+      r->dtype == WFST_F16 ? by_rows<__half>(a, zeros, st) : by_rows<__nv_bfloat16>(a, zeros, st);
   return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "matvec_quant launch");
 }

@@ -15,10 +15,11 @@ namespace wfst {
 int api_fail(int code, const char* msg);
 int api_cuda_fail(cudaError_t e, const char* what);
 
-// Every array of these calls is device memory of one device.  Returns that
-// device, or -1 when a pointer is not device memory or lies elsewhere; NULL
-// entries (optional arrays) are skipped.
-inline int ops_device(std::initializer_list<const void*> ptrs) {
+// Every array of these calls is device memory of one device: `given` where the
+// caller knows it.  Otherwise asks the driver; -1 when a pointer is not device
+// memory or lies elsewhere; NULL entries (optional arrays) are skipped.
+inline int ops_device(int given, std::initializer_list<const void*> ptrs) {
+  if (given >= 0) return given;
   int dev = -1;
   for (const void* p : ptrs) {
     if (!p) continue;
@@ -37,9 +38,11 @@ inline int ops_device(std::initializer_list<const void*> ptrs) {
 // Makes `dev` current for a launch and puts the caller's device back.
 struct OpsDevice {
   int prev = -1, dev;
+  cudaError_t err;
   explicit OpsDevice(int d) : dev(d) {
-    cudaGetDevice(&prev);
-    if (prev != dev) cudaSetDevice(dev);
+    err = cudaGetDevice(&prev);
+    if (err == cudaSuccess && prev != dev) err = cudaSetDevice(dev);
+    if (err != cudaSuccess) cudaGetLastError();
   }
   ~OpsDevice() {
     if (prev >= 0 && prev != dev) cudaSetDevice(prev);
@@ -47,8 +50,21 @@ struct OpsDevice {
   OpsDevice(const OpsDevice&) = delete;
 };
 
+// What a kernel needs set up once per device (its shared memory size): the
+// flags of the devices where that is done.
+struct OpsOnce {
+  uint64_t done = 0;
+  bool operator()(int dev) const { return dev < 64 && (done >> dev & 1); }
+  void set(int dev) { done |= dev < 64 ? (uint64_t)1 << dev : 0; }
+};
+
 // Multiprocessors of the current device (cached per device; 152 on GB300).
 int ops_sm_count();
+inline int ops_current() {
+  int d = 0;
+  cudaGetDevice(&d);
+  return d;
+}
 
 inline bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 

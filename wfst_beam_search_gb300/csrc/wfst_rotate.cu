@@ -175,24 +175,26 @@ extern "C" int wfst_norm_rotate(const wfst_rotate_args* r, void* stream) {
   for (const void* p : {r->q, r->k, r->v, r->q_gain, r->k_gain, (const void*)r->q_out, (const void*)r->k_pages,
                         (const void*)r->v_pages})
     if (!aligned(p, 16)) return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: arrays must be 16-byte aligned");
-  for (int64_t s : {r->q_stride[0], r->q_stride[1], r->k_stride[0], r->k_stride[1], r->v_stride[0], r->v_stride[1],
-                    r->out_stride[0], r->out_stride[1], r->k_page_stride[0], r->k_page_stride[1], r->k_page_stride[2],
-                    r->v_page_stride[0], r->v_page_stride[1], r->v_page_stride[2]})
-    if (s % 8) return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: strides must be multiples of 8 elements");
-  const int dev = ops_device({r->q, r->k, r->v, r->q_gain, r->k_gain, r->positions, r->slots, r->table, r->q_out,
+  auto stride = [&](int64_t s, int64_t n) { return n > 1 ? s : 0; };
+  Args a;
+  a.sq_t = stride(r->q_stride[0], r->tokens), a.sq_h = stride(r->q_stride[1], r->q_heads);
+  a.sk_t = stride(r->k_stride[0], r->tokens), a.sk_h = stride(r->k_stride[1], r->kv_heads);
+  a.sv_t = stride(r->v_stride[0], r->tokens), a.sv_h = stride(r->v_stride[1], r->kv_heads);
+  a.so_t = stride(r->out_stride[0], r->tokens), a.so_h = stride(r->out_stride[1], r->q_heads);
+  a.ck_p = stride(r->k_page_stride[0], r->num_pages), a.ck_s = stride(r->k_page_stride[1], r->page_size);
+  a.cv_p = stride(r->v_page_stride[0], r->num_pages), a.cv_s = stride(r->v_page_stride[1], r->page_size);
+  a.ck_h = stride(r->k_page_stride[2], r->kv_heads), a.cv_h = stride(r->v_page_stride[2], r->kv_heads);
+  if ((a.sq_t | a.sq_h | a.sk_t | a.sk_h | a.sv_t | a.sv_h | a.so_t | a.so_h | a.ck_p | a.ck_s | a.ck_h | a.cv_p |
+       a.cv_s | a.cv_h) & 7)
+    return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: strides must be multiples of 8 elements");
+  const int dev = ops_device(r->device, {r->q, r->k, r->v, r->q_gain, r->k_gain, r->positions, r->slots, r->table, r->q_out,
                               r->k_pages, r->v_pages});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: every array must be device memory of one device");
   OpsDevice guard(dev);
-  Args a;
+  if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "norm_rotate: device");
   a.q = r->q, a.k = r->k, a.v = r->v, a.qw = r->q_gain, a.kw = r->k_gain;
   a.pos = r->positions, a.slots = r->slots, a.table = r->table;
   a.qo = r->q_out, a.kc = r->k_pages, a.vc = r->v_pages;
-  a.sq_t = r->q_stride[0], a.sq_h = r->q_stride[1];
-  a.sk_t = r->k_stride[0], a.sk_h = r->k_stride[1];
-  a.sv_t = r->v_stride[0], a.sv_h = r->v_stride[1];
-  a.so_t = r->out_stride[0], a.so_h = r->out_stride[1];
-  a.ck_p = r->k_page_stride[0], a.ck_s = r->k_page_stride[1], a.ck_h = r->k_page_stride[2];
-  a.cv_p = r->v_page_stride[0], a.cv_s = r->v_page_stride[1], a.cv_h = r->v_page_stride[2];
   a.items = heads * r->tokens;
   a.capacity = r->kv_heads ? (int64_t)r->num_pages * r->page_size : 0;
   a.tokens = r->tokens, a.hq = r->q_heads, a.hkv = r->kv_heads, a.rot = r->rot;

@@ -18,9 +18,15 @@
 // A pass has to read the logits once, which takes microseconds; what bounds it
 // is the chain of row-wide decisions (largest logit, k-th logit, total weight,
 // weight's threshold, drawn token).  A cluster of CTAs takes one row, so a
-// decision costs a cluster barrier and not a launch.  Thresholds come from
-// radix selection on the logits' ordered bits, 11 bits a level, over counts
-// (k) or weights (p): no sort.
+// decision costs a cluster barrier and not a launch.  No sort of the row:
+//   - a histogram of the distance to the largest logit, in linear bins, counts
+//     (k) or weighs (p) the row and tells the bin where the rule is met.  Bins
+//     are at most 1/64 wide in y, so an element's weight is its bin's upper one
+//     times 1 - z + z^2/2 to 2^-20, and one 32-bit add per element does;
+//   - the elements of that bin are gathered, ordered exactly (logit, index) and
+//     walked with exact sums;
+//   - where the bin holds too many (flat or coarsely rounded rows), radix
+//     selection on the logits' ordered bits takes over, with exact sums.
 #include <cooperative_groups.h>
 
 #include "wfst_ops.h"
@@ -33,6 +39,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kList = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kFixed = 43;
 
@@ -84,88 +91,390 @@ struct Row {
       for (int j = 0; j < VEC; j++) v[j] = e + j >= 0 && e + j < vocab ? canonical(to_f32(p[e + j])) : -INFINITY;
     }
   }
-  __device__ __forceinline__ bool has(int i, int j) const {
-    const int e = i * VEC - pad + j;
-    return e >= 0 && e < vocab;
-  }
 };
 
 struct Shared {
-  uint32_t count[2][kBins];
-  unsigned long long weight[2][kBins];
-  unsigned long long warp_a[4][kWarps];  // one row per use: a reader is never overtaken
-  uint32_t warp_b[4][kWarps];
+  uint32_t hist[kBins];
+  uint64_t list[kList];           // every CTA's copy of what was gathered
+  uint64_t mine[kList];           // what this CTA gathered
+  uint64_t warp_a[4][kWarps];     // one row per use: a reader is never overtaken
+  uint32_t warp_b[2][kWarps];
   float top[kWarps];
-  uint32_t scan_c[kWarps];
-  unsigned long long scan_w[kWarps];
-  uint32_t bin;
-  unsigned long long above;
+  uint64_t scan[kWarps + 1];
+  uint64_t above, cut;
+  uint32_t bin, count, fits;
 };
 
-// From the largest bin down, the first one where the running sum reaches
-// `want` (1 <= want <= the bins' sum); *above is the sum before it.  Every CTA
-// of the cluster adds up all CTAs' bins and finds the same.
-template <typename V>
-__device__ __forceinline__ uint32_t find_bin(cg::cluster_group& cl, V* bins, unsigned long long want, Shared* sh,
-                                             unsigned long long* above) {
-  constexpr int P = kBins / kThreads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned long long v[P], mine = 0;
+// Order of the tokens: larger logit first, then lower index.
+__device__ __forceinline__ uint64_t order_of(float x, int e) {
+  return (uint64_t)key_of(x) << 32 | (0xffffffffu - (uint32_t)e);
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
-  for (int i = 0; i < P; i++) v[i] = 0;
-  const int top = kBins - 1 - tid * P;  // this thread's bins: top, top - 1, ...
-  for (unsigned r = 0; r < cl.num_blocks(); r++) {
-    const V* b = cl.map_shared_rank(bins, r);
-#pragma unroll
-    for (int i = 0; i < P; i++) v[i] += b[top - i];
-  }
-#pragma unroll
-  for (int i = 0; i < P; i++) mine += v[i];
-  unsigned long long incl = mine;
+  for (int x = 16; x; x /= 2) v += __shfl_xor_sync(0xffffffffu, v, x);
+  return v;
+}
+
+// Inclusive sums over the CTA's threads of one value each; *all is their total.
+__device__ __forceinline__ uint64_t cta_scan(uint64_t v, Shared* sh, uint64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const unsigned long long up = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += up;
+    const uint64_t up = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += up;
   }
-  if (lane == 31) sh->scan_w[warp] = incl;
   __syncthreads();
-  unsigned long long before = incl - mine;
-  for (int w = 0; w < warp; w++) before += sh->scan_w[w];
-  if (before < want && want <= before + mine) {
-    unsigned long long run = before;
+  if (lane == 31) sh->scan[warp] = v;
+  __syncthreads();
+  uint64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (w < warp) before += sh->scan[w];
+    total += sh->scan[w];
+  }
+  *all = total;
+  return before + v;
+}
+
+// Descending order of list[0 .. n), n <= kList (bitonic, padded with zeros).
+__device__ void sort_list(uint64_t* list, int n) {
+  int p = 2;
+  while (p < n) p *= 2;
+  for (int i = threadIdx.x; i < p; i += kThreads)
+    if (i >= n) list[i] = 0;
+  for (int k = 2; k <= p; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      __syncthreads();
+      for (int t = threadIdx.x; t < p / 2; t += kThreads) {
+        const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
+        const uint64_t a = list[lo], b = list[hi];
+        if ((a < b) == ((lo & k) == 0)) {
+          list[lo] = b;
+          list[hi] = a;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// One row, one cluster.
+template <typename T>
+struct Draw {
+  static constexpr int VEC = Row<T>::VEC;
+  Row<T> row;
+  Shared* sh;
+  cg::cluster_group cl;
+  int C, rank, tid, lane, warp, granules, parts, part, lo, hi;
+  float top, inv_t, per_x;  // per_x: bins of one unit of x
+
+  __device__ __forceinline__ float y_of(float x) const { return x == top ? 0.f : (x - top) * inv_t; }
+  __device__ __forceinline__ float w_of(float x) const { return expf(y_of(x)); }
+  __device__ __forceinline__ uint64_t f_of(float x) const { return fixed_of(w_of(x)); }
+  __device__ __forceinline__ int bin_of(float x) const {
+    return x == top ? 0 : (int)fminf((top - x) * per_x, (float)(kBins - 1));
+  }
+  template <typename V>
+  __device__ __forceinline__ V* at(V* p, int r) {
+    return cl.map_shared_rank(p, r);
+  }
+
+  // f(element, logit) for each element of this warp's run of granules
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+    for (int i = lo + lane; i < hi; i += 32) {
+      float v[VEC];
+      row.load(i, v);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const int e = i * VEC - row.pad + j;
+        if (e >= 0 && e < row.vocab) f(e, v[j]);
+      }
+    }
+  }
+
+  // Sum over the cluster of one value per warp; `use` names the row of warp_a.
+  __device__ __forceinline__ uint64_t cluster_sum(uint64_t v, int use) {
+    v = warp_sum(v);
+    if (lane == 0) sh->warp_a[use][warp] = v;
+    cl.sync();
+    uint64_t sum = 0;
+    for (int i = lane; i < parts; i += 32) sum += *at(&sh->warp_a[use][i % kWarps], i / kWarps);
+    return warp_sum(sum);
+  }
+
+  // The bin where the running sum over all CTAs' histograms, from bin 0 on (or
+  // from the last one down), reaches `want`; *above: the sum before it.  Bins
+  // count as value(bin, sum).  kBins if it is never reached.
+  template <typename F>
+  __device__ uint32_t find_bin(bool down, uint64_t want, uint64_t* above, F value) {
+    constexpr int P = kBins / kThreads;
+    uint64_t v[P], mine = 0;
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      const int k = tid * P + i, b = down ? kBins - 1 - k : k;
+      uint64_t sum = 0;
+      for (int r = 0; r < C; r++) sum += *at(&sh->hist[b], r);
+      v[i] = value(b, sum);
+      mine += v[i];
+    }
+    uint64_t all;
+    uint64_t run = cta_scan(mine, sh, &all) - mine;
+    if (tid == 0) sh->bin = kBins;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < P; i++) {
       if (run < want && want <= run + v[i]) {
-        sh->bin = top - i;
+        sh->bin = down ? kBins - 1 - (tid * P + i) : tid * P + i;
         sh->above = run;
       }
       run += v[i];
     }
+    __syncthreads();
+    *above = sh->above;
+    return sh->bin;
   }
-  __syncthreads();
-  const uint32_t bin = sh->bin;
-  *above = sh->above;
-  __syncthreads();
-  return bin;
+
+  __device__ void clear_hist() {
+    for (int i = tid; i < kBins; i += kThreads) sh->hist[i] = 0;
+    if (tid == 0) sh->count = 0;
+    __syncthreads();
+  }
+
+  // How many tokens the CTAs have put into their `mine`, -1 if they do not fit
+  // one list.  Gathers and orders them in `list`, in every CTA or the first one.
+  __device__ int gather(bool everywhere) {
+    cl.sync();
+    int n = 0, first = 0;
+    bool fits = true;
+    for (int r = 0; r < C; r++) {
+      const int c = (int)*at(&sh->count, r);
+      fits = fits && c <= kList;
+      n += c;
+    }
+    if (!fits || n > kList) return -1;
+    if (!everywhere && rank) return n;
+    for (int r = 0; r < C; r++) {
+      const int c = (int)*at(&sh->count, r);
+      const uint64_t* from = at(&sh->mine[0], r);
+      for (int i = tid; i < c; i += kThreads) sh->list[first + i] = from[i];
+      first += c;
+    }
+    __syncthreads();
+    sort_list(sh->list, n);
+    return n;
+  }
+  __device__ __forceinline__ void put(uint64_t v) {
+    const uint32_t i = atomicAdd(&sh->count, 1u);
+    if (i < (uint32_t)kList) sh->mine[i] = v;
+  }
+
+  // Radix selection over the tokens at or before `cut`: the order of the last
+  // one of the shortest prefix that reaches `want` tokens (or weight).
+  __device__ uint64_t select_slow(bool by_weight, uint64_t want, uint64_t cut) {
+    uint32_t prefix = 0, mask = 0;
+    for (int level = 0; level < 3; level++) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
+      const uint32_t width = level == 2 ? 0x3ffu : 0x7ffu;
+      // a weight is three pieces of 15 bits, whose sums over a CTA's share of a
+      // row stay below 2^32: one histogram after the other
+      uint64_t sum[kBins / kThreads] = {};
+      for (int piece = 0; piece < (by_weight ? 3 : 1); piece++) {
+        cl.sync();
+        clear_hist();
+        each([&](int e, float x) {
+          const uint32_t key = key_of(x);
+          if ((key & mask) != prefix || order_of(x, e) < cut) return;
+          const uint32_t v = by_weight ? (uint32_t)(f_of(x) >> (15 * piece)) & 0x7fffu : 1u;
+          if (v) atomicAdd(&sh->hist[key >> shift & width], v);
+        });
+        cl.sync();
+#pragma unroll
+        for (int i = 0; i < kBins / kThreads; i++) {
+          const int b = kBins - 1 - (tid * (kBins / kThreads) + i);
+          for (int r = 0; r < C; r++) sum[i] += (uint64_t)*at(&sh->hist[b], r) << (15 * piece);
+        }
+      }
+      uint64_t mine = 0, all;
+#pragma unroll
+      for (int i = 0; i < kBins / kThreads; i++) mine += sum[i];
+      uint64_t run = cta_scan(mine, sh, &all) - mine;
+#pragma unroll
+      for (int i = 0; i < kBins / kThreads; i++) {
+        if (run < want && want <= run + sum[i]) {
+          sh->bin = kBins - 1 - (tid * (kBins / kThreads) + i);
+          sh->above = run;
+        }
+        run += sum[i];
+      }
+      __syncthreads();
+      want -= sh->above;
+      prefix |= sh->bin << shift;
+      mask |= width << shift;
+    }
+    // equal logits: the n-th of them by index
+    uint64_t n = want;
+    if (by_weight) {
+      const uint64_t w = f_of(of_key(prefix));
+      n = (want + w - 1) / w;
+    }
+    uint32_t c = 0;
+    each([&](int e, float x) { c += key_of(x) == prefix && order_of(x, e) >= cut; });
+    const uint64_t here = warp_sum(c);
+    if (lane == 0) sh->warp_b[1][warp] = (uint32_t)here;
+    cl.sync();
+    uint64_t before = 0;
+    for (int i = 0; i < parts; i++) {
+      const uint64_t w = *at(&sh->warp_b[1][i % kWarps], i / kWarps);
+      if (before < n && n <= before + w && i == part) {  // this warp's run holds it
+        uint64_t left = n - before;
+        for (int i0 = lo; i0 < hi; i0 += 32) {
+          float v[VEC];
+          uint32_t mine = 0;
+          if (i0 + lane < hi) {
+            row.load(i0 + lane, v);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+              const int e = (i0 + lane) * VEC - row.pad + j;
+              mine += e >= 0 && e < row.vocab && key_of(v[j]) == prefix && order_of(v[j], e) >= cut;
+            }
+          }
+          uint32_t incl = mine;
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+          }
+          const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+          if (left > all) {
+            left -= all;
+            continue;
+          }
+          if (incl >= left && incl - mine < left) {
+            uint32_t k = incl - mine;
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+              const int e = (i0 + lane) * VEC - row.pad + j;
+              if (e >= 0 && e < row.vocab && key_of(v[j]) == prefix && order_of(v[j], e) >= cut && ++k == left)
+                for (int r = 0; r < C; r++) *at(&sh->cut, r) = order_of(v[j], e);
+            }
+          }
+          break;
+        }
+      }
+      before += w;
+    }
+    cl.sync();
+    return sh->cut;
+  }
+
+  // The same through the histogram of distances; `want` and the rule as there.
+  // *n: where k tokens and all before them were gathered, how many lie in
+  // `list` (the rest of the work happens there), else -1.
+  __device__ uint64_t select(bool by_weight, uint64_t want, uint64_t cut, bool filled, int* n) {
+    *n = -1;
+    if (!filled) {
+      each([&](int e, float x) {
+        if (order_of(x, e) >= cut) atomicAdd(&sh->hist[bin_of(x)], by_weight ? share_of(x) : 1u);
+      });
+      cl.sync();
+    }
+    uint64_t above;
+    const float width = inv_t / per_x;  // of a bin, in y
+    const uint32_t bin = find_bin(false, want, &above, [&](int b, uint64_t sum) {
+      return by_weight ? (uint64_t)((float)sum * expf(-width * b) * (float)(1 << (kFixed - 17))) : sum;
+    });
+    bool whole = false;
+    if (!by_weight) {
+      uint64_t held = 0;
+      for (int r = 0; r < C; r++) held += bin < kBins ? *at(&sh->hist[bin], r) : 0;
+      whole = above + held <= kList;
+    }
+    int got = -1;
+    uint64_t before = above;
+    if (bin < kBins) {
+      uint64_t sum = 0;
+      each([&](int e, float x) {
+        const uint64_t o = order_of(x, e);
+        if (o < cut) return;
+        const int b = bin_of(x);
+        if (b < (int)bin) {
+          if (by_weight) sum += f_of(x);
+          if (whole) put(o);
+        } else if (b == (int)bin) {
+          put(o);
+        }
+      });
+      if (by_weight) before = cluster_sum(sum, 2);
+      got = gather(!whole);
+    }
+    if (got >= 0 && whole) {
+      *n = got;
+      return cut;
+    }
+    if (got >= 0 && before < want) {
+      // walk the gathered ones with exact sums
+      constexpr int P = kList / kThreads;
+      uint64_t v[P], mine = 0, all;
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        const int k = tid * P + i;
+        v[i] = k >= got ? 0 : by_weight ? f_of(of_key((uint32_t)(sh->list[k] >> 32))) : 1;
+        mine += v[i];
+      }
+      uint64_t run = before + cta_scan(mine, sh, &all) - mine;
+      if (before + all >= want) {
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          if (run < want && want <= run + v[i]) sh->cut = sh->list[tid * P + i];
+          run += v[i];
+        }
+        __syncthreads();
+        return sh->cut;
+      }
+    }
+    return select_slow(by_weight, want, cut);
+  }
+
+  // An element's weight as a share of its bin's upper one, in units of 2^-17.
+  __device__ __forceinline__ uint32_t share_of(float x) const {
+    const float d = x == top ? 0.f : (top - x) * per_x;
+    const float z = (d - floorf(d)) * (inv_t / per_x);
+    return d < (float)(kBins - 1) ? (uint32_t)((1.f - z + 0.5f * z * z) * 131072.f + 0.5f) : 131072u;
+  }
+};
+
+__device__ __forceinline__ uint64_t goal_of(float p, uint64_t sum) {
+  const double goal = ceil((double)sum * (double)p);
+  const uint64_t want = goal >= 1.0 ? (uint64_t)goal : 1;
+  return want < sum ? want : sum;
+}
+__device__ __forceinline__ uint64_t aim_of(float u, uint64_t total) {
+  const double goal = (double)u * (double)total;
+  const uint64_t aim = goal > 0.0 ? (uint64_t)goal : 0;
+  return aim < total - 1 ? aim : total - 1;
+}
+__device__ __forceinline__ float logprob_of(float y, uint64_t total) {
+  return y - (float)log((double)total * (1.0 / (1ull << kFixed)));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  Shared* sh = reinterpret_cast<Shared*>(raw_smem);
-  cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  Draw<T> d{{}, reinterpret_cast<Shared*>(raw_smem), cg::this_cluster()};
+  Shared* sh = d.sh;
+  const int C = d.C = (int)d.cl.num_blocks(), rank = d.rank = (int)d.cl.block_rank();
   const int b = blockIdx.x / C;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = d.tid = threadIdx.x, lane = d.lane = tid & 31, warp = d.warp = tid >> 5;
   constexpr int VEC = Row<T>::VEC;
-  Row<T> row;
-  row.p = reinterpret_cast<const T*>(a.logits) + b * a.stride;
-  row.vocab = a.vocab;
-  row.pad = (int)(((uintptr_t)row.p & 15) / sizeof(T));
-  const int granules = (a.vocab + row.pad + VEC - 1) / VEC;
+  d.row.p = reinterpret_cast<const T*>(a.logits) + b * a.stride;
+  d.row.vocab = a.vocab;
+  d.row.pad = (int)(((uintptr_t)d.row.p & 15) / sizeof(T));
+  d.granules = (a.vocab + d.row.pad + VEC - 1) / VEC;
   // each warp of the cluster has a run of granules, in index order
-  const int parts = C * kWarps, part = rank * kWarps + warp;
-  const int lo = (int)((int64_t)granules * part / parts), hi = (int)((int64_t)granules * (part + 1) / parts);
+  const int parts = d.parts = C * kWarps, part = d.part = rank * kWarps + warp;
+  d.lo = (int)((int64_t)d.granules * part / parts), d.hi = (int)((int64_t)d.granules * (part + 1) / parts);
 
   float temp = a.temp_v ? a.temp_v[b] : a.temp;
   int k = a.top_k_v ? a.top_k_v[b] : a.top_k;
@@ -175,287 +484,199 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Args a) {
     temp = 1.f;
     k = 1;
   }
-  const float inv_t = 1.f / temp;
+  d.inv_t = 1.f / temp;
+  // the bins reach 32 in y, past which nothing weighs anything, or 24 in x
+  d.per_x = (float)kBins / fminf(32.f * temp, 24.f);
   const bool by_k = k > 0 && k < a.vocab, by_p = top_p < 1.f || top_p != top_p;
 
   // ---- the largest logit
   float top = -INFINITY;
-  for (int i = lo + lane; i < hi; i += 32) {
-    float v[VEC];
-    row.load(i, v);
-#pragma unroll
-    for (int j = 0; j < VEC; j++) top = fmaxf(top, v[j]);
-  }
+  d.each([&](int, float x) { top = fmaxf(top, x); });
 #pragma unroll
   for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   if (lane == 0) sh->top[warp] = top;
-  for (int i = tid; i < kBins; i += kThreads) {
-    sh->count[0][i] = sh->count[1][i] = 0;
-    sh->weight[0][i] = sh->weight[1][i] = 0;
-  }
-  cl.sync();
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, *cl.map_shared_rank(&sh->top[i % kWarps], i / kWarps));
+  d.clear_hist();
+  d.cl.sync();
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, *d.at(&sh->top[i % kWarps], i / kWarps));
 #pragma unroll
   for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  d.top = top;
   if (top == -INFINITY) {  // nothing to draw from (the same for the whole cluster)
     if (rank == 0 && tid == 0) {
       a.token[b] = -1;
       a.logprob[b] = -INFINITY;
       a.kept[b] = 0;
     }
-    cl.sync();
+    d.cl.sync();
     return;
   }
-  auto y_of = [&](float x) { return x == top ? 0.f : (x - top) * inv_t; };
-  auto w_of = [&](float x) { return fixed_of(expf(y_of(x))); };
+  const float u = a.u[b];
 
-  // kept so far: key > cut, or key == cut and among its first `ties` by index
-  uint32_t cut = 0;
-  uint64_t ties = UINT64_MAX;
-
-  auto clear_bins = [&](int buf) {
-    for (int i = tid; i < kBins; i += kThreads) {
-      sh->count[buf][i] = 0;
-      sh->weight[buf][i] = 0;
-    }
-  };
-
-  int buf = 0;
-  // ---- the k-th logit
-  if (by_k) {
-    uint32_t prefix = 0, mask = 0;
-    uint64_t want = (uint64_t)k;
-    for (int level = 0; level < 3; level++) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-      const uint32_t width = level == 2 ? 0x3ffu : 0x7ffu;
-      for (int i = lo + lane; i < hi; i += 32) {
-        float v[VEC];
-        row.load(i, v);
+  uint64_t cut = 0;  // kept are the tokens of at least this order
+  int n = -1;
+  if (by_k) cut = d.select(false, (uint64_t)k, 0, false, &n);
+  if (n >= 0) {
+    // ---- all that is left is in the list, in order: every CTA would find the same, the first one does
+    if (rank == 0) {
+      constexpr int P = kList / kThreads;
+      const int m0 = k;
+      uint64_t v[P], mine = 0, all;
+      float w[P];
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-          const uint32_t key = key_of(v[j]);
-          if (row.has(i, j) && (key & mask) == prefix) atomicAdd(&sh->count[buf][key >> shift & width], 1u);
-        }
+      for (int i = 0; i < P; i++) {
+        const int j = tid * P + i;
+        w[i] = j < m0 ? d.w_of(of_key((uint32_t)(sh->list[j] >> 32))) : 0.f;
+        v[i] = fixed_of(w[i]);
+        mine += v[i];
       }
-      cl.sync();
-      unsigned long long above;
-      const uint32_t bin = find_bin(cl, sh->count[buf], want, sh, &above);
-      want -= above;
-      prefix |= bin << shift;
-      mask |= width << shift;
-      buf ^= 1;  // the other buffer is clean, and cleared again once no one reads it
-      if (level < 2) {
-        // the buffer of the level before last: everyone has passed this level's barrier since
-        if (level == 1) clear_bins(buf);
-        __syncthreads();
+      uint64_t run = cta_scan(mine, sh, &all) - mine;
+      const uint64_t want = by_p ? goal_of(top_p, all) : UINT64_MAX;
+      uint32_t c = 0;
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        c += tid * P + i < m0 && run < want && w[i] >= min_p;
+        run += v[i];
+      }
+      uint64_t kept;
+      cta_scan(c, sh, &kept);
+      // in index order now, each with its place in the list of logits
+      const int m = (int)kept;
+      for (int i = tid; i < m; i += kThreads)
+        sh->mine[i] = (sh->list[i] & 0xffffffffull) << 32 | (uint32_t)i;
+      __syncthreads();
+      sort_list(sh->mine, m);
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        const int j = tid * P + i;
+        v[i] = j < m ? d.f_of(of_key((uint32_t)(sh->list[(uint32_t)sh->mine[j]] >> 32))) : 0;
+        mine += v[i];
+      }
+      run = cta_scan(mine, sh, &all) - mine;
+      const uint64_t aim = aim_of(u, all);
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        if (run <= aim && aim < run + v[i]) {
+          const uint64_t it = sh->mine[tid * P + i];
+          a.token[b] = (int32_t)(0xffffffffu - (uint32_t)(it >> 32));
+          a.logprob[b] = logprob_of(d.y_of(of_key((uint32_t)(sh->list[(uint32_t)it] >> 32))), all);
+          a.kept[b] = (int32_t)kept;
+        }
+        run += v[i];
       }
     }
-    cut = prefix;
-    ties = want;
-    cl.sync();
-    clear_bins(0);
-    clear_bins(1);
-    __syncthreads();
+    d.cl.sync();  // no CTA leaves while another may read its shared memory
+    return;
   }
 
-  // ---- the weight that is kept
   if (by_p) {
-    uint64_t sum = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-      float v[VEC];
-      row.load(i, v);
-#pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const uint32_t key = key_of(v[j]);
-        if (!by_k || key > cut) sum += w_of(v[j]);
-      }
+    // the weight of the first k, and the weight that min_p leaves of it
+    if (by_k) {
+      d.cl.sync();
+      d.clear_hist();
     }
-#pragma unroll
-    for (int x = 16; x; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0) sh->warp_a[0][warp] = sum;
-    cl.sync();
-    sum = 0;
-    for (int i = lane; i < parts; i += 32) sum += *cl.map_shared_rank(&sh->warp_a[0][i % kWarps], i / kWarps);
-#pragma unroll
-    for (int x = 16; x; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (by_k) sum += ties * w_of(of_key(cut));
-    const double goal = ceil((double)sum * (double)top_p);
-    uint64_t want = goal >= 1.0 ? (uint64_t)goal : 1;
-    if (want > sum) want = sum;
-    uint32_t prefix = 0, mask = 0;
-    buf = 0;
-    for (int level = 0; level < 3; level++) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-      const uint32_t width = level == 2 ? 0x3ffu : 0x7ffu;
-      for (int i = lo + lane; i < hi; i += 32) {
-        float v[VEC];
-        row.load(i, v);
-#pragma unroll
-        for (int j = 0; j < VEC; j++) {
-          const uint32_t key = key_of(v[j]);
-          if ((key & mask) == prefix && key >= cut) {
-            const uint64_t w = w_of(v[j]);
-            if (w) atomicAdd(&sh->weight[buf][key >> shift & width], (unsigned long long)w);
-          }
-        }
-      }
-      cl.sync();
-      unsigned long long above;
-      const uint32_t bin = find_bin(cl, sh->weight[buf], want, sh, &above);
-      want -= above;
-      prefix |= bin << shift;
-      mask |= width << shift;
-      buf ^= 1;
-      if (level < 2) {
-        if (level == 1) clear_bins(buf);
-        __syncthreads();
-      }
+    const bool early = !(min_p > 0.f);  // with min_p the histogram is seldom needed
+    uint64_t sum = 0, left = 0;
+    d.each([&](int e, float x) {
+      if (order_of(x, e) < cut) return;
+      const float w = d.w_of(x);
+      const uint64_t f = fixed_of(w);
+      sum += f;
+      if (early)
+        atomicAdd(&sh->hist[d.bin_of(x)], d.share_of(x));
+      else if (w >= min_p)
+        left += f;
+    });
+    if (!early) {
+      left = warp_sum(left);
+      if (lane == 0) sh->warp_a[3][warp] = left;
     }
-    const uint64_t each = w_of(of_key(prefix));
-    const uint64_t need = (want + each - 1) / each;
-    if (!by_k || prefix > cut) {
-      cut = prefix;
-      ties = need;
-    } else {
-      ties = need < ties ? need : ties;
+    sum = d.cluster_sum(sum, 0);
+    const uint64_t want = goal_of(top_p, sum);
+    bool binds = true;
+    if (!early) {
+      left = 0;
+      for (int i = lane; i < parts; i += 32) left += *d.at(&sh->warp_a[3][i % kWarps], i / kWarps);
+      binds = warp_sum(left) >= want;  // else min_p ends the prefix before
     }
-  }
-
-  // ---- where the equal logits end that are kept
-  int last = INT32_MAX;
-  if (by_k || by_p) {
-    uint32_t n = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-      float v[VEC];
-      row.load(i, v);
-#pragma unroll
-      for (int j = 0; j < VEC; j++) n += row.has(i, j) && key_of(v[j]) == cut;
-    }
-#pragma unroll
-    for (int x = 16; x; x /= 2) n += __shfl_xor_sync(0xffffffffu, n, x);
-    if (lane == 0) sh->warp_b[0][warp] = n;
-    cl.sync();
-    uint64_t before = 0;
-    int at = -1;
-    uint64_t left = 0;
-    for (int i = 0; i < parts; i++) {  // every thread the same
-      const uint32_t c = *cl.map_shared_rank(&sh->warp_b[0][i % kWarps], i / kWarps);
-      if (at < 0 && before + c >= ties) {
-        at = i;
-        left = ties - before;
-      }
-      before += c;
-    }
-    if (before > ties) {
-      // walk the run of granules that holds the last kept one
-      const int w_lo = (int)((int64_t)granules * at / parts), w_hi = (int)((int64_t)granules * (at + 1) / parts);
-      for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-        const int i = i0 + lane;
-        float v[VEC];
-        uint32_t mine = 0;
-        if (i < w_hi) {
-          row.load(i, v);
-#pragma unroll
-          for (int j = 0; j < VEC; j++) mine += row.has(i, j) && key_of(v[j]) == cut;
-        }
-        uint32_t incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += up;
-        }
-        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-        if (left > all) {
-          left -= all;
-          continue;
-        }
-        int found = INT32_MAX;
-        if (mine && incl >= left && incl - mine < left) {
-          uint32_t c = incl - mine;
-#pragma unroll
-          for (int j = 0; j < VEC; j++)
-            if (row.has(i, j) && key_of(v[j]) == cut && ++c == left) found = i * VEC - row.pad + j;
-        }
-#pragma unroll
-        for (int x = 16; x; x /= 2) found = min(found, __shfl_xor_sync(0xffffffffu, found, x));
-        last = found;
-        break;
-      }
-    }
+    if (binds) cut = d.select(true, want, cut, early, &n);
   }
 
   // ---- the draw
-  auto keeps = [&](int i, int j, float x, uint64_t* w) {
-    *w = 0;
-    if (!row.has(i, j)) return false;
-    const uint32_t key = key_of(x);
-    if (key < cut || (key == cut && i * VEC - row.pad + j > last)) return false;
-    const float e = expf(y_of(x));
-    if (e < min_p) return false;
-    *w = fixed_of(e);
+  auto keeps = [&](int e, float x, uint64_t* f) {
+    *f = 0;
+    if (order_of(x, e) < cut) return false;
+    const float w = d.w_of(x);
+    if (w < min_p) return false;
+    *f = fixed_of(w);
     return true;
   };
   uint64_t sum = 0;
-  uint32_t n = 0;
-  for (int i = lo + lane; i < hi; i += 32) {
-    float v[VEC];
-    row.load(i, v);
-#pragma unroll
-    for (int j = 0; j < VEC; j++) {
-      uint64_t w;
-      n += keeps(i, j, v[j], &w);
-      sum += w;
-    }
-  }
-#pragma unroll
-  for (int x = 16; x; x /= 2) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    n += __shfl_xor_sync(0xffffffffu, n, x);
-  }
+  uint32_t c = 0;
+  d.each([&](int e, float x) {
+    uint64_t f;
+    c += keeps(e, x, &f);
+    sum += f;
+  });
+  sum = warp_sum(sum);
+  c = (uint32_t)warp_sum(c);
   if (lane == 0) {
     sh->warp_a[1][warp] = sum;
-    sh->warp_b[1][warp] = n;
+    sh->warp_b[0][warp] = c;
   }
-  cl.sync();
-  uint64_t total = 0;
-  uint32_t kept = 0;
-  for (int i = 0; i < parts; i++) {
-    total += *cl.map_shared_rank(&sh->warp_a[1][i % kWarps], i / kWarps);
-    kept += *cl.map_shared_rank(&sh->warp_b[1][i % kWarps], i / kWarps);
+  d.cl.sync();
+  // parts in index order: four to a lane
+  constexpr int P = kMaxCluster * kWarps / 32;
+  uint64_t v[P], mine = 0, kept = 0;
+#pragma unroll
+  for (int i = 0; i < P; i++) {
+    const int j = lane * P + i;
+    v[i] = j < parts ? *d.at(&sh->warp_a[1][j % kWarps], j / kWarps) : 0;
+    kept += j < parts ? *d.at(&sh->warp_b[0][j % kWarps], j / kWarps) : 0;
+    mine += v[i];
   }
-  const float u = a.u[b];
-  const double goal = (double)u * (double)total;
-  uint64_t aim = goal > 0.0 ? (goal < 9.0e18 ? (uint64_t)goal : UINT64_MAX) : 0;
-  if (aim > total - 1) aim = total - 1;
-  uint64_t before = 0;
-  int at = 0;
-  for (int i = 0; i < parts; i++) {
-    const uint64_t w = *cl.map_shared_rank(&sh->warp_a[1][i % kWarps], i / kWarps);
-    if (before + w > aim) {
-      at = i;
-      break;
+  kept = warp_sum(kept);
+  uint64_t incl = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x *= 2) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, incl, x);
+    if (lane >= x) incl += up;
+  }
+  const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
+  const uint64_t aim = aim_of(u, total);
+  uint64_t run = incl - mine, left = 0;
+  bool ours = false;
+#pragma unroll
+  for (int i = 0; i < P; i++) {
+    if (lane * P + i == part && run <= aim && aim < run + v[i]) {
+      ours = true;
+      left = aim - run;
     }
-    before += w;
+    run += v[i];
   }
-  if (at == part) {
-    uint64_t left = aim - before;  // the first element whose running sum exceeds it
-    for (int i0 = lo; i0 < hi; i0 += 32) {
+  if (__any_sync(0xffffffffu, ours)) {
+    // the first element of this warp's run whose running sum exceeds it
+    left = warp_sum(left);
+    for (int i0 = d.lo; i0 < d.hi; i0 += 32) {
       const int i = i0 + lane;
-      float v[VEC];
-      uint64_t w[VEC], mine = 0;
-      if (i < hi) {
-        row.load(i, v);
+      float x[VEC];
+      uint64_t f[VEC];
+      mine = 0;
+      if (i < d.hi) {
+        d.row.load(i, x);
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          keeps(i, j, v[j], &w[j]);
-          mine += w[j];
+          const int e = i * VEC - d.row.pad + j;
+          f[j] = 0;
+          if (e >= 0 && e < a.vocab) keeps(e, x[j], &f[j]);
+          mine += f[j];
         }
       }
-      uint64_t incl = mine;
+      incl = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const uint64_t up = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += up;
+      for (int s = 1; s < 32; s *= 2) {
+        const uint64_t up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
       }
       const uint64_t all = __shfl_sync(0xffffffffu, incl, 31);
       if (all <= left) {
@@ -463,15 +684,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Args a) {
         continue;
       }
       if (incl > left && incl - mine <= left) {
-        uint64_t run = incl - mine;
+        run = incl - mine;
         bool done = false;
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          run += w[j];
+          run += f[j];
           if (!done && run > left) {
             done = true;
-            a.token[b] = i * VEC - row.pad + j;
-            a.logprob[b] = y_of(v[j]) - (float)log((double)total * (1.0 / (1ull << kFixed)));
+            a.token[b] = i * VEC - d.row.pad + j;
+            a.logprob[b] = logprob_of(d.y_of(x[j]), total);
             a.kept[b] = (int32_t)kept;
           }
         }
@@ -479,13 +700,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Args a) {
       break;
     }
   }
-  cl.sync();  // no CTA leaves while another may read its shared memory
+  d.cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
 template <typename T>
 cudaError_t launch(const Args& a, int lanes, cudaStream_t st) {
+  // a row is split until a CTA has 4096 logits, or the CTAs fill the device;
+  // a CTA's share stays below 2^17 logits (select_slow)
   int c = 1;
-  while (c < kMaxCluster && a.vocab > 8192 * c) c *= 2;
+  while (c < kMaxCluster &&
+         (a.vocab > (1 << 17) * c || (a.vocab > 4096 * c && (int64_t)lanes * c <= ops_sm_count())))
+    c *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)lanes * c);
   cfg.blockDim = dim3(kThreads);
@@ -497,8 +722,14 @@ cudaError_t launch(const Args& a, int lanes, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
-  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) : e;
+  static OpsOnce once;
+  if (const int dev = ops_current(); !once(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    once.set(dev);
+  }
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
 }
 
 }  // namespace
@@ -524,15 +755,16 @@ extern "C" int wfst_sample_tokens(const wfst_sample_args* r, void* stream) {
     return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: NULL argument");
   const size_t size = r->dtype == WFST_F32 ? 4 : 2;
   if (!aligned(r->logits, size)) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: logits not aligned to their type");
-  const int dev = ops_device({r->logits, r->uniform, r->temperature_v, r->top_k_v, r->top_p_v, r->min_p_v, r->tokens,
+  const int dev = ops_device(r->device, {r->logits, r->uniform, r->temperature_v, r->top_k_v, r->top_p_v, r->min_p_v, r->tokens,
                               r->logprobs, r->kept});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: every array must be device memory of one device");
   OpsDevice guard(dev);
+  if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "sample_tokens: device");
   Args a;
   a.logits = r->logits, a.u = r->uniform;
   a.temp_v = r->temperature_v, a.top_k_v = r->top_k_v, a.top_p_v = r->top_p_v, a.min_p_v = r->min_p_v;
   a.token = r->tokens, a.logprob = r->logprobs, a.kept = r->kept;
-  a.stride = r->stride, a.vocab = r->vocab;
+  a.stride = r->lanes > 1 ? r->stride : 0, a.vocab = r->vocab;
   a.temp = r->temperature, a.top_k = r->top_k, a.top_p = r->top_p, a.min_p = r->min_p;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = r->dtype == WFST_F32   ? launch<float>(a, r->lanes, st)
