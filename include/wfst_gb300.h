@@ -441,14 +441,14 @@ int wfst_blank_skip(const void* log_probs, int32_t dtype, int64_t stride_b, int6
  * A matrix w[n, k] = scales[n, k / group] * (codes[n, k] - zeros[n, k /
  * group]) with codes 0..15, laid out once for wfst_matvec_quant.  codes:
  * [n, k/2] bytes, the even k in the lower half of a byte.  scales and zeros:
- * [n, k / group], 16-bit values of the type that wfst_matvec_quant is given;
+ * [n, k / group], values of `dtype`, which wfst_matvec_quant is to be given too;
  * zeros NULL stands for 8 everywhere.  group is 32, 64, 128 or 256 and
  * divides k; n >= 1.  packed: 16-byte aligned, wfst_quant_size's bytes (its
  * `zeros` says whether there are zero points).  Errors: INVALID_ARG, CUDA.
  */
 int wfst_quant_size(int32_t n, int32_t k, int32_t group, int32_t zeros, int64_t* bytes);
-int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros, int32_t n, int32_t k,
-                    int32_t group, void* packed, void* stream);
+int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros, int32_t dtype, int32_t n,
+                    int32_t k, int32_t group, void* packed, void* stream);
 
 /*
  * y[r, n] = bias[n] + sum over k of x[r, k] * w[n, k], for rows r of x

@@ -27,7 +27,7 @@ def test_sizes_of_a_packed_matrix(lib):
             W.wfst_quant_size(n, k, group, 0)
         assert e.value.code == -1
     assert lib.wfst_quant_size(16, 64, 64, 0, None) == -1
-    assert lib.wfst_quant_pack(None, None, None, 16, 64, 64, None, None) == -1
+    assert lib.wfst_quant_pack(None, None, None, W.WFST_F16, 16, 64, 64, None, None) == -1
     assert b"NULL" in lib.wfst_last_error()
 
 

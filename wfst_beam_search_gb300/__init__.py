@@ -113,7 +113,7 @@ def load(build_if_missing: bool = False):
         L.wfst_probe_random_gather.argtypes = [P, i64, i32, i32, i32, i32, P, P]
         L.wfst_blank_skip.argtypes = [P, i32, i64, i64, i32, i32, C.c_float, P, i32, i32, P, P, P, P]
         L.wfst_quant_size.argtypes = [i32, i32, i32, i32, C.POINTER(i64)]
-        L.wfst_quant_pack.argtypes = [P, P, P, i32, i32, i32, P, P]
+        L.wfst_quant_pack.argtypes = [P, P, P, i32, i32, i32, i32, P, P]
         L.wfst_attend_size.argtypes = [C.POINTER(i64)]
         for name in ("wfst_matvec_quant", "wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens"):
             getattr(L, name).argtypes = [P, P]    # the argument block, the stream
@@ -282,8 +282,8 @@ def wfst_quant_size(n, k, group, zeros):
     return out.value
 
 
-def wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, stream):
-    _check(load().wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, n, k, group, packed_ptr, stream))
+def wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, dtype, n, k, group, packed_ptr, stream):
+    _check(load().wfst_quant_pack(codes_ptr, scales_ptr, zeros_ptr, dtype, n, k, group, packed_ptr, stream))
 
 
 def wfst_matvec_quant(args, stream):

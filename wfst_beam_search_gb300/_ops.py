@@ -108,8 +108,8 @@ def pack_quant(codes, scales, zeros=None, stream=None) -> QuantMatrix:
         raise ValueError("the number of groups must divide k")
     codes, scales, zeros = codes.contiguous(), scales.contiguous(), None if zeros is None else zeros.contiguous()
     packed = _empty(wfst_quant_size(n, k, k // groups, zeros is not None), dtype=_U8, device=codes.device)
-    wfst_quant_pack(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), n, k, k // groups,
-                    packed.data_ptr(), _raw_stream(dev))
+    wfst_quant_pack(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), _HALF[scales.dtype],
+                    n, k, k // groups, packed.data_ptr(), _raw_stream(dev))
     return QuantMatrix(packed, n, k, k // groups, int(zeros is not None), scales.dtype)
 
 
