@@ -16,16 +16,22 @@
 // still fits.  Weights themselves are fp32 (the plain expf).
 //
 // A pass has to read the logits once, which takes microseconds; what bounds it
-// is the chain of row-wide decisions (largest logit, k-th logit, total weight,
-// weight's threshold, drawn token).  A cluster of CTAs takes one row, so a
-// decision costs a cluster barrier and not a launch.  No sort of the row:
-//   - a histogram of the distance to the largest logit, in linear bins, counts
-//     (k) or weighs (p) the row and tells the bin where the rule is met.  Bins
-//     are at most 1/64 wide in y, so an element's weight is its bin's upper one
-//     times 1 - z + z^2/2 to 2^-20, and one 32-bit add per element does;
-//   - the elements of that bin are gathered, ordered exactly (logit, index) and
-//     walked with exact sums;
-//   - where the bin holds too many (flat or coarsely rounded rows), radix
+// is the chain of row-wide decisions (largest logit, total weight, the prefix's
+// end, the drawn token) and the arithmetic of the weights.  A cluster of CTAs
+// takes one row and holds it in shared memory, so a decision costs a cluster
+// barrier; a CTA leaves what the others need in their shared memory before it.
+//   - Candidates.  The kept tokens are among the logits from some value up: from
+//     min_p's, or from where k threads have their largest logit (each of those
+//     is one of the k largest or below them).  One pass adds up the weights, if
+//     p asks for the row's, and gathers the candidates; a few hundred of them
+//     are ordered exactly (logit, index) and walked with exact sums by one CTA.
+//   - Where they do not fit, or p keeps more than them: a histogram of the
+//     distance to the largest logit, in linear bins, counts (k) or weighs (p)
+//     the row.  Bins are at most 1/64 wide in y, so an element's weight is its
+//     bin's upper one times 1 - z + z^2/2 to 2^-20, and one 32-bit add per
+//     element does.  The bin where the rule is met is gathered, ordered and
+//     walked, and a last pass draws from the row.
+//   - Where that bin holds too many (flat or coarsely rounded rows), radix
 //     selection on the logits' ordered bits takes over, with exact sums.
 #include <cooperative_groups.h>
 
@@ -39,9 +45,14 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kList = 2048;
+constexpr int kCoarse = kBins / 32;
+constexpr int kList = 1024;          // candidates that are ordered
+constexpr int kSmall = 256;          // up to here by counting, from there on bitonic
+constexpr int kGuess = 512;          // threads whose largest logit p's first guess covers
+constexpr int kStage = 64 * 1024;    // bytes of a row's share that are held in shared memory
 constexpr int kMaxCluster = 8;
 constexpr int kFixed = 43;
+constexpr float kMost = 3.402823466e38f;
 
 struct Args {
   const void* logits;
@@ -51,26 +62,54 @@ struct Args {
   float* logprob;
   int32_t* kept;
   int64_t stride;
-  int32_t vocab, top_k;
+  int32_t vocab, top_k, staged;
   float temp, top_p, min_p;
 };
 
-// NaN counts as -inf; -0 and +0 are equal.
-__device__ __forceinline__ float canonical(float v) { return v == v ? v + 0.f : -INFINITY; }
-// Larger logit, larger key.
+// NaN counts as -inf, +inf as its type's largest number.
+template <typename T>
+constexpr float kLargest = kMost;
+template <>
+constexpr float kLargest<__half> = 65504.f;
+template <>
+constexpr float kLargest<__nv_bfloat16> = 3.38953138925e38f;
+template <typename T>
+__device__ __forceinline__ float canonical(T v) {
+  return fminf(fmaxf(to_f32(v), -INFINITY), kLargest<T>);
+}
+// Larger logit, larger key; -0 and +0 have one.
 __device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(v + 0.f);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
-// floor(w * 2^43) of 0 <= w <= 1
+// Order of the tokens: larger logit first, then lower index.
+__device__ __forceinline__ uint64_t order_of(float x, int e) {
+  return (uint64_t)key_of(x) << 32 | (0xffffffffu - (uint32_t)e);
+}
+__device__ __forceinline__ float logit_of(uint64_t order) { return of_key((uint32_t)(order >> 32)); }
+__device__ __forceinline__ int index_of(uint64_t order) { return (int)(0xffffffffu - (uint32_t)order); }
+
+// Sums of floor(w * 2^43), 0 <= w <= 1.  Adding 8 towards zero leaves
+// floor(w * 2^20) in the low mantissa bits, adding 2^-20 to the rest floor(rest *
+// 2^43): two 32-bit sums of bit patterns, each pattern less its constant.  They
+// hold 512 weights.
+struct Fixed {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(float w) {
+    const float t = __fadd_rz(w, 8.f);
+    const float rest = w - (t - 8.f);
+    hi += __float_as_uint(t) - 0x41000000u;
+    lo += __float_as_uint(__fadd_rz(rest, 9.5367431640625e-7f)) - 0x35800000u;
+  }
+  __device__ __forceinline__ uint64_t sum() const { return ((uint64_t)hi << 23) + lo; }
+};
 __device__ __forceinline__ uint64_t fixed_of(float w) {
-  const uint32_t b = __float_as_uint(w);
-  const uint32_t sh = 127u - (b >> 23);
-  const uint64_t m = (uint64_t)((b & 0x7fffffu) | 0x800000u) << (kFixed - 23);
-  return sh < 64u ? m >> sh : 0;
+  Fixed f;
+  f.add(w);
+  return f.sum();
 }
 
 template <typename T>
@@ -85,45 +124,46 @@ struct Row {
       const uint4 raw = *reinterpret_cast<const uint4*>(p + e);
       const T* r = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) v[j] = canonical(to_f32(r[j]));
+      for (int j = 0; j < VEC; j++) v[j] = canonical(r[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; j++) v[j] = e + j >= 0 && e + j < vocab ? canonical(to_f32(p[e + j])) : -INFINITY;
+      for (int j = 0; j < VEC; j++) v[j] = e + j >= 0 && e + j < vocab ? canonical(p[e + j]) : -INFINITY;
     }
   }
 };
 
 struct Shared {
   uint32_t hist[kBins];
-  uint64_t list[kList];           // every CTA's copy of what was gathered
-  uint64_t mine[kList];           // what this CTA gathered
-  uint64_t warp_a[4][kWarps];     // one row per use: a reader is never overtaken
-  uint32_t warp_b[2][kWarps];
-  float top[kWarps];
-  uint64_t scan[kWarps + 1];
-  uint64_t above, cut;
-  uint32_t bin, count, fits;
+  uint64_t list[kList];   // the candidates, gathered
+  uint64_t mine[kList];   // what this CTA found
+  uint64_t weight[kList];
+  // from the cluster's CTAs, one slot each; one array per use
+  uint64_t box_coarse[kMaxCluster][kCoarse], box_sum[4][kMaxCluster];
+  uint32_t box_count[2][kMaxCluster];
+  float box_top[kMaxCluster];
+  uint64_t warp_a[kWarps], scan[kWarps + 1];
+  uint32_t warp_b[kWarps];
+  uint64_t cut, above;
+  uint32_t bin, count;
 };
-
-// Order of the tokens: larger logit first, then lower index.
-__device__ __forceinline__ uint64_t order_of(float x, int e) {
-  return (uint64_t)key_of(x) << 32 | (0xffffffffu - (uint32_t)e);
-}
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int x = 16; x; x /= 2) v += __shfl_xor_sync(0xffffffffu, v, x);
   return v;
 }
-
-// Inclusive sums over the CTA's threads of one value each; *all is their total.
-__device__ __forceinline__ uint64_t cta_scan(uint64_t v, Shared* sh, uint64_t* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v) {  // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const uint64_t up = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += up;
+    if ((threadIdx.x & 31) >= d) v += up;
   }
+  return v;
+}
+// Inclusive sums over the CTA's threads of one value each; *all is their total.
+__device__ __forceinline__ uint64_t cta_scan(uint64_t v, Shared* sh, uint64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v);
   __syncthreads();
   if (lane == 31) sh->scan[warp] = v;
   __syncthreads();
@@ -137,8 +177,19 @@ __device__ __forceinline__ uint64_t cta_scan(uint64_t v, Shared* sh, uint64_t* a
   return before + v;
 }
 
-// Descending order of list[0 .. n), n <= kList (bitonic, padded with zeros).
-__device__ void sort_list(uint64_t* list, int n) {
+// Descending order of list[0 .. n), n <= kList, into `to` (kSmall and below) or
+// in place; returns where.
+__device__ uint64_t* sort_list(uint64_t* list, uint64_t* to, int n) {
+  if (n <= kSmall) {
+    if ((int)threadIdx.x < n) {
+      const uint64_t v = list[threadIdx.x];
+      int r = 0;
+      for (int i = 0; i < n; i++) r += list[i] > v;
+      to[r] = v;
+    }
+    __syncthreads();
+    return to;
+  }
   int p = 2;
   while (p < n) p *= 2;
   for (int i = threadIdx.x; i < p; i += kThreads)
@@ -156,84 +207,113 @@ __device__ void sort_list(uint64_t* list, int n) {
       }
     }
   __syncthreads();
+  return list;
 }
 
-// One row, one cluster.
+// One row, one cluster.  What is computed from all CTAs' values is computed by
+// all CTAs alike, so that branches on it are the cluster's.
 template <typename T>
 struct Draw {
   static constexpr int VEC = Row<T>::VEC;
   Row<T> row;
   Shared* sh;
+  uint4* stage;  // this CTA's granules, if they fit
   cg::cluster_group cl;
-  int C, rank, tid, lane, warp, granules, parts, part, lo, hi;
+  int C, rank, tid, lane, warp, granules, parts, part, first, lo, hi;
   float top, inv_t, per_x;  // per_x: bins of one unit of x
 
-  __device__ __forceinline__ float y_of(float x) const { return x == top ? 0.f : (x - top) * inv_t; }
+  __device__ __forceinline__ float y_of(float x) const { return (x - top) * inv_t; }
   __device__ __forceinline__ float w_of(float x) const { return expf(y_of(x)); }
-  __device__ __forceinline__ uint64_t f_of(float x) const { return fixed_of(w_of(x)); }
-  __device__ __forceinline__ int bin_of(float x) const {
-    return x == top ? 0 : (int)fminf((top - x) * per_x, (float)(kBins - 1));
-  }
+  __device__ __forceinline__ int bin_of(float x) const { return (int)fminf((top - x) * per_x, (float)(kBins - 1)); }
   template <typename V>
   __device__ __forceinline__ V* at(V* p, int r) {
     return cl.map_shared_rank(p, r);
   }
+  __device__ __forceinline__ void sync() {
+    if (C == 1)
+      __syncthreads();
+    else
+      cl.sync();
+  }
+  // Leaves a value that a whole warp has in this CTA's slot of every CTA's box.
+  template <typename V>
+  __device__ __forceinline__ void leave(V* box, V v) {
+    if (lane < C) *at(&box[rank], lane) = v;
+  }
+  // The sum over all warps of all CTAs; one array of boxes per use.
+  __device__ __forceinline__ uint64_t cluster_sum(uint64_t v, int use) {
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sh->warp_a[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      v = warp_sum(lane < kWarps ? sh->warp_a[lane] : 0);
+      leave(sh->box_sum[use], v);
+    }
+    sync();
+    v = 0;
+    for (int r = 0; r < C; r++) v += sh->box_sum[use][r];
+    return v;
+  }
 
-  // f(element, logit) for each element of this warp's run of granules
+  __device__ __forceinline__ void get(int i, float (&v)[VEC]) const {
+    if (stage) {
+      const uint4 raw = stage[i - first];
+      const T* r = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[j] = to_f32(r[j]);
+    } else {
+      row.load(i, v);
+    }
+  }
+  // f(element, logit) for each element of this warp's run of granules and for
+  // the places beside the row in its first and last granule, which are -inf
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
 #pragma unroll 2
     for (int i = lo + lane; i < hi; i += 32) {
       float v[VEC];
-      row.load(i, v);
+      get(i, v);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const int e = i * VEC - row.pad + j;
-        if (e >= 0 && e < row.vocab) f(e, v[j]);
-      }
+      for (int j = 0; j < VEC; j++) f(i * VEC - row.pad + j, v[j]);
     }
   }
+  __device__ __forceinline__ bool in_row(int e) const { return e >= 0 && e < row.vocab; }
 
-  // Sum over the cluster of one value per warp; `use` names the row of warp_a.
-  __device__ __forceinline__ uint64_t cluster_sum(uint64_t v, int use) {
-    v = warp_sum(v);
-    if (lane == 0) sh->warp_a[use][warp] = v;
-    cl.sync();
-    uint64_t sum = 0;
-    for (int i = lane; i < parts; i += 32) sum += *at(&sh->warp_a[use][i % kWarps], i / kWarps);
-    return warp_sum(sum);
-  }
-
-  // The bin where the running sum over all CTAs' histograms, from bin 0 on (or
-  // from the last one down), reaches `want`; *above: the sum before it.  Bins
-  // count as value(bin, sum).  kBins if it is never reached.
+  // The bin where the running sum over all CTAs' histograms reaches `want`;
+  // *above: the sum before it.  Bins count as value(bin, sum).  kBins if it is
+  // never reached.  The histogram must stay until the next cluster barrier.
   template <typename F>
-  __device__ uint32_t find_bin(bool down, uint64_t want, uint64_t* above, F value) {
-    constexpr int P = kBins / kThreads;
-    uint64_t v[P], mine = 0;
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-      const int k = tid * P + i, b = down ? kBins - 1 - k : k;
-      uint64_t sum = 0;
-      for (int r = 0; r < C; r++) sum += *at(&sh->hist[b], r);
-      v[i] = value(b, sum);
-      mine += v[i];
-    }
-    uint64_t all;
-    uint64_t run = cta_scan(mine, sh, &all) - mine;
-    if (tid == 0) sh->bin = kBins;
+  __device__ int find_bin(uint64_t want, uint64_t* above, F value) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < P; i++) {
-      if (run < want && want <= run + v[i]) {
-        sh->bin = down ? kBins - 1 - (tid * P + i) : tid * P + i;
-        sh->above = run;
-      }
-      run += v[i];
+    for (int i = 0; i < kCoarse / kWarps; i++) {
+      const int c = warp * (kCoarse / kWarps) + i;
+      const uint64_t v = warp_sum(value(c * 32 + lane, sh->hist[c * 32 + lane]));
+      if (lane < C) at(&sh->box_coarse[rank][0], lane)[c] = v;
     }
-    __syncthreads();
-    *above = sh->above;
-    return sh->bin;
+    sync();
+    // every warp the same
+    uint64_t v0 = 0, v1 = 0;
+    for (int r = 0; r < C; r++) {
+      v0 += sh->box_coarse[r][2 * lane];
+      v1 += sh->box_coarse[r][2 * lane + 1];
+    }
+    uint64_t run = warp_scan(v0 + v1) - (v0 + v1);
+    const bool here = run < want && want <= run + v0 + v1;
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (!who) return kBins;
+    const bool second = want > run + v0;
+    const int c = __shfl_sync(0xffffffffu, 2 * lane + (second ? 1 : 0), __ffs(who) - 1);
+    const uint64_t before = __shfl_sync(0xffffffffu, second ? run + v0 : run, __ffs(who) - 1);
+    const int b = c * 32 + lane;
+    uint64_t v = 0;
+    for (int r = 0; r < C; r++) v += value(b, *at(&sh->hist[b], r));
+    run = before + warp_scan(v) - v;
+    const unsigned at_bin = __ballot_sync(0xffffffffu, run < want && want <= run + v);
+    if (!at_bin) return kBins;  // (weights: their parts may round otherwise than their sum)
+    *above = __shfl_sync(0xffffffffu, run, __ffs(at_bin) - 1);
+    return __shfl_sync(0xffffffffu, b, __ffs(at_bin) - 1);
   }
 
   __device__ void clear_hist() {
@@ -242,68 +322,64 @@ struct Draw {
     __syncthreads();
   }
 
-  // How many tokens the CTAs have put into their `mine`, -1 if they do not fit
-  // one list.  Gathers and orders them in `list`, in every CTA or the first one.
-  __device__ int gather(bool everywhere) {
-    cl.sync();
-    int n = 0, first = 0;
-    bool fits = true;
-    for (int r = 0; r < C; r++) {
-      const int c = (int)*at(&sh->count, r);
-      fits = fits && c <= kList;
-      n += c;
-    }
-    if (!fits || n > kList) return -1;
-    if (!everywhere && rank) return n;
-    for (int r = 0; r < C; r++) {
-      const int c = (int)*at(&sh->count, r);
-      const uint64_t* from = at(&sh->mine[0], r);
-      for (int i = tid; i < c; i += kThreads) sh->list[first + i] = from[i];
-      first += c;
-    }
-    __syncthreads();
-    sort_list(sh->list, n);
-    return n;
-  }
   __device__ __forceinline__ void put(uint64_t v) {
     const uint32_t i = atomicAdd(&sh->count, 1u);
     if (i < (uint32_t)kList) sh->mine[i] = v;
+  }
+  // How many tokens the CTAs have put into their `mine`, -1 if they do not fit
+  // one list.  Gathers them in `list`, in every CTA or the first one.
+  __device__ int gather(bool everywhere, int use) {
+    __syncthreads();
+    if (warp == 0) leave(sh->box_count[use], sh->count);
+    sync();
+    int n = 0;
+    for (int r = 0; r < C; r++) n += (int)min(sh->box_count[use][r], (uint32_t)kList + 1);
+    if (n > kList) return -1;
+    if (!everywhere && rank) return n;
+    int from = 0;
+    for (int r = 0; r < C; r++) {
+      const int c = (int)sh->box_count[use][r];
+      const uint64_t* src = at(&sh->mine[0], r);
+      for (int i = tid; i < c; i += kThreads) sh->list[from + i] = src[i];
+      from += c;
+    }
+    __syncthreads();
+    return n;
   }
 
   // Radix selection over the tokens at or before `cut`: the order of the last
   // one of the shortest prefix that reaches `want` tokens (or weight).
   __device__ uint64_t select_slow(bool by_weight, uint64_t want, uint64_t cut) {
     uint32_t prefix = 0, mask = 0;
+    constexpr int P = kBins / kThreads;
     for (int level = 0; level < 3; level++) {
       const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
       const uint32_t width = level == 2 ? 0x3ffu : 0x7ffu;
       // a weight is three pieces of 15 bits, whose sums over a CTA's share of a
       // row stay below 2^32: one histogram after the other
-      uint64_t sum[kBins / kThreads] = {};
+      uint64_t sum[P] = {};
       for (int piece = 0; piece < (by_weight ? 3 : 1); piece++) {
-        cl.sync();
+        sync();
         clear_hist();
         each([&](int e, float x) {
           const uint32_t key = key_of(x);
-          if ((key & mask) != prefix || order_of(x, e) < cut) return;
-          const uint32_t v = by_weight ? (uint32_t)(f_of(x) >> (15 * piece)) & 0x7fffu : 1u;
+          if ((key & mask) != prefix || !in_row(e) || order_of(x, e) < cut) return;
+          const uint32_t v = by_weight ? (uint32_t)(fixed_of(w_of(x)) >> (15 * piece)) & 0x7fffu : 1u;
           if (v) atomicAdd(&sh->hist[key >> shift & width], v);
         });
-        cl.sync();
+        sync();
 #pragma unroll
-        for (int i = 0; i < kBins / kThreads; i++) {
-          const int b = kBins - 1 - (tid * (kBins / kThreads) + i);
-          for (int r = 0; r < C; r++) sum[i] += (uint64_t)*at(&sh->hist[b], r) << (15 * piece);
-        }
+        for (int i = 0; i < P; i++)
+          for (int r = 0; r < C; r++) sum[i] += (uint64_t)*at(&sh->hist[kBins - 1 - (tid * P + i)], r) << (15 * piece);
       }
       uint64_t mine = 0, all;
 #pragma unroll
-      for (int i = 0; i < kBins / kThreads; i++) mine += sum[i];
+      for (int i = 0; i < P; i++) mine += sum[i];
       uint64_t run = cta_scan(mine, sh, &all) - mine;
 #pragma unroll
-      for (int i = 0; i < kBins / kThreads; i++) {
+      for (int i = 0; i < P; i++) {
         if (run < want && want <= run + sum[i]) {
-          sh->bin = kBins - 1 - (tid * (kBins / kThreads) + i);
+          sh->bin = kBins - 1 - (tid * P + i);
           sh->above = run;
         }
         run += sum[i];
@@ -316,132 +392,104 @@ struct Draw {
     // equal logits: the n-th of them by index
     uint64_t n = want;
     if (by_weight) {
-      const uint64_t w = f_of(of_key(prefix));
+      const uint64_t w = fixed_of(w_of(of_key(prefix)));
       n = (want + w - 1) / w;
     }
     uint32_t c = 0;
-    each([&](int e, float x) { c += key_of(x) == prefix && order_of(x, e) >= cut; });
-    const uint64_t here = warp_sum(c);
-    if (lane == 0) sh->warp_b[1][warp] = (uint32_t)here;
-    cl.sync();
+    each([&](int e, float x) { c += key_of(x) == prefix && in_row(e) && order_of(x, e) >= cut; });
+    const uint32_t here = (uint32_t)warp_sum(c);
+    if (lane == 0) sh->warp_b[warp] = here;
+    sync();
     uint64_t before = 0;
-    for (int i = 0; i < parts; i++) {
-      const uint64_t w = *at(&sh->warp_b[1][i % kWarps], i / kWarps);
-      if (before < n && n <= before + w && i == part) {  // this warp's run holds it
-        uint64_t left = n - before;
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-          float v[VEC];
-          uint32_t mine = 0;
-          if (i0 + lane < hi) {
-            row.load(i0 + lane, v);
+    for (int i = 0; i < part; i++) before += *at(&sh->warp_b[i % kWarps], i / kWarps);
+    if (before < n && n <= before + here) {  // this warp's run holds it
+      uint64_t left = n - before;
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        float v[VEC];
+        uint32_t mine = 0;
+        auto counts = [&](int j) {
+          const int e = (i0 + lane) * VEC - row.pad + j;
+          return key_of(v[j]) == prefix && in_row(e) && order_of(v[j], e) >= cut;
+        };
+        if (i0 + lane < hi) {
+          get(i0 + lane, v);
 #pragma unroll
-            for (int j = 0; j < VEC; j++) {
-              const int e = (i0 + lane) * VEC - row.pad + j;
-              mine += e >= 0 && e < row.vocab && key_of(v[j]) == prefix && order_of(v[j], e) >= cut;
-            }
-          }
-          uint32_t incl = mine;
-#pragma unroll
-          for (int d = 1; d < 32; d *= 2) {
-            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += up;
-          }
-          const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-          if (left > all) {
-            left -= all;
-            continue;
-          }
-          if (incl >= left && incl - mine < left) {
-            uint32_t k = incl - mine;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-              const int e = (i0 + lane) * VEC - row.pad + j;
-              if (e >= 0 && e < row.vocab && key_of(v[j]) == prefix && order_of(v[j], e) >= cut && ++k == left)
-                for (int r = 0; r < C; r++) *at(&sh->cut, r) = order_of(v[j], e);
-            }
-          }
-          break;
+          for (int j = 0; j < VEC; j++) mine += counts(j);
         }
+        const uint32_t incl = (uint32_t)warp_scan(mine);
+        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+        if (left > all) {
+          left -= all;
+          continue;
+        }
+        if (incl >= left && incl - mine < left) {
+          uint32_t k = incl - mine;
+#pragma unroll
+          for (int j = 0; j < VEC; j++)
+            if (counts(j) && ++k == left)
+              for (int r = 0; r < C; r++) *at(&sh->cut, r) = order_of(v[j], (i0 + lane) * VEC - row.pad + j);
+        }
+        break;
       }
-      before += w;
     }
-    cl.sync();
+    sync();
     return sh->cut;
-  }
-
-  // The same through the histogram of distances; `want` and the rule as there.
-  // *n: where k tokens and all before them were gathered, how many lie in
-  // `list` (the rest of the work happens there), else -1.
-  __device__ uint64_t select(bool by_weight, uint64_t want, uint64_t cut, bool filled, int* n) {
-    *n = -1;
-    if (!filled) {
-      each([&](int e, float x) {
-        if (order_of(x, e) >= cut) atomicAdd(&sh->hist[bin_of(x)], by_weight ? share_of(x) : 1u);
-      });
-      cl.sync();
-    }
-    uint64_t above;
-    const float width = inv_t / per_x;  // of a bin, in y
-    const uint32_t bin = find_bin(false, want, &above, [&](int b, uint64_t sum) {
-      return by_weight ? (uint64_t)((float)sum * expf(-width * b) * (float)(1 << (kFixed - 17))) : sum;
-    });
-    bool whole = false;
-    if (!by_weight) {
-      uint64_t held = 0;
-      for (int r = 0; r < C; r++) held += bin < kBins ? *at(&sh->hist[bin], r) : 0;
-      whole = above + held <= kList;
-    }
-    int got = -1;
-    uint64_t before = above;
-    if (bin < kBins) {
-      uint64_t sum = 0;
-      each([&](int e, float x) {
-        const uint64_t o = order_of(x, e);
-        if (o < cut) return;
-        const int b = bin_of(x);
-        if (b < (int)bin) {
-          if (by_weight) sum += f_of(x);
-          if (whole) put(o);
-        } else if (b == (int)bin) {
-          put(o);
-        }
-      });
-      if (by_weight) before = cluster_sum(sum, 2);
-      got = gather(!whole);
-    }
-    if (got >= 0 && whole) {
-      *n = got;
-      return cut;
-    }
-    if (got >= 0 && before < want) {
-      // walk the gathered ones with exact sums
-      constexpr int P = kList / kThreads;
-      uint64_t v[P], mine = 0, all;
-#pragma unroll
-      for (int i = 0; i < P; i++) {
-        const int k = tid * P + i;
-        v[i] = k >= got ? 0 : by_weight ? f_of(of_key((uint32_t)(sh->list[k] >> 32))) : 1;
-        mine += v[i];
-      }
-      uint64_t run = before + cta_scan(mine, sh, &all) - mine;
-      if (before + all >= want) {
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-          if (run < want && want <= run + v[i]) sh->cut = sh->list[tid * P + i];
-          run += v[i];
-        }
-        __syncthreads();
-        return sh->cut;
-      }
-    }
-    return select_slow(by_weight, want, cut);
   }
 
   // An element's weight as a share of its bin's upper one, in units of 2^-17.
   __device__ __forceinline__ uint32_t share_of(float x) const {
-    const float d = x == top ? 0.f : (top - x) * per_x;
+    const float d = (top - x) * per_x;
     const float z = (d - floorf(d)) * (inv_t / per_x);
     return d < (float)(kBins - 1) ? (uint32_t)((1.f - z + 0.5f * z * z) * 131072.f + 0.5f) : 131072u;
+  }
+
+  // The same as select_slow's through the histogram of distances.
+  __device__ uint64_t select(bool by_weight, uint64_t want, uint64_t cut) {
+    sync();
+    clear_hist();
+    each([&](int e, float x) {
+      if (order_of(x, e) >= cut) atomicAdd(&sh->hist[bin_of(x)], by_weight ? share_of(x) : 1u);
+    });
+    uint64_t above = 0;
+    const float width = inv_t / per_x;  // of a bin, in y
+    const int bin = find_bin(want, &above, [&](int b, uint32_t sum) {
+      return by_weight ? (uint64_t)((float)sum * expf(-width * b) * (float)(1 << (kFixed - 17))) : (uint64_t)sum;
+    });
+    if (bin < kBins - 1) {  // (the last bin has no lower end)
+      Fixed f;
+      each([&](int e, float x) {
+        const int b = bin_of(x);
+        if (b > bin || order_of(x, e) < cut) return;
+        if (b == bin)
+          put(order_of(x, e));
+        else if (by_weight)
+          f.add(w_of(x));
+      });
+      if (by_weight) above = cluster_sum(f.sum(), 2 + (cut != 0));
+      const int n = gather(true, cut != 0);
+      if (n >= 0 && above < want) {
+        const uint64_t* order = sort_list(sh->list, sh->weight, n);
+        constexpr int P = kList / kThreads;
+        uint64_t v[P], mine = 0, all;
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          const int k = tid * P + i;
+          v[i] = k >= n ? 0 : by_weight ? fixed_of(w_of(logit_of(order[k]))) : 1;
+          mine += v[i];
+        }
+        uint64_t run = above + cta_scan(mine, sh, &all) - mine;
+        if (above + all >= want) {
+#pragma unroll
+          for (int i = 0; i < P; i++) {
+            if (run < want && want <= run + v[i]) sh->cut = order[tid * P + i];
+            run += v[i];
+          }
+          __syncthreads();
+          return sh->cut;
+        }
+      }
+    }
+    return select_slow(by_weight, want, cut);
   }
 };
 
@@ -462,7 +510,7 @@ __device__ __forceinline__ float logprob_of(float y, uint64_t total) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  Draw<T> d{{}, reinterpret_cast<Shared*>(raw_smem), cg::this_cluster()};
+  Draw<T> d{{}, reinterpret_cast<Shared*>(raw_smem), nullptr, cg::this_cluster()};
   Shared* sh = d.sh;
   const int C = d.C = (int)d.cl.num_blocks(), rank = d.rank = (int)d.cl.block_rank();
   const int b = blockIdx.x / C;
@@ -475,63 +523,116 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   // each warp of the cluster has a run of granules, in index order
   const int parts = d.parts = C * kWarps, part = d.part = rank * kWarps + warp;
   d.lo = (int)((int64_t)d.granules * part / parts), d.hi = (int)((int64_t)d.granules * (part + 1) / parts);
+  d.first = (int)((int64_t)d.granules * rank / C);
 
   float temp = a.temp_v ? a.temp_v[b] : a.temp;
   int k = a.top_k_v ? a.top_k_v[b] : a.top_k;
   const float top_p = a.top_p_v ? a.top_p_v[b] : a.top_p;
   const float min_p = fminf(a.min_p_v ? a.min_p_v[b] : a.min_p, 1.f);
+  const float u = a.u[b];
   if (!(temp > 0.f)) {
     temp = 1.f;
     k = 1;
   }
-  d.inv_t = 1.f / temp;
+  d.inv_t = fminf(1.f / temp, kMost);
   // the bins reach 32 in y, past which nothing weighs anything, or 24 in x
-  d.per_x = (float)kBins / fminf(32.f * temp, 24.f);
-  const bool by_k = k > 0 && k < a.vocab, by_p = top_p < 1.f || top_p != top_p;
+  d.per_x = fminf((float)kBins / fminf(32.f * temp, 24.f), kMost);
+  const bool by_k = k > 0 && k < a.vocab, by_p = top_p < 1.f || top_p != top_p, by_min = min_p > 0.f;
 
-  // ---- the largest logit
-  float top = -INFINITY;
-  d.each([&](int, float x) { top = fmaxf(top, x); });
+  // ---- the largest logit; the row comes into shared memory
+  float most = -INFINITY;  // this thread's
+  if (a.staged) {
+    uint4* stage = reinterpret_cast<uint4*>(raw_smem + sizeof(Shared));
+#pragma unroll 4
+    for (int i = d.lo + lane; i < d.hi; i += 32) {
+      float v[VEC];
+      d.row.load(i, v);
+      uint4 raw;
+      T* r = reinterpret_cast<T*>(&raw);
 #pragma unroll
-  for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  if (lane == 0) sh->top[warp] = top;
+      for (int j = 0; j < VEC; j++) {
+        r[j] = from_f32<T>(v[j]);
+        most = fmaxf(most, v[j]);
+      }
+      stage[i - d.first] = raw;  // read back by this lane alone
+    }
+    d.stage = stage;
+  } else {
+    d.each([&](int, float x) { most = fmaxf(most, x); });
+  }
   d.clear_hist();
-  d.cl.sync();
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, *d.at(&sh->top[i % kWarps], i / kWarps));
+  float top = most;
 #pragma unroll
   for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  if (lane == 0) sh->warp_b[warp] = __float_as_uint(top);
+  __syncthreads();
+  if (warp == 0) {
+    top = lane < kWarps ? __uint_as_float(sh->warp_b[lane]) : -INFINITY;
+#pragma unroll
+    for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    d.leave(sh->box_top, top);
+  }
+  d.sync();
+  top = sh->box_top[0];
+  for (int r = 1; r < C; r++) top = fmaxf(top, sh->box_top[r]);
   d.top = top;
-  if (top == -INFINITY) {  // nothing to draw from (the same for the whole cluster)
+  if (top == -INFINITY) {  // nothing to draw from
     if (rank == 0 && tid == 0) {
       a.token[b] = -1;
       a.logprob[b] = -INFINITY;
       a.kept[b] = 0;
     }
-    d.cl.sync();
+    d.sync();
     return;
   }
-  const float u = a.u[b];
 
-  uint64_t cut = 0;  // kept are the tokens of at least this order
+  // ---- the candidates: logits from x_c up, all kept ones among them
+  float x_c = -INFINITY;
+  if (by_k || (by_p && !by_min)) {
+    const int need = by_k ? k : kGuess;
+    if (need <= C * kThreads) {
+      if (most > -INFINITY) atomicAdd(&sh->hist[d.bin_of(most)], 1u);
+      uint64_t above;
+      const int bin = d.find_bin((uint64_t)need, &above, [](int, uint32_t sum) { return (uint64_t)sum; });
+      // at or below the bin's lower end
+      if (bin < kBins - 1) x_c = __fadd_rd(top, -(bin + 1) / d.per_x * 1.00001f);
+    }
+  }
+  // at or below the last logit whose weight is min_p (but p's share is of all k)
+  if (by_min && !(by_k && by_p)) x_c = fmaxf(x_c, __fadd_rd(top, (logf(min_p) * 1.0001f - 0.001f) * temp));
+  const bool some = x_c > -INFINITY, all_weights = by_p && !by_k;
+  uint64_t total = 0, cut = 0;
   int n = -1;
-  if (by_k) cut = d.select(false, (uint64_t)k, 0, false, &n);
+  if (some || all_weights) {
+    Fixed f;
+    d.each([&](int e, float x) {
+      if (all_weights) f.add(d.w_of(x));
+      if (some && x >= x_c) d.put(order_of(x, e));
+    });
+    if (all_weights) total = d.cluster_sum(f.sum(), 0);
+    if (some) n = d.gather(false, 0);
+  }
   if (n >= 0) {
-    // ---- all that is left is in the list, in order: every CTA would find the same, the first one does
+    // ---- the first CTA decides on the list
     if (rank == 0) {
+      uint64_t* order = sort_list(sh->list, sh->mine, n);
       constexpr int P = kList / kThreads;
-      const int m0 = k;
+      const int m0 = by_k && k < n ? k : n;
       uint64_t v[P], mine = 0, all;
       float w[P];
 #pragma unroll
       for (int i = 0; i < P; i++) {
         const int j = tid * P + i;
-        w[i] = j < m0 ? d.w_of(of_key((uint32_t)(sh->list[j] >> 32))) : 0.f;
-        v[i] = fixed_of(w[i]);
+        w[i] = j < m0 ? d.w_of(logit_of(order[j])) : 0.f;
+        v[i] = j < m0 ? fixed_of(w[i]) : 0;
+        if (j < n) sh->weight[j] = v[i];
         mine += v[i];
       }
       uint64_t run = cta_scan(mine, sh, &all) - mine;
-      const uint64_t want = by_p ? goal_of(top_p, all) : UINT64_MAX;
-      uint32_t c = 0;
+      const uint64_t want = by_p ? goal_of(top_p, by_k ? all : total) : UINT64_MAX;
+      // (with min_p alone behind the candidates' end, nothing before it is left out)
+      const bool enough = by_k || by_min || all >= want;
+      uint64_t c = 0;
 #pragma unroll
       for (int i = 0; i < P; i++) {
         c += tid * P + i < m0 && run < want && w[i] >= min_p;
@@ -539,156 +640,143 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       }
       uint64_t kept;
       cta_scan(c, sh, &kept);
-      // in index order now, each with its place in the list of logits
       const int m = (int)kept;
-      for (int i = tid; i < m; i += kThreads)
-        sh->mine[i] = (sh->list[i] & 0xffffffffull) << 32 | (uint32_t)i;
-      __syncthreads();
-      sort_list(sh->mine, m);
-      mine = 0;
-#pragma unroll
-      for (int i = 0; i < P; i++) {
-        const int j = tid * P + i;
-        v[i] = j < m ? d.f_of(of_key((uint32_t)(sh->list[(uint32_t)sh->mine[j]] >> 32))) : 0;
-        mine += v[i];
-      }
-      run = cta_scan(mine, sh, &all) - mine;
-      const uint64_t aim = aim_of(u, all);
-#pragma unroll
-      for (int i = 0; i < P; i++) {
-        if (run <= aim && aim < run + v[i]) {
-          const uint64_t it = sh->mine[tid * P + i];
-          a.token[b] = (int32_t)(0xffffffffu - (uint32_t)(it >> 32));
-          a.logprob[b] = logprob_of(d.y_of(of_key((uint32_t)(sh->list[(uint32_t)it] >> 32))), all);
-          a.kept[b] = (int32_t)kept;
+      if (!enough) {
+        n = -1;
+      } else if (m <= kSmall) {
+        // in index order, by counting
+        if (warp * 32 < m) {
+          uint64_t before = 0, sum = 0;
+          const uint32_t mine_at = tid < m ? (uint32_t)order[tid] : 0;
+          for (int i = 0; i < m; i++) {
+            const uint64_t f = sh->weight[i];
+            sum += f;
+            if ((uint32_t)order[i] > mine_at) before += f;  // a lower index
+          }
+          const uint64_t aim = aim_of(u, sum);
+          if (tid < m && before <= aim && aim < before + sh->weight[tid]) {
+            a.token[b] = index_of(order[tid]);
+            a.logprob[b] = logprob_of(d.y_of(logit_of(order[tid])), sum);
+            a.kept[b] = m;
+          }
         }
-        run += v[i];
+      } else {
+        // in index order, each with its place in the order of logits
+        uint64_t* by_index = order == sh->list ? sh->mine : sh->list;
+        for (int i = tid; i < m; i += kThreads) by_index[i] = (order[i] & 0xffffffffull) << 32 | (uint32_t)i;
+        __syncthreads();
+        by_index = sort_list(by_index, nullptr, m);
+        mine = 0;
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          const int j = tid * P + i;
+          v[i] = j < m ? sh->weight[(uint32_t)by_index[j]] : 0;
+          mine += v[i];
+        }
+        run = cta_scan(mine, sh, &all) - mine;
+        const uint64_t aim = aim_of(u, all);
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          if (run <= aim && aim < run + v[i]) {
+            const uint64_t it = order[(uint32_t)by_index[tid * P + i]];
+            a.token[b] = index_of(it);
+            a.logprob[b] = logprob_of(d.y_of(logit_of(it)), all);
+            a.kept[b] = m;
+          }
+          run += v[i];
+        }
       }
     }
-    d.cl.sync();  // no CTA leaves while another may read its shared memory
-    return;
+    if (all_weights && !by_min) {  // the guess for p may have been too small
+      if (warp == 0 && rank == 0 && lane < C) *d.at(&sh->bin, lane) = n >= 0;
+      d.sync();
+      n = sh->bin ? 0 : -1;
+    } else {
+      d.sync();  // no CTA leaves while another may read its shared memory
+    }
+    if (n >= 0) return;
   }
 
-  if (by_p) {
-    // the weight of the first k, and the weight that min_p leaves of it
-    if (by_k) {
-      d.cl.sync();
-      d.clear_hist();
+  // ---- the end of the kept prefix in the whole row
+  if (by_k) {
+    cut = d.select(false, (uint64_t)k, 0);
+    if (by_p) {
+      Fixed f;
+      d.each([&](int e, float x) {
+        if (order_of(x, e) >= cut) f.add(d.w_of(x));
+      });
+      total = d.cluster_sum(f.sum(), 0);
     }
-    const bool early = !(min_p > 0.f);  // with min_p the histogram is seldom needed
-    uint64_t sum = 0, left = 0;
-    d.each([&](int e, float x) {
-      if (order_of(x, e) < cut) return;
-      const float w = d.w_of(x);
-      const uint64_t f = fixed_of(w);
-      sum += f;
-      if (early)
-        atomicAdd(&sh->hist[d.bin_of(x)], d.share_of(x));
-      else if (w >= min_p)
-        left += f;
-    });
-    if (!early) {
-      left = warp_sum(left);
-      if (lane == 0) sh->warp_a[3][warp] = left;
-    }
-    sum = d.cluster_sum(sum, 0);
-    const uint64_t want = goal_of(top_p, sum);
-    bool binds = true;
-    if (!early) {
-      left = 0;
-      for (int i = lane; i < parts; i += 32) left += *d.at(&sh->warp_a[3][i % kWarps], i / kWarps);
-      binds = warp_sum(left) >= want;  // else min_p ends the prefix before
-    }
-    if (binds) cut = d.select(true, want, cut, early, &n);
   }
+  if (by_p) cut = d.select(true, goal_of(top_p, total), cut);
 
-  // ---- the draw
-  auto keeps = [&](int e, float x, uint64_t* f) {
-    *f = 0;
-    if (order_of(x, e) < cut) return false;
-    const float w = d.w_of(x);
-    if (w < min_p) return false;
-    *f = fixed_of(w);
-    return true;
+  // ---- the draw: kept are the tokens of at least this order, and of min_p's weight
+  const float x_cut = cut ? logit_of(cut) : -INFINITY;
+  auto weigh = [&](int e, float x, float* w) {
+    if (x < x_cut || (cut && order_of(x, e) < cut)) return false;
+    *w = d.w_of(x);
+    return *w >= min_p && d.in_row(e);
   };
-  uint64_t sum = 0;
+  Fixed f;
   uint32_t c = 0;
   d.each([&](int e, float x) {
-    uint64_t f;
-    c += keeps(e, x, &f);
-    sum += f;
-  });
-  sum = warp_sum(sum);
-  c = (uint32_t)warp_sum(c);
-  if (lane == 0) {
-    sh->warp_a[1][warp] = sum;
-    sh->warp_b[0][warp] = c;
-  }
-  d.cl.sync();
-  // parts in index order: four to a lane
-  constexpr int P = kMaxCluster * kWarps / 32;
-  uint64_t v[P], mine = 0, kept = 0;
-#pragma unroll
-  for (int i = 0; i < P; i++) {
-    const int j = lane * P + i;
-    v[i] = j < parts ? *d.at(&sh->warp_a[1][j % kWarps], j / kWarps) : 0;
-    kept += j < parts ? *d.at(&sh->warp_b[0][j % kWarps], j / kWarps) : 0;
-    mine += v[i];
-  }
-  kept = warp_sum(kept);
-  uint64_t incl = mine;
-#pragma unroll
-  for (int x = 1; x < 32; x *= 2) {
-    const uint64_t up = __shfl_up_sync(0xffffffffu, incl, x);
-    if (lane >= x) incl += up;
-  }
-  const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
-  const uint64_t aim = aim_of(u, total);
-  uint64_t run = incl - mine, left = 0;
-  bool ours = false;
-#pragma unroll
-  for (int i = 0; i < P; i++) {
-    if (lane * P + i == part && run <= aim && aim < run + v[i]) {
-      ours = true;
-      left = aim - run;
+    float w;
+    if (weigh(e, x, &w)) {
+      f.add(w);
+      c++;
     }
-    run += v[i];
+  });
+  const uint64_t mine = warp_sum(f.sum());
+  c = (uint32_t)warp_sum(c);
+  d.sync();  // the boxes are free
+  if (lane == 0) {
+    sh->warp_a[warp] = mine;
+    sh->warp_b[warp] = c;
   }
-  if (__any_sync(0xffffffffu, ours)) {
+  __syncthreads();
+  uint64_t before = 0;  // of this CTA's warps before this one
+  if (warp == 0) {
+    d.leave(sh->box_sum[1], warp_sum(lane < kWarps ? sh->warp_a[lane] : 0));
+    d.leave(sh->box_count[1], (uint32_t)warp_sum(lane < kWarps ? sh->warp_b[lane] : 0));
+  }
+  d.sync();
+  uint32_t kept = 0;
+  total = 0;
+  for (int r = 0; r < C; r++) {
+    if (r == rank) before = total;
+    total += sh->box_sum[1][r];
+    kept += sh->box_count[1][r];
+  }
+  for (int w = 0; w < warp; w++) before += sh->warp_a[w];
+  const uint64_t aim = aim_of(u, total);
+  if (before <= aim && aim < before + mine) {
     // the first element of this warp's run whose running sum exceeds it
-    left = warp_sum(left);
+    uint64_t left = aim - before;
     for (int i0 = d.lo; i0 < d.hi; i0 += 32) {
       const int i = i0 + lane;
       float x[VEC];
-      uint64_t f[VEC];
-      mine = 0;
+      uint64_t v[VEC], own = 0;
       if (i < d.hi) {
-        d.row.load(i, x);
+        d.get(i, x);
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          const int e = i * VEC - d.row.pad + j;
-          f[j] = 0;
-          if (e >= 0 && e < a.vocab) keeps(e, x[j], &f[j]);
-          mine += f[j];
+          float w;
+          v[j] = weigh(i * VEC - d.row.pad + j, x[j], &w) ? fixed_of(w) : 0;
+          own += v[j];
         }
       }
-      incl = mine;
-#pragma unroll
-      for (int s = 1; s < 32; s *= 2) {
-        const uint64_t up = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += up;
-      }
+      const uint64_t incl = warp_scan(own);
       const uint64_t all = __shfl_sync(0xffffffffu, incl, 31);
       if (all <= left) {
         left -= all;
         continue;
       }
-      if (incl > left && incl - mine <= left) {
-        run = incl - mine;
+      if (incl > left && incl - own <= left) {
+        uint64_t run = incl - own;
         bool done = false;
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          run += f[j];
+          run += v[j];
           if (!done && run > left) {
             done = true;
             a.token[b] = i * VEC - d.row.pad + j;
@@ -700,21 +788,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       break;
     }
   }
-  d.cl.sync();  // no CTA leaves while another may read its shared memory
+  if (C > 1) d.cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
 template <typename T>
-cudaError_t launch(const Args& a, int lanes, cudaStream_t st) {
-  // a row is split until a CTA has 4096 logits, or the CTAs fill the device;
-  // a CTA's share stays below 2^17 logits (select_slow)
+cudaError_t launch(Args& a, int lanes, cudaStream_t st) {
+  // a row is split until a CTA has 8192 logits, or the CTAs fill the device (two
+  // to a multiprocessor); a CTA's share stays below 2^17 logits (select_slow)
   int c = 1;
   while (c < kMaxCluster &&
-         (a.vocab > (1 << 17) * c || (a.vocab > 4096 * c && (int64_t)lanes * c <= ops_sm_count())))
+         (a.vocab > (1 << 17) * c || (a.vocab > 8192 * c && (int64_t)lanes * c <= ops_sm_count())))
     c *= 2;
+  const int share = ((a.vocab + 16) * (int)sizeof(T) / c / 16 + 2) * 16;  // bytes, at most
+  a.staged = share <= kStage;
+  const int smem = (int)sizeof(Shared) + (a.staged ? share : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)lanes * c);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -725,7 +816,8 @@ cudaError_t launch(const Args& a, int lanes, cudaStream_t st) {
   static OpsOnce once;
   if (const int dev = ops_current(); !once(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+        cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Shared) + kStage);
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
