@@ -35,6 +35,8 @@
 //     selection on the logits' ordered bits takes over, with exact sums.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "wfst_ops.h"
 
 namespace cg = cooperative_groups;
@@ -47,9 +49,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCoarse = kBins / 32;
 constexpr int kList = 1024;          // candidates that are ordered
-constexpr int kSmall = 256;          // up to here by counting, from there on bitonic
-constexpr int kGuess = 512;          // threads whose largest logit p's first guess covers
-constexpr int kStage = 64 * 1024;    // bytes of a row's share that are held in shared memory
+constexpr int kSmall = 64;           // ordered by counting all of them, from there on those of their bin
+constexpr int kGuess = 192;          // threads whose largest logit p's first guess covers
+constexpr int kStage = 65 * 1024;    // bytes of a row's share that are held in shared memory
 constexpr int kMaxCluster = 8;
 constexpr int kFixed = 43;
 constexpr float kMost = 3.402823466e38f;
@@ -132,11 +134,11 @@ struct Row {
   }
 };
 
-struct Shared {
+struct alignas(16) Shared {  // the row's granules lie behind it
   uint32_t hist[kBins];
   uint64_t list[kList];   // the candidates, gathered
   uint64_t mine[kList];   // what this CTA found
-  uint64_t weight[kList];
+  uint64_t weight[kList], extra[kList];
   // from the cluster's CTAs, one slot each; one array per use
   uint64_t box_coarse[kMaxCluster][kCoarse], box_sum[4][kMaxCluster];
   uint32_t box_count[2][kMaxCluster];
@@ -144,7 +146,7 @@ struct Shared {
   uint64_t warp_a[kWarps], scan[kWarps + 1];
   uint32_t warp_b[kWarps];
   uint64_t cut, above;
-  uint32_t bin, count;
+  uint32_t bin, count, least, most;
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -177,37 +179,64 @@ __device__ __forceinline__ uint64_t cta_scan(uint64_t v, Shared* sh, uint64_t* a
   return before + v;
 }
 
-// Descending order of list[0 .. n), n <= kList, into `to` (kSmall and below) or
-// in place; returns where.
-__device__ uint64_t* sort_list(uint64_t* list, uint64_t* to, int n) {
+// Descending order of list[0 .. n), n <= kList, into `to`.  bin(v) sorts no
+// higher value behind a lower one: a value's place is what the bins before hold
+// and what is larger in its own.  Uses sh->hist.
+template <typename F>
+__device__ void sort_list(const uint64_t* list, uint64_t* to, int n, Shared* sh, F bin) {
+  const int tid = threadIdx.x;
   if (n <= kSmall) {
-    if ((int)threadIdx.x < n) {
-      const uint64_t v = list[threadIdx.x];
+    if (tid < n) {
+      const uint64_t v = list[tid];
       int r = 0;
       for (int i = 0; i < n; i++) r += list[i] > v;
       to[r] = v;
     }
     __syncthreads();
-    return to;
+    return;
   }
-  int p = 2;
-  while (p < n) p *= 2;
-  for (int i = threadIdx.x; i < p; i += kThreads)
-    if (i >= n) list[i] = 0;
-  for (int k = 2; k <= p; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < p / 2; t += kThreads) {
-        const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
-        const uint64_t a = list[lo], b = list[hi];
-        if ((a < b) == ((lo & k) == 0)) {
-          list[lo] = b;
-          list[hi] = a;
-        }
-      }
+  constexpr int P = kBins / kThreads, Q = kList / kThreads;
+  for (int i = tid; i < kBins; i += kThreads) sh->hist[i] = 0;
+  __syncthreads();
+  uint32_t slot[Q];
+#pragma unroll
+  for (int q = 0; q < Q; q++)
+    if (tid + q * kThreads < n) slot[q] = atomicAdd(&sh->hist[bin(list[tid + q * kThreads])], 1u);
+  __syncthreads();
+  uint32_t c[P];
+  uint64_t mine = 0, all;
+#pragma unroll
+  for (int i = 0; i < P; i++) mine += c[i] = sh->hist[tid * P + i];
+  uint32_t run = (uint32_t)(cta_scan(mine, sh, &all) - mine);
+#pragma unroll
+  for (int i = 0; i < P; i++) {
+    sh->hist[tid * P + i] = run;  // where the bin begins
+    run += c[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < Q; q++)
+    if (tid + q * kThreads < n) {
+      const uint64_t v = list[tid + q * kThreads];
+      to[sh->hist[bin(v)] + slot[q]] = v;
     }
   __syncthreads();
-  return list;
+  uint64_t v[Q];
+  uint32_t r[Q];
+#pragma unroll
+  for (int q = 0; q < Q; q++)
+    if (tid + q * kThreads < n) {
+      v[q] = to[tid + q * kThreads];
+      const int b = bin(v[q]);
+      const uint32_t from = sh->hist[b], end = b + 1 < kBins ? sh->hist[b + 1] : (uint32_t)n;
+      r[q] = from;
+      for (uint32_t i = from; i < end; i++) r[q] += to[i] > v[q];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < Q; q++)
+    if (tid + q * kThreads < n) to[r[q]] = v[q];
+  __syncthreads();
 }
 
 // One row, one cluster.  What is computed from all CTAs' values is computed by
@@ -224,7 +253,12 @@ struct Draw {
 
   __device__ __forceinline__ float y_of(float x) const { return (x - top) * inv_t; }
   __device__ __forceinline__ float w_of(float x) const { return expf(y_of(x)); }
-  __device__ __forceinline__ int bin_of(float x) const { return (int)fminf((top - x) * per_x, (float)(kBins - 1)); }
+  // distance to the largest logit in bins, and its whole part (adding 2^23
+  // towards zero leaves it in the mantissa: conversions are slow)
+  __device__ __forceinline__ float far_of(float x) const { return fminf((top - x) * per_x, (float)(kBins - 1)); }
+  __device__ __forceinline__ int bin_of(float x) const {
+    return (int)(__float_as_uint(__fadd_rz(far_of(x), 8388608.f)) & (kBins - 1));
+  }
   template <typename V>
   __device__ __forceinline__ V* at(V* p, int r) {
     return cl.map_shared_rank(p, r);
@@ -278,18 +312,49 @@ struct Draw {
       for (int j = 0; j < VEC; j++) f(i * VEC - row.pad + j, v[j]);
     }
   }
+  // The candidates in order.  Their bins are linear in the logit's bits between
+  // the list's ends, and in the index among equal ones, of which rounded logits
+  // have many.
+  __device__ __forceinline__ void sort(uint64_t* to, int n) {
+    constexpr int kStep = std::is_same_v<T, float> ? 0 : std::is_same_v<T, __half> ? 13 : 16;  // bits without content
+    uint32_t k0 = 0xffffffffu, k1 = 0;
+    for (int i = tid; i < n; i += kThreads) {
+      k0 = min(k0, (uint32_t)(sh->list[i] >> 32));
+      k1 = max(k1, (uint32_t)(sh->list[i] >> 32));
+    }
+    if (tid == 0) sh->least = 0xffffffffu, sh->most = 0;
+    __syncthreads();
+    k0 = __reduce_min_sync(0xffffffffu, k0);
+    k1 = __reduce_max_sync(0xffffffffu, k1);
+    if (lane == 0 && k0 <= k1) {
+      atomicMin(&sh->least, k0);
+      atomicMax(&sh->most, k1);
+    }
+    __syncthreads();
+    const uint32_t last = sh->most;
+    const float scale = (float)kBins / ((float)((last - sh->least) >> kStep) + 1.f), per = 1.f / (float)row.vocab;
+    sort_list(sh->list, to, n, sh, [&](uint64_t v) {
+      const float at = (float)((last - (uint32_t)(v >> 32)) >> kStep) + fminf((float)index_of(v) * per, 1.f);
+      return min((int)(at * scale), kBins - 1);
+    });
+  }
   __device__ __forceinline__ bool in_row(int e) const { return e >= 0 && e < row.vocab; }
 
   // The bin where the running sum over all CTAs' histograms reaches `want`;
   // *above: the sum before it.  Bins count as value(bin, sum).  kBins if it is
-  // never reached.  The histogram must stay until the next cluster barrier.
-  template <typename F>
+  // never reached.  The histogram must stay until the next cluster barrier.  COUNT:
+  // value is the sum itself.
+  template <bool COUNT, typename F>
   __device__ int find_bin(uint64_t want, uint64_t* above, F value) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kCoarse / kWarps; i++) {
       const int c = warp * (kCoarse / kWarps) + i;
-      const uint64_t v = warp_sum(value(c * 32 + lane, sh->hist[c * 32 + lane]));
+      uint64_t v;
+      if constexpr (COUNT)
+        v = __reduce_add_sync(0xffffffffu, sh->hist[c * 32 + lane]);
+      else
+        v = warp_sum(value(c * 32 + lane, sh->hist[c * 32 + lane]));
       if (lane < C) at(&sh->box_coarse[rank][0], lane)[c] = v;
     }
     sync();
@@ -405,7 +470,7 @@ struct Draw {
     if (before < n && n <= before + here) {  // this warp's run holds it
       uint64_t left = n - before;
       for (int i0 = lo; i0 < hi; i0 += 32) {
-        float v[VEC];
+        float v[VEC] = {};
         uint32_t mine = 0;
         auto counts = [&](int j) {
           const int e = (i0 + lane) * VEC - row.pad + j;
@@ -438,37 +503,51 @@ struct Draw {
 
   // An element's weight as a share of its bin's upper one, in units of 2^-17.
   __device__ __forceinline__ uint32_t share_of(float x) const {
-    const float d = (top - x) * per_x;
-    const float z = (d - floorf(d)) * (inv_t / per_x);
-    return d < (float)(kBins - 1) ? (uint32_t)((1.f - z + 0.5f * z * z) * 131072.f + 0.5f) : 131072u;
+    const float d = far_of(x);
+    const float z = (d - (__fadd_rz(d, 8388608.f) - 8388608.f)) * (inv_t / per_x);
+    const float share = __fmaf_rn(__fmaf_rn(65536.f, z, -131072.f), z, 131072.5f);
+    return __float_as_uint(__fadd_rz(share, 8388608.f)) & 0x3ffffu;
   }
 
-  // The same as select_slow's through the histogram of distances.
-  __device__ uint64_t select(bool by_weight, uint64_t want, uint64_t cut) {
+  // The same as select_slow's through the histogram of distances.  *kept: this
+  // warp's share of the prefix, where `sums` says that it is known (for weights).
+  __device__ uint64_t select(bool by_weight, uint64_t want, uint64_t cut, uint64_t* kept_w, uint32_t* kept_c, bool* sums) {
+    *sums = false;
     sync();
     clear_hist();
+    const float x_first = logit_of(cut);
+    auto at_or_before = [&](int e, float x) { return !cut || x > x_first || (x == x_first && order_of(x, e) >= cut); };
     each([&](int e, float x) {
-      if (order_of(x, e) >= cut) atomicAdd(&sh->hist[bin_of(x)], by_weight ? share_of(x) : 1u);
+      if (at_or_before(e, x)) atomicAdd(&sh->hist[bin_of(x)], by_weight ? share_of(x) : 1u);
     });
     uint64_t above = 0;
     const float width = inv_t / per_x;  // of a bin, in y
-    const int bin = find_bin(want, &above, [&](int b, uint32_t sum) {
-      return by_weight ? (uint64_t)((float)sum * expf(-width * b) * (float)(1 << (kFixed - 17))) : (uint64_t)sum;
-    });
+    const int bin =
+        by_weight ? find_bin<false>(want, &above,
+                                    [&](int b, uint32_t sum) {
+                                      return (uint64_t)((float)sum * expf(-width * b) * (float)(1 << (kFixed - 17)));
+                                    })
+                  : find_bin<true>(want, &above, [](int, uint32_t sum) { return (uint64_t)sum; });
     if (bin < kBins - 1) {  // (the last bin has no lower end)
       Fixed f;
+      uint32_t c = 0;
       each([&](int e, float x) {
-        const int b = bin_of(x);
-        if (b > bin || order_of(x, e) < cut) return;
-        if (b == bin)
+        const float far = far_of(x);
+        if (far >= (float)(bin + 1) || !at_or_before(e, x)) return;
+        if (far >= (float)bin) {
           put(order_of(x, e));
-        else if (by_weight)
+        } else if (by_weight) {
           f.add(w_of(x));
+          c++;
+        }
       });
+      *kept_w = warp_sum(f.sum());
+      *kept_c = __reduce_add_sync(0xffffffffu, c);
       if (by_weight) above = cluster_sum(f.sum(), 2 + (cut != 0));
       const int n = gather(true, cut != 0);
       if (n >= 0 && above < want) {
-        const uint64_t* order = sort_list(sh->list, sh->weight, n);
+        uint64_t* order = sh->weight;
+        sort(order, n);
         constexpr int P = kList / kThreads;
         uint64_t v[P], mine = 0, all;
 #pragma unroll
@@ -485,7 +564,22 @@ struct Draw {
             run += v[i];
           }
           __syncthreads();
-          return sh->cut;
+          const uint64_t end = sh->cut;
+          // those of the bin that are in this warp's run of the row
+          const int e0 = lo * VEC - row.pad, e1 = hi * VEC - row.pad;
+          Fixed g;
+          c = 0;
+          for (int i = lane; i < n; i += 32) {
+            const int e = index_of(order[i]);
+            if (order[i] >= end && e >= e0 && e < e1) {
+              g.add(w_of(logit_of(order[i])));
+              c++;
+            }
+          }
+          *kept_w += warp_sum(g.sum());
+          *kept_c += __reduce_add_sync(0xffffffffu, c);
+          *sums = by_weight;
+          return end;
         }
       }
     }
@@ -504,8 +598,10 @@ __device__ __forceinline__ uint64_t aim_of(float u, uint64_t total) {
   return aim < total - 1 ? aim : total - 1;
 }
 __device__ __forceinline__ float logprob_of(float y, uint64_t total) {
-  return y - (float)log((double)total * (1.0 / (1ull << kFixed)));
+  return y - logf((float)total * (1.f / (1ull << kFixed)));
 }
+
+static_assert(sizeof(Shared) % 16 == 0);
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
@@ -593,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (need <= C * kThreads) {
       if (most > -INFINITY) atomicAdd(&sh->hist[d.bin_of(most)], 1u);
       uint64_t above;
-      const int bin = d.find_bin((uint64_t)need, &above, [](int, uint32_t sum) { return (uint64_t)sum; });
+      const int bin = d.template find_bin<true>((uint64_t)need, &above, [](int, uint32_t sum) { return (uint64_t)sum; });
       // at or below the bin's lower end
       if (bin < kBins - 1) x_c = __fadd_rd(top, -(bin + 1) / d.per_x * 1.00001f);
     }
@@ -603,22 +699,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const bool some = x_c > -INFINITY, all_weights = by_p && !by_k;
   uint64_t total = 0, cut = 0;
   int n = -1;
+  bool sums = false;  // this warp's share of the kept tokens is known:
+  uint64_t mine = 0;
+  uint32_t mine_c = 0;
   if (some || all_weights) {
-    Fixed f;
+    Fixed f, g;  // of all logits, of those that min_p keeps
+    uint32_t c = 0;
+    const bool apart = by_min && !by_k;
     d.each([&](int e, float x) {
       if (all_weights) f.add(d.w_of(x));
-      if (some && x >= x_c) d.put(order_of(x, e));
+      if (some && x >= x_c) {
+        d.put(order_of(x, e));
+        if (apart) {
+          const float w = d.w_of(x);
+          if (w >= min_p) {
+            g.add(w);
+            c++;
+          }
+        }
+      }
     });
     if (all_weights) total = d.cluster_sum(f.sum(), 0);
     if (some) n = d.gather(false, 0);
+    if (n < 0 && apart) {  // too many for the list; min_p may end the prefix before p does
+      mine = warp_sum(g.sum());
+      mine_c = __reduce_add_sync(0xffffffffu, c);
+      sums = !by_p || d.cluster_sum(g.sum(), 1) < goal_of(top_p, total);
+    }
   }
   if (n >= 0) {
     // ---- the first CTA decides on the list
     if (rank == 0) {
-      uint64_t* order = sort_list(sh->list, sh->mine, n);
+      uint64_t* order = sh->mine;
+      d.sort(order, n);
       constexpr int P = kList / kThreads;
       const int m0 = by_k && k < n ? k : n;
-      uint64_t v[P], mine = 0, all;
+      uint64_t v[P], part_sum = 0, all;
       float w[P];
 #pragma unroll
       for (int i = 0; i < P; i++) {
@@ -626,64 +742,77 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         w[i] = j < m0 ? d.w_of(logit_of(order[j])) : 0.f;
         v[i] = j < m0 ? fixed_of(w[i]) : 0;
         if (j < n) sh->weight[j] = v[i];
-        mine += v[i];
+        part_sum += v[i];
       }
-      uint64_t run = cta_scan(mine, sh, &all) - mine;
-      const uint64_t want = by_p ? goal_of(top_p, by_k ? all : total) : UINT64_MAX;
-      // (with min_p alone behind the candidates' end, nothing before it is left out)
+      uint64_t run = cta_scan(part_sum, sh, &all) - part_sum;
+      uint64_t want = UINT64_MAX;
+      if (by_p) {  // in one warp: 64-bit floating point is slow here
+        if (warp == 0) sh->above = goal_of(top_p, by_k ? all : total);
+        __syncthreads();
+        want = sh->above;
+      }
+      // (what min_p or k ends needs no more than the candidates)
       const bool enough = by_k || by_min || all >= want;
-      uint64_t c = 0;
+      int c = 0;
 #pragma unroll
       for (int i = 0; i < P; i++) {
         c += tid * P + i < m0 && run < want && w[i] >= min_p;
         run += v[i];
       }
-      uint64_t kept;
-      cta_scan(c, sh, &kept);
-      const int m = (int)kept;
+      // the kept ones are a prefix: threads with all of theirs, one with some
+      const int m = __syncthreads_count(c == P) * P + __syncthreads_count(c == 1);
+      static_assert(P == 2, "a thread keeps none, one or two");
       if (!enough) {
         n = -1;
-      } else if (m <= kSmall) {
-        // in index order, by counting
-        if (warp * 32 < m) {
-          uint64_t before = 0, sum = 0;
-          const uint32_t mine_at = tid < m ? (uint32_t)order[tid] : 0;
-          for (int i = 0; i < m; i++) {
-            const uint64_t f = sh->weight[i];
-            sum += f;
-            if ((uint32_t)order[i] > mine_at) before += f;  // a lower index
-          }
-          const uint64_t aim = aim_of(u, sum);
-          if (tid < m && before <= aim && aim < before + sh->weight[tid]) {
-            a.token[b] = index_of(order[tid]);
-            a.logprob[b] = logprob_of(d.y_of(logit_of(order[tid])), sum);
-            a.kept[b] = m;
-          }
-        }
       } else {
-        // in index order, each with its place in the order of logits
-        uint64_t* by_index = order == sh->list ? sh->mine : sh->list;
-        for (int i = tid; i < m; i += kThreads) by_index[i] = (order[i] & 0xffffffffull) << 32 | (uint32_t)i;
-        __syncthreads();
-        by_index = sort_list(by_index, nullptr, m);
-        mine = 0;
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-          const int j = tid * P + i;
-          v[i] = j < m ? sh->weight[(uint32_t)by_index[j]] : 0;
-          mine += v[i];
-        }
-        run = cta_scan(mine, sh, &all) - mine;
-        const uint64_t aim = aim_of(u, all);
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-          if (run <= aim && aim < run + v[i]) {
-            const uint64_t it = order[(uint32_t)by_index[tid * P + i]];
-            a.token[b] = index_of(it);
-            a.logprob[b] = logprob_of(d.y_of(logit_of(it)), all);
-            a.kept[b] = m;
+        auto answer = [&](uint64_t it, uint64_t sum) {
+          a.token[b] = index_of(it);
+          a.logprob[b] = logprob_of(d.y_of(logit_of(it)), sum);
+          a.kept[b] = m;
+        };
+        if (m <= kThreads / 4) {
+          // each kept token's place in the cumulative weight in index order, by
+          // counting; four lanes share a token
+          const int i = tid / 4;
+          if (warp * 8 < m) {
+            uint64_t before = 0, sum = 0;
+            const uint32_t own = i < m ? (uint32_t)order[i] : 0;
+            for (int j = tid % 4; j < m; j += 4) {
+              const uint64_t f = sh->weight[j];
+              sum += f;
+              if ((uint32_t)order[j] > own) before += f;  // a lower index
+            }
+            for (int x = 1; x < 4; x *= 2) {
+              sum += __shfl_xor_sync(0xffffffffu, sum, x);
+              before += __shfl_xor_sync(0xffffffffu, before, x);
+            }
+            const uint64_t aim = aim_of(u, sum);
+            if (i < m && tid % 4 == 0 && before <= aim && aim < before + sh->weight[i]) answer(order[i], sum);
           }
-          run += v[i];
+        } else {
+          // ordered by index, each with its place in the order of logits
+          for (int i = tid; i < m; i += kThreads) sh->list[i] = (order[i] & 0xffffffffull) << 32 | (uint32_t)i;
+          __syncthreads();
+          const float per = (float)kBins / (float)a.vocab;
+          sort_list(sh->list, sh->extra, m, sh, [&](uint64_t v) {
+            return min((int)((float)(0xffffffffu - (uint32_t)(v >> 32)) * per), kBins - 1);
+          });
+          part_sum = 0;
+#pragma unroll
+          for (int i = 0; i < P; i++) {
+            const int j = tid * P + i;
+            v[i] = j < m ? sh->weight[(uint32_t)sh->extra[j]] : 0;
+            part_sum += v[i];
+          }
+          run = cta_scan(part_sum, sh, &all) - part_sum;
+          if (warp == 0) sh->above = aim_of(u, all);
+          __syncthreads();
+          const uint64_t aim = sh->above;
+#pragma unroll
+          for (int i = 0; i < P; i++) {
+            if (run <= aim && aim < run + v[i]) answer(order[(uint32_t)sh->extra[tid * P + i]], all);
+            run += v[i];
+          }
         }
       }
     }
@@ -698,17 +827,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
 
   // ---- the end of the kept prefix in the whole row
-  if (by_k) {
-    cut = d.select(false, (uint64_t)k, 0);
-    if (by_p) {
-      Fixed f;
-      d.each([&](int e, float x) {
-        if (order_of(x, e) >= cut) f.add(d.w_of(x));
-      });
-      total = d.cluster_sum(f.sum(), 0);
+  if (!sums) {
+    if (by_k) {
+      cut = d.select(false, (uint64_t)k, 0, &mine, &mine_c, &sums);
+      if (by_p) {
+        Fixed f;
+        d.each([&](int e, float x) {
+          if (order_of(x, e) >= cut) f.add(d.w_of(x));
+        });
+        total = d.cluster_sum(f.sum(), 0);
+      }
     }
+    if (by_p) cut = d.select(true, goal_of(top_p, total), cut, &mine, &mine_c, &sums);
+    sums = sums && !by_min;
   }
-  if (by_p) cut = d.select(true, goal_of(top_p, total), cut);
 
   // ---- the draw: kept are the tokens of at least this order, and of min_p's weight
   const float x_cut = cut ? logit_of(cut) : -INFINITY;
@@ -717,21 +849,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     *w = d.w_of(x);
     return *w >= min_p && d.in_row(e);
   };
-  Fixed f;
-  uint32_t c = 0;
-  d.each([&](int e, float x) {
-    float w;
-    if (weigh(e, x, &w)) {
-      f.add(w);
-      c++;
-    }
-  });
-  const uint64_t mine = warp_sum(f.sum());
-  c = (uint32_t)warp_sum(c);
+  if (!sums) {
+    Fixed f;
+    uint32_t c = 0;
+    d.each([&](int e, float x) {
+      float w;
+      if (weigh(e, x, &w)) {
+        f.add(w);
+        c++;
+      }
+    });
+    mine = warp_sum(f.sum());
+    mine_c = __reduce_add_sync(0xffffffffu, c);
+  }
   d.sync();  // the boxes are free
   if (lane == 0) {
     sh->warp_a[warp] = mine;
-    sh->warp_b[warp] = c;
+    sh->warp_b[warp] = mine_c;
   }
   __syncthreads();
   uint64_t before = 0;  // of this CTA's warps before this one
