@@ -53,6 +53,7 @@ struct Args {
   uint32_t div_m;
   int32_t div_s;
   float scale2;  // scale * log2(e)
+  int32_t o_even;  // o's pairs of elements are 4-byte aligned
 };
 
 // What a lane sees: n tokens, the first `first` as they are, the others
@@ -124,118 +125,120 @@ template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
   constexpr int S = kStages<D>, kTile = 16 * D * 2, kSlot = 2 * kTile, KS = D / 16, DT = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t s_scan[kWarps * 32 + 1];
-  __shared__ int s_b, s_last;
-  __shared__ int64_t s_base;
+  __shared__ uint32_t s_last[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int runs = a.hkv * a.runs;
 
-  // ---- this CTA's units: all lanes' tiles, numbered through
-  const int per = (a.lanes + kWarps * 32 - 1) / (kWarps * 32);
-  const int b_lo = min(a.lanes, tid * per), b_hi = min(a.lanes, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; b++) mine += seen(a, b).tiles;
-  s_scan[tid + 1] = mine;
-  if (tid == 0) s_scan[0] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t run_sum = 0;
-    for (int i = 0; i < kWarps; i++) {
-      int64_t v = s_scan[1 + i * 32 + lane];
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += up;
-      }
-      v += run_sum;
-      s_scan[1 + i * 32 + lane] = v;
-      run_sum = __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  __syncthreads();
-  const int64_t units = s_scan[kWarps * 32] * runs;
+  // ---- this CTA's units: all lanes' tiles, numbered through (each warp for itself)
+  uint32_t units = 0;
+#pragma unroll 4
+  for (int b = lane; b < a.lanes; b += 32) units += seen(a, b).tiles;
+  units = __reduce_add_sync(0xffffffffu, units) * runs;
   // CTAs that share the units; each of them has one at least
-  const int64_t G = min((int64_t)gridDim.x, units);
+  const uint32_t G = min(gridDim.x, units), each = units / G, more = units - each * G;
   if (blockIdx.x >= G) return;
-  const int64_t u0 = units * blockIdx.x / G, u1 = units * (blockIdx.x + 1) / G;
-  {
-    int64_t base = s_scan[tid] * runs;
-    for (int b = b_lo; b < b_hi; b++) {
-      const int64_t w = (int64_t)seen(a, b).tiles * runs;
-      if (u0 >= base && u0 < base + w) s_b = b, s_base = base;
-      base += w;
-    }
-  }
-  __syncthreads();
+  auto first_of = [&](uint32_t c) { return c * each + min(c, more); };
+  auto cta_of = [&](uint32_t u) {
+    const uint32_t at = more * (each + 1);
+    return u < at ? u / (each + 1) : more + (u - at) / each;
+  };
+  const uint32_t u0 = first_of(blockIdx.x), u1 = first_of(blockIdx.x + 1);
   Cursor at;  // of the unit that is computed
-  at.b = s_b;
+  uint32_t seg0 = 0;  // first unit of the current lane and run
+  for (int b0 = 0;; b0 += 32) {
+    const uint32_t mine = b0 + lane < a.lanes ? seen(a, b0 + lane).tiles * runs : 0;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, seg0 + incl > u0);
+    if (past) {
+      at.b = b0 + __ffs(past) - 1;
+      seg0 += __shfl_sync(0xffffffffu, incl - mine, __ffs(past) - 1);
+      break;
+    }
+    seg0 += __shfl_sync(0xffffffffu, incl, 31);
+  }
   at.s = seen(a, at.b);
-  int64_t seg0 = s_base;  // first unit of the current lane and run
-  at.run = (int)((u0 - seg0) / at.s.tiles);
-  seg0 += (int64_t)at.run * at.s.tiles;
-  at.tile = (int)(u0 - seg0);
+  at.run = (u0 - seg0) / at.s.tiles;
+  seg0 += at.run * at.s.tiles;
+  at.tile = u0 - seg0;
 
   // ---- the warp's ring
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S * kSlot);
   float* xo = reinterpret_cast<float*>(smem + kWarps * S * kSlot);  // [2][NT][DT][32][4]
   float* xm = xo + 2 * D * 8 * NT;                                  // [warps][2][8 * NT]
   Cursor ahead = at;  // of the unit that is loaded next
-  int id[2];
-  int slot[2];
-  const int row = g;  // a lane copies rows g and g + 8 of a tile, and masks the same ones
+  struct Rows {  // of the pool, that a lane copies: rows g and g + 8 of a tile, which it also masks
+    int id[2], slot[2], head;
+  };
   auto look_up = [&]() {
+    Rows r;
+    r.head = ahead.run / a.runs;
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
-      const int i = ahead.tile * kUnit + warp * 16 + row + r * 8;
-      id[r] = -1;
-      slot[r] = 0;
-      if (i < ahead.s.n) {
-        const int key = i < ahead.s.first ? i : i + ahead.s.shift;
+    for (int i = 0; i < 2; i++) {
+      const int j = ahead.tile * kUnit + warp * 16 + g + i * 8;
+      r.id[i] = -1;
+      r.slot[i] = 0;
+      if (j < ahead.s.n) {
+        const int key = j < ahead.s.first ? j : j + ahead.s.shift;
         const int pg = (int)(((uint64_t)(uint32_t)key * a.div_m) >> a.div_s);
-        slot[r] = key - pg * a.page;
-        id[r] = __ldg(a.table + ahead.b * a.st_b + pg);
+        r.slot[i] = key - pg * a.page;
+        r.id[i] = __ldg(a.table + ahead.b * a.st_b + pg);
       }
     }
+    return r;
   };
   uint32_t ok_bits = 0;  // two bits per slot of the ring
-  int64_t u_ahead = u0;
-  int put = 0;
-  auto load_next = [&]() {
+  auto copy_tile = [&](const Rows& r, int put) {
+    const uint32_t dst = ring + put * kSlot;
+    uint32_t ok2 = 0;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const bool ok = (uint32_t)r.id[i] < (uint32_t)a.num_pages;
+      ok2 |= ok ? 1u << i : 0u;
+      const int64_t pg = ok ? r.id[i] : 0;
+      const T* k = reinterpret_cast<const T*>(a.kc) + (ok ? pg * a.ck_p + r.slot[i] * a.ck_s + r.head * a.ck_h : 0);
+      const T* v = reinterpret_cast<const T*>(a.vc) + (ok ? pg * a.cv_p + r.slot[i] * a.cv_s + r.head * a.cv_h : 0);
+      const uint32_t line = dst + (g + i * 8) * (D * 2);
+#pragma unroll
+      for (int j = 0; j < D / 32; j++) copy16(line + (((j * 4 + t) ^ g) * 16), k + (j * 4 + t) * 8, ok);
+#pragma unroll
+      for (int j = 0; j < D / 32; j++) copy16(line + kTile + (((j * 4 + t) ^ g) * 16), v + (j * 4 + t) * 8, ok);
+    }
+    ok_bits = (ok_bits & ~(3u << (2 * put))) | ok2 << (2 * put);
+  };
+  // the first tiles: all their page numbers at once, then the copies
+  Rows rows[S - 1];
+  uint32_t u_ahead = u0;
+#pragma unroll
+  for (int i = 0; i < S - 1; i++)
     if (u_ahead < u1) {
-      const int h = ahead.run / a.runs;
-      const uint32_t dst = ring + put * kSlot;
-      uint32_t ok2 = 0;
+      rows[i] = look_up();
+      if (++u_ahead < u1) ahead.next(a, runs);
+    }
 #pragma unroll
-      for (int r = 0; r < 2; r++) {
-        const bool ok = (uint32_t)id[r] < (uint32_t)a.num_pages;
-        ok2 |= ok ? 1u << r : 0u;
-        const int64_t pg = ok ? id[r] : 0;
-        const T* k = reinterpret_cast<const T*>(a.kc) + (ok ? pg * a.ck_p + slot[r] * a.ck_s + h * a.ck_h : 0);
-        const T* v = reinterpret_cast<const T*>(a.vc) + (ok ? pg * a.cv_p + slot[r] * a.cv_s + h * a.cv_h : 0);
-        const uint32_t line = dst + (row + r * 8) * (D * 2);
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) {
-          const int c = i * 4 + t;
-          copy16(line + ((c ^ row) * 16), k + c * 8, ok);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) {
-          const int c = i * 4 + t;
-          copy16(line + kTile + ((c ^ row) * 16), v + c * 8, ok);
-        }
-      }
-      ok_bits = (ok_bits & ~(3u << (2 * put))) | ok2 << (2 * put);
+  for (int i = 0; i < S - 1; i++) {
+    if (u0 + i < u1) copy_tile(rows[i], i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int put = S - 1;
+  // after that one tile's page numbers are on their way while another is copied
+  Rows next = {};
+  if (u_ahead < u1) next = look_up();
+  auto copy_next = [&]() {
+    if (u_ahead < u1) {
+      copy_tile(next, put);
       if (++u_ahead < u1) {
         ahead.next(a, runs);
-        look_up();
+        next = look_up();
       }
       put = put + 1 == S ? 0 : put + 1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  look_up();
-#pragma unroll
-  for (int i = 0; i < S - 1; i++) load_next();
 
   uint32_t qf[NT][KS][2];
   float o[NT][DT][4], m[NT][2], l[NT][2];
@@ -257,21 +260,58 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     }
   };
   begin_segment();
+  // 16 elements from 16 * d on of the eight heads of run n: rows g and g + 8,
+  // columns 2t and 2t + 1 of the transposed result
+  auto put_out = [&](int b, int run, int n, int d, const float (&w)[4], const float (&wl)[2]) {
+    const float i0 = wl[0] > 0.f || wl[0] != wl[0] ? 1.f / wl[0] : 0.f, i1 = wl[1] > 0.f || wl[1] != wl[1] ? 1.f / wl[1] : 0.f;
+    const uint32_t r0 = turn8x8(pack2<T>(w[0] * i0, w[1] * i1)), r1 = turn8x8(pack2<T>(w[2] * i0, w[3] * i1));
+    const int c = (run % a.runs) * (8 * NT) + n * 8 + g;  // head g, elements 2t and 2t + 1
+    if (c >= a.share) return;
+    T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + ((int64_t)(run / a.runs) * a.share + c) * a.so_h + d * 16 + 2 * t;
+    if (a.o_even) {
+      *reinterpret_cast<uint32_t*>(out) = r0;
+      *reinterpret_cast<uint32_t*>(out + 8) = r1;
+    } else {
+      reinterpret_cast<uint16_t*>(out)[0] = (uint16_t)r0, reinterpret_cast<uint16_t*>(out)[1] = (uint16_t)(r0 >> 16);
+      reinterpret_cast<uint16_t*>(out)[8] = (uint16_t)r1, reinterpret_cast<uint16_t*>(out)[9] = (uint16_t)(r1 >> 16);
+    }
+  };
+  auto put_lse = [&](int b, int run, const float (&wm)[NT][2], const float (&wl)[NT][2]) {
+    if (!a.lse) return;
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
+        if (c < a.share)
+          a.lse[b * a.sl_b + (int64_t)(run / a.runs) * a.share + c] = (wm[n][x] + log2f(wl[n][x])) * kLn2;
+      }
+  };
+  // lane and run whose units are shared with other CTAs: at this one's start and end
+  struct Shared_out {
+    bool some = false;
+    int b, run;
+    uint32_t seg0, tiles;
+  } left0, left1;
   bool whole_start = at.tile == 0;
   bool from_u0 = true;  // the segment holds the range's first unit
 
   int get = 0;
-  for (int64_t u = u0; u < u1; u++) {
+  for (uint32_t u = u0; u < u1; u++) {
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
     __syncwarp();
-    load_next();
+    copy_next();
     const uint32_t kt = ring + get * kSlot, vt = kt + kTile;
     const bool ok0 = ok_bits >> (2 * get) & 1u, ok1 = ok_bits >> (2 * get + 1) & 1u;
     get = get + 1 == S ? 0 : get + 1;
 
-    float s[NT][4];
+    // several sums, so that the instructions do not wait for one another
+    constexpr int P = 4 / NT;
+    float s[NT][4], sp[P][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int i = 0; i < P; i++) sp[i][n][0] = sp[i][n][1] = sp[i][n][2] = sp[i][n][3] = 0.f;
     {
       const int r = (lane & 7) + (lane >> 3 & 1) * 8;
 #pragma unroll
@@ -279,12 +319,18 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
         uint32_t f[4];
         ldm4(f, kt + r * (D * 2) + (((2 * k + (lane >> 4)) ^ (r & 7)) * 16));
 #pragma unroll
-        for (int n = 0; n < NT; n++) mma16816<T>(s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
+        for (int n = 0; n < NT; n++) mma16816<T>(sp[k % P][n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
       }
     }
     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        s[n][i] = sp[0][n][i];
+#pragma unroll
+        for (int j = 1; j < P; j++) s[n][i] += sp[j][n][i];
+      }
       // heads 2t and 2t + 1 of keys g and g + 8
       s[n][0] = ok0 ? s[n][0] * a.scale2 : -INFINITY;
       s[n][1] = ok0 ? s[n][1] * a.scale2 : -INFINITY;
@@ -374,123 +420,67 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
           o[n][d][3] *= f[1];
         }
       }
+      // warps 2 and 3 hand theirs to 0 and 1, which then exchange halves of the elements
+      if (warp >= 2) {
 #pragma unroll
-      for (int half = 2; half >= 1; half /= 2) {
-        if (warp >= half && warp < 2 * half) {
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int d = 0; d < DT; d++)
-              reinterpret_cast<float4*>(xo)[(((warp - half) * NT + n) * DT + d) * 32 + lane] =
-                  make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
-        }
-        __syncthreads();
-        if (warp < half) {
-#pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int d = 0; d < DT; d++) {
-              const float4 v = reinterpret_cast<float4*>(xo)[((warp * NT + n) * DT + d) * 32 + lane];
-              o[n][d][0] += v.x;
-              o[n][d][1] += v.y;
-              o[n][d][2] += v.z;
-              o[n][d][3] += v.w;
-            }
-        }
-        __syncthreads();
+          for (int d = 0; d < DT; d++)
+            reinterpret_cast<float4*>(xo)[(((warp - 2) * NT + n) * DT + d) * 32 + lane] =
+                make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
       }
-      const bool whole = whole_start && ends;
-      const int h = at.run / a.runs, c0 = (at.run % a.runs) * (8 * NT);
-      bool write = whole;
-      if (!whole) {
-        // ---- this CTA's part goes to the workspace; the last one adds them up
-        if (warp == 0) {
-          float* part = a.parts + ((int64_t)blockIdx.x * 2 + (from_u0 ? 0 : 1)) * kPartFloats;
+      __syncthreads();
+      if (warp < 2) {
 #pragma unroll
-          for (int n = 0; n < NT; n++) {
-            if (g == 0) {
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int d = 0; d < DT; d++) {
+            float4* at_xo = reinterpret_cast<float4*>(xo) + ((warp * NT + n) * DT + d) * 32 + lane;
+            const float4 v = *at_xo;
+            o[n][d][0] += v.x;
+            o[n][d][1] += v.y;
+            o[n][d][2] += v.z;
+            o[n][d][3] += v.w;
+            if ((d < DT / 2) != (warp == 0)) *at_xo = make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
+          }
+      }
+      __syncthreads();
+      const bool whole = whole_start && ends;
+      if (warp < 2) {
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int e = 0; e < DT / 2; e++) {
+            const int d = e + warp * (DT / 2);  // this warp's half
+            const float4 v = reinterpret_cast<float4*>(xo)[(((1 - warp) * NT + n) * DT + d) * 32 + lane];
+            float w[4] = {warp ? o[n][e + DT / 2][0] : o[n][e][0], warp ? o[n][e + DT / 2][1] : o[n][e][1],
+                          warp ? o[n][e + DT / 2][2] : o[n][e][2], warp ? o[n][e + DT / 2][3] : o[n][e][3]};
+            w[0] += v.x, w[1] += v.y, w[2] += v.z, w[3] += v.w;
+            if (whole) {
+              put_out(at.b, at.run, n, d, w, l[n]);
+            } else {  // to the workspace; the last CTA adds up, below
+              float* part = a.parts + ((int64_t)blockIdx.x * 2 + (from_u0 ? 0 : 1)) * kPartFloats;
+              reinterpret_cast<float4*>(part + 2 * kColsMost)[(n * DT + d) * 32 + lane] = make_float4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        if (warp == 0 && g == 0) {
+          if (whole) {
+            put_lse(at.b, at.run, m, l);
+          } else {
+            float* part = a.parts + ((int64_t)blockIdx.x * 2 + (from_u0 ? 0 : 1)) * kPartFloats;
+#pragma unroll
+            for (int n = 0; n < NT; n++)
 #pragma unroll
               for (int c = 0; c < 2; c++) {
                 part[n * 8 + 2 * t + c] = m[n][c];
                 part[kColsMost + n * 8 + 2 * t + c] = l[n][c];
               }
-            }
-#pragma unroll
-            for (int d = 0; d < DT; d++)
-              reinterpret_cast<float4*>(part + 2 * kColsMost)[(n * DT + d) * 32 + lane] =
-                  make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
-          }
-          __threadfence();
-        }
-        __syncthreads();
-        // CTA c holds the units from units * c / G on: its number from a unit's
-        const int64_t seg1 = seg0 + at.s.tiles;
-        const int64_t c_first = ((seg0 + 1) * G - 1) / units, c_last = (seg1 * G - 1) / units;
-        if (tid == 0) {
-          const uint32_t n = (uint32_t)(c_last - c_first + 1);
-          const uint32_t before = atomicAdd(a.counters + c_first, 1u);
-          s_last = before + 1 == n;
-          if (s_last) {
-            a.counters[c_first] = 0;  // as the next call wants it
-            __threadfence();
-          }
-        }
-        __syncthreads();
-        write = s_last != 0;
-        if (write && warp == 0) {
-#pragma unroll
-          for (int n = 0; n < NT; n++) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-            for (int d = 0; d < DT; d++) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
-          }
-          for (int64_t c = c_first; c <= c_last; c++) {
-            const int which = c > c_first || units * c / G == seg0 ? 0 : 1;
-            const float* part = a.parts + (c * 2 + which) * kPartFloats;
-#pragma unroll
-            for (int n = 0; n < NT; n++) {
-              float keep[2], add[2];
-#pragma unroll
-              for (int x = 0; x < 2; x++) {
-                const float pm = __ldcg(part + n * 8 + 2 * t + x);
-                const float pl = __ldcg(part + kColsMost + n * 8 + 2 * t + x);
-                const float now = fmaxf(m[n][x], pm);
-                const float ref = now == -INFINITY ? 0.f : now;
-                keep[x] = exp2a(m[n][x] - ref);
-                add[x] = exp2a(pm - ref);
-                m[n][x] = now;
-                l[n][x] = l[n][x] * keep[x] + pl * add[x];
-              }
-#pragma unroll
-              for (int d = 0; d < DT; d++) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 2 * kColsMost) + (n * DT + d) * 32 + lane);
-                o[n][d][0] = o[n][d][0] * keep[0] + v.x * add[0];
-                o[n][d][1] = o[n][d][1] * keep[1] + v.y * add[1];
-                o[n][d][2] = o[n][d][2] * keep[0] + v.z * add[0];
-                o[n][d][3] = o[n][d][3] * keep[1] + v.w * add[1];
-              }
-            }
           }
         }
       }
-      if (write && warp == 0) {
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int x = 0; x < 2; x++) {
-            const int c = c0 + n * 8 + 2 * t + x;
-            if (c >= a.share) continue;
-            const float inv = l[n][x] > 0.f || l[n][x] != l[n][x] ? 1.f / l[n][x] : 0.f;
-            const int64_t head = (int64_t)h * a.share + c;
-            T* out = reinterpret_cast<T*>(a.o) + at.b * a.so_b + head * a.so_h;
-#pragma unroll
-            for (int d = 0; d < DT; d++) {
-              out[d * 16 + g] = from_f32<T>(o[n][d][x] * inv);
-              out[d * 16 + g + 8] = from_f32<T>(o[n][d][x + 2] * inv);
-            }
-            if (a.lse && g == 0) a.lse[at.b * a.sl_b + head] = (m[n][x] + log2f(l[n][x])) * kLn2;
-          }
+      if (!whole) {
+        Shared_out& w = from_u0 ? left0 : left1;
+        w.some = true, w.b = at.b, w.run = at.run, w.seg0 = seg0, w.tiles = at.s.tiles;
       }
       if (u + 1 < u1) {
         seg0 += at.s.tiles;
@@ -503,7 +493,72 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
       at.tile++;
     }
   }
+
+  // ---- heads that are shared with other CTAs: the last one of them adds up, in CTA order
+  if (!left0.some && !left1.some) return;
+  if (warp < 2) __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const Shared_out& w = tid ? left1 : left0;
+    s_last[tid] = 0;
+    if (w.some) {
+      const uint32_t c0 = cta_of(w.seg0), c1 = cta_of(w.seg0 + w.tiles - 1);
+      const bool is_last = atomicAdd(a.counters + c0, 1u) == c1 - c0;
+      if (is_last) {
+        a.counters[c0] = 0;  // as the next call wants it
+        __threadfence();
+      }
+      s_last[tid] = is_last;
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; i++) {
+    if (!s_last[i]) continue;
+    const Shared_out w = i ? left1 : left0;
+    const uint32_t c0 = cta_of(w.seg0), c1 = cta_of(w.seg0 + w.tiles - 1);
+    constexpr int E = DT / kWarps;  // 16-element tiles of a warp
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f}, oo[E][4];
+#pragma unroll
+      for (int e = 0; e < E; e++) oo[e][0] = oo[e][1] = oo[e][2] = oo[e][3] = 0.f;
+#pragma unroll 2
+      for (uint32_t c = c0; c <= c1; c++) {
+        const int which = c > c0 || first_of(c) == w.seg0 ? 0 : 1;
+        const float* part = a.parts + ((int64_t)c * 2 + which) * kPartFloats;
+        const float2 pm = __ldcg(reinterpret_cast<const float2*>(part + n * 8) + t);
+        const float2 pl = __ldcg(reinterpret_cast<const float2*>(part + kColsMost + n * 8) + t);
+        float4 v[E];
+#pragma unroll
+        for (int e = 0; e < E; e++)
+          v[e] = __ldcg(reinterpret_cast<const float4*>(part + 2 * kColsMost) + (n * DT + warp * E + e) * 32 + lane);
+        float keep[2], add[2];
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const float one_m = x ? pm.y : pm.x, one_l = x ? pl.y : pl.x;
+          const float now = fmaxf(mm[x], one_m), ref = now == -INFINITY ? 0.f : now;
+          keep[x] = exp2a(mm[x] - ref);
+          add[x] = exp2a(one_m - ref);
+          mm[x] = now;
+          ll[x] = ll[x] * keep[x] + one_l * add[x];
+        }
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          oo[e][0] = oo[e][0] * keep[0] + v[e].x * add[0];
+          oo[e][1] = oo[e][1] * keep[1] + v[e].y * add[1];
+          oo[e][2] = oo[e][2] * keep[0] + v[e].z * add[0];
+          oo[e][3] = oo[e][3] * keep[1] + v[e].w * add[1];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; e++) put_out(w.b, w.run, n, warp * E + e, oo[e], ll);
+      m[n][0] = mm[0], m[n][1] = mm[1], l[n][0] = ll[0], l[n][1] = ll[1];
+    }
+    if (warp == 0 && g == 0) put_lse(w.b, w.run, m, l);
+  }
 }
+
 
 template <typename T, int D, int NT>
 cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
@@ -592,7 +647,7 @@ extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
   a.o = r->o, a.lse = r->lse;
   a.counters = reinterpret_cast<uint32_t*>(r->workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(r->workspace) + kCounterBytes);
-  a.so_b = r->o_stride[0], a.so_h = r->o_stride[1], a.sl_b = r->lse_stride;
+  a.so_b = stride(r->o_stride[0], r->lanes), a.so_h = stride(r->o_stride[1], r->q_heads), a.sl_b = r->lse_stride;
   a.st_b = stride(r->table_stride, r->lanes);
   a.lanes = r->lanes, a.hkv = r->kv_heads, a.share = r->q_heads / r->kv_heads, a.runs = 1;
   a.width = r->table_width, a.page = r->page_size, a.num_pages = r->num_pages;
@@ -603,9 +658,12 @@ extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
   a.div_m = (uint32_t)((((uint64_t)1 << (31 + l)) + r->page_size - 1) / r->page_size);
   a.div_s = 31 + l;
   a.scale2 = r->scale * kLog2e;
+  a.o_even = aligned(r->o, 4) && a.so_b % 2 == 0 && a.so_h % 2 == 0;
   int64_t most = (int64_t)r->table_width * r->page_size;
   if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
   const int64_t tiles = (int64_t)a.lanes * (most / kUnit + 1);
+  if (tiles * ((int64_t)a.hkv * ((a.share + 7) / 8)) > UINT32_MAX)
+    return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: lanes * kv_heads * tokens is too large");
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = r->dtype == WFST_F16 ? by_width<__half>(a, r->head_dim, tiles, st)
                                              : by_width<__nv_bfloat16>(a, r->head_dim, tiles, st);
