@@ -17,10 +17,10 @@
 // other's operand through a transposing move, as its 16-bit rounding plus the
 // rounding's rest: its error stays that of fp32.
 //
-// Work is split evenly whatever the lengths: a unit is 64 keys of one lane and
-// head run, units are numbered through, and each CTA takes an equal range.  A
-// CTA's warps each take 16 keys of a unit and copy them asynchronously into
-// their own ring in shared memory, so they meet only where a lane's head ends.
+// Work is split evenly whatever the lengths: a unit is 16 keys for each of a
+// CTA's warps, of one lane and head run; units are numbered through, and each CTA
+// takes an equal range.  A warp copies its keys and values asynchronously into a
+// ring of its own in shared memory, so warps meet only where a lane's head ends.
 // Where a head's units are shared among CTAs, each leaves its unscaled part in
 // the workspace and the last one to arrive adds them up, in CTA order.
 #include "wfst_ops.h"
@@ -28,8 +28,7 @@
 namespace wfst {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kUnit = 16 * kWarps;  // keys of a unit
+constexpr int kLeastUnit = 64;      // keys of a unit, at least
 constexpr int kMaxGrid = 1024;      // CTAs the workspace has room for
 constexpr int kColsMost = 16;       // query heads of a CTA's run at most
 constexpr int kWidthMost = 256;
@@ -62,6 +61,7 @@ struct Seen {
   int n, first, shift, tiles;
 };
 
+template <int UNIT>
 __device__ __forceinline__ Seen seen(const Args& a, int b) {
   Seen s;
   const int64_t room = (int64_t)a.width * a.page;
@@ -70,11 +70,12 @@ __device__ __forceinline__ Seen seen(const Args& a, int b) {
   s.first = min(a.sinks, start);
   s.shift = start - s.first;
   s.n = len - s.shift;
-  s.tiles = max(1, (s.n + kUnit - 1) / kUnit);
+  s.tiles = max(1, (s.n + UNIT - 1) / UNIT);
   return s;
 }
 
 // Where a unit lies: lane, run of query heads, tile of the lane's keys.
+template <int UNIT>
 struct Cursor {
   Seen s;
   int b, run, tile;
@@ -83,7 +84,7 @@ struct Cursor {
     tile = 0;
     if (++run < runs) return;
     run = 0;
-    if (++b < a.lanes) s = seen(a, b);
+    if (++b < a.lanes) s = seen<UNIT>(a, b);
   }
 };
 
@@ -114,16 +115,21 @@ __device__ __forceinline__ float exp2a(float v) {
   return r;
 }
 
+// Warps of a CTA, and 16-row tiles in a warp's ring, of which keys and values
+// take one each: what 227 KB hold for heads of 256, and what lets two CTAs (three
+// for heads of 64) share a multiprocessor otherwise.
 template <int D>
-constexpr int kStages = D == 64 ? 6 : 3;
+constexpr int kWarps = D == 256 ? 8 : 4;
+template <int D>
+constexpr int kRing = D == 64 ? 8 : D == 128 ? 5 : 3;
 // rings, two warps' results at a segment's end, m and l of the warps
 template <int D, int NT>
-constexpr int kSmem = kWarps * kStages<D> * 2 * 16 * D * 2 + 2 * D * 8 * NT * 4 + kWarps * 2 * 8 * NT * 4;
+constexpr int kSmem = kWarps<D> * kRing<D> * 16 * D * 2 + 2 * D * 8 * NT * 4 + kWarps<D> * 2 * 8 * NT * 4;
 
 // D: elements of a head; NT: runs of 8 * NT query heads.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
-  constexpr int S = kStages<D>, kTile = 16 * D * 2, kSlot = 2 * kTile, KS = D / 16, DT = D / 16;
+__global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
+  constexpr int W = kWarps<D>, UNIT = 16 * W, S = kRing<D>, kTile = 16 * D * 2, KS = D / 16, DT = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_last[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
   // ---- this CTA's units: all lanes' tiles, numbered through (each warp for itself)
   uint32_t units = 0;
 #pragma unroll 4
-  for (int b = lane; b < a.lanes; b += 32) units += seen(a, b).tiles;
+  for (int b = lane; b < a.lanes; b += 32) units += seen<UNIT>(a, b).tiles;
   units = __reduce_add_sync(0xffffffffu, units) * runs;
   // CTAs that share the units; each of them has one at least
   const uint32_t G = min(gridDim.x, units), each = units / G, more = units - each * G;
@@ -143,10 +149,10 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     return u < at ? u / (each + 1) : more + (u - at) / each;
   };
   const uint32_t u0 = first_of(blockIdx.x), u1 = first_of(blockIdx.x + 1);
-  Cursor at;  // of the unit that is computed
+  Cursor<UNIT> at;  // of the unit that is computed
   uint32_t seg0 = 0;  // first unit of the current lane and run
   for (int b0 = 0;; b0 += 32) {
-    const uint32_t mine = b0 + lane < a.lanes ? seen(a, b0 + lane).tiles * runs : 0;
+    const uint32_t mine = b0 + lane < a.lanes ? seen<UNIT>(a, b0 + lane).tiles * runs : 0;
     uint32_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -161,16 +167,16 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     }
     seg0 += __shfl_sync(0xffffffffu, incl, 31);
   }
-  at.s = seen(a, at.b);
+  at.s = seen<UNIT>(a, at.b);
   at.run = (u0 - seg0) / at.s.tiles;
   seg0 += at.run * at.s.tiles;
   at.tile = u0 - seg0;
 
   // ---- the warp's ring
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S * kSlot);
-  float* xo = reinterpret_cast<float*>(smem + kWarps * S * kSlot);  // [2][NT][DT][32][4]
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S * kTile);
+  float* xo = reinterpret_cast<float*>(smem + W * S * kTile);  // [2][NT][DT][32][4]
   float* xm = xo + 2 * D * 8 * NT;                                  // [warps][2][8 * NT]
-  Cursor ahead = at;  // of the unit that is loaded next
+  Cursor<UNIT> ahead = at;  // of the unit that is looked up last
   struct Rows {  // of the pool, that a lane copies: rows g and g + 8 of a tile, which it also masks
     int id[2], slot[2], head;
   };
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     r.head = ahead.run / a.runs;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const int j = ahead.tile * kUnit + warp * 16 + g + i * 8;
+      const int j = ahead.tile * UNIT + warp * 16 + g + i * 8;
       r.id[i] = -1;
       r.slot[i] = 0;
       if (j < ahead.s.n) {
@@ -191,57 +197,79 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     }
     return r;
   };
-  uint32_t ok_bits = 0;  // two bits per slot of the ring
-  auto copy_tile = [&](const Rows& r, int put) {
-    const uint32_t dst = ring + put * kSlot;
-    uint32_t ok2 = 0;
+  uint32_t ok_bits = 0;  // two bits per unit in flight
+  int put = 0;
+  auto copy_tile = [&](const Rows& r, const void* pool, int64_t s_p, int64_t s_s, int64_t s_h) {
+    const uint32_t dst = ring + put * kTile + g * (D * 2);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       const bool ok = (uint32_t)r.id[i] < (uint32_t)a.num_pages;
-      ok2 |= ok ? 1u << i : 0u;
-      const int64_t pg = ok ? r.id[i] : 0;
-      const T* k = reinterpret_cast<const T*>(a.kc) + (ok ? pg * a.ck_p + r.slot[i] * a.ck_s + r.head * a.ck_h : 0);
-      const T* v = reinterpret_cast<const T*>(a.vc) + (ok ? pg * a.cv_p + r.slot[i] * a.cv_s + r.head * a.cv_h : 0);
-      const uint32_t line = dst + (g + i * 8) * (D * 2);
+      const T* from = reinterpret_cast<const T*>(pool) + (ok ? r.id[i] * s_p + r.slot[i] * s_s + r.head * s_h : 0);
 #pragma unroll
-      for (int j = 0; j < D / 32; j++) copy16(line + (((j * 4 + t) ^ g) * 16), k + (j * 4 + t) * 8, ok);
-#pragma unroll
-      for (int j = 0; j < D / 32; j++) copy16(line + kTile + (((j * 4 + t) ^ g) * 16), v + (j * 4 + t) * 8, ok);
+      for (int j = 0; j < D / 32; j++) copy16(dst + i * (16 * D) + (((j * 4 + t) ^ g) * 16), from + (j * 4 + t) * 8, ok);
     }
-    ok_bits = (ok_bits & ~(3u << (2 * put))) | ok2 << (2 * put);
+    put = put + 1 == S ? 0 : put + 1;
   };
-  // the first tiles: all their page numbers at once, then the copies
-  Rows rows[S - 1];
-  uint32_t u_ahead = u0;
+  auto copy_keys = [&](const Rows& r, uint32_t u) {
+    copy_tile(r, a.kc, a.ck_p, a.ck_s, a.ck_h);
+    const uint32_t ok2 = ((uint32_t)r.id[0] < (uint32_t)a.num_pages ? 1u : 0u) | ((uint32_t)r.id[1] < (uint32_t)a.num_pages ? 2u : 0u);
+    ok_bits = (ok_bits & ~(3u << (2 * (u & 7)))) | ok2 << (2 * (u & 7));
+  };
+  auto copy_values = [&](const Rows& r) { copy_tile(r, a.vc, a.cv_p, a.cv_s, a.cv_h); };
+  // the first S - 1 tiles: all their page numbers at once, then the copies
+  constexpr int F = S / 2;  // units they belong to
+  Rows rows[F + 1] = {};
 #pragma unroll
-  for (int i = 0; i < S - 1; i++)
-    if (u_ahead < u1) {
+  for (int i = 0; i <= F; i++)
+    if (u0 + i < u1) {
+      if (i) ahead.next(a, runs);
       rows[i] = look_up();
-      if (++u_ahead < u1) ahead.next(a, runs);
     }
 #pragma unroll
   for (int i = 0; i < S - 1; i++) {
-    if (u0 + i < u1) copy_tile(rows[i], i);
+    if (u0 + i / 2 < u1) {
+      if (i % 2)
+        copy_values(rows[i / 2]);
+      else
+        copy_keys(rows[i / 2], i / 2);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  int put = S - 1;
-  // after that one tile's page numbers are on their way while another is copied
-  Rows next = {};
-  if (u_ahead < u1) next = look_up();
-  auto copy_next = [&]() {
+  // after that tile by tile, while the next unit's page numbers are on their way
+  Rows now = rows[S % 2 ? F : F - 1], next = rows[F];
+  uint32_t u_ahead = u0 + (S % 2 ? F : F - 1);
+  auto copy_next = [&](bool values) {
     if (u_ahead < u1) {
-      copy_tile(next, put);
-      if (++u_ahead < u1) {
-        ahead.next(a, runs);
-        next = look_up();
+      if (values) {
+        copy_values(now);
+        now = next;
+        u_ahead++;
+      } else {
+        copy_keys(now, u_ahead - u0);
+        if (u_ahead + 1 < u1) {
+          ahead.next(a, runs);
+          next = look_up();
+        }
       }
-      put = put + 1 == S ? 0 : put + 1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   uint32_t qf[NT][KS][2];
   float o[NT][DT][4], m[NT][2], l[NT][2];
+  // the next segment's queries, on their way to L1 while this one's keys are read
+  auto fetch_queries = [&]() {
+    int b = at.b, run = at.run + 1;
+    if (run == runs) run = 0, b++;
+    if (b >= a.lanes) return;
+    const int h = run / a.runs, c0 = (run % a.runs) * (8 * NT);
+    for (int i = lane; i < 8 * NT * (D / 64); i += 32) {
+      const int c = c0 + i / (D / 64);
+      if (c >= a.share) continue;
+      const T* q = reinterpret_cast<const T*>(a.q) + b * a.sq_b + (int64_t)(h * a.share + c) * a.sq_h + i % (D / 64) * 64;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+    }
+  };
   auto begin_segment = [&]() {
     const int h = at.run / a.runs, c0 = (at.run % a.runs) * (8 * NT);
 #pragma unroll
@@ -258,6 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
 #pragma unroll
       for (int d = 0; d < DT; d++) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
     }
+    if (warp == 0) fetch_queries();
   };
   begin_segment();
   // 16 elements from 16 * d on of the eight heads of run n: rows g and g + 8,
@@ -300,10 +329,10 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
   for (uint32_t u = u0; u < u1; u++) {
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
     __syncwarp();
-    copy_next();
-    const uint32_t kt = ring + get * kSlot, vt = kt + kTile;
-    const bool ok0 = ok_bits >> (2 * get) & 1u, ok1 = ok_bits >> (2 * get + 1) & 1u;
+    copy_next(S % 2 == 0);
+    const uint32_t kt = ring + get * kTile;
     get = get + 1 == S ? 0 : get + 1;
+    const bool ok0 = ok_bits >> (2 * ((u - u0) & 7)) & 1u, ok1 = ok_bits >> (2 * ((u - u0) & 7) + 1) & 1u;
 
     // several sums, so that the instructions do not wait for one another
     constexpr int P = 4 / NT;
@@ -366,6 +395,11 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
         o[n][d][3] *= keep[1];
       }
     }
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    __syncwarp();
+    copy_next(S % 2 == 1);
+    const uint32_t vt = ring + get * kTile;
+    get = get + 1 == S ? 0 : get + 1;
     {
       const int key = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
@@ -403,10 +437,10 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
           const int col = n * 8 + 2 * t + c;
           float top = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; w++) top = fmaxf(top, xm[(w * 2) * (8 * NT) + col]);
+          for (int w = 0; w < W; w++) top = fmaxf(top, xm[(w * 2) * (8 * NT) + col]);
           const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-          for (int w = 0; w < kWarps; w++)
+          for (int w = 0; w < W; w++)
             sum += xm[(w * 2 + 1) * (8 * NT) + col] * exp2a(xm[(w * 2) * (8 * NT) + col] - ref);
           f[c] = exp2a(m[n][c] - ref);
           m[n][c] = top;
@@ -420,31 +454,37 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
           o[n][d][3] *= f[1];
         }
       }
-      // warps 2 and 3 hand theirs to 0 and 1, which then exchange halves of the elements
-      if (warp >= 2) {
+      // the others hand theirs to warps 0 and 1, two at a time, which then exchange
+      // halves of the elements
+#pragma unroll 1
+      for (int from = 2; from < W; from += 2) {
+        if (warp == from || warp == from + 1) {
 #pragma unroll
-        for (int n = 0; n < NT; n++)
+          for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int d = 0; d < DT; d++)
-            reinterpret_cast<float4*>(xo)[(((warp - 2) * NT + n) * DT + d) * 32 + lane] =
-                make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
+            for (int d = 0; d < DT; d++)
+              reinterpret_cast<float4*>(xo)[(((warp - from) * NT + n) * DT + d) * 32 + lane] =
+                  make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
+        }
+        __syncthreads();
+        if (warp < 2) {
+          const bool last = from + 2 == W;
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int d = 0; d < DT; d++) {
+              float4* at_xo = reinterpret_cast<float4*>(xo) + ((warp * NT + n) * DT + d) * 32 + lane;
+              const float4 v = *at_xo;
+              o[n][d][0] += v.x;
+              o[n][d][1] += v.y;
+              o[n][d][2] += v.z;
+              o[n][d][3] += v.w;
+              if (last && (d < DT / 2) != (warp == 0))
+                *at_xo = make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
+            }
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      if (warp < 2) {
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int d = 0; d < DT; d++) {
-            float4* at_xo = reinterpret_cast<float4*>(xo) + ((warp * NT + n) * DT + d) * 32 + lane;
-            const float4 v = *at_xo;
-            o[n][d][0] += v.x;
-            o[n][d][1] += v.y;
-            o[n][d][2] += v.z;
-            o[n][d][3] += v.w;
-            if ((d < DT / 2) != (warp == 0)) *at_xo = make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
-          }
-      }
-      __syncthreads();
       const bool whole = whole_start && ends;
       if (warp < 2) {
 #pragma unroll
@@ -517,7 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Args a) {
     if (!s_last[i]) continue;
     const Shared_out w = i ? left1 : left0;
     const uint32_t c0 = cta_of(w.seg0), c1 = cta_of(w.seg0 + w.tiles - 1);
-    constexpr int E = DT / kWarps;  // 16-element tiles of a warp
+    constexpr int E = DT / W;  // 16-element tiles of a warp
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f}, oo[E][4];
@@ -570,7 +610,7 @@ cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int v = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps * 32, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps<D> * 32, smem);
     if (e != cudaSuccess) return e;
     resident = v > 0 ? v : 1;
     once.set(dev);
@@ -578,7 +618,7 @@ cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
   int64_t grid = (int64_t)resident * ops_sm_count();
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (grid > most_units) grid = most_units;
-  fn<<<(int)grid, kWarps * 32, smem, st>>>(a);
+  fn<<<(int)grid, kWarps<D> * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -661,7 +701,7 @@ extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
   a.o_even = aligned(r->o, 4) && a.so_b % 2 == 0 && a.so_h % 2 == 0;
   int64_t most = (int64_t)r->table_width * r->page_size;
   if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
-  const int64_t tiles = (int64_t)a.lanes * (most / kUnit + 1);
+  const int64_t tiles = (int64_t)a.lanes * (most / kLeastUnit + 1);
   if (tiles * ((int64_t)a.hkv * ((a.share + 7) / 8)) > UINT32_MAX)
     return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: lanes * kv_heads * tokens is too large");
   cudaStream_t st = (cudaStream_t)stream;
