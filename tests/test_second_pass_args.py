@@ -17,11 +17,11 @@ def lib():
 
 
 def test_sizes_of_a_packed_matrix(lib):
-    # 16 outputs by 64 k are 512 bytes of codes; a group's scales of a tile 32 bytes, with zero points 64
-    assert W.wfst_quant_size(16, 64, 64, 0) == 512 + 32
-    assert W.wfst_quant_size(17, 64, 64, 1) == 2 * (512 + 64)
-    assert W.wfst_quant_size(1, 32, 32, 0) == 512 + 2 * 32          # half a block is stored as a whole one
-    assert W.wfst_quant_size(100000, 65536, 128, 0) == 6250 * (1024 * 512 + 512 * 32)   # past 2^31 bytes
+    # 128 outputs by 64 k are 4096 bytes of codes; a group's scales of a tile 256 bytes, with zero points 512
+    assert W.wfst_quant_size(128, 64, 64, 0) == 4096 + 256
+    assert W.wfst_quant_size(129, 64, 64, 1) == 2 * (4096 + 512)
+    assert W.wfst_quant_size(1, 32, 32, 0) == 4096 + 2 * 256         # half a block is stored as a whole one
+    assert W.wfst_quant_size(100000, 65536, 128, 0) == 782 * (1024 * 4096 + 512 * 256)   # past 2^31 bytes
     for n, k, group in ((0, 64, 64), (16, 0, 64), (16, 64, 16), (16, 96, 64), (16, 64, 0), (-1, 64, 64)):
         with pytest.raises(W.WfstError) as e:
             W.wfst_quant_size(n, k, group, 0)

@@ -6,74 +6,40 @@
 // A pass has to read the codes (N*K/2 bytes) and the scales; x and y are small
 // beside them, so HBM bounds it up to some tens of rows.
 //
-// Matrix instructions do the products (m16n8k16: 16 outputs x 8 rows of x),
-// also for one row: products on the general lanes would not keep up with HBM.
-// What it costs to bring codes into the instructions' types is the next bound,
-// so a code is not converted but put in place: as the upper four bits of a
-// mantissa it makes the 16-bit number 1 + c / 16, one shift and one logical
-// operation for two codes, and less 1.5 it is (c - 8) / 16, exactly.  A group's
-// fp32 sum is scaled once, so nothing is rounded before y.  With zero points the
-// group adds s * (8 - z) * sum x, the sum of x coming from the same instruction
-// with ones in place of the codes, once for all outputs of a warp.
+// The products run on the tensor cores with the weights as the M side: a CTA
+// takes 128 outputs, its threads one each.  A thread brings its output's codes
+// into the operand type and stores them to tensor memory as row of A; x is B,
+// from shared memory; the sums of a group are read back, scaled and added up in
+// registers in fp32, so nothing is rounded before y.  Two things are then in
+// flight at a time: the products of one stage and the codes of the next ones.
+//   - What it costs to bring codes into the type is the next bound after HBM, so
+//     a code is not converted but put in place: as the upper four bits of a
+//     mantissa it makes the 16-bit number 1 + c / 16, one shift and one logical
+//     operation for two codes, and less 1 + z / 16 it is (c - z) / 16, exactly
+//     for whole z.  What z has beside its whole part is added as s * rest * sum x.
+//   - mma.sync instructions for the same work, fed from registers, came to half
+//     of HBM's rate at 8 rows and a fifth at 64 (8 x 131072 x 4096: 80 us).
 //
-// Layout ("packed", made once by wfst_quant_pack): tiles of 16 outputs, in
-// them blocks of 64 k, in them 16 bytes per lane, so that a warp's load is 512
-// consecutive bytes.  Inside a block, k is permuted so that a lane's x
-// elements are two runs of 8 consecutive ones: lane (g, t) = (lane / 4, lane %
-// 4) holds k = 64*blk + 32*(s/2) + 8*t + 4*(s%2) + {0..3} of outputs g and
-// g + 8 in word s, and uses them in step s as the instruction's columns 2t,
-// 2t+1, 2t+8, 2t+9.  The same permutation on both operands leaves the sum
-// unchanged, and steps 0-1 and 2-3 are the block's two halves, as groups of 32
-// want it.
+// Layout ("packed", made once by wfst_quant_pack): tiles of 128 outputs, in them
+// blocks of 64 k, in them two halves of 32 k with 16 bytes per output, so that a
+// warp copies 512 consecutive bytes.  Word q of an output's block holds k = 8 q
+// .. 8 q + 7 as four pairs.
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "wfst_ops.h"
 
+namespace cg = cooperative_groups;
+
 namespace wfst {
 namespace {
 
-constexpr int kWarps = 8;
-
-// Pair j of a word (0: output g, k 0/1; 1: output g+8, k 0/1; 2: output g, k
-// 2/3; 3: output g+8, k 2/3) lies where a rotation by 4 j to the right brings
-// its two codes to the upper mantissa bits of the word's two halves: bits 3-6
-// and 19-22 for bf16, bits 6-9 and 22-25 for fp16.
-template <int AT>
-__global__ void pack_codes(const uint8_t* __restrict__ codes, int64_t n, int64_t k, int64_t blocks, int64_t words,
-                           uint32_t* __restrict__ out) {
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step) {
-    const int s = (int)(i & 3), lane = (int)(i >> 2 & 31);
-    const int64_t blk = (i >> 7) % blocks, tile = (i >> 7) / blocks;
-    const int64_t k0 = blk * 64 + (s >> 1) * 32 + (lane & 3) * 8 + (s & 1) * 4;
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int64_t row = tile * 16 + (lane >> 2) + (j & 1) * 8, kk = k0 + (j >> 1) * 2;
-      uint32_t byte = 0;  // past the matrix's edge x or the scale is zero
-      if (row < n && kk < k) byte = codes[row * (k / 2) + kk / 2];
-      const uint32_t pair = (byte & 15u) << AT | (byte >> 4) << (AT + 16);
-      w |= __funnelshift_l(pair, pair, 4 * j);
-    }
-    out[i] = w;
-  }
-}
-
-// Scales of a tile and group: for g = 0..7 {s[g], s[g+8]} and, with zero
-// points, {z[g], z[g+8]} behind them; zero scales past the edge.
-__global__ void pack_scales(const uint16_t* __restrict__ scales, const uint16_t* __restrict__ zeros, int64_t n,
-                            int64_t groups, int64_t groups_p, int64_t count, uint16_t* __restrict__ out) {
-  const int per = zeros ? 4 : 2;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += step) {
-    const int j = (int)(i % per), g = (int)(i / per % 8);
-    const int64_t grp = i / (per * 8) % groups_p, tile = i / (per * 8) / groups_p;
-    const int64_t row = tile * 16 + g + (j & 1) * 8;
-    uint16_t v = 0;
-    if (row < n && grp < groups) v = (j < 2 ? scales : zeros)[row * groups + grp];
-    out[i] = v;
-  }
-}
+constexpr int kM = 128;       // outputs of a tile, threads of a CTA
+constexpr int kBlock = 64;    // k of a stage
+constexpr int kCodes = kM * kBlock / 2;  // bytes of a stage's codes
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kSpins = 1u << 22;    // waits give up after that
 
 // Where a code lies in a 16-bit number, and the bits of 1 around it.
 template <typename T>
@@ -81,28 +47,46 @@ constexpr int kCodeAt = std::is_same_v<T, __half> ? 6 : 3;
 template <typename T>
 constexpr uint32_t kOnes = std::is_same_v<T, __half> ? 0x3c003c00u : 0x3f803f80u;
 
-// Pair j of a word: its two codes as (c - 8) / 16.
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t w, int j) {
-  using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
-  const uint32_t v = ((j ? __funnelshift_r(w, w, 4 * j) : w) & (0x000f000fu << kCodeAt<T>)) | kOnes<T>;
-  const uint32_t off = std::is_same_v<T, __half> ? 0x3e003e00u : 0x3fc03fc0u;  // 1.5
-  const T2 r = __hsub2(*reinterpret_cast<const T2*>(&v), *reinterpret_cast<const T2*>(&off));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Pair j of a word (k = 2 j and 2 j + 1 of the word's eight) lies where a
+// rotation by 4 j to the right brings its two codes to the upper mantissa bits
+// of the word's two halves: bits 3-6 and 19-22 for bf16, 6-9 and 22-25 for fp16.
+template <int AT>
+__global__ void pack_codes(const uint8_t* __restrict__ codes, int64_t n, int64_t k, int64_t blocks, int64_t words,
+                           uint32_t* __restrict__ out) {
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step) {
+    const int q = (int)(i & 3) + (int)(i >> 9 & 1) * 4;  // words 0-3 in the first half, 4-7 in the second
+    const int64_t blk = (i >> 10) % blocks, tile = (i >> 10) / blocks;
+    const int64_t row = tile * kM + (i >> 2 & (kM - 1)), k0 = blk * kBlock + q * 8;
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint32_t byte = 0;  // past the matrix's edge x or the scale is zero
+      if (row < n && k0 + 2 * j < k) byte = codes[row * (k / 2) + k0 / 2 + j];
+      const uint32_t pair = (byte & 15u) << AT | (byte >> 4) << (AT + 16);
+      w |= __funnelshift_l(pair, pair, 4 * j);
+    }
+    out[i] = w;
+  }
 }
 
-__device__ __forceinline__ uint32_t first_of(uint32_t v) { return v; }
-__device__ __forceinline__ uint32_t first_of(uint2 v) { return v.x; }
-__device__ __forceinline__ uint32_t second_of(uint32_t) { return 0; }
-__device__ __forceinline__ uint32_t second_of(uint2 v) { return v.y; }
-
-// CTAs of a multiprocessor that the registers are held down for
-template <int NT>
-constexpr int kResident = NT <= 1 ? 4 : NT == 2 ? 3 : NT == 4 ? 2 : 1;
+// Scales of a tile and group: one per output, with zero points {s, z}; zero
+// scales past the edge.
+__global__ void pack_scales(const uint16_t* __restrict__ scales, const uint16_t* __restrict__ zeros, int64_t n,
+                            int64_t groups, int64_t groups_p, int64_t count, uint16_t* __restrict__ out) {
+  const int per = zeros ? 2 : 1;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += step) {
+    const int64_t row_in = i / per % kM, grp = i / (per * kM) % groups_p, row = i / (per * kM) / groups_p * kM + row_in;
+    uint16_t v = 0;
+    if (row < n && grp < groups) v = (i % per ? zeros : scales)[row * groups + grp];
+    out[i] = v;
+  }
+}
 
 struct Args {
-  const uint4* codes;
-  const void* scales;
+  const unsigned char* codes;
+  const unsigned char* scales;
   const void* x;
   const void* bias;
   void* y;
@@ -110,215 +94,327 @@ struct Args {
   int32_t n, k, rows, tiles, blocks, groups_p, group_log;
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// ---- instructions
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;  // 0: sixteen zero bytes
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kSpins; i++) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+// 32 columns of this warp's 32 lanes from registers
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+
+// Pair j of a word as (c - z) / 16 of its two codes; one: 1 + z / 16, twice.
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, int j, uint32_t one) {
+  using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+  const uint32_t v = ((j ? __funnelshift_r(w, w, 4 * j) : w) & (0x000f000fu << kCodeAt<T>)) | kOnes<T>;
+  const T2 r = __hsub2(*reinterpret_cast<const T2*>(&v), *reinterpret_cast<const T2*>(&one));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---- sizes that go with N rows of x (16, 32 or 64) and groups of 32 (SUB)
+
+// tensor memory: two stages of A, and two sums of 16, 32 or 64 columns (four with SUB)
+template <int N, bool SUB>
+constexpr int kColumns = 64 + (SUB ? 4 : 2) * N <= 128 ? 128 : 64 + (SUB ? 4 : 2) * N <= 256 ? 256 : 512;
 template <int N>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
+constexpr int kStages = N == 64 ? 7 : 6;
+template <int N, bool SUB, bool ZERO>
+constexpr int kStage = N * 128 + kCodes + (SUB ? 2 : 1) * kM * (ZERO ? 4 : 2);
+// CTAs of a multiprocessor: what its 512 columns hold, and no more, since one
+// that waits for columns would hold up its cluster; shared memory sees to it
+template <int N, bool SUB>
+constexpr int kResident = 512 / kColumns<N, SUB>;
+template <int N, bool SUB, bool ZERO>
+constexpr int kSmem = 1024 + (kStages<N> * ((kStage<N, SUB, ZERO> + 1023) / 1024 * 1024) > 233472 / (kResident<N, SUB> + 1)
+                                  ? kStages<N> * ((kStage<N, SUB, ZERO> + 1023) / 1024 * 1024)
+                                  : 233472 / (kResident<N, SUB> + 1));
 
-// bytes of one stage of a warp's ring: the codes and scales of a block, of MT tiles
-template <int MT, bool SUB, bool ZERO>
-constexpr int kStage = MT * (512 + (SUB ? 2 : 1) * (ZERO ? 64 : 32));
-
-// A CTA takes MT tiles of 16 outputs by NT*8 rows at a time, and then the next
-// ones gridDim.x further on.  Its warps share the blocks of k among them (warp w
-// takes blocks w, w + kWarps, ...) and add up at the end, in warp order.  A warp
-// copies S blocks ahead, across the tiles' borders too, into a ring of its own
-// in shared memory; a lane reads back what it copied itself, but for the scales.
-// SUB: groups of 32, two to a block; otherwise a group is whole blocks.
-template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
-__global__ void __launch_bounds__(kWarps * 32, kResident<NT>) matvec_kernel(const Args a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kParts = SUB ? 2 : 1;      // scale groups of a block
-  constexpr int kSteps = 4 / kParts;       // matrix steps of a group
-  constexpr int kOut = MT * 16;
-  constexpr int kSize = kStage<MT, SUB, ZERO>, kScale = ZERO ? 8 : 4;
-  using Scale = std::conditional_t<ZERO, uint2, uint32_t>;  // scales (and zero points) of outputs g, g + 8
-  float* red = reinterpret_cast<float*>(smem + kWarps * S * kSize);  // [2][warp][row of x][kOut]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int row0 = blockIdx.y * (NT * 8), tile_step = gridDim.x * MT;
-
-  // rows of x past the last one read the last one; their results are dropped
-  const T* xp[NT];
-#pragma unroll
-  for (int j = 0; j < NT; j++)
-    xp[j] = reinterpret_cast<const T*>(a.x) + (int64_t)min(row0 + j * 8 + g, a.rows - 1) * a.sx + t * 8;
-
-  // ---- copying ahead
-  const unsigned char* ring = smem + warp * (S * kSize);
+// One CTA: 128 outputs by N rows of x, a share of k; a cluster adds up its
+// CTAs' shares in order.  SUB: groups of 32, two to a stage; otherwise a group
+// is whole stages.
+template <typename T, int N, bool SUB, bool ZERO>
+__global__ void __launch_bounds__(kM) matvec_kernel(const Args a) {
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ uint32_t tmem_at;
+  constexpr int S = kStages<N>, kSlot = (kStage<N, SUB, ZERO> + 1023) / 1024 * 1024, kParts = SUB ? 2 : 1;
+  constexpr int kScale = ZERO ? 4 : 2;
+  cg::cluster_group cl = cg::this_cluster();
+  const int shares = (int)cl.num_blocks(), share = (int)cl.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, tile = blockIdx.x / shares, row0 = blockIdx.y * N;
+  const int b0 = (int)((int64_t)a.blocks * share / shares), b1 = (int)((int64_t)a.blocks * (share + 1) / shares);
+  // x's tiles are read by the tensor cores in a pattern of 1024 bytes
+  unsigned char* ring = raw_smem + ((1024 - ((uint32_t)__cvta_generic_to_shared(raw_smem) & 1023)) & 1023);
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  int t_ahead = warp < a.blocks ? blockIdx.x * MT : a.tiles, b_ahead = warp, put = 0;
-  auto copy_next = [&]() {
-    if (t_ahead < a.tiles) {
+  const uint32_t bar = (uint32_t)__cvta_generic_to_shared(bars);
+
+  // ---- copying a stage: x (rows of 128 bytes, 16-byte pieces exchanged by row), codes, scales
+  auto copy_stage = [&](int blk) {
+    if (blk < b1) {
+      const uint32_t dst = ring_at + (blk - b0) % S * kSlot;
 #pragma unroll
-      for (int m = 0; m < MT; m++) {
-        const int tile = min(t_ahead + m, a.tiles - 1);  // a tile past the end repeats the last one
-        const uint32_t dst = ring_at + put * kSize;
-        copy16(dst + m * 512 + lane * 16, a.codes + ((int64_t)tile * a.blocks + b_ahead) * 32 + lane);
-        if (t < kParts) {
-          const int grp = SUB ? b_ahead * 2 + t : b_ahead * 64 >> a.group_log;
-          copy_small<kScale>(dst + MT * 512 + ((m * kParts + t) * 8 + g) * kScale,
-                             reinterpret_cast<const Scale*>(a.scales) + ((int64_t)tile * a.groups_p + grp) * 8 + g);
-        }
+      for (int i = 0; i < N * 8 / kM; i++) {
+        const int piece = tid + i * kM, r = piece / 8, c = piece % 8;
+        const bool ok = row0 + r < a.rows && blk * kBlock + c * 8 < a.k;
+        copy16(dst + r * 128 + ((c ^ (r & 7)) * 16),
+               reinterpret_cast<const T*>(a.x) + (ok ? (row0 + r) * a.sx + blk * kBlock + c * 8 : 0), ok);
       }
-      b_ahead += kWarps;
-      if (b_ahead >= a.blocks) {
-        b_ahead = warp;
-        t_ahead += tile_step;
+      const unsigned char* codes = a.codes + ((int64_t)tile * a.blocks + blk) * kCodes + tid * 16;
+      copy16(dst + N * 128 + tid * 16, codes, true);
+      copy16(dst + N * 128 + kCodes / 2 + tid * 16, codes + kCodes / 2, true);
+      if (tid < kParts * kM * kScale / 16) {
+        const int grp = SUB ? blk * 2 : blk * kBlock >> a.group_log;
+        copy16(dst + N * 128 + kCodes + tid * 16, a.scales + ((int64_t)tile * a.groups_p + grp) * (kM * kScale) + tid * 16,
+               true);
       }
-      put = put + 1 == S ? 0 : put + 1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < S - 1; i++) copy_next();
+  for (int i = 0; i < S - 2; i++) copy_stage(b0 + i);
 
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; m++)
-#pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) acc[m][j][i] = 0.f;
-
-  int get = 0, buf = 0;
-  for (int tile0 = blockIdx.x * MT; tile0 < a.tiles; tile0 += tile_step) {
-    for (int blk = warp; blk < a.blocks; blk += kWarps) {
-      uint4 xv[NT][2];
-      const bool second = blk * 64 + 32 < a.k;  // k is whole halves of a block
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const uint4* p = reinterpret_cast<const uint4*>(xp[j] + blk * 64);
-        xv[j][0] = __ldg(p);
-        xv[j][1] = second ? __ldg(p + 4) : make_uint4(0, 0, 0, 0);
-      }
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-      __syncwarp();
-      copy_next();
-      const unsigned char* stage = ring + get * kSize;
-      get = get + 1 == S ? 0 : get + 1;
-#pragma unroll
-      for (int part = 0; part < kParts; part++) {
-        float2 sc[MT], off[MT];  // 16 s and (8 - z) s of outputs g and g + 8
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-          const Scale v = reinterpret_cast<const Scale*>(stage + MT * 512)[(m * kParts + part) * 8 + g];
-          sc[m] = unpack2<T>(first_of(v));
-          if (ZERO) {
-            const float2 z = unpack2<T>(second_of(v));
-            off[m] = make_float2(sc[m].x * (8.f - z.x), sc[m].y * (8.f - z.y));
-          }
-          sc[m].x *= 16.f;
-          sc[m].y *= 16.f;
-        }
-        if (ZERO) {
-#pragma unroll
-          for (int j = 0; j < NT; j++) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // every row is the same: columns 2t, 2t + 1
-#pragma unroll
-            for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
-              const uint32_t* xw = reinterpret_cast<const uint32_t*>(xv[j]) + 2 * s;
-              mma16816<T>(sum, kOnes<T>, kOnes<T>, kOnes<T>, kOnes<T>, xw[0], xw[1]);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-              acc[m][j][0] += off[m].x * sum[0];
-              acc[m][j][1] += off[m].x * sum[1];
-              acc[m][j][2] += off[m].y * sum[0];
-              acc[m][j][3] += off[m].y * sum[1];
-            }
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-          float d[NT][4];
-#pragma unroll
-          for (int j = 0; j < NT; j++) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-          const uint4 c = reinterpret_cast<const uint4*>(stage)[m * 32 + lane];
-#pragma unroll
-          for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(&c)[s];
-            const uint32_t a0 = widen2<T>(w, 0), a1 = widen2<T>(w, 1), a2 = widen2<T>(w, 2), a3 = widen2<T>(w, 3);
-#pragma unroll
-            for (int j = 0; j < NT; j++) {
-              const uint32_t* xw = reinterpret_cast<const uint32_t*>(xv[j]) + 2 * s;
-              mma16816<T>(d[j], a0, a1, a2, a3, xw[0], xw[1]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; j++) {
-            acc[m][j][0] += sc[m].x * d[j][0];
-            acc[m][j][1] += sc[m].x * d[j][1];
-            acc[m][j][2] += sc[m].y * d[j][2];
-            acc[m][j][3] += sc[m].y * d[j][3];
-          }
-        }
-      }
-    }
-    // two buffers in turn: a warp can be one tile ahead of the others' reads
-    float* part = red + buf * (kWarps * NT * 8 * kOut);
-    float* mine = part + warp * (NT * 8 * kOut);
-    buf ^= 1;
-#pragma unroll
-    for (int m = 0; m < MT; m++)
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          mine[(j * 8 + 2 * t + (i & 1)) * kOut + m * 16 + g + (i >> 1) * 8] = acc[m][j][i];
-          acc[m][j][i] = 0.f;
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 8 * kOut; i += kWarps * 32) {
-      const int r = row0 + i / kOut, n = tile0 * 16 + i % kOut;
-      if (r >= a.rows || n >= a.n) continue;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; w++) v += part[w * (NT * 8 * kOut) + i];
-      if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
-      reinterpret_cast<T*>(a.y)[r * a.sy + n] = from_f32<T>(v);
-    }
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nmbarrier.init.shared::cta.b64 [%1], 1;" ::"r"(bar), "r"(bar + 8)
+                 : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&tmem_at)),
+                 "n"(kColumns<N, SUB>)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_at, mine = tmem + (uint32_t)(warp * 32 << 16);  // this warp's lanes
+
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) acc[i] = 0.f;
+  // a sum of this thread's output, scaled: the columns from `column` on
+  auto add_up = [&](int column, float scale) {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) {
+      uint32_t r[16];
+      tmem_load16(r, mine + column + i);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 16; j++) acc[i + j] += scale * __uint_as_float(r[j]);
+    }
+  };
+  // kind::f16: fp32 sums, both operands T with k innermost, N columns, 128 rows
+  constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
+  constexpr uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | (uint32_t)(kM / 16) << 24;
+
+  bool good = true;
+  bool ends[2] = {false, false};    // of the two stages before: a group ended there
+  float scale[2][kParts] = {};
+  int sums[2] = {0, 0};             // the sum that the stage added to
+  int sum = 0;
+  bool begins = true;
+  for (int blk = b0; blk < b1 + 2; blk++) {
+    const int p = (blk - b0) & 1;
+    if (blk >= b0 + 2) {  // the stage before the last one is through
+      good = good && wait_bar(bar + p * 8, ((blk - b0) / 2 - 1) & 1);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    if (blk < b1) {
+      copy_stage(blk + S - 2);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (ends[p]) {
+#pragma unroll
+      for (int h = 0; h < kParts; h++) add_up(64 + (sums[p] * kParts + h) * N, scale[p][h]);
+    }
+    ends[p] = false;
+    if (blk >= b1) continue;
+
+    const unsigned char* stage = ring + (blk - b0) % S * kSlot;
+    float rest[kParts], s_one[kParts];
+    uint32_t one[kParts];
+    __syncthreads();  // others copied this thread's scales, and x
+#pragma unroll
+    for (int h = 0; h < kParts; h++) {
+      const unsigned char* at = stage + N * 128 + kCodes + (h * kM + tid) * kScale;
+      float s, z = 8.f;
+      if (ZERO) {
+        const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at));
+        s = v.x, z = v.y;
+      } else {
+        s = to_f32(*reinterpret_cast<const T*>(at));
+      }
+      const float whole = fminf(fmaxf(rintf(z), 0.f), 15.f);
+      rest[h] = whole - z;
+      s_one[h] = s;
+      scale[p][h] = 16.f * s;
+      one[h] = pack2<T>(1.f + whole * 0.0625f, 1.f + whole * 0.0625f);
+    }
+    {
+      const uint4* words = reinterpret_cast<const uint4*>(stage + N * 128) + tid;
+      const uint4 w0 = words[0], w1 = words[kM];
+      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      uint32_t r[32];
+#pragma unroll
+      for (int i = 0; i < 32; i++) r[i] = widen2<T>(w[i / 4], i % 4, one[SUB ? i / 16 : 0]);
+      tmem_store32(mine + p * 32, r);
+    }
+    if (ZERO) {  // zero points that are not whole
+      bool some = false;
+#pragma unroll
+      for (int h = 0; h < kParts; h++) some = some || !(rest[h] == 0.f);
+      if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          float t[kParts] = {};
+          for (int c = 0; c < 8; c++) {
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + i * 128 + ((c ^ (i & 7)) * 16));
+            const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z), f3 = unpack2<T>(v.w);
+            t[SUB ? c / 4 : 0] += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+          }
+#pragma unroll
+          for (int h = 0; h < kParts; h++) acc[i] += s_one[h] * rest[h] * t[h];
+        }
+      }
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    const bool last = SUB || blk + 1 == b1 || ((blk + 1) * kBlock & ((1 << a.group_log) - 1)) == 0;
+    if (tid == 0) {
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      // rows of 128 bytes, groups of eight rows 1024 bytes apart, pieces exchanged within 128 bytes
+      const uint64_t desc = (uint64_t)((ring_at + (blk - b0) % S * kSlot) >> 4 & 0x3fffu) | 1ull << 16 |
+                            (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint32_t d = tmem + 64 + (sum * kParts + (SUB ? i / 2 : 0)) * N;
+        const uint32_t fresh = SUB ? i % 2 == 0 : i == 0 && begins;
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.eq.u32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+            "r"(tmem + p * 32 + i * 8), "l"(desc + 2 * i), "r"(idesc), "r"(fresh)
+            : "memory");
+      }
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar + p * 8)
+                   : "memory");
+    }
+    ends[p] = last;
+    sums[p] = sum;
+    begins = last;
+    if (last) sum ^= 1;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  // (before the cluster meets: a CTA elsewhere may be waiting for the columns)
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns<N, SUB>));
+  if (!good) {  // a wait gave up: the result says so
+#pragma unroll
+    for (int i = 0; i < N; i++) acc[i] = __int_as_float(0x7fffffff);
+  }
+
+  const int n = tile * kM + tid;
+  auto write = [&](int r, float v) {
+    if (row0 + r >= a.rows || n >= a.n) return;
+    if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
+    reinterpret_cast<T*>(a.y)[(row0 + r) * a.sy + n] = from_f32<T>(v);
+  };
+  if (shares == 1) {
+#pragma unroll
+    for (int i = 0; i < N; i++) write(i, acc[i]);
+    return;
+  }
+  float* part = reinterpret_cast<float*>(ring);  // [row of x][output]
+#pragma unroll
+  for (int i = 0; i < N; i++) part[i * kM + tid] = acc[i];
+  cl.sync();
+  for (int i = share; i < N && row0 + i < a.rows; i += shares) {
+    float v[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; r++) v[r] = r < shares ? *cl.map_shared_rank(part + i * kM + tid, r) : 0.f;
+    float all = v[0];
+#pragma unroll
+    for (int r = 1; r < kMaxCluster; r++) all += v[r];
+    write(i, all);
+  }
+  cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
-template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
+template <typename T, int N, bool SUB, bool ZERO>
 cudaError_t launch(const Args& a, cudaStream_t st) {
-  constexpr int smem = kWarps * S * kStage<MT, SUB, ZERO> + 2 * kWarps * NT * 8 * MT * 16 * (int)sizeof(float);
-  auto* fn = matvec_kernel<T, MT, NT, S, SUB, ZERO>;
+  auto* fn = matvec_kernel<T, N, SUB, ZERO>;
+  constexpr int smem = kSmem<N, SUB, ZERO>;
   static OpsOnce once;
-  static int resident = 1;  // CTAs of a multiprocessor
   if (const int dev = ops_current(); !once(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int v = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps * 32, smem);
-    if (e != cudaSuccess) return e;
-    resident = v > 0 ? v : 1;
     once.set(dev);
   }
-  const int rows = (a.rows + NT * 8 - 1) / (NT * 8), tiles = (a.tiles + MT - 1) / MT;
-  const int most = (resident * ops_sm_count() + rows - 1) / rows;
-  fn<<<dim3(tiles < most ? tiles : most, rows), kWarps * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  // k is shared among CTAs until they fill the device, down to four stages each
+  const int rows = (a.rows + N - 1) / N;
+  int shares = 1;
+  while (shares < kMaxCluster && (int64_t)a.tiles * rows * shares < (int64_t)ops_sm_count() * kResident<N, SUB> &&
+         a.blocks >= shares * 2 * 4)
+    shares *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.tiles * shares, rows);
+  cfg.blockDim = dim3(kM);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = shares;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <typename T, int MT, int NT, int S>
+template <typename T, int N>
 cudaError_t by_group(const Args& a, bool zeros, cudaStream_t st) {
-  if (a.group_log == 5) return zeros ? launch<T, MT, NT, S, true, true>(a, st) : launch<T, MT, NT, S, true, false>(a, st);
-  return zeros ? launch<T, MT, NT, S, false, true>(a, st) : launch<T, MT, NT, S, false, false>(a, st);
+  if (a.group_log == 5) return zeros ? launch<T, N, true, true>(a, st) : launch<T, N, true, false>(a, st);
+  return zeros ? launch<T, N, false, true>(a, st) : launch<T, N, false, false>(a, st);
 }
 
 template <typename T>
 cudaError_t by_rows(const Args& a, bool zeros, cudaStream_t st) {
-  // two tiles of outputs share a CTA's loads of x where that leaves CTAs for
-  // every multiprocessor
-  const bool two = a.tiles >= 4 * ops_sm_count();
-  if (a.rows <= 8) return two ? by_group<T, 2, 1, 4>(a, zeros, st) : by_group<T, 1, 1, 8>(a, zeros, st);
-  if (a.rows <= 16) return two ? by_group<T, 2, 2, 4>(a, zeros, st) : by_group<T, 1, 2, 8>(a, zeros, st);
-  if (a.rows <= 32) return by_group<T, 2, 4, 4>(a, zeros, st);
-  return by_group<T, 2, 8, 4>(a, zeros, st);
+  if (a.rows <= 16) return by_group<T, 16>(a, zeros, st);
+  if (a.rows <= 32) return by_group<T, 32>(a, zeros, st);
+  return by_group<T, 64>(a, zeros, st);
 }
 
 struct Sizes {
@@ -330,12 +426,12 @@ const char* sizes(int32_t n, int32_t k, int32_t group, bool zeros, Sizes* s) {
   if (n < 1 || k < 1) return "n and k must be >= 1";
   if (group != 32 && group != 64 && group != 128 && group != 256) return "group must be 32, 64, 128 or 256";
   if (k % group) return "k must be a multiple of group";
-  s->tiles = ((int64_t)n + 15) / 16;
-  s->blocks = ((int64_t)k + 63) / 64;
+  s->tiles = ((int64_t)n + kM - 1) / kM;
+  s->blocks = ((int64_t)k + kBlock - 1) / kBlock;
   s->groups = k / group;
   s->groups_p = group == 32 ? s->blocks * 2 : s->groups;
-  s->code_bytes = s->tiles * s->blocks * 512;
-  s->bytes = s->code_bytes + s->tiles * s->groups_p * (zeros ? 64 : 32);
+  s->code_bytes = s->tiles * s->blocks * kCodes;
+  s->bytes = s->code_bytes + s->tiles * s->groups_p * (kM * (zeros ? 4 : 2));
   return nullptr;
 }
 
@@ -408,8 +504,8 @@ extern "C" int wfst_matvec_quant(const wfst_matvec_args* r, void* stream) {
   OpsDevice guard(dev);
   if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "matvec_quant: device");
   Args a;
-  a.codes = reinterpret_cast<const uint4*>(r->packed);
-  a.scales = static_cast<const char*>(r->packed) + s.code_bytes;
+  a.codes = static_cast<const unsigned char*>(r->packed);
+  a.scales = a.codes + s.code_bytes;
   a.x = r->x;
   a.bias = r->bias;
   a.y = r->y;
