@@ -7,18 +7,25 @@
 // beside them, so HBM bounds it up to some tens of rows.
 //
 // The products run on the tensor cores with the weights as the M side: a CTA
-// takes 128 outputs, its threads one each.  A thread brings its output's codes
-// into the operand type and stores them to tensor memory as row of A; x is B,
-// from shared memory; the sums of a group are read back, scaled and added up in
-// registers in fp32, so nothing is rounded before y.  Two things are then in
-// flight at a time: the products of one stage and the codes of the next ones.
+// takes 128 outputs, and 128 of its threads one each.  Such a thread brings its
+// output's codes into the operand type and stores them to tensor memory as its
+// row of A; x is B, from shared memory; a group's sums are read back, scaled and
+// added up in registers in fp32, so nothing is rounded before y.  A fifth warp
+// copies ahead, a sixth one issues the products; they meet through mbarriers.
 //   - What it costs to bring codes into the type is the next bound after HBM, so
 //     a code is not converted but put in place: as the upper four bits of a
 //     mantissa it makes the 16-bit number 1 + c / 16, one shift and one logical
-//     operation for two codes, and less 1 + z / 16 it is (c - z) / 16, exactly
-//     for whole z.  What z has beside its whole part is added as s * rest * sum x.
+//     operation for two codes.
+//   - The 1 + z / 16 too much is taken off by the tensor cores, which have time:
+//     a second product of the same x with -(1 + z / 16) in every column of A
+//     goes into the same fp32 sum, whose terms are then about five times those
+//     of sum x (c - z) / 16.  Where tensor memory has no room for it (groups of
+//     32, 17 to 32 rows), the threads subtract, exactly.  Both hold for whole z;
+//     what z has beside its whole part is added as s * rest * sum x.
 //   - mma.sync instructions for the same work, fed from registers, came to half
-//     of HBM's rate at 8 rows and a fifth at 64 (8 x 131072 x 4096: 80 us).
+//     of HBM's rate at 8 rows (8 x 131072 x 4096: 80 us) and were bound by the
+//     tensor cores' older path from 32 rows on.
+// A non-finite x makes its row of y NaN.
 //
 // Layout ("packed", made once by wfst_quant_pack): tiles of 128 outputs, in them
 // blocks of 64 k, in them two halves of 32 k with 16 bytes per output, so that a
@@ -35,7 +42,8 @@ namespace cg = cooperative_groups;
 namespace wfst {
 namespace {
 
-constexpr int kM = 128;       // outputs of a tile, threads of a CTA
+constexpr int kM = 128;       // outputs of a tile, one to a thread of the first four warps
+constexpr int kThreads = kM + 64;
 constexpr int kBlock = 64;    // k of a stage
 constexpr int kCodes = kM * kBlock / 2;  // bytes of a stage's codes
 constexpr int kMaxCluster = 8;
@@ -112,6 +120,27 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t is;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+  return is != 0;
+}
+// d (+)= a * b; a in tensor memory
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
 // 32 columns of this warp's 32 lanes from registers
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
@@ -132,80 +161,81 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
       : "memory");
 }
 
-// Pair j of a word as (c - z) / 16 of its two codes; one: 1 + z / 16, twice.
+// 8 columns with one value
+__device__ __forceinline__ void tmem_fill8(uint32_t at, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(at), "r"(v) : "memory");
+}
+
+// Pair j of a word as 1 + c / 16 of its two codes.
 template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t w, int j, uint32_t one) {
+__device__ __forceinline__ uint32_t widen2(uint32_t w, int j) {
+  return ((j ? __funnelshift_r(w, w, 4 * j) : w) & (0x000f000fu << kCodeAt<T>)) | kOnes<T>;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
   using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
-  const uint32_t v = ((j ? __funnelshift_r(w, w, 4 * j) : w) & (0x000f000fu << kCodeAt<T>)) | kOnes<T>;
-  const T2 r = __hsub2(*reinterpret_cast<const T2*>(&v), *reinterpret_cast<const T2*>(&one));
+  const T2 r = __hsub2(*reinterpret_cast<const T2*>(&v), *reinterpret_cast<const T2*>(&off));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // ---- sizes that go with N rows of x (16, 32 or 64) and groups of 32 (SUB)
 
-// tensor memory: two stages of A, and two sums of 16, 32 or 64 columns (four with SUB)
+// whether the tensor cores take off 1 + z / 16
 template <int N, bool SUB>
-constexpr int kColumns = 64 + (SUB ? 4 : 2) * N <= 128 ? 128 : 64 + (SUB ? 4 : 2) * N <= 256 ? 256 : 512;
+constexpr bool kFold = !SUB && N != 32;
+// tensor memory: two stages of A (32 columns each); two constants for kFold (8);
+// two sums of N columns (four with SUB)
+template <int N, bool SUB>
+constexpr int kSumAt = 64 + (kFold<N, SUB> ? 16 : 0);
+template <int N, bool SUB>
+constexpr int kUsed = kSumAt<N, SUB> + (SUB ? 4 : 2) * N;
+template <int N, bool SUB>
+constexpr int kColumns = kUsed<N, SUB> <= 128 ? 128 : kUsed<N, SUB> <= 256 ? 256 : 512;
 template <int N>
 constexpr int kStages = N == 64 ? 7 : 6;
 template <int N, bool SUB, bool ZERO>
-constexpr int kStage = N * 128 + kCodes + (SUB ? 2 : 1) * kM * (ZERO ? 4 : 2);
+constexpr int kSlot = (N * 128 + kCodes + (SUB ? 2 : 1) * kM * (ZERO ? 4 : 2) + 1023) / 1024 * 1024;
 // CTAs of a multiprocessor: what its 512 columns hold, and no more, since one
 // that waits for columns would hold up its cluster; shared memory sees to it
 template <int N, bool SUB>
 constexpr int kResident = 512 / kColumns<N, SUB>;
 template <int N, bool SUB, bool ZERO>
-constexpr int kSmem = 1024 + (kStages<N> * ((kStage<N, SUB, ZERO> + 1023) / 1024 * 1024) > 233472 / (kResident<N, SUB> + 1)
-                                  ? kStages<N> * ((kStage<N, SUB, ZERO> + 1023) / 1024 * 1024)
+constexpr int kSmem = 1024 + (kStages<N> * kSlot<N, SUB, ZERO> > 233472 / (kResident<N, SUB> + 1)
+                                  ? kStages<N> * kSlot<N, SUB, ZERO>
                                   : 233472 / (kResident<N, SUB> + 1));
 
 // One CTA: 128 outputs by N rows of x, a share of k; a cluster adds up its
 // CTAs' shares in order.  SUB: groups of 32, two to a stage; otherwise a group
 // is whole stages.
 template <typename T, int N, bool SUB, bool ZERO>
-__global__ void __launch_bounds__(kM) matvec_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(const Args a) {
   extern __shared__ unsigned char raw_smem[];
-  __shared__ __align__(8) uint64_t bars[2];
+  constexpr int S = kStages<N>, kSize = kSlot<N, SUB, ZERO>, kParts = SUB ? 2 : 1, kScale = ZERO ? 4 : 2;
+  constexpr bool FOLD = kFold<N, SUB>;
+  // a slot's codes and x are there, a slot is free; A is written, the products of a stage are through
+  __shared__ __align__(8) uint64_t bars[3 * S + 4];
   __shared__ uint32_t tmem_at;
-  constexpr int S = kStages<N>, kSlot = (kStage<N, SUB, ZERO> + 1023) / 1024 * 1024, kParts = SUB ? 2 : 1;
-  constexpr int kScale = ZERO ? 4 : 2;
+  __shared__ int failed;
   cg::cluster_group cl = cg::this_cluster();
   const int shares = (int)cl.num_blocks(), share = (int)cl.block_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, tile = blockIdx.x / shares, row0 = blockIdx.y * N;
-  const int b0 = (int)((int64_t)a.blocks * share / shares), b1 = (int)((int64_t)a.blocks * (share + 1) / shares);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tile = blockIdx.x / shares, row0 = blockIdx.y * N;
+  const int b0 = (int)((int64_t)a.blocks * share / shares), count = (int)((int64_t)a.blocks * (share + 1) / shares) - b0;
   // x's tiles are read by the tensor cores in a pattern of 1024 bytes
   unsigned char* ring = raw_smem + ((1024 - ((uint32_t)__cvta_generic_to_shared(raw_smem) & 1023)) & 1023);
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   const uint32_t bar = (uint32_t)__cvta_generic_to_shared(bars);
-
-  // ---- copying a stage: x (rows of 128 bytes, 16-byte pieces exchanged by row), codes, scales
-  auto copy_stage = [&](int blk) {
-    if (blk < b1) {
-      const uint32_t dst = ring_at + (blk - b0) % S * kSlot;
-#pragma unroll
-      for (int i = 0; i < N * 8 / kM; i++) {
-        const int piece = tid + i * kM, r = piece / 8, c = piece % 8;
-        const bool ok = row0 + r < a.rows && blk * kBlock + c * 8 < a.k;
-        copy16(dst + r * 128 + ((c ^ (r & 7)) * 16),
-               reinterpret_cast<const T*>(a.x) + (ok ? (row0 + r) * a.sx + blk * kBlock + c * 8 : 0), ok);
-      }
-      const unsigned char* codes = a.codes + ((int64_t)tile * a.blocks + blk) * kCodes + tid * 16;
-      copy16(dst + N * 128 + tid * 16, codes, true);
-      copy16(dst + N * 128 + kCodes / 2 + tid * 16, codes + kCodes / 2, true);
-      if (tid < kParts * kM * kScale / 16) {
-        const int grp = SUB ? blk * 2 : blk * kBlock >> a.group_log;
-        copy16(dst + N * 128 + kCodes + tid * 16, a.scales + ((int64_t)tile * a.groups_p + grp) * (kM * kScale) + tid * 16,
-               true);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < S - 2; i++) copy_stage(b0 + i);
+  auto codes_in = [&](int slot) { return bar + slot * 8; };
+  auto x_in = [&](int slot) { return bar + (S + slot) * 8; };
+  auto is_free = [&](int slot) { return bar + (2 * S + slot) * 8; };
+  auto a_in = [&](int p) { return bar + (3 * S + p) * 8; };
+  auto through = [&](int p) { return bar + (3 * S + 2 + p) * 8; };
 
   if (tid == 0) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nmbarrier.init.shared::cta.b64 [%1], 1;" ::"r"(bar), "r"(bar + 8)
-                 : "memory");
+    failed = 0;
+    for (int i = 0; i < 3 * S + 4; i++) {
+      const int n = i < 2 * S ? 1 : i < 3 * S + 2 ? 4 : 1;
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar + i * 8), "r"(n) : "memory");
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -218,131 +248,177 @@ __global__ void __launch_bounds__(kM) matvec_kernel(const Args a) {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = tmem_at, mine = tmem + (uint32_t)(warp * 32 << 16);  // this warp's lanes
+  const uint32_t tmem = tmem_at;
+  bool good = true;
 
   float acc[N];
+  if (warp == 4) {
+    // ---- copies: x (rows of 128 bytes, 16-byte pieces exchanged by row), codes and scales
+    constexpr int kLag = 3;  // stages of x in flight
+    for (int i = 0; i < count + kLag; i++) {
+      if (i < count) {
+        const int slot = i % S, blk = b0 + i;
+        if (i >= S) good = good && wait_bar(is_free(slot), (i / S - 1) & 1);
+        const uint32_t dst = ring_at + slot * kSize;
+        if (lane == 0) {
+          constexpr uint32_t bytes = kCodes + kParts * kM * kScale;
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(codes_in(slot)), "n"(bytes) : "memory");
+          const int grp = SUB ? blk * 2 : blk * kBlock >> a.group_log;
+          copy_bulk(dst + N * 128, a.codes + ((int64_t)tile * a.blocks + blk) * kCodes, kCodes, codes_in(slot));
+          copy_bulk(dst + N * 128 + kCodes, a.scales + ((int64_t)tile * a.groups_p + grp) * (kM * kScale),
+                    kParts * kM * kScale, codes_in(slot));
+        }
+        __syncwarp();
 #pragma unroll
-  for (int i = 0; i < N; i++) acc[i] = 0.f;
-  // a sum of this thread's output, scaled: the columns from `column` on
-  auto add_up = [&](int column, float scale) {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) {
-      uint32_t r[16];
-      tmem_load16(r, mine + column + i);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-      for (int j = 0; j < 16; j++) acc[i + j] += scale * __uint_as_float(r[j]);
-    }
-  };
-  // kind::f16: fp32 sums, both operands T with k innermost, N columns, 128 rows
-  constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
-  constexpr uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | (uint32_t)(kM / 16) << 24;
-
-  bool good = true;
-  bool ends[2] = {false, false};    // of the two stages before: a group ended there
-  float scale[2][kParts] = {};
-  int sums[2] = {0, 0};             // the sum that the stage added to
-  int sum = 0;
-  bool begins = true;
-  for (int blk = b0; blk < b1 + 2; blk++) {
-    const int p = (blk - b0) & 1;
-    if (blk >= b0 + 2) {  // the stage before the last one is through
-      good = good && wait_bar(bar + p * 8, ((blk - b0) / 2 - 1) & 1);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    }
-    if (blk < b1) {
-      copy_stage(blk + S - 2);
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    if (ends[p]) {
-#pragma unroll
-      for (int h = 0; h < kParts; h++) add_up(64 + (sums[p] * kParts + h) * N, scale[p][h]);
-    }
-    ends[p] = false;
-    if (blk >= b1) continue;
-
-    const unsigned char* stage = ring + (blk - b0) % S * kSlot;
-    float rest[kParts], s_one[kParts];
-    uint32_t one[kParts];
-    __syncthreads();  // others copied this thread's scales, and x
-#pragma unroll
-    for (int h = 0; h < kParts; h++) {
-      const unsigned char* at = stage + N * 128 + kCodes + (h * kM + tid) * kScale;
-      float s, z = 8.f;
-      if (ZERO) {
-        const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at));
-        s = v.x, z = v.y;
-      } else {
-        s = to_f32(*reinterpret_cast<const T*>(at));
+        for (int j = 0; j < N / 4; j++) {
+          const int piece = lane + j * 32, r = piece / 8, c = piece % 8;
+          const bool ok = row0 + r < a.rows && blk * kBlock + c * 8 < a.k;
+          copy16(dst + r * 128 + ((c ^ (r & 7)) * 16),
+                 reinterpret_cast<const T*>(a.x) + (ok ? (row0 + r) * a.sx + blk * kBlock + c * 8 : 0), ok);
+        }
       }
-      const float whole = fminf(fmaxf(rintf(z), 0.f), 15.f);
-      rest[h] = whole - z;
-      s_one[h] = s;
-      scale[p][h] = 16.f * s;
-      one[h] = pack2<T>(1.f + whole * 0.0625f, 1.f + whole * 0.0625f);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i >= kLag) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive(x_in((i - kLag) % S));
+      }
     }
-    {
+    // nothing may be on its way when the CTA ends
+    for (int i = count > S ? count - S : 0; i < count; i++) good = good && wait_bar(codes_in(i % S), (i / S) & 1);
+  } else if (warp == 5) {
+    // ---- products.  kind::f16: fp32 sums, both operands T with k innermost, N columns, 128 rows
+    constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
+    constexpr uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | (uint32_t)(kM / 16) << 24;
+    // x: rows of 128 bytes, groups of eight rows 1024 bytes apart, pieces exchanged within 128 bytes
+    const uint64_t desc0 = (uint64_t)(ring_at >> 4 & 0x3fffu) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+    int sum = 0;
+    bool begins = true;
+    for (int i = 0; i < count; i++) {
+      const int slot = i % S, p = i & 1, blk = b0 + i;
+      good = good && wait_bar(x_in(slot), (i / S) & 1);
+      good = good && wait_bar(a_in(p), (i / 2) & 1);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint64_t desc = desc0 + (uint64_t)(slot * (kSize >> 4));
+      if (elected()) {
+        const uint32_t d = tmem + kSumAt<N, SUB> + sum * kParts * N;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          product(d + (SUB ? j / 2 * N : 0), tmem + p * 32 + j * 8, desc + 2 * j, idesc, SUB ? j % 2 != 0 : j || !begins);
+          if (FOLD) product(d, tmem + 64 + (ZERO ? sum * 8 : 0), desc + 2 * j, idesc, true);
+        }
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(through(p)) : "memory");
+      }
+      __syncwarp();
+      begins = SUB || ((blk + 1) * kBlock & ((1 << a.group_log) - 1)) == 0;
+      if (begins) sum ^= 1;
+    }
+  } else {
+    // ---- codes into the operand type; the groups' sums, scaled
+    const uint32_t mine = tmem + (uint32_t)(warp * 32 << 16);  // this warp's lanes
+#pragma unroll
+    for (int i = 0; i < N; i++) acc[i] = 0.f;
+    auto add_up = [&](int column, float scale) {
+#pragma unroll
+      for (int i = 0; i < N; i += 16) {
+        uint32_t r[16];
+        tmem_load16(r, mine + column + i);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < 16; j++) acc[i + j] += scale * __uint_as_float(r[j]);
+      }
+    };
+    if (FOLD && !ZERO) tmem_fill8(mine + 64, pack2<T>(-1.5f, -1.5f));
+    int slot = 0, phase = 0, sum = 0;
+    bool begins = true;
+    // of the two stages before: where a group ended, and its scale
+    int end0 = -1, end1 = -1;
+    float scale0[kParts], scale1[kParts];
+    auto step = [&](int i, int& end, float (&scale)[kParts]) {
+      const int p = i & 1;
+      if (i >= 2) {  // the products of the stage before the last one are through: its slot and A are free
+        good = good && wait_bar(through(p), (i / 2 - 1) & 1);
+        if (lane == 0) arrive(is_free((i - 2) % S));
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (end >= 0) {
+#pragma unroll
+          for (int h = 0; h < kParts; h++) add_up(kSumAt<N, SUB> + (end * kParts + h) * N, scale[h]);
+        }
+      }
+      end = -1;
+      if (i >= count) return;
+      good = good && wait_bar(codes_in(slot), phase);
+      const unsigned char* stage = ring + slot * kSize;
+      float s_one[kParts], rest[kParts];
+      uint32_t one[kParts];
+#pragma unroll
+      for (int h = 0; h < kParts; h++) {
+        const unsigned char* at = stage + N * 128 + kCodes + (h * kM + tid) * kScale;
+        rest[h] = 0.f;
+        one[h] = pack2<T>(1.5f, 1.5f);
+        if (ZERO) {
+          const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at));
+          const float whole = fminf(fmaxf(rintf(v.y), 0.f), 15.f);
+          s_one[h] = v.x;
+          rest[h] = whole - v.y;
+          one[h] = pack2<T>(1.f + whole * 0.0625f, 1.f + whole * 0.0625f);
+        } else {
+          s_one[h] = to_f32(*reinterpret_cast<const T*>(at));
+        }
+        scale[h] = 16.f * s_one[h];
+      }
       const uint4* words = reinterpret_cast<const uint4*>(stage + N * 128) + tid;
       const uint4 w0 = words[0], w1 = words[kM];
       const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       uint32_t r[32];
 #pragma unroll
-      for (int i = 0; i < 32; i++) r[i] = widen2<T>(w[i / 4], i % 4, one[SUB ? i / 16 : 0]);
+      for (int j = 0; j < 32; j++) {
+        r[j] = widen2<T>(w[j / 4], j % 4);
+        if (!FOLD) r[j] = less2<T>(r[j], one[SUB ? j / 16 : 0]);
+      }
       tmem_store32(mine + p * 32, r);
-    }
-    if (ZERO) {  // zero points that are not whole
-      bool some = false;
+      if (FOLD && ZERO && begins) tmem_fill8(mine + 64 + sum * 8, one[0] ^ 0x80008000u);
+      if (ZERO) {  // zero points that are not whole
+        bool some = false;
 #pragma unroll
-      for (int h = 0; h < kParts; h++) some = some || !(rest[h] == 0.f);
-      if (__any_sync(0xffffffffu, some)) {
+        for (int h = 0; h < kParts; h++) some = some || !(rest[h] == 0.f);
+        if (__any_sync(0xffffffffu, some)) {
+          good = good && wait_bar(x_in(slot), phase);
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-          float t[kParts] = {};
-          for (int c = 0; c < 8; c++) {
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + i * 128 + ((c ^ (i & 7)) * 16));
-            const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z), f3 = unpack2<T>(v.w);
-            t[SUB ? c / 4 : 0] += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+          for (int j = 0; j < N; j++) {
+            float t[kParts] = {};
+            for (int c = 0; c < 8; c++) {
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + j * 128 + ((c ^ (j & 7)) * 16));
+              const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z), f3 = unpack2<T>(v.w);
+              t[SUB ? c / 4 : 0] += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+            }
+#pragma unroll
+            for (int h = 0; h < kParts; h++) acc[j] += s_one[h] * rest[h] * t[h];
           }
-#pragma unroll
-          for (int h = 0; h < kParts; h++) acc[i] += s_one[h] * rest[h] * t[h];
         }
       }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(a_in(p));
+      if (++slot == S) slot = 0, phase ^= 1;
+      begins = SUB || ((b0 + i + 1) * kBlock & ((1 << a.group_log) - 1)) == 0;
+      if (begins || i + 1 == count) end = sum;
+      if (begins) sum ^= 1;
+    };
+    for (int i = 0; i < count + 2; i += 2) {
+      step(i, end0, scale0);
+      if (i + 1 < count + 2) step(i + 1, end1, scale1);
     }
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    const bool last = SUB || blk + 1 == b1 || ((blk + 1) * kBlock & ((1 << a.group_log) - 1)) == 0;
-    if (tid == 0) {
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      // rows of 128 bytes, groups of eight rows 1024 bytes apart, pieces exchanged within 128 bytes
-      const uint64_t desc = (uint64_t)((ring_at + (blk - b0) % S * kSlot) >> 4 & 0x3fffu) | 1ull << 16 |
-                            (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const uint32_t d = tmem + 64 + (sum * kParts + (SUB ? i / 2 : 0)) * N;
-        const uint32_t fresh = SUB ? i % 2 == 0 : i == 0 && begins;
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.eq.u32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-            "r"(tmem + p * 32 + i * 8), "l"(desc + 2 * i), "r"(idesc), "r"(fresh)
-            : "memory");
-      }
-      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar + p * 8)
-                   : "memory");
-    }
-    ends[p] = last;
-    sums[p] = sum;
-    begins = last;
-    if (last) sum ^= 1;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!good) failed = 1;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   // (before the cluster meets: a CTA elsewhere may be waiting for the columns)
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns<N, SUB>));
-  if (!good) {  // a wait gave up: the result says so
+  if (warp < 4 && failed) {  // a wait gave up: the result says so
 #pragma unroll
     for (int i = 0; i < N; i++) acc[i] = __int_as_float(0x7fffffff);
   }
@@ -354,22 +430,28 @@ __global__ void __launch_bounds__(kM) matvec_kernel(const Args a) {
     reinterpret_cast<T*>(a.y)[(row0 + r) * a.sy + n] = from_f32<T>(v);
   };
   if (shares == 1) {
+    if (warp < 4) {
 #pragma unroll
-    for (int i = 0; i < N; i++) write(i, acc[i]);
+      for (int i = 0; i < N; i++) write(i, acc[i]);
+    }
     return;
   }
   float* part = reinterpret_cast<float*>(ring);  // [row of x][output]
+  if (warp < 4) {
 #pragma unroll
-  for (int i = 0; i < N; i++) part[i * kM + tid] = acc[i];
+    for (int i = 0; i < N; i++) part[i * kM + tid] = acc[i];
+  }
   cl.sync();
-  for (int i = share; i < N && row0 + i < a.rows; i += shares) {
-    float v[kMaxCluster];
+  if (warp < 4) {
+    for (int i = share; i < N && row0 + i < a.rows; i += shares) {
+      float v[kMaxCluster];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; r++) v[r] = r < shares ? *cl.map_shared_rank(part + i * kM + tid, r) : 0.f;
-    float all = v[0];
+      for (int r = 0; r < kMaxCluster; r++) v[r] = r < shares ? *cl.map_shared_rank(part + i * kM + tid, r) : 0.f;
+      float all = v[0];
 #pragma unroll
-    for (int r = 1; r < kMaxCluster; r++) all += v[r];
-    write(i, all);
+      for (int r = 1; r < kMaxCluster; r++) all += v[r];
+      write(i, all);
+    }
   }
   cl.sync();  // no CTA leaves while another may read its shared memory
 }
@@ -384,15 +466,16 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
-  // k is shared among CTAs until they fill the device, down to four stages each
+  // k is shared among CTAs until there are several rounds of them, down to four
+  // stages each in the first round and to sixteen after it
   const int rows = (a.rows + N - 1) / N;
   int shares = 1;
-  while (shares < kMaxCluster && (int64_t)a.tiles * rows * shares < (int64_t)ops_sm_count() * kResident<N, SUB> &&
-         a.blocks >= shares * 2 * 4)
+  const int64_t slots = (int64_t)ops_sm_count() * kResident<N, SUB>, ctas = (int64_t)a.tiles * rows;
+  while (shares < kMaxCluster && ctas * shares < 4 * slots && a.blocks >= shares * 2 * (ctas * shares < slots ? 4 : 16))
     shares *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.tiles * shares, rows);
-  cfg.blockDim = dim3(kM);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
