@@ -452,7 +452,8 @@ int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros,
 
 /*
  * y[r, n] = bias[n] + sum over k of x[r, k] * w[n, k], for rows r of x
- * [rows, k] (16-byte aligned, stride_x a multiple of 8) and a packed matrix.
+ * [rows, k] (16-byte aligned, stride_x >= k and a multiple of 8) and a packed
+ * matrix.
  * bias [n] may be NULL.  rows = 0 does nothing.  Errors: INVALID_ARG, CUDA.
  */
 typedef struct {

@@ -35,6 +35,8 @@
 
 #include <type_traits>
 
+#include <cuda.h>
+
 #include "wfst_ops.h"
 
 namespace cg = cooperative_groups;
@@ -47,7 +49,7 @@ constexpr int kThreads = kM + 64;
 constexpr int kBlock = 64;    // k of a stage
 constexpr int kCodes = kM * kBlock / 2;  // bytes of a stage's codes
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kSpins = 1u << 22;    // waits give up after that
+constexpr uint32_t kNap = 20000, kSpins = 1u << 16;  // a wait sleeps so many ns at a time, and gives up after so many times
 
 // Where a code lies in a 16-bit number, and the bits of 1 around it.
 template <typename T>
@@ -109,12 +111,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kSpins; i++) {
     uint32_t done;
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(kNap)
         : "memory");
     if (done) return true;
   }
@@ -172,13 +175,15 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, int j) {
   return ((j ? __funnelshift_r(w, w, 4 * j) : w) & (0x000f000fu << kCodeAt<T>)) | kOnes<T>;
 }
 template <typename T>
+constexpr uint32_t kHalves = std::is_same_v<T, __half> ? 0x3e003e00u : 0x3fc03fc0u;  // 1.5, twice
+template <typename T>
 __device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
   using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
   const T2 r = __hsub2(*reinterpret_cast<const T2*>(&v), *reinterpret_cast<const T2*>(&off));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// ---- sizes that go with N rows of x (16, 32 or 64) and groups of 32 (SUB)
+// ---- many rows: sizes that go with N rows of x (32 or 64) and groups of 32 (SUB)
 
 // whether the tensor cores take off 1 + z / 16
 template <int N, bool SUB>
@@ -208,12 +213,13 @@ constexpr int kSmem = 1024 + (kStages<N> * kSlot<N, SUB, ZERO> > 233472 / (kResi
 // CTAs' shares in order.  SUB: groups of 32, two to a stage; otherwise a group
 // is whole stages.
 template <typename T, int N, bool SUB, bool ZERO>
-__global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
+    matvec_wide(const Args a, const __grid_constant__ CUtensorMap x_map) {
   extern __shared__ unsigned char raw_smem[];
   constexpr int S = kStages<N>, kSize = kSlot<N, SUB, ZERO>, kParts = SUB ? 2 : 1, kScale = ZERO ? 4 : 2;
   constexpr bool FOLD = kFold<N, SUB>;
-  // a slot's codes and x are there, a slot is free; A is written, the products of a stage are through
-  __shared__ __align__(8) uint64_t bars[3 * S + 4];
+  // a slot is filled, a slot is free; A is written, the products of a stage are through
+  __shared__ __align__(8) uint64_t bars[2 * S + 4];
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
   cg::cluster_group cl = cg::this_cluster();
@@ -224,16 +230,15 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
   unsigned char* ring = raw_smem + ((1024 - ((uint32_t)__cvta_generic_to_shared(raw_smem) & 1023)) & 1023);
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   const uint32_t bar = (uint32_t)__cvta_generic_to_shared(bars);
-  auto codes_in = [&](int slot) { return bar + slot * 8; };
-  auto x_in = [&](int slot) { return bar + (S + slot) * 8; };
-  auto is_free = [&](int slot) { return bar + (2 * S + slot) * 8; };
-  auto a_in = [&](int p) { return bar + (3 * S + p) * 8; };
-  auto through = [&](int p) { return bar + (3 * S + 2 + p) * 8; };
+  auto filled = [&](int slot) { return bar + slot * 8; };
+  auto is_free = [&](int slot) { return bar + (S + slot) * 8; };
+  auto a_in = [&](int p) { return bar + (2 * S + p) * 8; };
+  auto through = [&](int p) { return bar + (2 * S + 2 + p) * 8; };
 
   if (tid == 0) {
     failed = 0;
-    for (int i = 0; i < 3 * S + 4; i++) {
-      const int n = i < 2 * S ? 1 : i < 3 * S + 2 ? 4 : 1;
+    for (int i = 0; i < 2 * S + 4; i++) {
+      const int n = i < S || i >= 2 * S + 2 ? 1 : 4;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar + i * 8), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -254,51 +259,40 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
   float acc[N];
   if (warp == 4) {
     // ---- copies: x (rows of 128 bytes, 16-byte pieces exchanged by row), codes and scales
-    constexpr int kLag = 3;  // stages of x in flight
-    for (int i = 0; i < count + kLag; i++) {
-      if (i < count) {
-        const int slot = i % S, blk = b0 + i;
-        if (i >= S) good = good && wait_bar(is_free(slot), (i / S - 1) & 1);
+    int slot = 0, round = 0;
+    for (int i = 0; i < count; i++) {
+      const int blk = b0 + i;
+      if (round) good = good && wait_bar(is_free(slot), (round - 1) & 1);
+      if (elected()) {
         const uint32_t dst = ring_at + slot * kSize;
-        if (lane == 0) {
-          constexpr uint32_t bytes = kCodes + kParts * kM * kScale;
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(codes_in(slot)), "n"(bytes) : "memory");
-          const int grp = SUB ? blk * 2 : blk * kBlock >> a.group_log;
-          copy_bulk(dst + N * 128, a.codes + ((int64_t)tile * a.blocks + blk) * kCodes, kCodes, codes_in(slot));
-          copy_bulk(dst + N * 128 + kCodes, a.scales + ((int64_t)tile * a.groups_p + grp) * (kM * kScale),
-                    kParts * kM * kScale, codes_in(slot));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < N / 4; j++) {
-          const int piece = lane + j * 32, r = piece / 8, c = piece % 8;
-          const bool ok = row0 + r < a.rows && blk * kBlock + c * 8 < a.k;
-          copy16(dst + r * 128 + ((c ^ (r & 7)) * 16),
-                 reinterpret_cast<const T*>(a.x) + (ok ? (row0 + r) * a.sx + blk * kBlock + c * 8 : 0), ok);
-        }
+        constexpr uint32_t bytes = N * 128 + kCodes + kParts * kM * kScale;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(filled(slot)), "n"(bytes) : "memory");
+        const int grp = SUB ? blk * 2 : blk * kBlock >> a.group_log;
+        copy_bulk(dst + N * 128, a.codes + ((int64_t)tile * a.blocks + blk) * kCodes, kCodes, filled(slot));
+        copy_bulk(dst + N * 128 + kCodes, a.scales + ((int64_t)tile * a.groups_p + grp) * (kM * kScale),
+                  kParts * kM * kScale, filled(slot));
+        // (zeros come for rows and k past x's ends)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(&x_map), "r"(blk * kBlock), "r"(row0), "r"(filled(slot))
+            : "memory");
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i >= kLag) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive(x_in((i - kLag) % S));
-      }
+      __syncwarp();
+      if (++slot == S) slot = 0, round++;
     }
     // nothing may be on its way when the CTA ends
-    for (int i = count > S ? count - S : 0; i < count; i++) good = good && wait_bar(codes_in(i % S), (i / S) & 1);
+    for (int i = count > S ? count - S : 0; i < count; i++) good = good && wait_bar(filled(i % S), (i / S) & 1);
   } else if (warp == 5) {
     // ---- products.  kind::f16: fp32 sums, both operands T with k innermost, N columns, 128 rows
     constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
     constexpr uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | (uint32_t)(kM / 16) << 24;
     // x: rows of 128 bytes, groups of eight rows 1024 bytes apart, pieces exchanged within 128 bytes
     const uint64_t desc0 = (uint64_t)(ring_at >> 4 & 0x3fffu) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-    int sum = 0;
+    int sum = 0, slot = 0, phase = 0;
     bool begins = true;
     for (int i = 0; i < count; i++) {
-      const int slot = i % S, p = i & 1, blk = b0 + i;
-      good = good && wait_bar(x_in(slot), (i / S) & 1);
-      good = good && wait_bar(a_in(p), (i / 2) & 1);
+      const int p = i & 1, blk = b0 + i;
+      good = good && wait_bar(filled(slot), phase) && wait_bar(a_in(p), (i / 2) & 1);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint64_t desc = desc0 + (uint64_t)(slot * (kSize >> 4));
       if (elected()) {
@@ -313,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
       __syncwarp();
       begins = SUB || ((blk + 1) * kBlock & ((1 << a.group_log) - 1)) == 0;
       if (begins) sum ^= 1;
+      if (++slot == S) slot = 0, phase ^= 1;
     }
   } else {
     // ---- codes into the operand type; the groups' sums, scaled
@@ -330,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
       }
     };
     if (FOLD && !ZERO) tmem_fill8(mine + 64, pack2<T>(-1.5f, -1.5f));
-    int slot = 0, phase = 0, sum = 0;
+    int slot = 0, phase = 0, sum = 0, old = 0;
     bool begins = true;
     // of the two stages before: where a group ended, and its scale
     int end0 = -1, end1 = -1;
@@ -339,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
       const int p = i & 1;
       if (i >= 2) {  // the products of the stage before the last one are through: its slot and A are free
         good = good && wait_bar(through(p), (i / 2 - 1) & 1);
-        if (lane == 0) arrive(is_free((i - 2) % S));
+        if (lane == 0) arrive(is_free(old));
+        if (++old == S) old = 0;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (end >= 0) {
 #pragma unroll
@@ -348,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
       }
       end = -1;
       if (i >= count) return;
-      good = good && wait_bar(codes_in(slot), phase);
+      good = good && wait_bar(filled(slot), phase);
       const unsigned char* stage = ring + slot * kSize;
       float s_one[kParts], rest[kParts];
       uint32_t one[kParts];
@@ -384,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
 #pragma unroll
         for (int h = 0; h < kParts; h++) some = some || !(rest[h] == 0.f);
         if (__any_sync(0xffffffffu, some)) {
-          good = good && wait_bar(x_in(slot), phase);
 #pragma unroll
           for (int j = 0; j < N; j++) {
             float t[kParts] = {};
@@ -423,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
     for (int i = 0; i < N; i++) acc[i] = __int_as_float(0x7fffffff);
   }
 
-  const int n = tile * kM + tid;
-  auto write = [&](int r, float v) {
+  auto write = [&](int r, int n, float v) {
     if (row0 + r >= a.rows || n >= a.n) return;
     if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
     reinterpret_cast<T*>(a.y)[(row0 + r) * a.sy + n] = from_f32<T>(v);
@@ -432,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
   if (shares == 1) {
     if (warp < 4) {
 #pragma unroll
-      for (int i = 0; i < N; i++) write(i, acc[i]);
+      for (int i = 0; i < N; i++) write(i, tile * kM + tid, acc[i]);
     }
     return;
   }
@@ -443,22 +437,42 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>) matvec_kernel(con
   }
   cl.sync();
   if (warp < 4) {
-    for (int i = share; i < N && row0 + i < a.rows; i += shares) {
-      float v[kMaxCluster];
+    // a warp takes a row at a time, a lane four of its outputs
+    for (int i = share + warp * shares; i < N && row0 + i < a.rows; i += 4 * shares) {
+      float4 v[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; r++) v[r] = r < shares ? *cl.map_shared_rank(part + i * kM + tid, r) : 0.f;
-      float all = v[0];
+      for (int r = 0; r < kMaxCluster; r++)
+        v[r] = r < shares ? *cl.map_shared_rank(reinterpret_cast<float4*>(part + i * kM) + lane, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 all = v[0];
 #pragma unroll
-      for (int r = 1; r < kMaxCluster; r++) all += v[r];
-      write(i, all);
+      for (int r = 1; r < kMaxCluster; r++) all.x += v[r].x, all.y += v[r].y, all.z += v[r].z, all.w += v[r].w;
+      const float w[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) write(i, tile * kM + lane * 4 + j, w[j]);
     }
   }
   cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
+// x as the tensor cores' copies want it: boxes of N rows by 64 k
+CUresult map_x(CUtensorMap* map, const Args& a, CUtensorMapDataType type, int n) {
+  static const auto encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &how) != cudaSuccess)
+      fn = nullptr;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn);
+  }();
+  if (!encode) return CUDA_ERROR_NOT_SUPPORTED;
+  const cuuint64_t size[2] = {(cuuint64_t)a.k, (cuuint64_t)a.rows}, stride[1] = {(cuuint64_t)a.sx * 2};
+  const cuuint32_t box[2] = {kBlock, (cuuint32_t)n}, step[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(a.x), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 template <typename T, int N, bool SUB, bool ZERO>
-cudaError_t launch(const Args& a, cudaStream_t st) {
-  auto* fn = matvec_kernel<T, N, SUB, ZERO>;
+cudaError_t launch_wide(const Args& a, cudaStream_t st) {
+  auto* fn = matvec_wide<T, N, SUB, ZERO>;
   constexpr int smem = kSmem<N, SUB, ZERO>;
   static OpsOnce once;
   if (const int dev = ops_current(); !once(dev)) {
@@ -466,6 +480,10 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
+  CUtensorMap map;
+  if (map_x(&map, a, std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N) !=
+      CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   // k is shared among CTAs until there are several rounds of them, down to four
   // stages each in the first round and to sixteen after it
   const int rows = (a.rows + N - 1) / N;
@@ -484,20 +502,233 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, a);
+  return cudaLaunchKernelEx(&cfg, fn, a, map);
 }
 
 template <typename T, int N>
-cudaError_t by_group(const Args& a, bool zeros, cudaStream_t st) {
-  if (a.group_log == 5) return zeros ? launch<T, N, true, true>(a, st) : launch<T, N, true, false>(a, st);
-  return zeros ? launch<T, N, false, true>(a, st) : launch<T, N, false, false>(a, st);
+cudaError_t wide(const Args& a, bool zeros, cudaStream_t st) {
+  if (a.group_log == 5) return zeros ? launch_wide<T, N, true, true>(a, st) : launch_wide<T, N, true, false>(a, st);
+  return zeros ? launch_wide<T, N, false, true>(a, st) : launch_wide<T, N, false, false>(a, st);
+}
+
+// ---- few rows
+
+constexpr int kWarps = 8;
+// CTAs of a multiprocessor that the registers are held down for
+template <int NT>
+constexpr int kHeld = NT == 1 ? 4 : 3;
+
+// bytes of one stage of a warp's ring: the codes and scales of a block, of MT tiles
+template <int MT, bool SUB, bool ZERO>
+constexpr int kStage = MT * (512 + (SUB ? 2 : 1) * (ZERO ? 64 : 32));
+
+// A CTA takes MT tiles of 16 outputs by NT*8 rows at a time, and then the next
+// ones gridDim.x further on.  Its warps share the blocks of k among them (warp w
+// takes blocks w, w + kWarps, ...) and add up at the end, in warp order.  A warp
+// copies S blocks ahead, across the tiles' borders too, into a ring of its own
+// in shared memory.  K is permuted within the instructions' steps, alike on both
+// sides: lane (g, t) has k = 8 t .. 8 t + 7 of a half block, of outputs g and g + 8
+// and of row g of x.
+// SUB: groups of 32, two to a block; otherwise a group is whole blocks.
+template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
+__global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Args a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int kParts = SUB ? 2 : 1;      // scale groups of a block
+  constexpr int kSteps = 4 / kParts;       // matrix steps of a group
+  constexpr int kOut = MT * 16;
+  constexpr int kSize = kStage<MT, SUB, ZERO>, kScale = ZERO ? 4 : 2;
+  float* red = reinterpret_cast<float*>(smem + kWarps * S * kSize);  // [2][warp][row of x][kOut]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int row0 = blockIdx.y * (NT * 8), tile_step = gridDim.x * MT, tiles = (a.n + 15) / 16;
+
+  // rows of x past the last one read the last one; their results are dropped
+  const T* xp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; j++)
+    xp[j] = reinterpret_cast<const T*>(a.x) + (int64_t)min(row0 + j * 8 + g, a.rows - 1) * a.sx + t * 8;
+
+  // ---- copying ahead
+  const unsigned char* ring = smem + warp * (S * kSize);
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  int t_ahead = warp < a.blocks ? blockIdx.x * MT : tiles, b_ahead = warp, put = 0;
+  auto copy_next = [&]() {
+    if (t_ahead < tiles) {
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        const int tile = min(t_ahead + m, tiles - 1);  // a tile past the end repeats the last one
+        const uint32_t dst = ring_at + put * kSize;
+        copy16(dst + m * 512 + lane * 16,
+               a.codes + ((int64_t)(tile / 8) * a.blocks + b_ahead) * kCodes + lane / 16 * (kCodes / 2) +
+                   (tile % 8 * 16 + lane % 16) * 16, true);
+        if (lane < kParts * kScale) {
+          const int grp = SUB ? b_ahead * 2 + lane / kScale : b_ahead * kBlock >> a.group_log;
+          copy16(dst + MT * 512 + (m * kParts * kScale + lane) * 16,
+                 a.scales + ((int64_t)(tile / 8) * a.groups_p + grp) * (kM * kScale) + tile % 8 * (16 * kScale) +
+                     lane % kScale * 16, true);
+        }
+      }
+      b_ahead += kWarps;
+      if (b_ahead >= a.blocks) {
+        b_ahead = warp;
+        t_ahead += tile_step;
+      }
+      put = put + 1 == S ? 0 : put + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; i++) copy_next();
+
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[m][j][i] = 0.f;
+
+  int get = 0, buf = 0;
+  for (int tile0 = blockIdx.x * MT; tile0 < tiles; tile0 += tile_step) {
+    for (int blk = warp; blk < a.blocks; blk += kWarps) {
+      uint4 xv[NT][2];
+      const bool second = blk * 64 + 32 < a.k;  // k is whole halves of a block
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const uint4* p = reinterpret_cast<const uint4*>(xp[j] + blk * 64);
+        xv[j][0] = __ldg(p);
+        xv[j][1] = second ? __ldg(p + 4) : make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();
+      copy_next();
+      const unsigned char* stage = ring + get * kSize;
+      get = get + 1 == S ? 0 : get + 1;
+#pragma unroll
+      for (int part = 0; part < kParts; part++) {
+        float2 sc[MT], off[MT];  // 16 s and (8 - z) s of outputs g and g + 8
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          const unsigned char* at = stage + MT * 512 + ((m * kParts + part) * 16 + g) * kScale;
+          if (ZERO) {
+            const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at)),
+                         w = unpack2<T>(*reinterpret_cast<const uint32_t*>(at + 8 * kScale));
+            sc[m] = make_float2(v.x, w.x);
+            off[m] = make_float2(v.x * (8.f - v.y), w.x * (8.f - w.y));
+          } else {
+            sc[m] = make_float2(to_f32(*reinterpret_cast<const T*>(at)), to_f32(*reinterpret_cast<const T*>(at + 8 * kScale)));
+          }
+          sc[m].x *= 16.f;
+          sc[m].y *= 16.f;
+        }
+        if (ZERO) {
+#pragma unroll
+          for (int j = 0; j < NT; j++) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // every row is the same: columns 2t, 2t + 1
+#pragma unroll
+            for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
+              const uint32_t* xw = reinterpret_cast<const uint32_t*>(xv[j]) + 2 * s;
+              mma16816<T>(sum, kOnes<T>, kOnes<T>, kOnes<T>, kOnes<T>, xw[0], xw[1]);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; m++) {
+              acc[m][j][0] += off[m].x * sum[0];
+              acc[m][j][1] += off[m].x * sum[1];
+              acc[m][j][2] += off[m].y * sum[0];
+              acc[m][j][3] += off[m].y * sum[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          float d[NT][4];
+#pragma unroll
+          for (int j = 0; j < NT; j++) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+#pragma unroll
+          for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + m * 512 + s / 2 * 256 + g * 16) + t;
+            const uint32_t w0 = w[0], w8 = w[32];  // outputs g and g + 8
+            const uint32_t a0 = less2<T>(widen2<T>(w0, s % 2 * 2), kHalves<T>), a1 = less2<T>(widen2<T>(w8, s % 2 * 2), kHalves<T>);
+            const uint32_t a2 = less2<T>(widen2<T>(w0, s % 2 * 2 + 1), kHalves<T>),
+                           a3 = less2<T>(widen2<T>(w8, s % 2 * 2 + 1), kHalves<T>);
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+              const uint32_t* xw = reinterpret_cast<const uint32_t*>(xv[j]) + 2 * s;
+              mma16816<T>(d[j], a0, a1, a2, a3, xw[0], xw[1]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; j++) {
+            acc[m][j][0] += sc[m].x * d[j][0];
+            acc[m][j][1] += sc[m].x * d[j][1];
+            acc[m][j][2] += sc[m].y * d[j][2];
+            acc[m][j][3] += sc[m].y * d[j][3];
+          }
+        }
+      }
+    }
+    // two buffers in turn: a warp can be one tile ahead of the others' reads
+    float* part = red + buf * (kWarps * NT * 8 * kOut);
+    float* mine = part + warp * (NT * 8 * kOut);
+    buf ^= 1;
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          mine[(j * 8 + 2 * t + (i & 1)) * kOut + m * 16 + g + (i >> 1) * 8] = acc[m][j][i];
+          acc[m][j][i] = 0.f;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 8 * kOut; i += kWarps * 32) {
+      const int r = row0 + i / kOut, n = tile0 * 16 + i % kOut;
+      if (r >= a.rows || n >= a.n) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) v += part[w * (NT * 8 * kOut) + i];
+      if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
+      reinterpret_cast<T*>(a.y)[r * a.sy + n] = from_f32<T>(v);
+    }
+  }
+}
+
+template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
+cudaError_t launch_narrow(const Args& a, cudaStream_t st) {
+  constexpr int smem = kWarps * S * kStage<MT, SUB, ZERO> + 2 * kWarps * NT * 8 * MT * 16 * (int)sizeof(float);
+  auto* fn = matvec_narrow<T, MT, NT, S, SUB, ZERO>;
+  static OpsOnce once;
+  static int resident = 1;  // CTAs of a multiprocessor
+  if (const int dev = ops_current(); !once(dev)) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int v = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps * 32, smem);
+    if (e != cudaSuccess) return e;
+    resident = v > 0 ? v : 1;
+    once.set(dev);
+  }
+  const int rows = (a.rows + NT * 8 - 1) / (NT * 8), tiles = ((a.n + 15) / 16 + MT - 1) / MT;
+  const int most = (resident * ops_sm_count() + rows - 1) / rows;
+  fn<<<dim3(tiles < most ? tiles : most, rows), kWarps * 32, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int MT, int NT, int S>
+cudaError_t narrow(const Args& a, bool zeros, cudaStream_t st) {
+  if (a.group_log == 5)
+    return zeros ? launch_narrow<T, MT, NT, S, true, true>(a, st) : launch_narrow<T, MT, NT, S, true, false>(a, st);
+  return zeros ? launch_narrow<T, MT, NT, S, false, true>(a, st) : launch_narrow<T, MT, NT, S, false, false>(a, st);
 }
 
 template <typename T>
 cudaError_t by_rows(const Args& a, bool zeros, cudaStream_t st) {
-  if (a.rows <= 16) return by_group<T, 16>(a, zeros, st);
-  if (a.rows <= 32) return by_group<T, 32>(a, zeros, st);
-  return by_group<T, 64>(a, zeros, st);
+  // two tiles of outputs share a CTA's loads of x where that leaves CTAs for
+  // every multiprocessor
+  const bool two = (a.n + 15) / 16 >= 4 * ops_sm_count();
+  if (a.rows <= 8) return two ? narrow<T, 2, 1, 4>(a, zeros, st) : narrow<T, 1, 1, 8>(a, zeros, st);
+  if (a.rows <= 16) return two ? narrow<T, 2, 2, 4>(a, zeros, st) : narrow<T, 1, 2, 8>(a, zeros, st);
+  if (a.rows <= 32) return wide<T, 32>(a, zeros, st);
+  return wide<T, 64>(a, zeros, st);
 }
 
 struct Sizes {
@@ -579,8 +810,8 @@ extern "C" int wfst_matvec_quant(const wfst_matvec_args* r, void* stream) {
   if (!r->packed || !r->x || !r->y) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: NULL argument");
   if (!aligned(r->packed, 16) || !aligned(r->x, 16) || (r->rows > 1 && r->stride_x % 8))
     return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: packed and the rows of x must be 16-byte aligned");
-  if (r->rows > 1 && (r->stride_x < 0 || r->stride_y < r->n))
-    return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: stride_y must be >= n and stride_x >= 0");
+  if (r->rows > 1 && (r->stride_x < r->k || r->stride_y < r->n))
+    return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: stride_x must be >= k and stride_y >= n");
   if (r->rows > 65535 * 64) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: too many rows");
   const int dev = ops_device(r->device, {r->packed, r->x, r->bias, r->y});
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "matvec_quant: every array must be device memory of one device");
