@@ -4,33 +4,30 @@
 //
 // c are codes 0..15, G the group size, z = 8 where no zero points are given.
 // A pass has to read the codes (N*K/2 bytes) and the scales; x and y are small
-// beside them, so HBM bounds it up to some tens of rows.
-//
-// The products run on the tensor cores with the weights as the M side: a CTA
-// takes 128 outputs, and 128 of its threads one each.  Such a thread brings its
-// output's codes into the operand type and stores them to tensor memory as its
-// row of A; x is B, from shared memory; a group's sums are read back, scaled and
-// added up in registers in fp32, so nothing is rounded before y.  A fifth warp
-// copies ahead, a sixth one issues the products; they meet through mbarriers.
-//   - What it costs to bring codes into the type is the next bound after HBM, so
-//     a code is not converted but put in place: as the upper four bits of a
-//     mantissa it makes the 16-bit number 1 + c / 16, one shift and one logical
-//     operation for two codes.
-//   - The 1 + z / 16 too much is taken off by the tensor cores, which have time:
-//     a second product of the same x with -(1 + z / 16) in every column of A
-//     goes into the same fp32 sum, whose terms are then about five times those
-//     of sum x (c - z) / 16.  Where tensor memory has no room for it (groups of
-//     32, 17 to 32 rows), the threads subtract, exactly.  Both hold for whole z;
-//     what z has beside its whole part is added as s * rest * sum x.
-//   - mma.sync instructions for the same work, fed from registers, came to half
-//     of HBM's rate at 8 rows (8 x 131072 x 4096: 80 us) and were bound by the
-//     tensor cores' older path from 32 rows on.
-// A non-finite x makes its row of y NaN.
+// beside them.  HBM would bound it up to some tens of rows; what it costs to
+// bring the codes into the type is the bound that is met before that.  So a code
+// is not converted but put in place: as the upper four bits of a mantissa it
+// makes the 16-bit number 1 + c / 16, one shift and one logical operation for
+// two codes.  A group's sums are in fp32, scaled and added up in fp32, so nothing
+// is rounded before y.  Two kernels, by the number of rows:
+//   - Few rows: mma.sync fed from registers, eight warps sharing k.  1 x 4096 x
+//     4096 takes 4.6 us, 8 x 131072 x 4096 77 us (3.6 TB/s; the floor is 41).
+//   - Many rows: tcgen05, the weights widened once into tensor memory by one
+//     thread per output, x from shared memory.  64 x 32768 x 4096 takes 41 us,
+//     64 x 65536 x 8192 147 us (1.9 TB/s).
+// The first one's work goes with the rows, the second one's hardly does, but it
+// starts and ends more slowly (barriers, tensor memory, a cluster's sum): 16 x
+// 4096 x 4096 is 6.4 against 10.5 us, 32 x 16384 x 4096 32 against 21.  Up to 16
+// rows the first one is taken, and above where its CTAs fit on the device at
+// once: 64 x 1024 x 4096 is 6.3 against 8.1 us, 32 x 4096 x 4096, which does not
+// fit, 11.3 against 10.5, 24 x 5000 x 1056 7.6 against 7.0.
 //
 // Layout ("packed", made once by wfst_quant_pack): tiles of 128 outputs, in them
-// blocks of 64 k, in them two halves of 32 k with 16 bytes per output, so that a
-// warp copies 512 consecutive bytes.  Word q of an output's block holds k = 8 q
-// .. 8 q + 7 as four pairs.
+// blocks of 64 k, in them eight parts of 16 outputs with 512 bytes each: 16 bytes
+// for (t, g), t = 0..3, g = 0..7, hold the codes of outputs g and g + 8 for k = 8 t
+// .. 8 t + 7 of either half of the block, a word each (first half g, g + 8, second
+// half g, g + 8).  A warp of the one kernel reads 512 consecutive bytes with that,
+// a thread of the other one four times 16 bytes without bank conflicts.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -65,9 +62,9 @@ __global__ void pack_codes(const uint8_t* __restrict__ codes, int64_t n, int64_t
                            uint32_t* __restrict__ out) {
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step) {
-    const int q = (int)(i & 3) + (int)(i >> 9 & 1) * 4;  // words 0-3 in the first half, 4-7 in the second
+    const int hi = (int)(i & 1), half = (int)(i >> 1 & 1), g = (int)(i >> 2 & 7), t = (int)(i >> 5 & 3), part = (int)(i >> 7 & 7);
     const int64_t blk = (i >> 10) % blocks, tile = (i >> 10) / blocks;
-    const int64_t row = tile * kM + (i >> 2 & (kM - 1)), k0 = blk * kBlock + q * 8;
+    const int64_t row = tile * kM + part * 16 + hi * 8 + g, k0 = blk * kBlock + half * 32 + t * 8;
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -80,16 +77,18 @@ __global__ void pack_codes(const uint8_t* __restrict__ codes, int64_t n, int64_t
   }
 }
 
-// Scales of a tile and group: one per output, with zero points {s, z}; zero
-// scales past the edge.
+// Scales of a tile and group: for each part of 16 outputs and g = 0..7 {s[g],
+// s[g + 8]}, with zero points {s[g], s[g + 8], z[g], z[g + 8]}; zero scales past
+// the edge.
 __global__ void pack_scales(const uint16_t* __restrict__ scales, const uint16_t* __restrict__ zeros, int64_t n,
                             int64_t groups, int64_t groups_p, int64_t count, uint16_t* __restrict__ out) {
-  const int per = zeros ? 2 : 1;
+  const int per = zeros ? 4 : 2;
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += step) {
-    const int64_t row_in = i / per % kM, grp = i / (per * kM) % groups_p, row = i / (per * kM) / groups_p * kM + row_in;
+    const int j = (int)(i % per), g = (int)(i / per % 8), part = (int)(i / (per * 8) % 8);
+    const int64_t grp = i / (per * 64) % groups_p, row = i / (per * 64) / groups_p * kM + part * 16 + (j & 1) * 8 + g;
     uint16_t v = 0;
-    if (row < n && grp < groups) v = (i % per ? zeros : scales)[row * groups + grp];
+    if (row < n && grp < groups) v = (j < 2 ? scales : zeros)[row * groups + grp];
     out[i] = v;
   }
 }
@@ -106,10 +105,6 @@ struct Args {
 
 // ---- instructions
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  const int n = ok ? 16 : 0;  // 0: sixteen zero bytes
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kSpins; i++) {
@@ -183,7 +178,23 @@ __device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// ---- many rows: sizes that go with N rows of x (32 or 64) and groups of 32 (SUB)
+// ---- many rows
+//
+// A CTA takes 128 outputs, and 128 of its threads one each.  Such a thread stores
+// its output's codes to tensor memory as its row of A; x is B; a group's sums are
+// read back and scaled by the same thread.  A fifth warp copies ahead, a sixth
+// one issues the products; they meet through mbarriers, every wait with a limit.
+// The 1 + z / 16 too much is taken off by the tensor cores, which have time: a
+// second product of the same x with -(1 + z / 16) in every column of A goes into
+// the same fp32 sum, whose terms are then about five times those of sum x (c - z)
+// / 16 (at 64 rows 6% faster than subtracting).  Where tensor memory has no room
+// for it (groups of 32, 17 to 32 rows), the threads subtract, exactly.  Both hold
+// for whole z; what z has beside its whole part is added as s * rest * sum x.
+// What bounds it is the chain of a stage (wait, widen, store, product, read back)
+// and the instructions in it, not HBM.  A non-finite x can make NaN of a sum that
+// would be infinite, in its own row of y only.
+//
+// Sizes that go with N rows of x (32 or 64) and groups of 32 (SUB):
 
 // whether the tensor cores take off 1 + z / 16
 template <int N, bool SUB>
@@ -200,10 +211,11 @@ template <int N>
 constexpr int kStages = N == 64 ? 7 : 6;
 template <int N, bool SUB, bool ZERO>
 constexpr int kSlot = (N * 128 + kCodes + (SUB ? 2 : 1) * kM * (ZERO ? 4 : 2) + 1023) / 1024 * 1024;
-// CTAs of a multiprocessor: what its 512 columns hold, and no more, since one
-// that waits for columns would hold up its cluster; shared memory sees to it
+// CTAs of a multiprocessor: what its 512 columns (and, at N = 32, its registers)
+// hold, and no more, since one that waits for columns would hold up its cluster;
+// shared memory sees to it
 template <int N, bool SUB>
-constexpr int kResident = 512 / kColumns<N, SUB>;
+constexpr int kResident = N == 32 && !SUB ? 3 : 512 / kColumns<N, SUB>;
 template <int N, bool SUB, bool ZERO>
 constexpr int kSmem = 1024 + (kStages<N> * kSlot<N, SUB, ZERO> > 233472 / (kResident<N, SUB> + 1)
                                   ? kStages<N> * kSlot<N, SUB, ZERO>
@@ -350,23 +362,28 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
       uint32_t one[kParts];
 #pragma unroll
       for (int h = 0; h < kParts; h++) {
-        const unsigned char* at = stage + N * 128 + kCodes + (h * kM + tid) * kScale;
+        // {s[g], s[g + 8]} or {s[g], s[g + 8], z[g], z[g + 8]}
+        const T* at = reinterpret_cast<const T*>(stage + N * 128 + kCodes + h * kM * kScale) +
+                      (tid / 16 * 8 + tid % 8) * kScale + tid / 8 % 2;
+        s_one[h] = to_f32(at[0]);
         rest[h] = 0.f;
         one[h] = pack2<T>(1.5f, 1.5f);
         if (ZERO) {
-          const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at));
-          const float whole = fminf(fmaxf(rintf(v.y), 0.f), 15.f);
-          s_one[h] = v.x;
-          rest[h] = whole - v.y;
+          const float z = to_f32(at[2]), whole = fminf(fmaxf(rintf(z), 0.f), 15.f);
+          rest[h] = whole - z;
           one[h] = pack2<T>(1.f + whole * 0.0625f, 1.f + whole * 0.0625f);
-        } else {
-          s_one[h] = to_f32(*reinterpret_cast<const T*>(at));
         }
         scale[h] = 16.f * s_one[h];
       }
-      const uint4* words = reinterpret_cast<const uint4*>(stage + N * 128) + tid;
-      const uint4 w0 = words[0], w1 = words[kM];
-      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const uint4* words = reinterpret_cast<const uint4*>(stage + N * 128 + tid / 16 * 512) + tid % 8;
+      const bool upper = tid / 8 % 2;
+      uint32_t w[8];
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+        const uint4 v = words[t * 8];
+        w[t] = upper ? v.y : v.x;
+        w[4 + t] = upper ? v.w : v.z;
+      }
       uint32_t r[32];
 #pragma unroll
       for (int j = 0; j < 32; j++) {
@@ -484,13 +501,18 @@ cudaError_t launch_wide(const Args& a, cudaStream_t st) {
   if (map_x(&map, a, std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N) !=
       CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  // k is shared among CTAs until there are several rounds of them, down to four
-  // stages each in the first round and to sixteen after it
+  // k is shared among as many CTAs as cost least: rounds of CTAs times the stages
+  // of one, its start and end taking about as long as kEnds stages (64 x 5000 x
+  // 1056 9 us, without it, split as far as CTAs fit, 15; 64 x 32768 x 4096 41, 50)
+  constexpr int kEnds = 7;
   const int rows = (a.rows + N - 1) / N;
-  int shares = 1;
   const int64_t slots = (int64_t)ops_sm_count() * kResident<N, SUB>, ctas = (int64_t)a.tiles * rows;
-  while (shares < kMaxCluster && ctas * shares < 4 * slots && a.blocks >= shares * 2 * (ctas * shares < slots ? 4 : 16))
-    shares *= 2;
+  int shares = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= kMaxCluster && s <= a.blocks; s++) {
+    const int64_t cost = (ctas * s + slots - 1) / slots * ((a.blocks + s - 1) / s + kEnds);
+    if (cost < least) least = cost, shares = s;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.tiles * shares, rows);
   cfg.blockDim = dim3(kThreads);
@@ -514,71 +536,32 @@ cudaError_t wide(const Args& a, bool zeros, cudaStream_t st) {
 // ---- few rows
 
 constexpr int kWarps = 8;
-// CTAs of a multiprocessor that the registers are held down for
-template <int NT>
-constexpr int kHeld = NT == 1 ? 4 : 3;
+// CTAs of a multiprocessor that the registers are held down for: 8 x 32768 x 4096
+// in groups of 32 with zero points 28 us; at three the registers spill, 39
+constexpr int kHeld = 2;
 
-// bytes of one stage of a warp's ring: the codes and scales of a block, of MT tiles
-template <int MT, bool SUB, bool ZERO>
-constexpr int kStage = MT * (512 + (SUB ? 2 : 1) * (ZERO ? 64 : 32));
+__device__ __forceinline__ uint32_t first_of(uint32_t v) { return v; }
+__device__ __forceinline__ uint32_t first_of(uint2 v) { return v.x; }
+__device__ __forceinline__ uint32_t second_of(uint32_t) { return 0; }
+__device__ __forceinline__ uint32_t second_of(uint2 v) { return v.y; }
 
-// A CTA takes MT tiles of 16 outputs by NT*8 rows at a time, and then the next
-// ones gridDim.x further on.  Its warps share the blocks of k among them (warp w
-// takes blocks w, w + kWarps, ...) and add up at the end, in warp order.  A warp
-// copies S blocks ahead, across the tiles' borders too, into a ring of its own
-// in shared memory.  K is permuted within the instructions' steps, alike on both
-// sides: lane (g, t) has k = 8 t .. 8 t + 7 of a half block, of outputs g and g + 8
-// and of row g of x.
+// One CTA: MT parts of 16 outputs by NT*8 rows; its warps share the blocks of k
+// among them (warp w takes blocks w, w + kWarps, ...) and add up at the end, in
+// warp order.  A warp loads the codes and scales of U blocks while it works on the
+// U before.  (Copies into a ring in shared memory, and CTAs that stay and load
+// across the parts' ends, took 10 to 20% longer: the instructions count.)  K is
+// permuted within the instructions' steps, alike on both sides: lane (g, t) has k
+// = 8 t .. 8 t + 7 of a half block, of outputs g and g + 8 and of row g of x.
 // SUB: groups of 32, two to a block; otherwise a group is whole blocks.
-template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
-__global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Args a) {
-  extern __shared__ __align__(16) unsigned char smem[];
+template <typename T, int MT, int NT, int U, bool SUB, bool ZERO>
+__global__ void __launch_bounds__(kWarps * 32, kHeld) matvec_narrow(const Args a) {
+  extern __shared__ float red[];  // [warp][row of x][kOut]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int part0 = blockIdx.x * MT, row0 = blockIdx.y * (NT * 8), parts = (a.n + 15) / 16;
   constexpr int kParts = SUB ? 2 : 1;      // scale groups of a block
   constexpr int kSteps = 4 / kParts;       // matrix steps of a group
   constexpr int kOut = MT * 16;
-  constexpr int kSize = kStage<MT, SUB, ZERO>, kScale = ZERO ? 4 : 2;
-  float* red = reinterpret_cast<float*>(smem + kWarps * S * kSize);  // [2][warp][row of x][kOut]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int row0 = blockIdx.y * (NT * 8), tile_step = gridDim.x * MT, tiles = (a.n + 15) / 16;
-
-  // rows of x past the last one read the last one; their results are dropped
-  const T* xp[NT];
-#pragma unroll
-  for (int j = 0; j < NT; j++)
-    xp[j] = reinterpret_cast<const T*>(a.x) + (int64_t)min(row0 + j * 8 + g, a.rows - 1) * a.sx + t * 8;
-
-  // ---- copying ahead
-  const unsigned char* ring = smem + warp * (S * kSize);
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  int t_ahead = warp < a.blocks ? blockIdx.x * MT : tiles, b_ahead = warp, put = 0;
-  auto copy_next = [&]() {
-    if (t_ahead < tiles) {
-#pragma unroll
-      for (int m = 0; m < MT; m++) {
-        const int tile = min(t_ahead + m, tiles - 1);  // a tile past the end repeats the last one
-        const uint32_t dst = ring_at + put * kSize;
-        copy16(dst + m * 512 + lane * 16,
-               a.codes + ((int64_t)(tile / 8) * a.blocks + b_ahead) * kCodes + lane / 16 * (kCodes / 2) +
-                   (tile % 8 * 16 + lane % 16) * 16, true);
-        if (lane < kParts * kScale) {
-          const int grp = SUB ? b_ahead * 2 + lane / kScale : b_ahead * kBlock >> a.group_log;
-          copy16(dst + MT * 512 + (m * kParts * kScale + lane) * 16,
-                 a.scales + ((int64_t)(tile / 8) * a.groups_p + grp) * (kM * kScale) + tile % 8 * (16 * kScale) +
-                     lane % kScale * 16, true);
-        }
-      }
-      b_ahead += kWarps;
-      if (b_ahead >= a.blocks) {
-        b_ahead = warp;
-        t_ahead += tile_step;
-      }
-      put = put + 1 == S ? 0 : put + 1;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < S - 1; i++) copy_next();
-
+  using Scale = std::conditional_t<ZERO, uint2, uint32_t>;  // scales (and zero points) of outputs g, g + 8
   float acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; m++)
@@ -587,35 +570,71 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Ar
 #pragma unroll
       for (int i = 0; i < 4; i++) acc[m][j][i] = 0.f;
 
-  int get = 0, buf = 0;
-  for (int tile0 = blockIdx.x * MT; tile0 < tiles; tile0 += tile_step) {
-    for (int blk = warp; blk < a.blocks; blk += kWarps) {
+  // rows of x past the last one read the last one; their results are dropped
+  const T* xp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; j++)
+    xp[j] = reinterpret_cast<const T*>(a.x) + (int64_t)min(row0 + j * 8 + g, a.rows - 1) * a.sx + t * 8;
+  const uint4* cp[MT];
+  const Scale* sp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; m++) {
+    const int part = min(part0 + m, parts - 1);  // one past the end repeats the last one
+    cp[m] = reinterpret_cast<const uint4*>(a.codes) + ((int64_t)(part / 8) * a.blocks * 8 + part % 8) * 32 + t * 8 + g;
+    sp[m] = reinterpret_cast<const Scale*>(a.scales) + ((int64_t)(part / 8) * a.groups_p * 8 + part % 8) * 8 + g;
+  }
+
+  uint4 next[U][MT];
+  Scale next_s[U][MT][kParts];
+  auto load = [&](int b0) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int blk = b0 + u * kWarps;
+      if (blk < a.blocks) {
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          next[u][m] = __ldcs(cp[m] + (int64_t)blk * 256);
+#pragma unroll
+          for (int p = 0; p < kParts; p++)
+            next_s[u][m][p] = __ldg(sp[m] + (int64_t)(SUB ? blk * 2 + p : blk * kBlock >> a.group_log) * 64);
+        }
+      }
+    }
+  };
+  load(warp);
+  for (int b0 = warp; b0 < a.blocks; b0 += U * kWarps) {
+    uint4 c[U][MT];
+    Scale cs[U][MT][kParts];
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        c[u][m] = next[u][m];
+#pragma unroll
+        for (int p = 0; p < kParts; p++) cs[u][m][p] = next_s[u][m][p];
+      }
+    load(b0 + U * kWarps);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int blk = b0 + u * kWarps;
+      if (blk >= a.blocks) break;
       uint4 xv[NT][2];
-      const bool second = blk * 64 + 32 < a.k;  // k is whole halves of a block
+      const bool second = blk * kBlock + 32 < a.k;  // k is whole halves of a block
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        const uint4* p = reinterpret_cast<const uint4*>(xp[j] + blk * 64);
+        const uint4* p = reinterpret_cast<const uint4*>(xp[j] + blk * kBlock);
         xv[j][0] = __ldg(p);
         xv[j][1] = second ? __ldg(p + 4) : make_uint4(0, 0, 0, 0);
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-      __syncwarp();
-      copy_next();
-      const unsigned char* stage = ring + get * kSize;
-      get = get + 1 == S ? 0 : get + 1;
 #pragma unroll
-      for (int part = 0; part < kParts; part++) {
+      for (int p = 0; p < kParts; p++) {
         float2 sc[MT], off[MT];  // 16 s and (8 - z) s of outputs g and g + 8
 #pragma unroll
         for (int m = 0; m < MT; m++) {
-          const unsigned char* at = stage + MT * 512 + ((m * kParts + part) * 16 + g) * kScale;
+          sc[m] = unpack2<T>(first_of(cs[u][m][p]));
           if (ZERO) {
-            const float2 v = unpack2<T>(*reinterpret_cast<const uint32_t*>(at)),
-                         w = unpack2<T>(*reinterpret_cast<const uint32_t*>(at + 8 * kScale));
-            sc[m] = make_float2(v.x, w.x);
-            off[m] = make_float2(v.x * (8.f - v.y), w.x * (8.f - w.y));
-          } else {
-            sc[m] = make_float2(to_f32(*reinterpret_cast<const T*>(at)), to_f32(*reinterpret_cast<const T*>(at + 8 * kScale)));
+            const float2 z = unpack2<T>(second_of(cs[u][m][p]));
+            off[m] = make_float2(sc[m].x * (8.f - z.x), sc[m].y * (8.f - z.y));
           }
           sc[m].x *= 16.f;
           sc[m].y *= 16.f;
@@ -625,7 +644,7 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Ar
           for (int j = 0; j < NT; j++) {
             float sum[4] = {0.f, 0.f, 0.f, 0.f};  // every row is the same: columns 2t, 2t + 1
 #pragma unroll
-            for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
+            for (int s = p * kSteps; s < (p + 1) * kSteps; s++) {
               const uint32_t* xw = reinterpret_cast<const uint32_t*>(xv[j]) + 2 * s;
               mma16816<T>(sum, kOnes<T>, kOnes<T>, kOnes<T>, kOnes<T>, xw[0], xw[1]);
             }
@@ -644,9 +663,8 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Ar
 #pragma unroll
           for (int j = 0; j < NT; j++) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
 #pragma unroll
-          for (int s = part * kSteps; s < (part + 1) * kSteps; s++) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + m * 512 + s / 2 * 256 + g * 16) + t;
-            const uint32_t w0 = w[0], w8 = w[32];  // outputs g and g + 8
+          for (int s = p * kSteps; s < (p + 1) * kSteps; s++) {
+            const uint32_t w0 = s / 2 ? c[u][m].z : c[u][m].x, w8 = s / 2 ? c[u][m].w : c[u][m].y;
             const uint32_t a0 = less2<T>(widen2<T>(w0, s % 2 * 2), kHalves<T>), a1 = less2<T>(widen2<T>(w8, s % 2 * 2), kHalves<T>);
             const uint32_t a2 = less2<T>(widen2<T>(w0, s % 2 * 2 + 1), kHalves<T>),
                            a3 = less2<T>(widen2<T>(w8, s % 2 * 2 + 1), kHalves<T>);
@@ -666,70 +684,58 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<NT>) matvec_narrow(const Ar
         }
       }
     }
-    // two buffers in turn: a warp can be one tile ahead of the others' reads
-    float* part = red + buf * (kWarps * NT * 8 * kOut);
-    float* mine = part + warp * (NT * 8 * kOut);
-    buf ^= 1;
+  }
+
+  float* mine = red + warp * (NT * 8 * kOut);
 #pragma unroll
-    for (int m = 0; m < MT; m++)
+  for (int m = 0; m < MT; m++)
 #pragma unroll
-      for (int j = 0; j < NT; j++)
+    for (int j = 0; j < NT; j++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          mine[(j * 8 + 2 * t + (i & 1)) * kOut + m * 16 + g + (i >> 1) * 8] = acc[m][j][i];
-          acc[m][j][i] = 0.f;
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 8 * kOut; i += kWarps * 32) {
-      const int r = row0 + i / kOut, n = tile0 * 16 + i % kOut;
-      if (r >= a.rows || n >= a.n) continue;
-      float v = 0.f;
+      for (int i = 0; i < 4; i++) mine[(j * 8 + 2 * t + (i & 1)) * kOut + m * 16 + g + (i >> 1) * 8] = acc[m][j][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * 8 * kOut; i += kWarps * 32) {
+    const int r = row0 + i / kOut, n = part0 * 16 + i % kOut;
+    if (r >= a.rows || n >= a.n) continue;
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; w++) v += part[w * (NT * 8 * kOut) + i];
-      if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
-      reinterpret_cast<T*>(a.y)[r * a.sy + n] = from_f32<T>(v);
-    }
+    for (int w = 0; w < kWarps; w++) v += red[w * (NT * 8 * kOut) + i];
+    if (a.bias) v += to_f32(reinterpret_cast<const T*>(a.bias)[n]);
+    reinterpret_cast<T*>(a.y)[r * a.sy + n] = from_f32<T>(v);
   }
 }
 
-template <typename T, int MT, int NT, int S, bool SUB, bool ZERO>
+template <typename T, int MT, int NT, int U, bool SUB, bool ZERO>
 cudaError_t launch_narrow(const Args& a, cudaStream_t st) {
-  constexpr int smem = kWarps * S * kStage<MT, SUB, ZERO> + 2 * kWarps * NT * 8 * MT * 16 * (int)sizeof(float);
-  auto* fn = matvec_narrow<T, MT, NT, S, SUB, ZERO>;
-  static OpsOnce once;
-  static int resident = 1;  // CTAs of a multiprocessor
-  if (const int dev = ops_current(); !once(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    int v = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, kWarps * 32, smem);
-    if (e != cudaSuccess) return e;
-    resident = v > 0 ? v : 1;
-    once.set(dev);
-  }
-  const int rows = (a.rows + NT * 8 - 1) / (NT * 8), tiles = ((a.n + 15) / 16 + MT - 1) / MT;
-  const int most = (resident * ops_sm_count() + rows - 1) / rows;
-  fn<<<dim3(tiles < most ? tiles : most, rows), kWarps * 32, smem, st>>>(a);
+  constexpr int smem = kWarps * NT * 8 * MT * 16 * (int)sizeof(float);
+  static_assert(smem <= 48 * 1024);
+  const dim3 grid(((a.n + 15) / 16 + MT - 1) / MT, (a.rows + NT * 8 - 1) / (NT * 8));
+  matvec_narrow<T, MT, NT, U, SUB, ZERO><<<grid, kWarps * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int MT, int NT, int S>
+template <typename T, int MT, int NT, int U>
 cudaError_t narrow(const Args& a, bool zeros, cudaStream_t st) {
   if (a.group_log == 5)
-    return zeros ? launch_narrow<T, MT, NT, S, true, true>(a, st) : launch_narrow<T, MT, NT, S, true, false>(a, st);
-  return zeros ? launch_narrow<T, MT, NT, S, false, true>(a, st) : launch_narrow<T, MT, NT, S, false, false>(a, st);
+    return zeros ? launch_narrow<T, MT, NT, U, true, true>(a, st) : launch_narrow<T, MT, NT, U, true, false>(a, st);
+  return zeros ? launch_narrow<T, MT, NT, U, false, true>(a, st) : launch_narrow<T, MT, NT, U, false, false>(a, st);
 }
 
 template <typename T>
 cudaError_t by_rows(const Args& a, bool zeros, cudaStream_t st) {
-  // two tiles of outputs share a CTA's loads of x where that leaves CTAs for
-  // every multiprocessor
-  const bool two = (a.n + 15) / 16 >= 4 * ops_sm_count();
-  if (a.rows <= 8) return two ? narrow<T, 2, 1, 4>(a, zeros, st) : narrow<T, 1, 1, 8>(a, zeros, st);
-  if (a.rows <= 16) return two ? narrow<T, 2, 2, 4>(a, zeros, st) : narrow<T, 1, 2, 8>(a, zeros, st);
+  const int64_t parts = ((int64_t)a.n + 15) / 16, room = (int64_t)kHeld * ops_sm_count();
+  if (a.rows <= 16 || parts * ((a.rows + 15) / 16) <= room) {
+    // two parts of outputs share a CTA's loads of x where that leaves CTAs for
+    // every place: 8 x 131072 x 4096 77 us, with one part 81
+    const bool two = parts >= 2 * room;
+    if (a.rows <= 8) return two ? narrow<T, 2, 1, 2>(a, zeros, st) : narrow<T, 1, 1, 4>(a, zeros, st);
+    return two ? narrow<T, 2, 2, 2>(a, zeros, st) : narrow<T, 1, 2, 4>(a, zeros, st);
+  }
   if (a.rows <= 32) return wide<T, 32>(a, zeros, st);
   return wide<T, 64>(a, zeros, st);
 }
+
+constexpr int32_t kMost = INT32_MAX - 256;  // rounded up to whole tiles they still fit an int
 
 struct Sizes {
   int64_t tiles, blocks, groups, groups_p, code_bytes, bytes;
@@ -737,7 +743,7 @@ struct Sizes {
 
 // NULL, or what is wrong with the matrix's sizes.
 const char* sizes(int32_t n, int32_t k, int32_t group, bool zeros, Sizes* s) {
-  if (n < 1 || k < 1) return "n and k must be >= 1";
+  if (n < 1 || k < 1 || n > kMost || k > kMost) return "n and k must be between 1 and 2^31 - 257";
   if (group != 32 && group != 64 && group != 128 && group != 256) return "group must be 32, 64, 128 or 256";
   if (k % group) return "k must be a multiple of group";
   s->tiles = ((int64_t)n + kM - 1) / kM;
@@ -752,16 +758,16 @@ const char* sizes(int32_t n, int32_t k, int32_t group, bool zeros, Sizes* s) {
 }  // namespace
 
 int ops_sm_count() {
-  static int count[64];
+  static std::atomic<int> count[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return 152;
-  if (!count[dev]) {
-    int v = 0;
+  int v = count[dev].load(std::memory_order_relaxed);
+  if (!v) {
     cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    count[dev] = v > 0 ? v : 152;
+    count[dev].store(v = v > 0 ? v : 152, std::memory_order_relaxed);
   }
-  return count[dev];
+  return v;
 }
 
 }  // namespace wfst

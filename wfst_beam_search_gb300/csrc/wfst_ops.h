@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <initializer_list>
 
@@ -53,9 +54,9 @@ struct OpsDevice {
 // What a kernel needs set up once per device (its shared memory size): the
 // flags of the devices where that is done.
 struct OpsOnce {
-  uint64_t done = 0;
-  bool operator()(int dev) const { return dev < 64 && (done >> dev & 1); }
-  void set(int dev) { done |= dev < 64 ? (uint64_t)1 << dev : 0; }
+  std::atomic<uint64_t> done{0};
+  bool operator()(int dev) const { return dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1); }
+  void set(int dev) { done.fetch_or(dev < 64 ? (uint64_t)1 << dev : 0, std::memory_order_release); }
 };
 
 // Multiprocessors of the current device (cached per device; 152 on GB300).
