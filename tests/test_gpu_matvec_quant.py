@@ -68,6 +68,32 @@ def test_against_64_bits(W, n, k, group, zeros, dtype):
             check(y, *reference(x, codes, scales, z, b), k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("zeros", ["none", "any", "whole"])
+@pytest.mark.parametrize("n,k,group", [(2449, 96, 32), (2600, 1056, 32), (2449, 640, 64), (2560, 1152, 128),
+                                       (3001, 768, 256)])
+def test_many_rows(W, n, k, group, zeros, dtype):
+    """Enough outputs and rows that the weights are widened once for all rows;
+    rows that are not finite stay in their rows."""
+    codes, scales, z = matrix(n + k, n, k, group, zeros != "none", dtype)
+    if zeros == "whole":
+        z = z.round()
+    w = W.pack_quant(codes, scales, z)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    for rows in (17, 32, 33, 50, 64, 65, 200):
+        x = torch.randn(rows, k + 8, generator=g, device="cuda").to(dtype)[:, :k]
+        y = W.matvec_quant(x, w)
+        check(y, *reference(x, codes, scales, z, None), k)
+        assert torch.equal(W.matvec_quant(x, w), y)
+        x[rows // 2, k - 1] = float("inf")
+        x[0, 0] = float("nan")
+        other = W.matvec_quant(x, w)
+        whole = [r for r in range(rows) if r not in (0, rows // 2)]
+        assert torch.equal(other[whole], y[whole])
+        assert bool(other[0].isnan().all())
+
+
 def test_strides_streams_and_repeats(W):
     """Rows of a wider tensor in, rows of a wider tensor out, another stream,
     and the same bits every time."""

@@ -1,0 +1,135 @@
+"""The second pass: the operators together, against the same model in 64 bits.
+
+Tolerance, of a row of logits by its norm: with u = 2^-11 a layer rounds some
+14 times by u of its vector; q and k, off by 3 u each, move a score (at most
+sqrt(d) in size times the gains, d = 64, the heads being normed) by 6 u sqrt(d)
+and a weight of the softmax by twice that, 96 u.  110 u for each of two layers, doubled for what
+later layers make of it.  A wrong head, place or page is off by the whole
+norm."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+LIMIT = 2 * 2 * 110 * 2.0 ** -11
+
+
+@pytest.fixture(scope="module")
+def P():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import wfst_beam_search_gb300 as W
+    W.load()
+    from wfst_beam_search_gb300 import second_pass
+    return second_pass
+
+
+def shape(P, **more):
+    return P.Shape(**{**dict(vocab=777, width=128, layers=2, q_heads=6, kv_heads=2, head_dim=64, hidden=160, group=32),
+                      **more})
+
+
+def norm(x, eps):
+    return x / (x.square().mean(-1, keepdim=True) + eps).sqrt()
+
+
+def plain(P, s, tensors, tokens):
+    """Logits in 64 bits of one lane's tokens, one after the other."""
+    def take(name):
+        t = tensors[name]
+        if t.dim() == 1 or name == "embed":
+            return t.half().double()
+        codes, scales = P.quantize(t, s.group, torch.float16)
+        c = torch.stack([codes & 15, codes >> 4], 2).reshape(t.shape).double()
+        return (c - 8) * scales.double().repeat_interleave(s.group, 1)
+
+    n, d, hq, hkv = len(tokens), s.head_dim, s.q_heads, s.kv_heads
+    angle = torch.arange(n).double()[:, None] * s.base ** (-torch.arange(0, d, 2).double() / d)
+
+    def turn(x):
+        a, b = x[..., :d // 2], x[..., d // 2:]
+        c, t = angle.cos()[:, None], angle.sin()[:, None]
+        return torch.cat([a * c - b * t, b * c + a * t], -1)
+
+    i = torch.arange(n)
+    sees = i[:, None] >= i
+    if s.window:
+        sees &= (i[:, None] - i < s.window) | (i < s.sinks)
+    x = take("embed")[tokens]
+    for layer in range(s.layers):
+        def w(name):
+            return take(f"{layer}.{name}")
+        h = ((norm(x, s.eps) * w("gain1")) @ w("qkv").t()).view(n, hq + 2 * hkv, d)
+        q = turn(norm(h[:, :hq], s.eps) * w("q_gain"))
+        k = turn(norm(h[:, hq:hq + hkv], s.eps) * w("k_gain")).repeat_interleave(hq // hkv, 1)
+        v = h[:, hq + hkv:].repeat_interleave(hq // hkv, 1)
+        scores = torch.einsum("ihd,jhd->hij", q, k) * d ** -0.5
+        p = scores.masked_fill(~sees, float("-inf")).softmax(-1)
+        x = x + torch.einsum("hij,jhd->ihd", p, v).reshape(n, -1) @ w("out").t()
+        h = (norm(x, s.eps) * w("gain2")) @ w("up").t()
+        x = x + (torch.nn.functional.silu(h[:, :s.hidden]) * h[:, s.hidden:]) @ w("down").t()
+    return (norm(x, s.eps) * take("gain")) @ take("head").t()
+
+
+@pytest.mark.parametrize("window,sinks,lanes", [(0, 0, 3), (7, 2, 3), (5, 0, 20)])
+def test_against_64_bits(P, window, sinks, lanes):
+    """Lanes of several lengths, one of them without words, in one pool of
+    small pages: every step's logits."""
+    s = shape(P, window=window, sinks=sinks)
+    tensors = P.random_tensors(s, 1)
+    tensors = {n: t * (0.5 + torch.rand(t.shape, generator=torch.Generator().manual_seed(2))) if "gain" in n else t
+               for n, t in tensors.items()}
+    g = torch.Generator().manual_seed(3)
+    words = [torch.randint(0, s.vocab, (n % 29,), generator=g).tolist() for n in range(0, 9 * lanes, 9)]
+    second = P.SecondPass(P.LanguageModel(s, tensors, torch.float16), lanes, 40, page_size=4)
+    plan, table = second.plan_lanes(words, 1)
+    second.table.copy_(torch.from_numpy(table))
+    got = torch.stack([second.logits(*torch.from_numpy(row).cuda().unbind()).double().cpu() for row in plan])
+    for b, w in enumerate(words):
+        ref = plain(P, s, tensors, [s.start, *w])
+        mine = got[:len(w) + 1, b]
+        assert bool(((mine - ref).norm(dim=1) <= LIMIT * ref.norm(dim=1)).all())
+
+
+def test_graph_and_steps_agree(P):
+    lm = P.LanguageModel.random(shape(P))
+    second = P.SecondPass(lm, 5, 64, page_size=16, pages=14)
+    words = [[1, 2, 3], [], list(range(20, 50)), [700]]
+    first = second.run(words, 12, top_p=0.9, seed=4)
+    assert [len(a["tokens"]) for a in first] == [12] * 4
+    assert all(0 <= t < 777 for a in first for t in a["tokens"])
+    assert all(v <= 0 for a in first for v in a["logprobs"])
+    assert second.run(words, 12, top_p=0.9, seed=4, graph=False) == first
+    assert second.run(words, 12, top_p=0.9, seed=5) != first
+    assert second.run(words, 12, top_p=0.9, seed=4) == first
+    # the largest logit needs no random number
+    assert second.run(words, 12, temperature=0.0, seed=1) == second.run(words, 12, temperature=0.0, seed=2)
+    assert second.run([], 3) == []
+
+
+def test_refusals(P):
+    lm = P.LanguageModel.random(shape(P))
+    second = P.SecondPass(lm, 2, 32, page_size=16, pages=3)
+    for words, new in (([[1]] * 3, 4), ([[1]], 0), ([[1] * 30], 3), ([[1] * 20, [1] * 20], 4), ([[777]], 1), ([[-1]], 1)):
+        with pytest.raises(ValueError):
+            second.run(words, new)
+    tensors = P.random_tensors(shape(P))
+    del tensors["1.up"]
+    with pytest.raises(ValueError):
+        P.LanguageModel(shape(P), tensors)
+
+
+def test_after_a_first_pass(P):
+    import synth
+    import wfst_beam_search_gb300 as W
+    wl, g = synth.workload(0), synth.make_graph(0)
+    dec = W.Decoder(W.Graph(g, device=0), W.make_params(wl.search_beam, wl.output_beam, wl.min_active, wl.max_active, True),
+                    max_lanes=wl.B, max_frames=wl.T)
+    before = dec.decode(torch.from_numpy(synth.make_log_probs(0)).cuda(), synth.make_lens(0))
+    words = [[int(w) for w in r["words"]] for r in before]
+    lm = P.LanguageModel.random(shape(P, vocab=int(g["olabel"].max()) + 1))
+    second = P.SecondPass(lm, len(words), max(map(len, words)) + 8)
+    assert all(len(a["tokens"]) == 8 for a in second.run(words, 8))
+    after = dec.decode(torch.from_numpy(synth.make_log_probs(0)).cuda(), synth.make_lens(0))
+    assert [list(r["words"]) for r in after] == [list(r["words"]) for r in before]

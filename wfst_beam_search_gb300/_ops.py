@@ -34,10 +34,21 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty = torch.empty
 
 # the argument blocks of the C calls, field by field as the header declares them
-_MATVEC = struct.Struct("4P2q7i4x").pack
-_ROTATE = struct.Struct("11P14q11if").pack
-_ATTEND = struct.Struct("8P12q11if").pack
-_SAMPLE = struct.Struct("9Pq5i3f").pack
+def _block(fields):
+    pack = struct.Struct(fields).pack
+
+    def block(*values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"an argument does not fit its type: {e}") from None
+    return block
+
+
+_MATVEC = _block("4P2q7i4x")
+_ROTATE = _block("11P14q11if")
+_ATTEND = _block("8P12q11if")
+_SAMPLE = _block("9Pq5i3f")
 
 _lib = None
 
