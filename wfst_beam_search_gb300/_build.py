@@ -1,22 +1,28 @@
 """Compile the CUDA decoder library for GB300 (sm_103a), in tree.
 
 Ten translation units are compiled in parallel and linked into
-``wfst_beam_search_gb300/_build/libwfst_gb300.so``.
+``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch is installed,
+``ops_binding.so`` is compiled beside it: the second-pass operators' path from
+torch tensors into that library.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libwfst_gb300.so")
+BINDING = os.path.join(BUILD, "ops_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["wfst_kernel.cu", "wfst_api.cu", "wfst_static.cu", "wfst_preslice.cu", "wfst_vmm.cu", "wfst_probe.cu",
            "wfst_matvec.cu", "wfst_rotate.cu", "wfst_attend.cu", "wfst_sample.cu"]
+BINDING_SOURCE = "ops_binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -27,8 +33,14 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA decoder cannot be built")
 
 
+def _torch():
+    """torch's folder, or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES + [BINDING_SOURCE]]
     files += [os.path.join(CSRC, "wfst_internal.h"), os.path.join(CSRC, "wfst_vmm.h"),
               os.path.join(CSRC, "wfst_ops.h"),
               os.path.join(INCLUDE, "wfst_gb300.h")]
@@ -36,9 +48,10 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    made = [LIB, BINDING] if _torch() else [LIB]
+    if not all(map(os.path.exists, made)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(map(os.path.getmtime, made))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -51,23 +64,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         flags += ["-Xptxas", "-v"]
 
+    torch = _torch()
+    binding_flags = ["-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-I", sysconfig.get_paths()["include"]]
+    if torch:
+        binding_flags += ["-I", os.path.join(torch, "include"),
+                          "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include")]
+
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [cc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [cc] + (binding_flags if src == BINDING_SOURCE else flags) + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
-    objs = [o for o, _ in results]
+    sources = SOURCES + ([BINDING_SOURCE] if torch else [])
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        results = list(ex.map(compile_one, sources))
+    objs = [o for o, _ in results[:len(SOURCES)]]
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if torch:
+        tmp = BINDING + f".{os.getpid()}.tmp"
+        cmd = [cc] + ARCH + ["-shared", "-o", tmp, results[-1][0], "-L", BUILD, "-lwfst_gb300",
+                             "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch",
+                             "-lc10_cuda", "-lc10", "-Xlinker", "-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
     if verbose:
         for _, log in results:
             print(log)
