@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
   __shared__ __align__(8) uint64_t bars[2 * S + 4];
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
+  __shared__ __align__(16) float sums[ZERO ? 4 : 1][kParts][ZERO ? N : 4];  // of x's rows, a copy for each warp
   cg::cluster_group cl = cg::this_cluster();
   const int shares = (int)cl.num_blocks(), share = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tile = blockIdx.x / shares, row0 = blockIdx.y * N;
@@ -396,18 +397,29 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
         bool some = false;
 #pragma unroll
         for (int h = 0; h < kParts; h++) some = some || !(rest[h] == 0.f);
-        if (__any_sync(0xffffffffu, some)) {
+        if (__any_sync(0xffffffffu, some)) {  // each warp sums the rows of x, a lane one or two
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < N; j++) {
+          for (int j = lane; j < N; j += 32) {
             float t[kParts] = {};
+#pragma unroll
             for (int c = 0; c < 8; c++) {
               const uint4 v = *reinterpret_cast<const uint4*>(stage + j * 128 + ((c ^ (j & 7)) * 16));
               const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z), f3 = unpack2<T>(v.w);
               t[SUB ? c / 4 : 0] += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
             }
 #pragma unroll
-            for (int h = 0; h < kParts; h++) acc[j] += s_one[h] * rest[h] * t[h];
+            for (int h = 0; h < kParts; h++) sums[warp][h][j] = t[h];
           }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < N; j += 4)
+#pragma unroll
+            for (int h = 0; h < kParts; h++) {
+              const float4 t = *reinterpret_cast<const float4*>(&sums[warp][h][j]);
+              const float f = s_one[h] * rest[h];
+              acc[j] += f * t.x, acc[j + 1] += f * t.y, acc[j + 2] += f * t.z, acc[j + 3] += f * t.w;
+            }
         }
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
