@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   __shared__ uint32_t s_last[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int runs = a.hkv * a.runs;
+  ops_begin();
+  ops_next();
 
   // ---- this CTA's units: all lanes' tiles, numbered through (each warp for itself)
   uint32_t units = 0;
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         const int key = j < ahead.s.first ? j : j + ahead.s.shift;
         const int pg = (int)(((uint64_t)(uint32_t)key * a.div_m) >> a.div_s);
         r.slot[i] = key - pg * a.page;
-        r.id[i] = __ldg(a.table + ahead.b * a.st_b + pg);
+        r.id[i] = ops_load(a.table + ahead.b * a.st_b + pg);
       }
     }
     return r;
@@ -278,8 +280,8 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
       const T* q = reinterpret_cast<const T*>(a.q) + at.b * a.sq_b + (int64_t)(h * a.share + c) * a.sq_h + 2 * t;
 #pragma unroll
       for (int k = 0; k < KS; k++) {
-        qf[n][k][0] = c < a.share ? __ldg(reinterpret_cast<const uint32_t*>(q + k * 16)) : 0u;
-        qf[n][k][1] = c < a.share ? __ldg(reinterpret_cast<const uint32_t*>(q + k * 16 + 8)) : 0u;
+        qf[n][k][0] = c < a.share ? ops_load(reinterpret_cast<const uint32_t*>(q + k * 16)) : 0u;
+        qf[n][k][1] = c < a.share ? ops_load(reinterpret_cast<const uint32_t*>(q + k * 16 + 8)) : 0u;
       }
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
@@ -618,8 +620,7 @@ cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
   int64_t grid = (int64_t)resident * ops_sm_count();
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (grid > most_units) grid = most_units;
-  fn<<<(int)grid, kWarps<D> * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  return ops_launch(fn, (unsigned)grid, kWarps<D> * 32, smem, 0, st, a);
 }
 
 template <typename T, int D>

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/wfst_gb300.h"
 
@@ -66,6 +67,47 @@ inline int ops_current() {
   cudaGetDevice(&d);
   return d;
 }
+
+#ifdef __CUDACC__
+
+// Launches `fn` so that its CTAs may be set up while the kernel before it in the
+// stream ends (a step is a chain of short kernels).  Every kernel launched like
+// this calls ops_begin in all its threads before it touches memory that any
+// kernel writes, and before it takes tensor memory; ops_next, after that, lets
+// the one behind it set up.
+template <typename... P>
+cudaError_t ops_launch(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
+                       const std::common_type_t<P>&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;  // 0: a kernel that knows no clusters
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+__device__ __forceinline__ void ops_begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads that the compiler keeps behind ops_begin, as it need not keep those of
+// the read-only path; the second one's data are not read again.
+template <typename V>
+__device__ __forceinline__ V ops_load(const V* p) {
+  return *p;
+}
+__device__ __forceinline__ uint4 ops_load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void ops_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+#endif
 
 inline bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 

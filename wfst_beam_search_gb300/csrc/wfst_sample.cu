@@ -606,6 +606,8 @@ static_assert(sizeof(Shared) % 16 == 0);
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char raw_smem[];
+  ops_begin();
+  ops_next();
   Draw<T> d{{}, reinterpret_cast<Shared*>(raw_smem), nullptr, cg::this_cluster()};
   Shared* sh = d.sh;
   const int C = d.C = (int)d.cl.num_blocks(), rank = d.rank = (int)d.cl.block_rank();
@@ -936,17 +938,6 @@ cudaError_t launch(Args& a, int lanes, cudaStream_t st) {
   const int share = ((a.vocab + 16) * (int)sizeof(T) / c / 16 + 2) * 16;  // bytes, at most
   a.staged = share <= kStage;
   const int smem = (int)sizeof(Shared) + (a.staged ? share : 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)lanes * c);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   static OpsOnce once;
   if (const int dev = ops_current(); !once(dev)) {
     const cudaError_t e =
@@ -955,7 +946,7 @@ cudaError_t launch(Args& a, int lanes, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  return ops_launch(sample_kernel<T>, (unsigned)lanes * c, kThreads, smem, c, st, a);
 }
 
 }  // namespace
