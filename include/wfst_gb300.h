@@ -453,8 +453,8 @@ int wfst_quant_pack(const uint8_t* codes, const void* scales, const void* zeros,
 /*
  * y[r, n] = bias[n] + sum over k of x[r, k] * w[n, k], for rows r of x
  * [rows, k] (16-byte aligned, stride_x >= k and a multiple of 8) and a packed
- * matrix.
- * bias [n] may be NULL.  rows = 0 does nothing.  Errors: INVALID_ARG, CUDA.
+ * matrix.  bias [n] may be NULL.  Where a row of x is not finite, that row of
+ * y may be NaN throughout.  rows = 0 does nothing.  Errors: INVALID_ARG, CUDA.
  */
 typedef struct {
   const void *packed, *x, *bias;

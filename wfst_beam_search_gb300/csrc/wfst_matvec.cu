@@ -11,10 +11,10 @@
 // two codes.  A group's sums are in fp32, scaled and added up in fp32, so nothing
 // is rounded before y.  Two kernels, by the number of rows:
 //   - Few rows: mma.sync fed from registers, eight warps sharing k.  1 x 4096 x
-//     4096 takes 4.6 us, 8 x 131072 x 4096 77 us (3.6 TB/s; the floor is 41).
+//     4096 takes 4.5 us, 8 x 131072 x 4096 77 us (3.6 TB/s; the floor is 41).
 //   - Many rows: tcgen05, the weights widened once into tensor memory by one
-//     thread per output, x from shared memory.  64 x 32768 x 4096 takes 41 us,
-//     64 x 65536 x 8192 147 us (1.9 TB/s).
+//     thread per output, x from shared memory.  64 x 32768 x 4096 takes 40 us,
+//     64 x 65536 x 8192 146 us (1.9 TB/s), 64 x 5000 x 1056 in groups of 32 9 us.
 // The first one's work goes with the rows, the second one's hardly does, but it
 // starts and ends more slowly (barriers, tensor memory, a cluster's sum): 16 x
 // 4096 x 4096 is 6.4 against 10.5 us, 32 x 16384 x 4096 32 against 21.  Up to 16
@@ -189,8 +189,8 @@ __device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
 // the same fp32 sum, whose terms are then about five times those of sum x (c - z)
 // / 16 (at 64 rows 6% faster than subtracting).  Where tensor memory has no room
 // for it (groups of 32, 17 to 32 rows), the threads subtract, exactly.  Both hold
-// for whole z; what z has beside its whole part is added as s * rest * sum x.
-// What bounds it is the chain of a stage (wait, widen, store, product, read back)
+// for whole z; what z has beside its whole part is added as s * rest * sum x (64 x
+// 32768 x 4096 with such z 72 us, with whole ones 46).  What bounds it is the chain of a stage (wait, widen, store, product, read back)
 // and the instructions in it, not HBM.  A non-finite x can make NaN of a sum that
 // would be infinite, in its own row of y only.
 //
