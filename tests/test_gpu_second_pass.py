@@ -133,3 +133,57 @@ def test_after_a_first_pass(P):
     assert all(len(a["tokens"]) == 8 for a in second.run(words, 8))
     after = dec.decode(torch.from_numpy(synth.make_log_probs(0)).cuda(), synth.make_lens(0))
     assert [list(r["words"]) for r in after] == [list(r["words"]) for r in before]
+
+
+@pytest.mark.parametrize("scale", [0.0055, 0.0012])     # values that leave fp16's range, ones that stay
+@pytest.mark.parametrize("lanes", [3, 40])
+def test_calls_follow_each_other(P, lanes, scale):
+    """A chain of calls that read what the one before wrote, in buffers that
+    are used again, gives the same bits as with a wait after each call."""
+    import wfst_beam_search_gb300 as W
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    hq, hkv, d, page, steps = 24, 8, 64, 16, 60
+
+    def matrix(n, k):
+        codes = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+        return W.pack_quant(codes, torch.full((n, k // 128), scale, device="cuda").half())
+
+    up, down = matrix((hq + 2 * hkv) * d, hq * d), matrix(hq * d, hq * d)
+    start = torch.randn(lanes, hq * d, generator=g, device="cuda").half()
+    uniform = torch.rand(steps, lanes, generator=g, device="cuda")
+    angle = torch.rand(steps, d // 2, generator=g, device="cuda") * 6
+    rotary = torch.cat([angle.cos(), angle.sin()], 1)
+    width = -(-steps // page)
+    table = torch.randperm(lanes * width, generator=g, device="cuda").int().view(lanes, width)
+    at = torch.arange(steps, device="cuda")
+    slots = (table[:, at // page] * page + at % page).t().int().contiguous()
+    lengths = (at + 1).int()[:, None].repeat(1, lanes)
+    positions = at.int()[:, None].repeat(1, lanes)
+    ws = W.attend_workspace()
+
+    def chain(wait):
+        x, h, o = start.clone(), start.new_empty(lanes, (hq + 2 * hkv) * d), start.new_empty(lanes, hq, d)
+        cache = torch.zeros(2, lanes * width, page, hkv, d, device="cuda").half()
+        tokens = []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            W.matvec_quant(x, up, out=h)
+            wait()
+            heads = h.view(lanes, -1, d)
+            W.norm_rotate(heads[:, :hq], heads[:, hq:hq + hkv], heads[:, hq + hkv:], positions[i], rotary, None, None,
+                          cache[0], cache[1], slots[i], out=heads[:, :hq])
+            wait()
+            W.attend_paged(heads[:, :hq], cache[0], cache[1], table, lengths[i], workspace=ws, out=o)
+            wait()
+            W.matvec_quant(o.view(lanes, -1), down, out=x)
+            wait()
+            tokens.append(W.sample_tokens(x, uniform[i], top_p=0.9)[0])
+            wait()
+        assert bool(x.isfinite().all()) == (scale < 0.002)
+        return x.view(torch.int16), cache.view(torch.int16), torch.stack(tokens)
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        got = chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

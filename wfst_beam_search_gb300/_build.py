@@ -1,8 +1,8 @@
 """Compile the CUDA decoder library for GB300 (sm_103a), in tree.
 
 Ten translation units are compiled in parallel and linked into
-``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch is installed,
-``ops_binding.so`` is compiled beside it: the second-pass operators' path from
+``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch and Python's
+headers are installed, ``ops_binding.so`` is compiled beside it: the second-pass operators' path from
 torch tensors into that library.
 """
 from __future__ import annotations
@@ -34,9 +34,10 @@ def nvcc() -> str:
 
 
 def _torch():
-    """torch's folder, or None."""
+    """torch's folder; None where it or Python's headers are missing, and the decoder is built alone."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec and spec.origin else None
+    headers = os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+    return os.path.dirname(spec.origin) if spec and spec.origin and headers else None
 
 
 def _inputs():

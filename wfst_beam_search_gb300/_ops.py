@@ -45,7 +45,7 @@ _SAMPLE = struct.Struct("9Pq5i3f").pack
 def _load_binding():
     load()
     if not os.path.exists(_build.BINDING):
-        raise ImportError("ops_binding.so is not built; run __graft_entry__.build() (the operators have no CPU fallback)")
+        raise ImportError("ops_binding.so is not built (it needs torch and Python's headers); run __graft_entry__.build()")
     spec = importlib.util.spec_from_file_location("ops_binding", _build.BINDING)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
