@@ -211,11 +211,12 @@ template <int N>
 constexpr int kStages = N == 64 ? 7 : 6;
 template <int N, bool SUB, bool ZERO>
 constexpr int kSlot = (N * 128 + kCodes + (SUB ? 2 : 1) * kM * (ZERO ? 4 : 2) + 1023) / 1024 * 1024;
-// CTAs of a multiprocessor: what its 512 columns (and, at N = 32, its registers)
-// hold, and no more, since one that waits for columns would hold up its cluster;
+// CTAs of a multiprocessor: two if its 512 columns hold them, and no more, since
+// one that waits for columns would hold up its cluster, and three only share what
+// two get done (32 x 8192 x 4096 12 us, with three, split in more shares, 16);
 // shared memory sees to it
 template <int N, bool SUB>
-constexpr int kResident = N == 32 && !SUB ? 3 : 512 / kColumns<N, SUB>;
+constexpr int kResident = kColumns<N, SUB> <= 256 ? 2 : 1;
 template <int N, bool SUB, bool ZERO>
 constexpr int kSmem = 1024 + (kStages<N> * kSlot<N, SUB, ZERO> > 233472 / (kResident<N, SUB> + 1)
                                   ? kStages<N> * kSlot<N, SUB, ZERO>
