@@ -17,10 +17,10 @@
 //     64 x 65536 x 8192 146 us (1.9 TB/s), 64 x 5000 x 1056 in groups of 32 9 us.
 // The first one's work goes with the rows, the second one's hardly does, but it
 // starts and ends more slowly (barriers, tensor memory, a cluster's sum): 16 x
-// 4096 x 4096 is 6.4 against 10.5 us, 32 x 16384 x 4096 32 against 21.  Up to 16
+// 4096 x 4096 is 6.0 against 8.4 us, 32 x 16384 x 4096 31 against 21.  Up to 16
 // rows the first one is taken, and above where its CTAs fit on the device at
-// once: 64 x 1024 x 4096 is 6.3 against 8.1 us, 32 x 4096 x 4096, which does not
-// fit, 11.3 against 10.5, 24 x 5000 x 1056 7.6 against 7.0.
+// once: 64 x 1024 x 4096 is 5.8 against 7.1 us, 32 x 4096 x 4096, which does not
+// fit, 10.8 against 9.1, 24 x 5000 x 1056 7.0 against 6.1.
 //
 // Layout ("packed", made once by wfst_quant_pack): tiles of 128 outputs, in them
 // blocks of 64 k, in them eight parts of 16 outputs with 512 bytes each: 16 bytes
@@ -187,8 +187,9 @@ __device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
 // The 1 + z / 16 too much is taken off by the tensor cores, which have time: a
 // second product of the same x with -(1 + z / 16) in every column of A goes into
 // the same fp32 sum, whose terms are then about five times those of sum x (c - z)
-// / 16 (at 64 rows 6% faster than subtracting).  Where tensor memory has no room
-// for it (groups of 32, 17 to 32 rows), the threads subtract, exactly.  Both hold
+// / 16 (at 64 rows 6% faster than subtracting).  Groups of 32 leave no room for it
+// in tensor memory, and up to 32 rows it is no faster (24 x 9262 x 7936 24 against
+// 23 us): there the threads subtract, exactly.  Both hold
 // for whole z; what z has beside its whole part is added as s * rest * sum x (64 x
 // 32768 x 4096 with such z 72 us, with whole ones 46).  What bounds it is the chain of a stage (wait, widen, store, product, read back)
 // and the instructions in it, not HBM.  A non-finite x can make NaN of a sum that
