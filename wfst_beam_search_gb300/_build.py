@@ -2,8 +2,8 @@
 
 Ten translation units are compiled in parallel and linked into
 ``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch and Python's
-headers are installed, ``ops_binding.so`` is compiled beside it: the second-pass operators' path from
-torch tensors into that library.
+headers are installed, ``ops_binding.so`` is compiled beside it: the
+second-pass operators' path from torch tensors into that library.
 """
 from __future__ import annotations
 

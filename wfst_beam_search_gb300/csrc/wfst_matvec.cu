@@ -189,11 +189,11 @@ __device__ __forceinline__ uint32_t less2(uint32_t v, uint32_t off) {
 // the same fp32 sum, whose terms are then about five times those of sum x (c - z)
 // / 16 (at 64 rows 6% faster than subtracting).  Groups of 32 leave no room for it
 // in tensor memory, and up to 32 rows it is no faster (24 x 9262 x 7936 24 against
-// 23 us): there the threads subtract, exactly.  Both hold
-// for whole z; what z has beside its whole part is added as s * rest * sum x (64 x
-// 32768 x 4096 with such z 72 us, with whole ones 46).  What bounds it is the chain of a stage (wait, widen, store, product, read back)
-// and the instructions in it, not HBM.  A non-finite x can make NaN of a sum that
-// would be infinite, in its own row of y only.
+// 23 us): there the threads subtract, exactly.  Both hold for whole z; what z has
+// beside its whole part is added as s * rest * sum x (64 x 32768 x 4096 with such z
+// 72 us, with whole ones 46).  What bounds it is the chain of a stage (wait, widen,
+// store, product, read back) and the instructions in it, not HBM.  A non-finite x
+// can make NaN of a sum that would be infinite, in its own row of y only.
 //
 // Sizes that go with N rows of x (32 or 64) and groups of 32 (SUB):
 
