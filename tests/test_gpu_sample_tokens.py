@@ -145,6 +145,30 @@ def test_masked_and_infinite_logits(W):
     check(W, x[:, :3], u, p=0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [8200, 40001, 131071])
+def test_masked_rows_of_a_cluster(W, vocab, dtype):
+    """Rows that several CTAs share, with masks that leave nothing, one logit,
+    fewer than k of them, those of one CTA, or every other one."""
+    x, u = logits(vocab, 8, vocab, dtype)
+    x[0] = -math.inf
+    x[1] = math.nan
+    x[2, :] = -math.inf
+    x[2, vocab - 3] = -5.0
+    few = torch.randperm(vocab, generator=torch.Generator().manual_seed(1))[:30].cuda()
+    some = x[3, few].clone()
+    x[3] = -math.inf
+    x[3, few] = some
+    x[4, 700:] = -math.inf
+    x[5, ::2] = math.nan
+    x[6, :vocab - 900] = -math.inf
+    x[7, [5, vocab // 2, vocab - 1]] = math.inf
+    for kw in (dict(), dict(k=50), dict(p=0.9), dict(k=200, p=0.5, min_p=0.1), dict(p=0.95, min_p=0.02),
+               dict(temp=0.0), dict(k=vocab - 1)):
+        tokens = check(W, x, u, **kw)[0].tolist()
+        assert tokens[0] == tokens[1] == -1 and tokens[2] == vocab - 3 and tokens[7] in (5, vocab // 2, vocab - 1)
+
+
 def test_strides_alignment_streams_and_repeats(W):
     """Rows at every alignment, rows of a wider tensor, another stream; the same answer every time."""
     for dtype in (torch.float32, torch.float16):

@@ -611,11 +611,14 @@ static_assert(sizeof(Shared) % 16 == 0);
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  ops_begin();
-  ops_next();
   Draw<T> d{{}, reinterpret_cast<Shared*>(raw_smem), nullptr, cg::this_cluster()};
   Shared* sh = d.sh;
   const int C = d.C = (int)d.cl.num_blocks(), rank = d.rank = (int)d.cl.block_rank();
+  // A CTA's shared memory may be written by the others once it runs: that all of
+  // them do is known at the wait before the first `leave`, behind the row's reading.
+  if (C > 1) d.cl.barrier_arrive();
+  ops_begin();
+  ops_next();
   const int b = blockIdx.x / C;
   const int tid = d.tid = threadIdx.x, lane = d.lane = tid & 31, warp = d.warp = tid >> 5;
   constexpr int VEC = Row<T>::VEC;
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   for (int x = 16; x; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   if (lane == 0) sh->warp_b[warp] = __float_as_uint(top);
   __syncthreads();
+  if (C > 1) d.cl.barrier_wait();  // all CTAs of the cluster run
   if (warp == 0) {
     top = lane < kWarps ? __uint_as_float(sh->warp_b[lane]) : -INFINITY;
 #pragma unroll
