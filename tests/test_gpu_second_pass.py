@@ -108,6 +108,25 @@ def test_graph_and_steps_agree(P):
     assert second.run([], 3) == []
 
 
+def test_logits_without_a_number_end_an_answer(P):
+    """A lane that reads a token whose embedding is not finite has no logits
+    from there on: its answer is -1, its neighbours' answers stay, and the
+    model goes on being of use."""
+    s = shape(P)
+    tensors = P.random_tensors(s)
+    clean = [[1, 2], [3, 4, 5], [6]]
+    want = P.SecondPass(P.LanguageModel(s, tensors), 3, 32).run(clean, 9, top_p=0.9, seed=4)
+    drawn = {t for a in want for t in a["tokens"]}
+    bad = next(t for t in range(7, s.vocab) if t not in drawn)
+    tensors["embed"][bad] = float("nan")
+    for graph in (True, False):
+        second = P.SecondPass(P.LanguageModel(s, tensors), 3, 32)
+        got = second.run([clean[0], [3, bad, 5], clean[2]], 9, top_p=0.9, seed=4, graph=graph)
+        assert got[0] == want[0] and got[2] == want[2]
+        assert got[1] == {"tokens": [-1] * 9, "logprobs": [-float("inf")] * 9}
+        assert second.run(clean, 9, top_p=0.9, seed=4, graph=graph) == want
+
+
 def test_refusals(P):
     lm = P.LanguageModel.random(shape(P))
     second = P.SecondPass(lm, 2, 32, page_size=16, pages=3)

@@ -164,7 +164,8 @@ class SecondPass:
 
     def _step(self):
         tokens, positions, slots, lengths = self.plan.index_select(0, self.at)[0]
-        tokens = torch.where(tokens < 0, self.last, tokens)
+        # (a lane whose logits were all NaN drew -1: it goes on from token 0, and ``run`` ends its answer)
+        tokens = torch.where(tokens < 0, self.last.clamp_min(0), tokens)
         drawn, logprobs, _ = _ops.sample_tokens(self.logits(tokens, positions, slots, lengths),
                                                 self.uniform.index_select(0, self.at)[0], **self.settings)
         self.last.copy_(drawn)
@@ -223,7 +224,9 @@ class SecondPass:
 
     def run(self, words, new_tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, seed=0, graph=True):
         """Read each lane's ``words`` and draw ``new_tokens`` tokens after
-        them: [{"tokens", "logprobs"}, ...].  The same seed draws the same."""
+        them: [{"tokens", "logprobs"}, ...].  The same seed draws the same.
+        An answer ends where its logits hold no number (weights or activations
+        that left the type's range): tokens -1, logprobs -inf from there on."""
         plan, table = self.plan_lanes(words, new_tokens)
         if not len(plan):
             return []
@@ -239,8 +242,12 @@ class SecondPass:
         for _ in range(len(plan)):
             self.graph.replay() if graph else self._step()
         drawn, logprobs = self.drawn[:len(plan)].cpu().numpy(), self.logprobs[:len(plan)].cpu().numpy()
-        return [{"tokens": drawn[len(w):len(w) + new_tokens, b].tolist(),
-                 "logprobs": logprobs[len(w):len(w) + new_tokens, b].tolist()} for b, w in enumerate(words)]
+        answers = []
+        for b, w in enumerate(words):
+            t, lp = drawn[len(w):len(w) + new_tokens, b], logprobs[len(w):len(w) + new_tokens, b]
+            ended = np.logical_or.accumulate(t < 0)
+            answers.append({"tokens": np.where(ended, -1, t).tolist(), "logprobs": np.where(ended, -np.inf, lp).tolist()})
+        return answers
 
 
 def main():
