@@ -92,3 +92,11 @@ def test_host_tensors_are_refused():
         W.attend_paged(h[:, None], pages, pages, i[:, None], i)
     with pytest.raises(ValueError):
         W.norm_rotate(h[:, None], h[:, None], h[:, None], i, torch.zeros(4, 64), None, None, pages, pages, i)
+
+
+def test_a_start_token_outside_the_vocabulary_is_refused():
+    from wfst_beam_search_gb300 import second_pass as P
+    for start in (-1, 50, 51):
+        s = P.Shape(vocab=50, width=64, layers=1, start=start)
+        with pytest.raises(ValueError, match="start token"):
+            P.LanguageModel(s, P.random_tensors(s), device="cpu")

@@ -71,6 +71,8 @@ class LanguageModel:
         q_heads * head_dim], "i.gain2", "i.up" [2 hidden, width] (gate first),
         "i.down" [width, hidden], in any floating type."""
         s, heads = shape, shape.q_heads * shape.head_dim
+        if not 0 <= s.start < s.vocab:
+            raise ValueError(f"the start token {s.start} is outside the vocabulary of {s.vocab}")
         sizes = {"embed": (s.vocab, s.width), "gain": (s.width,), "head": (s.vocab, s.width)}
         for i in range(s.layers):
             sizes.update({f"{i}.gain1": (s.width,), f"{i}.gain2": (s.width,), f"{i}.q_gain": (s.head_dim,),
