@@ -2,8 +2,9 @@
 
 Shared memory of another CTA may be touched once that CTA runs, which a
 cluster barrier says.  A kernel that goes without it works until the day a CTA
-of the cluster starts late, so the order is read from the source here, and not
-run."""
+of the cluster starts late.  A kernel whose wait gave up starts no more copies
+and products and waits for those that it started.  Neither can be made to
+happen without harm, so both are read from the source here, and not run."""
 import os
 import re
 
@@ -35,3 +36,17 @@ def test_a_cluster_meets_before_its_memory_is_shared(name, kernel):
     assert "this_cluster" in body
     waited, remote = WAITED.search(body), REMOTE.search(body)
     assert remote and waited and waited.start() < remote.start()
+
+
+def test_a_wait_that_gave_up_leaves_nothing_on_its_way():
+    body = re.sub(r"\s+", " ", kernels("wfst_matvec.cu")["matvec_wide"])
+    # what is started: only while no wait gave up, and counted
+    assert len(re.findall(r"elected\(\)", body)) == 2
+    starts = [m.end() for m in re.finditer(r"if \(elected\(\) && good\) \{ issued = i \+ 1;", body)]
+    assert len(starts) == 2
+    # what is waited for behind either loop: all that was started, whatever `good` says
+    for start, bar, depth in zip(starts, ("filled", "through"), ("S", "2")):
+        m = re.search(r"for \(int i = issued > %s \? issued - %s : 0; i < issued; i\+\+\) good = wait_bar\(%s\(" %
+                      (depth, depth, bar), body)
+        assert m and m.start() > start
+        assert body.index("tcgen05.dealloc") > m.start()

@@ -276,11 +276,12 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
   float acc[N];
   if (warp == 4) {
     // ---- copies: x (rows of 128 bytes, 16-byte pieces exchanged by row), codes and scales
-    int slot = 0, round = 0;
+    int slot = 0, round = 0, issued = 0;  // issued: by the elected lane, the others have none
     for (int i = 0; i < count; i++) {
       const int blk = b0 + i;
       if (round) good = good && wait_bar(is_free(slot), (round - 1) & 1);
-      if (elected()) {
+      if (elected() && good) {
+        issued = i + 1;
         const uint32_t dst = ring_at + slot * kSize;
         constexpr uint32_t bytes = N * 128 + kCodes + kParts * kM * kScale;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(filled(slot)), "n"(bytes) : "memory");
@@ -297,22 +298,24 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
       __syncwarp();
       if (++slot == S) slot = 0, round++;
     }
-    // nothing may be on its way when the CTA ends
-    for (int i = count > S ? count - S : 0; i < count; i++) good = good && wait_bar(filled(i % S), (i / S) & 1);
+    // nothing may be on its way when the CTA ends, nor where a wait gave up
+    for (int i = issued > S ? issued - S : 0; i < issued; i++) good = wait_bar(filled(i % S), (i / S) & 1) && good;
+    __syncwarp();
   } else if (warp == 5) {
     // ---- products.  kind::f16: fp32 sums, both operands T with k innermost, N columns, 128 rows
     constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
     constexpr uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | (uint32_t)(kM / 16) << 24;
     // x: rows of 128 bytes, groups of eight rows 1024 bytes apart, pieces exchanged within 128 bytes
     const uint64_t desc0 = (uint64_t)(ring_at >> 4 & 0x3fffu) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-    int sum = 0, slot = 0, phase = 0;
+    int sum = 0, slot = 0, phase = 0, issued = 0;  // issued: as above
     bool begins = true;
     for (int i = 0; i < count; i++) {
       const int p = i & 1, blk = b0 + i;
       good = good && wait_bar(filled(slot), phase) && wait_bar(a_in(p), (i / 2) & 1);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint64_t desc = desc0 + (uint64_t)(slot * (kSize >> 4));
-      if (elected()) {
+      if (elected() && good) {
+        issued = i + 1;
         const uint32_t d = tmem + kSumAt<N, SUB> + sum * kParts * N;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -326,6 +329,9 @@ __global__ void __launch_bounds__(kThreads, kResident<N, SUB>)
       if (begins) sum ^= 1;
       if (++slot == S) slot = 0, phase ^= 1;
     }
+    // nor a product when its tensor memory is given back
+    for (int i = issued > 2 ? issued - 2 : 0; i < issued; i++) good = wait_bar(through(i & 1), (i / 2) & 1) && good;
+    __syncwarp();
   } else {
     // ---- codes into the operand type; the groups' sums, scaled
     const uint32_t mine = tmem + (uint32_t)(warp * 32 << 16);  // this warp's lanes
