@@ -110,6 +110,41 @@ def test_large_scores_and_other_scale(W, ws):
     check(*W.attend_paged(*a, scale=-0.02, workspace=ws, with_lse=True), *a, -0.02)
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 2), (128, 12, 1), (256, 8, 1)])
+@pytest.mark.parametrize("gap", [8.0, 12.0, 14.0, 16.0, 17.0, 17.4, 20.0])
+def test_weights_far_below_the_largest_fp16(W, ws, gap, d, hq, hkv):
+    """One key `gap` above thousands of others, whose value is zero: what o
+    holds comes from the others alone.  Here P's halves have to hold small
+    weights: each is rounded twice to 11 bits, 2^-24 of it, or by half a step
+    below fp16's smallest exponent, 2^-25 where the largest weight is 2^15.
+    (No slack of 2^-16.)"""
+    n, page = 20011, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(gap * 10) + d)
+    pages = -(-n // page)
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for peak in (0, 7000, n - 1):
+        kc = torch.zeros(pages, page, hkv, d, device="cuda").half()
+        vc = ((torch.rand(pages, page, hkv, d, generator=g, device="cuda") + 0.5) * 4096).half()
+        q = torch.zeros(1, hq, d, device="cuda").half()
+        q[..., 3] = 1.0
+        kc[..., 3] = (torch.rand(pages, page, hkv, generator=g, device="cuda") * 0.5).half()
+        at = int(table[0, peak // page])
+        kc[at, peak % page, :, 3] = gap
+        vc[at, peak % page] = 0
+        o, lse = W.attend_paged(q, kc, vc, table, lens, scale=1.0, workspace=ws, with_lse=True)
+        j = torch.arange(n, device="cuda")
+        k, v = (c[table[0][j // page].long(), j % page].double().repeat_interleave(hq // hkv, 1) for c in (kc, vc))
+        x = torch.einsum("hd,jhd->hj", q[0].double(), k)
+        p = torch.softmax(x, 1)
+        ref = torch.einsum("hj,jhd->hd", p, v)
+        fp = (2 * gap * (d + 8) + n / 8 + 64) * 2.0 ** -23
+        lost = 2.0 ** -40 * v.sum(0) / torch.exp(x - x.amax(1, keepdim=True)).sum(1)[:, None]
+        assert bool(((o[0].double() - ref).abs() <= (2.0 ** -11 + fp + 2.0 ** -23) * ref + lost + 2.0 ** -24).all()), peak
+        assert bool(((lse[0].double() - torch.logsumexp(x, 1)).abs() <= fp).all())
+
+
 def test_missing_pages_and_long_lengths(W, ws):
     """Tokens of pages outside the pool are not seen; a length past the table ends with it."""
     lens = [100, 100, 64]

@@ -15,7 +15,7 @@
 // so that a run of up to 8 query heads wastes nothing of the keys' side and a
 // key is read once for all of them.  P goes from the one's result to the
 // other's operand through a transposing move, as its 16-bit rounding plus the
-// rounding's rest: its error stays that of fp32.
+// rounding's rest: fp16 keeps 23 bits of it so, bf16 17.
 //
 // Work is split evenly whatever the lengths: a unit is 16 keys for each of a
 // CTA's warps, of one lane and head run; units are numbered through, and each CTA
@@ -40,6 +40,13 @@ constexpr int kColsMost = 16;       // query heads of a CTA's run at most
 constexpr int kWidthMost = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// P is kept as its rounding to T plus the rest's rounding.  fp16 has no exponents
+// below 2^-24, at which a weight 17 below the largest score would be lost: there P,
+// and with it l and o, is held times 2^15, so that the largest is 2^15 and what
+// is lost below 2^-40 of it.
+template <typename T>
+constexpr float kLift = std::is_same_v<T, __half> ? 15.f : 0.f;
 
 // workspace: counters [kMaxGrid], then per CTA two parts of {m, l, o}
 constexpr int64_t kPartFloats = 2 * kColsMost + kWidthMost * kColsMost;
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
       for (int x = 0; x < 2; x++) {
         const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
         if (c < a.share)
-          a.lse[b * a.sl_b + (int64_t)(run / a.runs) * a.share + c] = (wm[n][x] + log2f(wl[n][x])) * kLn2;
+          a.lse[b * a.sl_b + (int64_t)(run / a.runs) * a.share + c] = (wm[n][x] + (log2f(wl[n][x]) - kLift<T>)) * kLn2;
       }
   };
   // lane and run whose units are shared with other CTAs: at this one's start and end
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         const float ref = now == -INFINITY ? 0.f : now;
         keep[c] = exp2a(m[n][c] - ref);
         m[n][c] = now;
-        top[c] = ref;
+        top[c] = ref - kLift<T>;
       }
       const float p0 = exp2a(s[n][0] - top[0]), p1 = exp2a(s[n][1] - top[1]);
       const float p2 = exp2a(s[n][2] - top[0]), p3 = exp2a(s[n][3] - top[1]);
