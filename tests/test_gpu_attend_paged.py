@@ -145,6 +145,34 @@ def test_weights_far_below_the_largest_fp16(W, ws, gap, d, hq, hkv):
         assert bool(((lse[0].double() - torch.logsumexp(x, 1)).abs() <= fp).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_weights_keep_their_fp32_value(W, ws, dtype):
+    """Values that cancel all but the last bits of a weight: three keys of
+    weight 1 hold p = exp(-x) in three parts of the type, the fourth, of weight
+    p, holds -1.  What is left is the error of p itself: exp2 (2^-22), the
+    score's three roundings (3 times 2^-24 of at most 4) and the sums (a few
+    2^-24), below 2^-20 of the terms; p in 16 bits would leave up to 2^-19."""
+    lanes, d = 3000, 64
+    x = torch.linspace(0.02, 2.7, lanes, device="cuda").to(dtype).double()
+    p, parts = torch.exp(-x), []
+    rest = p.clone()
+    for _ in range(3):
+        parts.append(rest.to(dtype))
+        rest = rest - parts[-1].double()
+    kc = torch.zeros(lanes, 4, 1, d, device="cuda", dtype=dtype)
+    kc[:, 3, 0, 0] = -x.to(dtype)
+    vc = torch.stack([*parts, -torch.ones_like(parts[0])], 1)[:, :, None, None].expand(lanes, 4, 1, d).contiguous()
+    q = torch.zeros(lanes, 1, d, device="cuda", dtype=dtype)
+    q[..., 0] = 1.0
+    table = torch.arange(lanes, device="cuda").int()[:, None]
+    lens = torch.full((lanes,), 4, device="cuda").int()
+    o = W.attend_paged(q, kc, vc, table, lens, scale=1.0, workspace=ws)[:, 0].double()
+    w = torch.stack([torch.ones_like(p)] * 3 + [p], 1) / (3 + p)[:, None]
+    ref, size = (w * vc[:, :, 0, 0].double()).sum(1), (w * vc[:, :, 0, 0].double().abs()).sum(1)
+    bound = UNIT[dtype] * ref.abs() + 2.0 ** -20 * size + (2.0 ** -25 if dtype == torch.float16 else 0)
+    assert bool(((o - ref[:, None]).abs() <= bound[:, None]).all())
+
+
 def test_missing_pages_and_long_lengths(W, ws):
     """Tokens of pages outside the pool are not seen; a length past the table ends with it."""
     lens = [100, 100, 64]

@@ -14,8 +14,10 @@
 // by 8 query heads, O^T = V^T P^T 16 elements of the value by 8 query heads,
 // so that a run of up to 8 query heads wastes nothing of the keys' side and a
 // key is read once for all of them.  P goes from the one's result to the
-// other's operand through a transposing move, as its 16-bit rounding plus the
-// rounding's rest: fp16 keeps 23 bits of it so, bf16 17.
+// other's operand through a transposing move, in 16-bit parts that add up to its
+// fp32 value: two of fp16, three of bf16.  (With two of bf16, 2^-18 of P is lost;
+// the third costs 0 to 0.5% with up to 8 query heads to a key-value head and 4 to 6%
+// with 12: 32 lanes of 4096 tokens with heads of 256 216 to 228 us.)
 //
 // Work is split evenly whatever the lengths: a unit is 16 keys for each of a
 // CTA's warps, of one lane and head run; units are numbered through, and each CTA
@@ -41,10 +43,10 @@ constexpr int kWidthMost = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// P is kept as its rounding to T plus the rest's rounding.  fp16 has no exponents
-// below 2^-24, at which a weight 17 below the largest score would be lost: there P,
-// and with it l and o, is held times 2^15, so that the largest is 2^15 and what
-// is lost below 2^-40 of it.
+// P's parts are its rounding to T, the rest's, and bf16's second rest's.  fp16 has
+// no exponents below 2^-24, at which a weight 17 below the largest score would be
+// lost: there P, and with it l and o, is held times 2^15, so that the largest is
+// 2^15 and what is lost below 2^-40 of it.
 template <typename T>
 constexpr float kLift = std::is_same_v<T, __half> ? 15.f : 0.f;
 
@@ -369,7 +371,8 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         for (int n = 0; n < NT; n++) mma16816<T>(sp[k % P][n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
       }
     }
-    uint32_t hi[NT][2], lo[NT][2];
+    constexpr bool kThird = std::is_same_v<T, __nv_bfloat16>;  // P's parts
+    uint32_t hi[NT][2], lo[NT][2], last[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -403,8 +406,14 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
       const float2 f0 = unpack2<T>(h0), f1 = unpack2<T>(h1);
       hi[n][0] = turn8x8(h0);
       hi[n][1] = turn8x8(h1);
-      lo[n][0] = turn8x8(pack2<T>(p0 - f0.x, p1 - f0.y));
-      lo[n][1] = turn8x8(pack2<T>(p2 - f1.x, p3 - f1.y));
+      const uint32_t l0 = pack2<T>(p0 - f0.x, p1 - f0.y), l1 = pack2<T>(p2 - f1.x, p3 - f1.y);
+      lo[n][0] = turn8x8(l0);
+      lo[n][1] = turn8x8(l1);
+      if (kThird) {
+        const float2 g0 = unpack2<T>(l0), g1 = unpack2<T>(l1);
+        last[n][0] = turn8x8(pack2<T>(p0 - f0.x - g0.x, p1 - f0.y - g0.y));
+        last[n][1] = turn8x8(pack2<T>(p2 - f1.x - g1.x, p3 - f1.y - g1.y));
+      }
 #pragma unroll
       for (int d = 0; d < DT; d++) {
         o[n][d][0] *= keep[0];
@@ -428,6 +437,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         for (int n = 0; n < NT; n++) {
           mma16816<T>(o[n][d], f[0], f[1], f[2], f[3], hi[n][0], hi[n][1]);
           mma16816<T>(o[n][d], f[0], f[1], f[2], f[3], lo[n][0], lo[n][1]);
+          if (kThird) mma16816<T>(o[n][d], f[0], f[1], f[2], f[3], last[n][0], last[n][1]);
         }
       }
     }
