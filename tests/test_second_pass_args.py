@@ -100,3 +100,61 @@ def test_a_start_token_outside_the_vocabulary_is_refused():
         s = P.Shape(vocab=50, width=64, layers=1, start=start)
         with pytest.raises(ValueError, match="start token"):
             P.LanguageModel(s, P.random_tensors(s), device="cpu")
+
+
+def test_a_pass_runs_on_its_models_device(monkeypatch):
+    """With another device current, capture and replay are of the model's.  No
+    machine here has two GPUs: torch.cuda is a stand-in that keeps count of
+    what is current."""
+    import contextlib
+    from types import SimpleNamespace
+
+    from wfst_beam_search_gb300 import second_pass as P
+
+    now = SimpleNamespace(device=0, stream=None, seen=[])
+
+    class Stream:
+        def __init__(self, device=None):
+            self.device = now.device if device is None else torch.device(device).index
+
+        def wait_stream(self, other):
+            assert other.device == self.device
+
+    class Graph:
+        def replay(self):
+            now.seen.append(("replay", now.device))
+
+    @contextlib.contextmanager
+    def use(**change):
+        before = dict(vars(now))
+        vars(now).update(change)
+        yield
+        vars(now).update({name: before[name] for name in ("device", "stream")})
+
+    def graph(made, stream=None):
+        stream = Stream() if stream is None else stream
+        return use(device=stream.device, stream=stream)
+
+    for name, fake in dict(Stream=Stream, CUDAGraph=Graph, graph=graph, device=lambda d: use(device=torch.device(d).index),
+                           stream=lambda s: use(device=s.device, stream=s),
+                           current_stream=lambda d=None: Stream(d)).items():
+        monkeypatch.setattr(torch.cuda, name, fake)
+
+    class Pass(P.SecondPass):
+        def __init__(self):
+            self.model = SimpleNamespace(device=torch.device("cuda", 1), shape=P.Shape(vocab=9))
+            self.lanes, self.max_tokens, self.page, self.pages, self.graph = 2, 8, 4, 4, None
+            self.table, self.plan = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(8, 4, 2, dtype=torch.int32)
+            self.uniform, self.logprobs, self.at = torch.zeros(8, 2), torch.zeros(8, 2), torch.zeros(1, dtype=torch.int64)
+            self.settings = {n: torch.zeros(2) for n in ("temperature", "top_k", "top_p", "min_p")}
+            self.drawn = torch.zeros(8, 2, dtype=torch.int32)
+
+        def _step(self):
+            now.seen.append(("step", now.device, now.stream and now.stream.device))
+
+    second = Pass()
+    assert len(second.run([[1, 2]], 2)) == 1
+    assert now.seen == [("step", 1, 1), ("step", 1, 1)] + [("replay", 1)] * 4 and now.device == 0
+    now.seen.clear()
+    second.run([[1]], 1, graph=False)
+    assert now.seen == [("step", 1, None)] * 2

@@ -89,8 +89,9 @@ class LanguageModel:
                 return t.to(dtype).contiguous()
             return _ops.pack_quant(*quantize(t, s.group, dtype))
 
-        self.shape, self.dtype, self.device = shape, dtype, torch.device(device)
+        self.shape, self.dtype = shape, dtype
         self.embed, self.gain, self.head = take("embed"), take("gain"), take("head")
+        self.device = self.embed.device    # with its number, whatever is the current device later
         self.layers = [{name: take(f"{i}.{name}") for name in
                         ("gain1", "qkv", "q_gain", "k_gain", "out", "gain2", "up", "down")} for i in range(s.layers)]
 
@@ -176,16 +177,18 @@ class SecondPass:
         self.at.add_(1)
 
     def _capture(self):
-        """The step as a graph, after one that only idle lanes take part in."""
+        """The step as a graph, after one that only idle lanes take part in.
+        The model's device is the current one."""
         self._load(np.zeros((1, 4, self.lanes), np.int32) + np.array([0, 0, -1, 0], np.int32)[None, :, None])
         side = torch.cuda.Stream(self.model.device)
         side.wait_stream(torch.cuda.current_stream(self.model.device))
         with torch.cuda.stream(side):
             self._step()
         torch.cuda.current_stream(self.model.device).wait_stream(side)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):    # (torch's own capture stream may be another device's)
             self._step()
+        self.graph = graph
 
     def _load(self, plan):
         self.plan[:len(plan)].copy_(torch.from_numpy(np.ascontiguousarray(plan)))
@@ -232,17 +235,18 @@ class SecondPass:
         plan, table = self.plan_lanes(words, new_tokens)
         if not len(plan):
             return []
-        if graph and self.graph is None:
-            self._capture()
-        self._load(plan)
-        self.table.copy_(torch.from_numpy(table))
-        g = torch.Generator()
-        g.manual_seed(seed)
-        self.uniform[:len(plan)].copy_(torch.rand(len(plan), self.lanes, generator=g))
-        for name, value in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
-            self.settings[name].fill_(value)
-        for _ in range(len(plan)):
-            self.graph.replay() if graph else self._step()
+        with torch.cuda.device(self.model.device):    # streams, capture and replay are of the current device
+            if graph and self.graph is None:
+                self._capture()
+            self._load(plan)
+            self.table.copy_(torch.from_numpy(table))
+            g = torch.Generator()
+            g.manual_seed(seed)
+            self.uniform[:len(plan)].copy_(torch.rand(len(plan), self.lanes, generator=g))
+            for name, value in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+                self.settings[name].fill_(value)
+            for _ in range(len(plan)):
+                self.graph.replay() if graph else self._step()
         drawn, logprobs = self.drawn[:len(plan)].cpu().numpy(), self.logprobs[:len(plan)].cpu().numpy()
         answers = []
         for b, w in enumerate(words):
