@@ -537,8 +537,11 @@ int wfst_attend_paged(const wfst_attend_args* args, void* stream);
  * largest one, so results do not depend on any order.  -inf and NaN logits
  * weigh nothing; a lane with no other logit gets token -1, logprob -inf and
  * kept 0; +inf logits share all the weight.  The four settings apply to every
- * lane, or per lane where the array beside them is not NULL.  vocab <= 2^20.
- * Errors: INVALID_ARG, CUDA.
+ * lane, or per lane where the array beside them is not NULL.  A setting for
+ * every lane is refused out of its range (temperature 0 to 3e38, top_k >= 0,
+ * top_p > 0, min_p 0 to 1); one of a lane counts as the range's nearest end
+ * (top_p: the first token alone), NaN as temperature 0, top_p 0 or min_p 1.
+ * vocab <= 2^20.  Errors: INVALID_ARG, CUDA.
  */
 typedef struct {
   const void* logits;

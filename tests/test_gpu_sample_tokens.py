@@ -104,6 +104,29 @@ def test_settings_for_each_lane(W):
           torch.tensor([0.0, 0.1, 0.0, 0.01, 0.5, 0.0, 1.0, 0.2], **dev))
 
 
+def test_settings_of_a_lane_that_are_out_of_range(W):
+    """Nothing is refused on the device: they count as the nearest ones in range."""
+    vocab = 3000
+    x, _ = logits(7, 12, vocab, torch.float32)
+    x[:] = x[0].clone()
+    x[:, 5::7] = -math.inf
+    u = torch.full((12,), 0.37, device="cuda")
+    inf, nan = math.inf, math.nan
+    rows = [(inf, 0, 1.0, 0.0), (3e38, 0, 1.0, 0.0), (-1.0, 0, 1.0, 0.0), (nan, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0),
+            (1.0, -7, 2.0, -0.5), (1.0, 0, 1.0, 0.0), (1.0, 50, -0.3, 0.0), (1.0, 50, nan, 0.0), (1.0, 1, 1.0, 0.0),
+            (1.0, 0, 1.0, 7.0), (1.0, 0, 1.0, nan)]
+    temp, k, p, min_p = zip(*rows)
+    got = W.sample_tokens(x, u, temperature=torch.tensor(temp, device="cuda"),
+                          top_k=torch.tensor(k, device="cuda", dtype=torch.int32),
+                          top_p=torch.tensor(p, device="cuda"), min_p=torch.tensor(min_p, device="cuda"))
+    got = list(zip(*(t.tolist() for t in got)))
+    assert got[0] == got[1] and got[2] == got[3] == got[4] and got[5] == got[6]
+    assert got[7] == got[8] == got[9] == got[10] == got[11] == got[4]
+    host = x[0].cpu().numpy()
+    for b in (0, 1, 4, 6):
+        check_lane(host, float(u[0]), *((3e38,) + rows[b][1:] if b == 0 else rows[b]), *got[b])
+
+
 def test_ends_of_the_uniform_range(W):
     x, _ = logits(2, 4, 999, torch.float32)
     u = torch.tensor([0.0, 1.0 - 2.0 ** -24, 0.5, 2.0 ** -40], device="cuda")

@@ -61,6 +61,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kFixed = 43;
 constexpr float kMost = 3.402823466e38f;
 
+constexpr float kHottest = 3.0e38f;  // temperature at most: its reciprocal is not zero
+
 struct Args {
   const void* logits;
   const float *u, *temp_v, *top_p_v, *min_p_v;
@@ -640,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     temp = 1.f;
     k = 1;
   }
+  temp = fminf(temp, kHottest);
   d.inv_t = fminf(1.f / temp, kMost);
   // the bins reach 32 in y, past which nothing weighs anything, or 24 in x
   d.per_x = fminf((float)kBins / fminf(32.f * temp, 24.f), kMost);
@@ -972,7 +975,7 @@ extern "C" int wfst_sample_tokens(const wfst_sample_args* r, void* stream) {
   if (r->lanes < 0 || r->lanes > (1 << 27)) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: lanes out of range");
   if (r->vocab < 1 || r->vocab > (1 << 20)) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: vocab must be in [1, 2^20]");
   if (r->lanes > 1 && r->stride < r->vocab) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: stride must be >= vocab");
-  if (!r->temperature_v && !(r->temperature >= 0.f && r->temperature <= 3.0e38f))
+  if (!r->temperature_v && !(r->temperature >= 0.f && r->temperature <= kHottest))
     return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: temperature must be >= 0");
   if (!r->top_k_v && r->top_k < 0) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: top_k must be >= 0");
   if (!r->top_p_v && !(r->top_p > 0.f)) return api_fail(WFST_ERR_INVALID_ARG, "sample_tokens: top_p must be > 0");
