@@ -536,7 +536,8 @@ int wfst_attend_paged(const wfst_attend_args* args, void* stream);
  * first largest logit.  Weights are summed as whole multiples of 2^-43 of the
  * largest one, so results do not depend on any order.  -inf and NaN logits
  * weigh nothing; a lane with no other logit gets token -1, logprob -inf and
- * kept 0; +inf logits share all the weight.  The four settings apply to every
+ * kept 0; +inf logits share all the weight (with those of the type's largest
+ * number, if there are any).  The four settings apply to every
  * lane, or per lane where the array beside them is not NULL.  A setting for
  * every lane is refused out of its range (temperature 0 to 3e38, top_k >= 0,
  * top_p > 0, min_p 0 to 1); one of a lane counts as the range's nearest end

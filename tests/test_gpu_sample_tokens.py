@@ -192,6 +192,22 @@ def test_masked_rows_of_a_cluster(W, vocab, dtype):
         assert tokens[0] == tokens[1] == -1 and tokens[2] == vocab - 3 and tokens[7] in (5, vocab // 2, vocab - 1)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [900, 60000, 1000000])
+def test_infinite_logits_leave_no_weight_to_others(W, vocab, dtype):
+    """At any temperature, beside logits next to the type's largest number."""
+    x, u = logits(9, 4, vocab, dtype)
+    large = float(torch.tensor(torch.finfo(dtype).max, dtype=dtype).view(torch.int16 if dtype != torch.float32 else
+                                                                         torch.int32).sub(1).view(dtype))
+    x[1:, ::3] = large
+    x[:2, [17, vocab - 2]] = math.inf
+    for temp in (1.0, 5000.0, 3e38):
+        for kw in (dict(), dict(k=2), dict(p=0.9), dict(k=700, p=0.999, min_p=1e-6), dict(min_p=1e-7)):
+            tokens = check(W, x[:2], u[:2], temp, **kw)[0].tolist()
+            assert tokens[0] in (17, vocab - 2) and tokens[1] in (17, vocab - 2)
+    check(W, x[2:], u[2:], 5000.0, p=0.9)
+
+
 def test_strides_alignment_streams_and_repeats(W):
     """Rows at every alignment, rows of a wider tensor, another stream; the same answer every time."""
     for dtype in (torch.float32, torch.float16):

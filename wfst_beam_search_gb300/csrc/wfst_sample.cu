@@ -75,16 +75,18 @@ struct Args {
   float temp, top_p, min_p;
 };
 
-// NaN counts as -inf, +inf as its type's largest number.
+// NaN counts as -inf, +inf as its type's largest number (and a row that has it is
+// drawn from at next to no temperature, so that no other logit weighs anything).
 template <typename T>
 constexpr float kLargest = kMost;
 template <>
 constexpr float kLargest<__half> = 65504.f;
 template <>
 constexpr float kLargest<__nv_bfloat16> = 3.38953138925e38f;
+constexpr float kCold = 1e-36f;
 template <typename T>
-__device__ __forceinline__ float canonical(T v) {
-  return fminf(fmaxf(to_f32(v), -INFINITY), kLargest<T>);
+__device__ __forceinline__ float finite(float v) {
+  return fminf(v, kLargest<T>);
 }
 // Larger logit, larger key; -0 and +0 have one.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -126,17 +128,17 @@ struct Row {
   static constexpr int VEC = 16 / (int)sizeof(T);
   const T* p;
   int vocab, pad;  // pad: elements between the 16-byte boundary before p and p
-  // granule i: elements [i * VEC - pad, i * VEC - pad + VEC), -inf outside
+  // granule i: elements [i * VEC - pad, i * VEC - pad + VEC), -inf outside and for NaN
   __device__ __forceinline__ void load(int i, float (&v)[VEC]) const {
     const int e = i * VEC - pad;
     if (e >= 0 && e + VEC <= vocab) {
       const uint4 raw = *reinterpret_cast<const uint4*>(p + e);
       const T* r = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) v[j] = canonical(r[j]);
+      for (int j = 0; j < VEC; j++) v[j] = fmaxf(to_f32(r[j]), -INFINITY);
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; j++) v[j] = e + j >= 0 && e + j < vocab ? canonical(p[e + j]) : -INFINITY;
+      for (int j = 0; j < VEC; j++) v[j] = e + j >= 0 && e + j < vocab ? fmaxf(to_f32(p[e + j]), -INFINITY) : -INFINITY;
     }
   }
 };
@@ -305,6 +307,8 @@ struct Draw {
       for (int j = 0; j < VEC; j++) v[j] = to_f32(r[j]);
     } else {
       row.load(i, v);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[j] = finite<T>(v[j]);
     }
   }
   // f(element, logit) for each element of this warp's run of granules and for
@@ -643,32 +647,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     k = 1;
   }
   temp = fminf(temp, kHottest);
-  d.inv_t = fminf(1.f / temp, kMost);
-  // the bins reach 32 in y, past which nothing weighs anything, or 24 in x
-  d.per_x = fminf((float)kBins / fminf(32.f * temp, 24.f), kMost);
   const bool by_k = k > 0 && k < a.vocab, by_p = top_p < 1.f || top_p != top_p, by_min = min_p > 0.f;
 
   // ---- the largest logit; the row comes into shared memory
   float most = -INFINITY;  // this thread's
-  if (a.staged) {
-    uint4* stage = reinterpret_cast<uint4*>(raw_smem + sizeof(Shared));
+  uint4* stage = a.staged ? reinterpret_cast<uint4*>(raw_smem + sizeof(Shared)) : nullptr;
 #pragma unroll 4
-    for (int i = d.lo + lane; i < d.hi; i += 32) {
-      float v[VEC];
-      d.row.load(i, v);
-      uint4 raw;
-      T* r = reinterpret_cast<T*>(&raw);
+  for (int i = d.lo + lane; i < d.hi; i += 32) {
+    float v[VEC];
+    d.row.load(i, v);
+    uint4 raw;
+    T* r = reinterpret_cast<T*>(&raw);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        r[j] = from_f32<T>(v[j]);
-        most = fmaxf(most, v[j]);
-      }
-      stage[i - d.first] = raw;  // read back by this lane alone
+    for (int j = 0; j < VEC; j++) {
+      r[j] = from_f32<T>(finite<T>(v[j]));
+      most = fmaxf(most, v[j]);
     }
-    d.stage = stage;
-  } else {
-    d.each([&](int, float x) { most = fmaxf(most, x); });
+    if (stage) stage[i - d.first] = raw;  // read back by this lane alone
   }
+  d.stage = stage;
   d.clear_hist();
   float top = most;
 #pragma unroll
@@ -685,7 +682,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   d.sync();
   top = sh->box_top[0];
   for (int r = 1; r < C; r++) top = fmaxf(top, sh->box_top[r]);
-  d.top = top;
+  if (top == INFINITY) temp = kCold;
+  d.top = top = finite<T>(top);
+  most = finite<T>(most);
+  d.inv_t = fminf(1.f / temp, kMost);
+  // the bins reach 32 in y, past which nothing weighs anything, or 24 in x
+  d.per_x = fminf((float)kBins / fminf(32.f * temp, 24.f), kMost);
   if (top == -INFINITY) {  // nothing to draw from
     if (rank == 0 && tid == 0) {
       a.token[b] = -1;
