@@ -158,3 +158,19 @@ def test_a_pass_runs_on_its_models_device(monkeypatch):
     now.seen.clear()
     second.run([[1]], 1, graph=False)
     assert now.seen == [("step", 1, None)] * 2
+
+
+def test_settings_of_a_pass_are_checked():
+    from types import SimpleNamespace
+
+    from wfst_beam_search_gb300 import second_pass as P
+    second = P.SecondPass.__new__(P.SecondPass)
+    second.model, second.lanes, second.max_tokens, second.page, second.pages = SimpleNamespace(shape=P.Shape(9)), 2, 8, 4, 4
+    second.table = torch.zeros(2, 2, dtype=torch.int32)
+    assert second.run([], 1, temperature=0, top_k=3, top_p=1.5, min_p=1.0) == []
+    nan = float("nan")
+    for name, values in dict(temperature=(-1.0, nan, float("inf")), top_k=(-1, 2 ** 31), top_p=(0.0, -0.5, nan),
+                             min_p=(-0.1, 1.1, nan)).items():
+        for value in values:
+            with pytest.raises(ValueError, match=name):
+                second.run([], 1, **{name: value})

@@ -232,6 +232,11 @@ class SecondPass:
         them: [{"tokens", "logprobs"}, ...].  The same seed draws the same.
         An answer ends where its logits hold no number (weights or activations
         that left the type's range): tokens -1, logprobs -inf from there on."""
+        # (``sample_tokens`` refuses numbers, but here they reach it as a value per lane)
+        for name, fits in (("temperature", 0 <= temperature <= 3e38), ("top_k", 0 <= top_k < 2 ** 31), ("top_p", top_p > 0),
+                           ("min_p", 0 <= min_p <= 1)):
+            if not fits:
+                raise ValueError(f"{name} is out of range")
         plan, table = self.plan_lanes(words, new_tokens)
         if not len(plan):
             return []
