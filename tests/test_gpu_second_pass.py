@@ -206,3 +206,44 @@ def test_calls_follow_each_other(P, lanes, scale):
     for _ in range(5):
         got = chain(lambda: None)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gradients_are_refused_and_writes_are_known(P):
+    """No operator gives a gradient, so none cuts one off in silence; what is
+    written in place counts as changed."""
+    import wfst_beam_search_gb300 as W
+    dev = dict(device="cuda")
+    x = torch.randn(2, 64, **dev).half()
+    w = W.pack_quant(torch.zeros(64, 32, dtype=torch.uint8, **dev), torch.ones(64, 1, **dev).half())
+    i, one = torch.zeros(2, dtype=torch.int32, **dev), torch.ones(2, dtype=torch.int32, **dev)
+    pages, rotary = torch.zeros(2, 2, 16, 1, 64, **dev).half(), torch.zeros(4, 64, **dev)
+    slots = torch.arange(2, dtype=torch.int32, **dev)
+
+    def calls(x, out, kc, vc):
+        h = x[:, None]
+        yield lambda: W.matvec_quant(x, w, out=out)
+        yield lambda: W.norm_rotate(h, h, h, i, rotary, None, None, kc, vc, slots, out=out[:, None])
+        yield lambda: W.attend_paged(h, kc, vc, i[:, None], one, out=out[:, None])
+        yield lambda: W.sample_tokens(x, torch.zeros(2, **dev))
+
+    asks = x.clone().requires_grad_()
+    for out, kc, vc, writes in [(torch.empty_like(x), pages[0].clone(), pages[1].clone(), [(1, 0), (1, 1), (1, 0), (0, 0)])]:
+        for call in calls(asks, out, kc, vc):
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+            with torch.no_grad():
+                call()
+        for call, (of_out, of_cache) in zip(calls(x, out, kc, vc), writes):
+            before = out._version, kc._version, vc._version
+            call()
+            assert (out._version, kc._version, vc._version) == (before[0] + of_out, before[1] + of_cache, before[2] + of_cache)
+    with torch.inference_mode():
+        for call in calls(x.clone(), torch.empty_like(x), *pages.clone()):
+            call()
+    with pytest.raises(ValueError, match="gradient"):
+        W.pack_quant(torch.zeros(64, 32, dtype=torch.uint8, **dev), torch.ones(64, 1, **dev).half().requires_grad_())
+    # weights that are parameters
+    s = shape(P)
+    tensors = {n: torch.nn.Parameter(t) for n, t in P.random_tensors(s).items()}
+    want = P.SecondPass(P.LanguageModel.random(s), 1, 16).run([[1, 2]], 3)
+    assert P.SecondPass(P.LanguageModel(s, tensors), 1, 16).run([[1, 2]], 3) == want

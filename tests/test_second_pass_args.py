@@ -174,3 +174,17 @@ def test_settings_of_a_pass_are_checked():
         for value in values:
             with pytest.raises(ValueError, match=name):
                 second.run([], 1, **{name: value})
+
+
+def test_inputs_that_require_a_gradient_are_refused():
+    h = torch.zeros(2, 64, dtype=torch.float16, requires_grad=True)
+    i = torch.zeros(2, dtype=torch.int32)
+    pages = torch.zeros(1, 16, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="gradient"):
+        W.sample_tokens(h, torch.zeros(2))
+    with pytest.raises(ValueError, match="gradient"):
+        W.attend_paged(h[:, None], pages, pages, i[:, None], i)
+    with pytest.raises(ValueError, match="gradient"):
+        W.norm_rotate(h[:, None], h[:, None], h[:, None], i, torch.zeros(4, 64), None, None, pages, pages, i)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        W.sample_tokens(h, torch.zeros(2))

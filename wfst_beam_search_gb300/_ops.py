@@ -12,7 +12,8 @@ limits).  A call runs on ``stream``, by default torch's current stream of the
 tensors' device; results are allocated on the stream the call runs on.  Inputs
 that belong to another stream are the caller's to order, as anywhere in torch.
 Wrong types, shapes or layouts raise ``TypeError`` or ``ValueError``, what the
-library refuses raises ``WfstError``.
+library refuses raises ``WfstError``.  There are no backward passes: an input
+that requires a gradient is refused while gradients are recorded.
 
 A call for one token is over on the GPU before Python has asked its arguments
 one by one what they are, so ``csrc/ops_binding.cpp`` asks them all and makes
@@ -69,6 +70,8 @@ def _explain(dev, tensors):
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, and there is none to give: detach it, or use torch.no_grad()")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.get_device() != dev or dev < 0:

@@ -13,6 +13,7 @@
 #include <cmath>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -42,10 +43,12 @@ struct Reader {
   int dev = -1;
   ScalarType type = ScalarType::Undefined;
 
-  // a tensor of `dim` axes on the call's device, which the first one sets
+  // a tensor of `dim` axes on the call's device, which the first one sets; none
+  // that waits for a gradient, since there is none to give
   const Tensor* tensor(PyObject* o, int64_t dim, ScalarType t) {
     if (!THPVariable_Check(o)) return fail();
     const Tensor& x = THPVariable_Unpack(o);
+    if (x.requires_grad() && at::GradMode::is_enabled()) return fail();
     if (!x.is_cuda() || x.layout() != at::kStrided || x.dim() != dim || x.scalar_type() != t) return fail();
     if (dev < 0) dev = x.get_device();
     if (x.get_device() != dev) return fail();
@@ -81,6 +84,11 @@ bool unit(const Tensor& t) { return t.stride(-1) == 1 || t.size(-1) < 2; }
 
 Tensor empty(at::IntArrayRef size, ScalarType t, int dev) {
   return at::detail::empty_cuda(size, t, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+}
+
+// Lets torch know that a caller's tensor has other values now.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 PyObject* look() { return PyLong_FromLong(kLook); }
@@ -132,6 +140,7 @@ PyObject* matvec_quant(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   a.rows = r.i32(rows);
   if (!r.ok) return look();
   if (const int rc = call(wfst_matvec_quant, a, r.dev)) return PyLong_FromLong(rc);
+  if (arg[3] != Py_None) written(y);
   return THPVariable_Wrap(std::move(y));
   END_HANDLE_TH_ERRORS
 }
@@ -198,6 +207,8 @@ PyObject* norm_rotate(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   a.page_size = r.i32(kp->size(1));
   if (!r.ok) return look();
   if (const int rc = call(wfst_norm_rotate, a, r.dev)) return PyLong_FromLong(rc);
+  written(*kp), written(*vp);
+  if (arg[12] != Py_None) written(y);
   return THPVariable_Wrap(std::move(y));
   END_HANDLE_TH_ERRORS
 }
@@ -268,6 +279,7 @@ PyObject* attend_paged(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   a.page_size = r.i32(kp->size(1));
   if (!r.ok) return look();
   if (const int rc = call(wfst_attend_paged, a, r.dev)) return PyLong_FromLong(rc);
+  if (arg[10] != Py_None) written(y);
   if (!with_lse) return THPVariable_Wrap(std::move(y));
   PyObject* both = PyTuple_New(2);
   if (!both) return nullptr;

@@ -84,7 +84,7 @@ class LanguageModel:
                 raise ValueError(f"{name} must be a tensor of shape {size}")
 
         def take(name):
-            t = tensors[name].to(device)
+            t = tensors[name].detach().to(device)
             if t.dim() == 1 or name == "embed":
                 return t.to(dtype).contiguous()
             return _ops.pack_quant(*quantize(t, s.group, dtype))
