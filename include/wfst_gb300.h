@@ -506,9 +506,9 @@ int wfst_norm_rotate(const wfst_rotate_args* args, void* stream);
  * sees nothing has o = 0 and lse = -inf.  head_dim: 64, 128 or 256.  q, the
  * pages and the workspace are 16-byte aligned, strides of q and the pages
  * multiples of 8.
- * workspace: wfst_attend_size's bytes, zeros before its first use; calls that
- * use the same one must follow each other on a stream, and each leaves it
- * ready for the next.  lanes = 0 does nothing.  Errors: INVALID_ARG, CUDA.
+ * workspace: wfst_attend_size's bytes, of which the first WFST_ATTEND_ZEROED
+ * have to be zeros before its first use; calls that use the same one must
+ * follow each other on a stream, and each leaves it ready for the next.  lanes = 0 does nothing.  Errors: INVALID_ARG, CUDA.
  */
 typedef struct {
   const void *q, *k_pages, *v_pages; /* q: [lanes, q_heads, head_dim] */
@@ -521,6 +521,7 @@ typedef struct {
   int32_t device, dtype, lanes, q_heads, kv_heads, head_dim, table_width, num_pages, page_size, window, sinks;
   float scale;
 } wfst_attend_args;
+#define WFST_ATTEND_ZEROED 4096
 int wfst_attend_size(int64_t* bytes);
 int wfst_attend_paged(const wfst_attend_args* args, void* stream);
 

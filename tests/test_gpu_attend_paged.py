@@ -103,6 +103,16 @@ def test_splits(W, ws, lens):
     check(*W.attend_paged(*a, workspace=ws, with_lse=True), *a, 128 ** -0.5)
 
 
+def test_a_workspace_whose_parts_hold_anything(W):
+    """Only its first bytes have to be zeros; the parts are written before they are read."""
+    a = make(3, [20000, 1, 30011, 0, 700], 24, 2, 128, 32, torch.bfloat16)
+    ws = W.attend_workspace("cuda")
+    ws[W.WFST_ATTEND_ZEROED:] = 255                      # NaN
+    for _ in range(2):
+        check(*W.attend_paged(*a, workspace=ws, with_lse=True), *a, 128 ** -0.5)
+        assert not bool(ws[:W.WFST_ATTEND_ZEROED].any())
+
+
 def test_large_scores_and_other_scale(W, ws):
     """Weights that are nearly all on one key, and a negative scale."""
     a = make(5, [700, 64, 33], 8, 4, 64, 16, torch.float16, spread=30.0)

@@ -188,3 +188,19 @@ def test_inputs_that_require_a_gradient_are_refused():
         W.norm_rotate(h[:, None], h[:, None], h[:, None], i, torch.zeros(4, 64), None, None, pages, pages, i)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         W.sample_tokens(h, torch.zeros(2))
+
+
+def test_a_workspace_is_zeroed_where_it_has_to_be(monkeypatch):
+    import os
+    import re
+    header = open(os.path.join(_build.INCLUDE, "wfst_gb300.h")).read()
+    assert int(re.search(r"#define WFST_ATTEND_ZEROED (\d+)", header).group(1)) == W.WFST_ATTEND_ZEROED
+    full = torch.full
+
+    def garbage(size, dtype, device):
+        return full((size,), 255, dtype=dtype, device=device)
+
+    monkeypatch.setattr(torch, "empty", garbage)
+    ws = W.attend_workspace("cpu")
+    assert ws.shape == (W.wfst_attend_size(),)
+    assert not bool(ws[:W.WFST_ATTEND_ZEROED].any()) and bool((ws[W.WFST_ATTEND_ZEROED:] == 255).all())

@@ -21,6 +21,7 @@ from . import _build
 
 WFST_OK = 0
 WFST_F32, WFST_F16, WFST_BF16 = 0, 1, 2
+WFST_ATTEND_ZEROED = 4096
 OVF_ARENA, OVF_KEPT, OVF_PATH = 4, 16, 32
 REC_EPS, REC_FINAL, REC_REDIRECT = 1, 2, 4
 STAT_NAMES = ["frames", "arcs_expanded", "sum_n", "sum_D", "sum_a", "sum_m", "eps",

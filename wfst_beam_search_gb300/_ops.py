@@ -28,8 +28,8 @@ import struct
 
 import torch
 
-from . import (WFST_BF16, WFST_F16, WFST_F32, _build, _check, load, wfst_attend_size, wfst_quant_pack,
-               wfst_quant_size)
+from . import (WFST_ATTEND_ZEROED, WFST_BF16, WFST_F16, WFST_F32, _build, _check, load, wfst_attend_size,
+               wfst_quant_pack, wfst_quant_size)
 
 _HALF = {torch.float16: WFST_F16, torch.bfloat16: WFST_BF16}
 _ANY = {torch.float32: WFST_F32, **_HALF}
@@ -206,7 +206,9 @@ def attend_workspace(device=None):
     """The workspace of ``attend_paged`` on a device.  Calls that share one
     must follow each other on a stream; make one for each stream that attends
     at the same time."""
-    return torch.zeros(wfst_attend_size(), dtype=_U8, device="cuda" if device is None else device)
+    workspace = torch.empty(wfst_attend_size(), dtype=_U8, device="cuda" if device is None else device)
+    workspace[:WFST_ATTEND_ZEROED].zero_()
+    return workspace
 
 
 def attend_paged(q, k_pages, v_pages, page_table, lengths, scale=None, window=0, sinks=0, workspace=None,
@@ -220,15 +222,11 @@ def attend_paged(q, k_pages, v_pages, page_table, lengths, scale=None, window=0,
     entries of tokens that are not seen are never read.  Returns o [lanes,
     q_heads, d], with ``with_lse`` also the float32 [lanes, q_heads] log of
     the sum of exponentials.  Without ``workspace`` (see
-    ``attend_workspace``) the call makes one of its own."""
+    ``attend_workspace``) the call makes one of its own, 34 MB."""
     if stream is not None:
         with torch.cuda.stream(_as_stream(stream, q.device)):
             return attend_paged(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, workspace, with_lse,
                                 out)
-    if workspace is None:
-        _half_type("q", q.dtype)
-        _explain(q.get_device(), [("q", q, q.dtype, q.shape)])
-        workspace = attend_workspace(q.device)
     y = _binding.attend_paged(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, workspace, with_lse, out)
     if y.__class__ is int:
         def why():
@@ -241,7 +239,8 @@ def attend_paged(q, k_pages, v_pages, page_table, lengths, scale=None, window=0,
             _explain(q.get_device(), [
                 ("q", q, t, q.shape), ("k_pages", k_pages, t, cache), ("v_pages", v_pages, t, cache),
                 ("page_table", page_table, _I32, (lanes, page_table.shape[1])), ("lengths", lengths, _I32, (lanes,)),
-                ("workspace", workspace, _U8, (max(workspace.numel(), wfst_attend_size()),)), ("out", out, t, q.shape)])
+                ("workspace", workspace, _U8, (max(workspace.numel(), wfst_attend_size()),) if workspace is not None else ()),
+                ("out", out, t, q.shape)])
             _last_axis(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, out=out)
             _contiguous(lengths=lengths, workspace=workspace)
         _refused(y, why)

@@ -221,7 +221,8 @@ PyObject* attend_paged(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   const Tensor* q = r.first(arg[0], 3);
   if (!q || type_code(r.type) <= 0) return look();
   const Tensor *kp = r.tensor(arg[1], 4, r.type), *vp = r.tensor(arg[2], 4, r.type);
-  const Tensor *table = r.tensor(arg[3], 2, ScalarType::Int), *ws = r.tensor(arg[8], 1, ScalarType::Byte);
+  const Tensor* table = r.tensor(arg[3], 2, ScalarType::Int);
+  const Tensor* ws = arg[8] == Py_None ? nullptr : r.tensor(arg[8], 1, ScalarType::Byte);
   if (!r.ok) return look();
   const int64_t lanes = q->size(0), hq = q->size(1), d = q->size(2);
   static const int64_t ws_bytes = [] {
@@ -230,7 +231,7 @@ PyObject* attend_paged(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     return n;
   }();
   if (kp->size(3) != d || vp->sizes() != kp->sizes() || table->size(0) != lanes || !unit(*q) || !unit(*kp) ||
-      !unit(*vp) || !unit(*table) || !ws->is_contiguous() || ws->numel() < ws_bytes)
+      !unit(*vp) || !unit(*table) || (ws && (!ws->is_contiguous() || ws->numel() < ws_bytes)))
     return look();
   wfst_attend_args a = {};
   a.lengths = (const int32_t*)r.vector(arg[4], lanes, ScalarType::Int);
@@ -247,6 +248,12 @@ PyObject* attend_paged(PyObject*, PyObject* const* arg, Py_ssize_t count) {
     const Tensor* out = r.tensor(arg[10], 3, r.type);
     if (!out || out->sizes() != q->sizes() || !unit(*out)) return look();
     y = *out;
+  }
+  Tensor own;
+  if (!ws) {  // as attend_workspace makes it
+    own = empty({ws_bytes}, ScalarType::Byte, r.dev);
+    own.narrow(0, 0, WFST_ATTEND_ZEROED).zero_();
+    ws = &own;
   }
   if (with_lse) {
     lse = empty({lanes, hq}, ScalarType::Float, r.dev);

@@ -53,6 +53,7 @@ constexpr float kLift = std::is_same_v<T, __half> ? 15.f : 0.f;
 // workspace: counters [kMaxGrid], then per CTA two parts of {m, l, o}
 constexpr int64_t kPartFloats = 2 * kColsMost + kWidthMost * kColsMost;
 constexpr int64_t kCounterBytes = kMaxGrid * 4;
+static_assert(kCounterBytes == WFST_ATTEND_ZEROED, "the parts are written before they are read");
 
 struct Args {
   const void *q, *kc, *vc;
