@@ -1,8 +1,8 @@
 """Compile the CUDA decoder library for GB300 (sm_103a), in tree.
 
 Ten translation units are compiled in parallel and linked into
-``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch and Python's
-headers are installed, ``ops_binding.so`` is compiled beside it: the
+``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch with CUDA and
+Python's headers are installed, ``ops_binding.so`` is compiled beside it: the
 second-pass operators' path from torch tensors into that library.
 """
 from __future__ import annotations
@@ -34,10 +34,27 @@ def nvcc() -> str:
 
 
 def _torch():
-    """torch's folder; None where it or Python's headers are missing, and the decoder is built alone."""
+    """torch's folder; None where it, its CUDA part or Python's headers are missing, and the decoder is built alone."""
     spec = importlib.util.find_spec("torch")
-    headers = os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
-    return os.path.dirname(spec.origin) if spec and spec.origin and headers else None
+    if not (spec and spec.origin and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
+        return None
+    folder = os.path.dirname(spec.origin)
+    needed = ("lib/libc10_cuda.so", "lib/libtorch_cuda.so", "include/c10/cuda/CUDAStream.h")
+    return folder if all(os.path.exists(os.path.join(folder, *n.split("/"))) for n in needed) else None
+
+
+def _made_for(torch):
+    """What the binding's binary interface goes by: this Python and this torch."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{torch}\n{f.read()}"
+
+
+def _stamp():
+    try:
+        with open(BINDING + ".made_for") as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _inputs():
@@ -49,8 +66,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    made = [LIB, BINDING] if _torch() else [LIB]
-    if not all(map(os.path.exists, made)):
+    torch = _torch()
+    made = [LIB, BINDING] if torch else [LIB]
+    if not all(map(os.path.exists, made)) or (torch and _stamp() != _made_for(torch)):
         return False
     t = min(map(os.path.getmtime, made))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -98,6 +116,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, BINDING)
+        with open(BINDING + ".made_for", "w") as f:
+            f.write(_made_for(torch))
     if verbose:
         for _, log in results:
             print(log)
