@@ -204,3 +204,29 @@ def test_a_workspace_is_zeroed_where_it_has_to_be(monkeypatch):
     ws = W.attend_workspace("cpu")
     assert ws.shape == (W.wfst_attend_size(),)
     assert not bool(ws[:W.WFST_ATTEND_ZEROED].any()) and bool((ws[W.WFST_ATTEND_ZEROED:] == 255).all())
+
+
+def test_what_is_no_tensor_is_a_type_error():
+    h = torch.zeros(2, 1, 64, dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    pages, table = torch.zeros(1, 16, 1, 64, dtype=torch.float16), torch.zeros(4, 64)
+    codes, scales = torch.zeros(4, 32, dtype=torch.uint8), torch.ones(4, 1).half()
+    calls = [(W.pack_quant, dict(codes=codes, scales=scales)),
+             (W.norm_rotate, dict(q=h, k=h, v=h, positions=i, table=table, q_gain=None, k_gain=None, k_pages=pages,
+                                  v_pages=pages, slots=i)),
+             (W.attend_paged, dict(q=h, k_pages=pages, v_pages=pages, page_table=i[:, None], lengths=i)),
+             (W.sample_tokens, dict(logits=h[:, 0], uniform=torch.zeros(2)))]
+    for call, args in calls:
+        for name, value in args.items():
+            if value is not None:
+                for bad in (None, [1, 2], 3.0):
+                    with pytest.raises(TypeError, match=name):
+                        call(**{**args, name: bad})
+        first = next(iter(args))
+        with pytest.raises(TypeError, match=first):
+            call(**{**args, first: None}, stream=0)
+    with pytest.raises(TypeError, match="workspace"):
+        W.attend_paged(**calls[2][1], workspace=7)
+    for x, weights in ((None, None), (h[:, 0], None), (h[:, 0], codes)):
+        with pytest.raises(TypeError):
+            W.matvec_quant(x, weights)

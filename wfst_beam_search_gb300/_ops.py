@@ -56,10 +56,18 @@ def _load_binding():
 _binding = _load_binding()
 
 
-def _as_stream(stream, device):
+def _tensors(**named):
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+
+
+def _on(stream, **first):
+    """The context in which a call runs on ``stream``; ``first``: a tensor of its device."""
+    _tensors(**first)
     if isinstance(stream, int):
-        return torch.cuda.ExternalStream(stream, device=device)
-    return stream
+        stream = torch.cuda.ExternalStream(stream, device=next(iter(first.values())).device)
+    return torch.cuda.stream(stream)
 
 
 def _explain(dev, tensors):
@@ -126,8 +134,9 @@ def pack_quant(codes, scales, zeros=None, stream=None) -> QuantMatrix:
     and zeros: float16 or bfloat16 [n, k / G] with G 32, 64, 128 or 256
     (zeros None: 8 everywhere).  Done once per matrix."""
     if stream is not None:
-        with torch.cuda.stream(_as_stream(stream, codes.device)):
+        with _on(stream, codes=codes):
             return pack_quant(codes, scales, zeros)
+    _tensors(codes=codes, scales=scales)
     dev = codes.get_device()
     _half_type("scales", scales.dtype)
     if codes.dim() != 2 or scales.dim() != 2:
@@ -149,11 +158,14 @@ def matvec_quant(x, weights: QuantMatrix, bias=None, out=None, stream=None):
     [rows, n] of x's type, which is the scales' type.  Made for few rows (one
     new token per lane); any number is right."""
     if stream is not None:
-        with torch.cuda.stream(_as_stream(stream, x.device)):
+        with _on(stream, x=x):
             return matvec_quant(x, weights, bias, out)
-    y = _binding.matvec_quant(x, weights.spec, bias, out)
+    y = _binding.matvec_quant(x, getattr(weights, "spec", None), bias, out)
     if y.__class__ is int:
         def why():
+            _tensors(x=x)
+            if not isinstance(weights, QuantMatrix):
+                raise TypeError("weights must be a QuantMatrix (see pack_quant)")
             t, dev, n = weights.dtype, weights.device, weights.n
             rows = x.shape[0] if x.dim() else 0
             _explain(dev, [("x", x, t, (rows, weights.k)), ("bias", bias, t, (n,)), ("out", out, t, (rows, n))])
@@ -177,12 +189,13 @@ def norm_rotate(q, k, v, positions, table, q_gain, k_gain, k_pages, v_pages, slo
     place; negative: the token's k and v are not kept).  Pairs are (i, i +
     rot/2), or (2i, 2i + 1) if ``interleaved``.  ``out`` may be q itself."""
     if stream is not None:
-        with torch.cuda.stream(_as_stream(stream, q.device)):
+        with _on(stream, q=q):
             return norm_rotate(q, k, v, positions, table, q_gain, k_gain, k_pages, v_pages, slots, eps, interleaved,
                                out)
     y = _binding.norm_rotate(q, k, v, positions, table, q_gain, k_gain, k_pages, v_pages, slots, eps, interleaved, out)
     if y.__class__ is int:
         def why():
+            _tensors(q=q, k=k, v=v, positions=positions, table=table, k_pages=k_pages, v_pages=v_pages, slots=slots)
             _half_type("q", q.dtype)
             if q.dim() != 3 or k.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
                 raise ValueError("q, k and v must be [tokens, heads, d], pages [pages, page_size, heads, d], table "
@@ -224,22 +237,24 @@ def attend_paged(q, k_pages, v_pages, page_table, lengths, scale=None, window=0,
     the sum of exponentials.  Without ``workspace`` (see
     ``attend_workspace``) the call makes one of its own, 34 MB."""
     if stream is not None:
-        with torch.cuda.stream(_as_stream(stream, q.device)):
+        with _on(stream, q=q):
             return attend_paged(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, workspace, with_lse,
                                 out)
     y = _binding.attend_paged(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, workspace, with_lse, out)
     if y.__class__ is int:
         def why():
+            _tensors(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, lengths=lengths,
+                     **({} if workspace is None else {"workspace": workspace}))
             _half_type("q", q.dtype)
             if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2:
                 raise ValueError("q must be [lanes, heads, d], pages [pages, page_size, heads, d], page_table "
                                  "[lanes, width]")
             t, (lanes, _, d) = q.dtype, q.shape
-            cache = (*k_pages.shape[:3], d)
+            cache, room = (*k_pages.shape[:3], d), 0 if workspace is None else workspace.numel()
             _explain(q.get_device(), [
                 ("q", q, t, q.shape), ("k_pages", k_pages, t, cache), ("v_pages", v_pages, t, cache),
                 ("page_table", page_table, _I32, (lanes, page_table.shape[1])), ("lengths", lengths, _I32, (lanes,)),
-                ("workspace", workspace, _U8, (max(workspace.numel(), wfst_attend_size()),) if workspace is not None else ()),
+                ("workspace", workspace, _U8, (max(room, wfst_attend_size()),)),
                 ("out", out, t, q.shape)])
             _last_axis(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, out=out)
             _contiguous(lengths=lengths, workspace=workspace)
@@ -259,11 +274,12 @@ def sample_tokens(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.
     ``top_k`` int32).  top_k 0, top_p 1 and min_p 0 keep everything,
     temperature 0 takes the first largest logit."""
     if stream is not None:
-        with torch.cuda.stream(_as_stream(stream, logits.device)):
+        with _on(stream, logits=logits):
             return sample_tokens(logits, uniform, temperature, top_k, top_p, min_p)
     y = _binding.sample_tokens(logits, uniform, temperature, top_k, top_p, min_p)
     if y.__class__ is int:
         def why():
+            _tensors(logits=logits, uniform=uniform)
             if logits.dtype not in _ANY:
                 raise TypeError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
             if logits.dim() != 2:
