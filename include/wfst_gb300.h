@@ -503,7 +503,9 @@ int wfst_norm_rotate(const wfst_rotate_args* args, void* stream);
  * page_size].  q_heads is a multiple of kv_heads: query head h reads
  * key-value head h / (q_heads / kv_heads).  o = softmax(scale * q k^T) v;
  * lse (may be NULL) receives the log of the sum of exponentials.  A lane that
- * sees nothing has o = 0 and lse = -inf.  head_dim: 64, 128 or 256.  q, the
+ * sees nothing has o = 0 and lse = -inf.  A seen value that is infinite may make
+ * NaN of its element of o (its weight is held in parts).  o may be q, with the
+ * same strides; otherwise nothing that is written may overlap what is read.  head_dim: 64, 128 or 256.  q, the
  * pages and the workspace are 16-byte aligned, strides of q and the pages
  * multiples of 8.
  * workspace: wfst_attend_size's bytes, of which the first WFST_ATTEND_ZEROED

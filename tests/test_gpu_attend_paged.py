@@ -217,6 +217,32 @@ def test_infinities_and_nan_in_seen_places(W, ws):
     check(o, lse, q, kc2, vc, table, n, 0.125, seen=seen)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lens,hq,hkv,d", [([30000], 16, 2, 64), ([9000, 1, 0, 20011, 3], 40, 2, 128), ([130] * 331, 6, 2, 256),
+                                           ([70, 64, 5000], 4, 4, 64)])
+def test_into_the_queries_themselves(W, ws, lens, hq, hkv, d, dtype):
+    """Lanes that many CTAs share, and many lanes of one CTA: all have read a
+    head's query before its result is written."""
+    q, kc, vc, table, n = make(len(lens), lens, hq, hkv, d, 32, dtype)
+    for shift in (0, 8):                # heads on cache lines of their own, and across them
+        for _ in range(5):
+            room = torch.zeros(len(lens) * hq * d + 8, device="cuda", dtype=dtype)
+            x = room[shift:shift + q.numel()].view(q.shape).copy_(q)
+            want = W.attend_paged(x, kc, vc, table, n, workspace=ws, with_lse=True)
+            got = W.attend_paged(x, kc, vc, table, n, workspace=ws, with_lse=True, out=x)
+            assert got[0] is x and torch.equal(x, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_an_infinite_value_stays_in_its_element(W, ws):
+    q, kc, vc, table, n = make(12, [50, 3000], 4, 2, 64, 16, torch.bfloat16)
+    clean = W.attend_paged(q, kc, vc, table, n, workspace=ws)
+    vc[table[1, 1].long(), 3, 1, 5] = math.inf
+    o = W.attend_paged(q, kc, vc, table, n, workspace=ws)
+    assert not bool(o[1, 2:, 5].isfinite().any())
+    o[1, 2:, 5] = clean[1, 2:, 5]
+    assert torch.equal(o, clean)
+
+
 def test_layouts_streams_and_repeats(W, ws):
     """Heads before places, q and o as parts of wider tensors, a table with
     longer rows, another stream with a workspace of its own; the same bits

@@ -232,8 +232,8 @@ def attend_paged(q, k_pages, v_pages, page_table, lengths, scale=None, window=0,
     of strides; page_table int32 [lanes, width]; lengths int32 [lanes], the
     new token among them.  ``scale`` is 1/sqrt(d) by default.  With ``window``
     a lane sees its last ``window`` tokens and the first ``sinks`` ones; table
-    entries of tokens that are not seen are never read.  Returns o [lanes,
-    q_heads, d], with ``with_lse`` also the float32 [lanes, q_heads] log of
+    entries of tokens that are not seen are never read.  ``out`` may be q
+    itself.  Returns o [lanes, q_heads, d], with ``with_lse`` also the float32 [lanes, q_heads] log of
     the sum of exponentials.  Without ``workspace`` (see
     ``attend_workspace``) the call makes one of its own, 34 MB."""
     if stream is not None:
