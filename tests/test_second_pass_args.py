@@ -230,3 +230,17 @@ def test_what_is_no_tensor_is_a_type_error():
     for x, weights in ((None, None), (h[:, 0], None), (h[:, 0], codes)):
         with pytest.raises(TypeError):
             W.matvec_quant(x, weights)
+
+
+def test_a_copied_matrix_points_to_its_own_memory():
+    import copy
+    import io
+    import pickle
+    w = W.QuantMatrix(torch.arange(64, dtype=torch.uint8), 16, 64, 64, 0, torch.float16)
+    file = io.BytesIO()
+    torch.save(w, file)
+    file.seek(0)
+    for other in (copy.deepcopy(w), pickle.loads(pickle.dumps(w)), torch.load(file, weights_only=False)):
+        assert torch.equal(other.packed, w.packed) and other.packed.data_ptr() != w.packed.data_ptr()
+        assert other.ptr == other.packed.data_ptr() and other.spec == (other.ptr, *w.spec[1:])
+    assert copy.copy(w).packed is w.packed

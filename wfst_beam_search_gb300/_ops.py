@@ -126,6 +126,9 @@ class QuantMatrix:
         self.ptr, self.device = packed.data_ptr(), packed.get_device()
         self.spec = (self.ptr, _HALF[dtype], n, k, group, zeros, self.device)
 
+    def __reduce__(self):    # a copy, or what is loaded from a file, has its own address
+        return QuantMatrix, (self.packed, self.n, self.k, self.group, self.zeros, self.dtype)
+
 
 def pack_quant(codes, scales, zeros=None, stream=None) -> QuantMatrix:
     """Lay out a matrix w[n, k] = scales[n, k // G] * (codes[n, k] - zeros[n, k // G]).
