@@ -183,6 +183,35 @@ def test_weights_keep_their_fp32_value(W, ws, dtype):
     assert bool(((o - ref[:, None]).abs() <= bound[:, None]).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("power", range(8, 31, 2))
+def test_huge_scores(W, ws, power, dtype):
+    """Scores of up to 2^30 whose differences leave one key all the weight: o
+    is its value to the bit, lse its score to the roundings of a product."""
+    n, d, page = 1500, 64, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(power)
+    pages = -(-n // page)
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None]
+    kc = torch.zeros(pages, page, 1, d, device="cuda", dtype=dtype)
+    vc = torch.randn(pages, page, 1, d, generator=g, device="cuda").to(dtype)
+    size = 2.0 ** (power // 2)                     # of q's one element and of the keys'
+    q = torch.zeros(1, 3, d, device="cuda", dtype=dtype)
+    q[0, 0, 7], q[0, 1, 7], q[0, 2, 7] = size, -size, size * 0.75
+    score = torch.linspace(-0.5, 0.5, n, device="cuda", dtype=torch.float64)[torch.randperm(n, generator=g, device="cuda")] * size
+    best, worst = 777, 40
+    score[best], score[worst] = size, -size
+    j = torch.arange(n, device="cuda")
+    at = table[0][j // page].long(), j % page
+    kc[at[0], at[1], 0, 7] = score.to(dtype)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    o, lse = W.attend_paged(q, kc, vc, table, lens, scale=1.0, workspace=ws, with_lse=True)
+    v = vc[at][:, 0]
+    assert torch.equal(o[0], torch.stack([v[best], v[worst], v[best]]))
+    want = torch.tensor([1.0, 1.0, 0.75], device="cuda", dtype=torch.float64) * 4.0 ** (power // 2)
+    assert bool(((lse[0].double() - want).abs() <= 8 * 2.0 ** -24 * want).all())
+
+
 def test_missing_pages_and_long_lengths(W, ws):
     """Tokens of pages outside the pool are not seen; a length past the table ends with it."""
     lens = [100, 100, 64]

@@ -397,10 +397,12 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         const float ref = now == -INFINITY ? 0.f : now;
         keep[c] = exp2a(m[n][c] - ref);
         m[n][c] = now;
-        top[c] = ref - kLift<T>;
+        top[c] = ref;
       }
-      const float p0 = exp2a(s[n][0] - top[0]), p1 = exp2a(s[n][1] - top[1]);
-      const float p2 = exp2a(s[n][2] - top[0]), p3 = exp2a(s[n][3] - top[1]);
+      // (the difference first: it is 0 at most however large the scores are)
+      auto weight = [&](float x, float ref) { return exp2a(kLift<T> != 0.f ? (x - ref) + kLift<T> : x - ref); };
+      const float p0 = weight(s[n][0], top[0]), p1 = weight(s[n][1], top[1]);
+      const float p2 = weight(s[n][2], top[0]), p3 = weight(s[n][3], top[1]);
       l[n][0] = l[n][0] * keep[0] + (p0 + p2);
       l[n][1] = l[n][1] * keep[1] + (p1 + p3);
       const uint32_t h0 = pack2<T>(p0, p1), h1 = pack2<T>(p2, p3);
