@@ -128,6 +128,17 @@ def test_zero_rows_and_no_tokens(W):
     assert W.norm_rotate(e, e, e, pos[:0], table, None, None, kc, vc, slots[:0]).shape == (0, 2, d)
 
 
+def test_a_pool_without_pages(W):
+    """Nothing can be kept; q is turned all the same."""
+    q, k = torch.randn(3, 2, 64, device="cuda").half(), torch.randn(3, 1, 64, device="cuda").half()
+    table, i = make_table(4, 64), torch.arange(3, device="cuda", dtype=torch.int32)
+    pages = torch.zeros(2, 16, 1, 64, device="cuda").half()
+    want = W.norm_rotate(q, k, k, i, table, None, None, pages, pages.clone(), i)
+    assert torch.equal(W.norm_rotate(q, k, k, i, table, None, None, pages[:0], pages[:0], i), want)
+    none = torch.zeros(0, 16, 1, 64, device="cuda").half()
+    assert torch.equal(W.norm_rotate(q, k, k, i, table, None, None, none, none, i), want)
+
+
 def test_refusals(W):
     d = 64
     q = torch.randn(3, 2, d, device="cuda").half()

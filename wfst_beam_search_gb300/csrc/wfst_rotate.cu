@@ -368,7 +368,7 @@ extern "C" int wfst_norm_rotate(const wfst_rotate_args* r, void* stream) {
   if (r->tokens == 0 || heads == 0) return WFST_OK;
   if (heads > (1 << 20)) return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: too many heads");
   if ((r->q_heads && (!r->q || !r->q_out)) || (r->rot && (!r->positions || !r->table)) ||
-      (r->kv_heads && (!r->k || !r->v || !r->k_pages || !r->v_pages || !r->slots)))
+      (r->kv_heads && (!r->k || !r->v || !r->slots || (r->num_pages && (!r->k_pages || !r->v_pages)))))
     return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: NULL argument");
   if (r->kv_heads && (r->page_size < 1 || r->num_pages < 0))
     return api_fail(WFST_ERR_INVALID_ARG, "norm_rotate: page_size must be >= 1 and num_pages >= 0");
