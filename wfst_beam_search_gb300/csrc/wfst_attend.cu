@@ -27,10 +27,10 @@
 // the workspace and the last one to arrive adds them up, in CTA order.
 //
 // Heads of 128, 32 or 64 query and 8 key-value heads: 2 lanes of 100000 to 131072
-// tokens (0.95 GB) take 155 to 160 us, 6.0 TB/s, 64 lanes of 1 to 8192 (1.0 GB)
-// 173 to 177, 128 lanes with a window of 2047 (1.07 GB) 171 to 177: 83 to 92% of
-// a plain copy's rate.  One lane of 500 tokens takes 7.3 us: finding the units, two
-// round trips to memory (page, keys), the join.
+// tokens (0.95 to 0.97 GB) take 157 to 160 us, 6.0 TB/s, 64 lanes of 1 to 8192 (1.0
+// to 1.08 GB) 176 to 179, 128 lanes with a window of 2047 (1.07 GB) 178: 83 to 91%
+// of a plain copy's rate.  One lane of 500 tokens takes 7.5 us: finding the units,
+// two round trips to memory (page, keys), the join.
 #include "wfst_ops.h"
 
 namespace wfst {
@@ -134,9 +134,9 @@ __device__ __forceinline__ float exp2a(float v) {
 // Warps of a CTA, and 16-row tiles in a warp's ring, of which keys and values
 // take one each: what 227 KB hold for heads of 256, and what lets two CTAs (three
 // for heads of 64) share a multiprocessor otherwise.  With a tile less each, 74
-// lanes of 450 tokens with heads of 256 take 47 instead of 44 us, 2 x 131072 159
-// instead of 156; with eight warps for heads of 128, 64 lanes of 1 to 8192 tokens
-// take 186 instead of 173 (2 x 131072 152 instead of 156).
+// lanes of 450 tokens with heads of 256 take 47 instead of 43 us, 2 x 131072 160
+// instead of 158; with eight warps for heads of 128, 64 lanes of 1 to 8192 tokens
+// take 190 instead of 177 (2 x 131072 154 instead of 158).
 template <int D>
 constexpr int kWarps = D == 256 ? 8 : 4;
 template <int D>

@@ -34,10 +34,11 @@
 //   - Where that bin holds too many (flat or coarsely rounded rows), radix
 //     selection on the logits' ordered bits takes over, with exact sums.
 //
-// One row of 5000 takes 8.3 us (k and p: some seven barriers and an ordered list),
+// One row of 5000 takes 8.4 us (k and p: some seven barriers and an ordered list),
 // 64 rows of 131071 with p and min_p 30 us (0.56 TB/s: 2.5 us of reading, the
 // rest the passes over shared memory and the barriers, at which the warps wait
-// most), with p alone, mostly by the histogram, 66.
+// most), with p alone, mostly by the histogram, 66, with k alone 18, and where
+// fewer logits than k are not masked, by radix selection, 81.
 #include <cooperative_groups.h>
 
 #include <type_traits>
