@@ -434,6 +434,7 @@ int wfst_blank_skip(const void* log_probs, int32_t dtype, int64_t stride_b, int6
  *     are held in fp32 or wider and rounded once at the end;
  *   - strides count elements; the innermost axis has unit stride, and a
  *     stride along an axis of one entry is not read;
+ *   - what is written overlaps nothing else, but where a call says that it may;
  *   - results do not depend on the order in which CTAs run.
  */
 
@@ -505,7 +506,7 @@ int wfst_norm_rotate(const wfst_rotate_args* args, void* stream);
  * lse (may be NULL) receives the log of the sum of exponentials.  A lane that
  * sees nothing has o = 0 and lse = -inf.  A seen value that is infinite may make
  * NaN of its element of o (its weight is held in parts).  o may be q, with the
- * same strides; otherwise nothing that is written may overlap what is read.  head_dim: 64, 128 or 256.  q, the
+ * same strides.  head_dim: 64, 128 or 256.  q, the
  * pages and the workspace are 16-byte aligned, strides of q and the pages
  * multiples of 8.
  * workspace: wfst_attend_size's bytes, of which the first WFST_ATTEND_ZEROED
@@ -528,24 +529,25 @@ int wfst_attend_size(int64_t* bytes);
 int wfst_attend_paged(const wfst_attend_args* args, void* stream);
 
 /*
- * One token per lane from its logits [lanes, vocab] and a uniform number in
- * [0, 1).  With weights exp((x - max x) / temperature), the tokens kept are
- * the first top_k in order of descending logit (equal ones by ascending
- * index; 0: all), of those the shortest prefix whose weight reaches top_p of
- * theirs (1: all), and of those the ones whose weight is at least min_p of
- * the largest.  The token is the first index whose cumulative kept weight
- * exceeds uniform times their total; logprobs receives the log of its share
- * of that total, kept the number of tokens kept.  temperature = 0 takes the
- * first largest logit.  Weights are summed as whole multiples of 2^-43 of the
- * largest one, so results do not depend on any order.  -inf and NaN logits
- * weigh nothing; a lane with no other logit gets token -1, logprob -inf and
- * kept 0; +inf logits share all the weight (with those of the type's largest
- * number, if there are any).  The four settings apply to every
- * lane, or per lane where the array beside them is not NULL.  A setting for
- * every lane is refused out of its range (temperature 0 to 3e38, top_k >= 0,
- * top_p > 0, min_p 0 to 1); one of a lane counts as the range's nearest end
- * (top_p: the first token alone), NaN as temperature 0, top_p 0 or min_p 1.
- * vocab <= 2^20.  Errors: INVALID_ARG, CUDA.
+ * One token per lane from its logits [lanes, vocab] (stride >= vocab) and a
+ * uniform number in [0, 1).  With weights exp((x - max x) / temperature), the
+ * tokens kept are the first top_k in order of descending logit (equal ones by
+ * ascending index; 0: all), of those the shortest prefix whose weight reaches
+ * top_p of theirs (1: all), and of those the ones whose weight is at least
+ * min_p of the largest.  The token is the first index whose cumulative kept
+ * weight exceeds uniform times their total; logprobs receives the log of its
+ * share of that total, kept the number of tokens kept.  temperature = 0 takes
+ * the first largest logit.  Weights are summed as whole multiples of 2^-43 of
+ * the largest one, so results do not depend on any order.  -inf and NaN
+ * logits weigh nothing (they count as kept where no rule ends before them); a
+ * lane with no other logit gets token -1, logprob -inf and kept 0; +inf
+ * logits share all the weight (with those of the type's largest number, if
+ * there are any).  The four settings apply to every lane, or per lane where
+ * the array beside them is not NULL.  A setting for every lane is refused out
+ * of its range (temperature 0 to 3e38, top_k >= 0, top_p > 0, min_p 0 to 1);
+ * one of a lane counts as the range's nearest end (top_p: the first token
+ * alone), NaN as temperature 0, top_p 0 or min_p 1. vocab <= 2^20.  Errors:
+ * INVALID_ARG, CUDA.
  */
 typedef struct {
   const void* logits;

@@ -27,9 +27,9 @@
 // the workspace and the last one to arrive adds them up, in CTA order.
 //
 // Heads of 128, 32 or 64 query and 8 key-value heads: 2 lanes of 100000 to 131072
-// tokens (0.95 to 0.97 GB) take 157 to 160 us, 6.0 TB/s, 64 lanes of 1 to 8192 (1.0
-// to 1.08 GB) 176 to 179, 128 lanes with a window of 2047 (1.07 GB) 178: 83 to 91%
-// of a plain copy's rate.  One lane of 500 tokens takes 7.5 us: finding the units,
+// tokens (0.95 to 0.97 GB) take 153 to 160 us, 6.2 TB/s, 64 lanes of 1 to 8192 (1.0
+// to 1.08 GB) 174 to 179, 128 lanes with a window of 2047 (1.07 GB) 173 to 178: 83
+// to 94% of a plain copy's rate.  One lane of 500 tokens takes 7.5 us: finding the units,
 // two round trips to memory (page, keys), the join.
 #include "wfst_ops.h"
 
