@@ -103,9 +103,9 @@ def test_a_start_token_outside_the_vocabulary_is_refused():
 
 
 def test_a_pass_runs_on_its_models_device(monkeypatch):
-    """With another device current, capture and replay are of the model's.  No
-    machine here has two GPUs: torch.cuda is a stand-in that keeps count of
-    what is current."""
+    """With another device current, capture and replay are of the model's.
+    torch.cuda is a stand-in that keeps count of what is current, so that no
+    second GPU is needed."""
     import contextlib
     from types import SimpleNamespace
 
