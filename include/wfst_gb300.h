@@ -562,6 +562,90 @@ typedef struct {
 } wfst_sample_args;
 int wfst_sample_tokens(const wfst_sample_args* args, void* stream);
 
+/*
+ * Attention of one new token per lane, where all lanes' tokens follow one
+ * prefix that is in the cache once.  Lane b sees the prefix' prefix_length[0]
+ * tokens (token j in page prefix_table[j / page_size] at place j % page_size)
+ * and after them its own lengths[b] ones, as in wfst_attend_paged without a
+ * window: pages from table, the new token among them.  Both kinds of pages come
+ * from one pool.  Lengths are clamped to what their table holds, a length of 0
+ * or below sees the prefix alone; a token whose entry is outside [0, num_pages)
+ * counts as not seen.  Heads, o, lse, what sees nothing, infinite values,
+ * alignment and strides are as in wfst_attend_paged; o may be q, with the same
+ * strides.  The prefix' products run on 16-bit operands with fp32 sums, its
+ * weights in two 16-bit parts (2^-16 of a weight is lost at most, 2^-22 with
+ * fp16, and there what is below 2^-35 of the largest one).
+ * workspace: wfst_prefix_size's bytes for these counts or more lanes, of which
+ * the first WFST_ATTEND_ZEROED have to be zeros before its first use; calls that
+ * use the same one must follow each other on a stream, and each leaves it ready
+ * for the next.  lanes * q_heads stays below 2^31.  lanes = 0 does nothing.
+ * Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  const void *q, *k_pages, *v_pages;           /* q: [lanes, q_heads, head_dim] */
+  const int32_t *prefix_table, *prefix_length; /* [prefix_width], [1] */
+  const int32_t *table, *lengths;              /* [lanes, table_width], [lanes] */
+  void* o;                                     /* [lanes, q_heads, head_dim] */
+  float* lse;                                  /* [lanes, q_heads] or NULL */
+  void* workspace;
+  int64_t q_stride[2], o_stride[2], lse_stride, table_stride;
+  int64_t k_page_stride[3], v_page_stride[3]; /* page, place, head */
+  int32_t device, dtype, lanes, q_heads, kv_heads, head_dim, prefix_width, table_width, num_pages, page_size;
+  float scale;
+} wfst_prefix_args;
+int wfst_prefix_size(int32_t lanes, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t* bytes);
+int wfst_attend_prefix(const wfst_prefix_args* args, void* stream);
+
+/*
+ * How likely given tokens are.  For each row of logits [rows, vocab] (stride >=
+ * vocab) and its token: logprobs receives x[token] - log sum exp x, entropy the
+ * entropy of the row's distribution (in nats), and with top > 0 top_tokens and
+ * top_logprobs [rows, top] (contiguous) the `top` likeliest tokens in order of
+ * descending logit, equal ones by ascending index, and their log
+ * probabilities.  -inf logits weigh nothing and are no alternatives: what a row
+ * has too few of is token -1 with logprob -inf.  A row without any other logit
+ * has logprob -inf and entropy 0.  Where a row holds NaN or +inf its log
+ * probabilities and entropy are NaN; NaN is no alternative.  A negative token is
+ * not scored: its logprob is 0 (rows that only fill up a batch); a token >= vocab
+ * has NaN.  top <= 64, vocab <= 2^20.  rows = 0 does nothing.  Errors:
+ * INVALID_ARG, CUDA.
+ */
+#define WFST_SCORE_TOP 64
+typedef struct {
+  const void* logits;
+  const int32_t* tokens; /* [rows] */
+  float *logprobs, *entropy;
+  int32_t* top_tokens; /* [rows, top], as top_logprobs; not used with top = 0 */
+  float* top_logprobs;
+  int64_t stride; /* between rows of logits */
+  int32_t device, dtype, rows, vocab, top;
+} wfst_score_args;
+int wfst_score_tokens(const wfst_score_args* args, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: for each row r
+ * with a = adapter[r],
+ *   out[r, n] = y[r, n] + scales[a] * sum over j of t[j] * expand[a, n, j],
+ *   t[j] = sum over k of x[r, k] * shrink[a, j, k].
+ * A row whose adapter is outside [0, adapters) is y as it is.  scales [adapters]
+ * may be NULL (one).  t is held in fp32 and multiplied in two parts of dtype
+ * (2^-16 of it is lost at most); sums are fp32 and out is rounded once.  Where a
+ * row of x is not finite, that row of out may be NaN throughout.  x, shrink and
+ * expand are 16-byte aligned, their strides multiples of 8; k is a multiple of
+ * 8, rank a multiple of 8 up to 128.  out may be y, with the same stride.  rows =
+ * 0 does nothing.  Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  const void *y, *x, *shrink, *expand; /* [rows, n], [rows, k], [adapters, rank, k], [adapters, n, rank] */
+  const int32_t* adapter;              /* [rows] */
+  const float* scales;
+  void* out;                           /* [rows, n] */
+  int64_t y_stride, x_stride, out_stride;
+  int64_t shrink_stride[2], expand_stride[2]; /* adapter, rank; adapter, output */
+  int32_t device, dtype, rows, n, k, rank, adapters;
+} wfst_lowrank_args;
+int wfst_add_lowrank(const wfst_lowrank_args* args, void* stream);
+
 const char* wfst_last_error(void);
 
 #ifdef __cplusplus

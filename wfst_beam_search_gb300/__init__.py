@@ -22,6 +22,7 @@ from . import _build
 WFST_OK = 0
 WFST_F32, WFST_F16, WFST_BF16 = 0, 1, 2
 WFST_ATTEND_ZEROED = 4096
+WFST_SCORE_TOP = 64
 OVF_ARENA, OVF_KEPT, OVF_PATH = 4, 16, 32
 REC_EPS, REC_FINAL, REC_REDIRECT = 1, 2, 4
 STAT_NAMES = ["frames", "arcs_expanded", "sum_n", "sum_D", "sum_a", "sum_m", "eps",
@@ -41,7 +42,7 @@ EXPORTED = ["wfst_graph_upload", "wfst_graph_info", "wfst_graph_free", "wfst_dec
             "wfst_decode_static", "wfst_mem_stats", "wfst_blank_skip", "wfst_test_barrier_timeout",
             "wfst_probe_random_gather", "wfst_quant_size", "wfst_quant_pack", "wfst_matvec_quant",
             "wfst_norm_rotate", "wfst_attend_size", "wfst_attend_paged", "wfst_sample_tokens",
-            "wfst_last_error"]
+            "wfst_prefix_size", "wfst_attend_prefix", "wfst_score_tokens", "wfst_add_lowrank", "wfst_last_error"]
 
 
 class WfstError(RuntimeError):
@@ -116,7 +117,9 @@ def load(build_if_missing: bool = False):
         L.wfst_quant_size.argtypes = [i32, i32, i32, i32, C.POINTER(i64)]
         L.wfst_quant_pack.argtypes = [P, P, P, i32, i32, i32, i32, P, P]
         L.wfst_attend_size.argtypes = [C.POINTER(i64)]
-        for name in ("wfst_matvec_quant", "wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens"):
+        L.wfst_prefix_size.argtypes = [i32, i32, i32, i32, C.POINTER(i64)]
+        for name in ("wfst_matvec_quant", "wfst_norm_rotate", "wfst_attend_paged", "wfst_sample_tokens",
+                     "wfst_attend_prefix", "wfst_score_tokens", "wfst_add_lowrank"):
             getattr(L, name).argtypes = [P, P]    # the argument block, the stream
         for name in EXPORTED:
             if name not in ("wfst_last_error", "wfst_graph_free", "wfst_decoder_free"):
@@ -310,9 +313,27 @@ def wfst_sample_tokens(args, stream):
     _check(load().wfst_sample_tokens(args, stream))
 
 
+def wfst_prefix_size(lanes, q_heads, kv_heads, head_dim):
+    out = C.c_int64()
+    _check(load().wfst_prefix_size(lanes, q_heads, kv_heads, head_dim, C.byref(out)))
+    return out.value
+
+
+def wfst_attend_prefix(args, stream):
+    _check(load().wfst_attend_prefix(args, stream))
+
+
+def wfst_score_tokens(args, stream):
+    _check(load().wfst_score_tokens(args, stream))
+
+
+def wfst_add_lowrank(args, stream):
+    _check(load().wfst_add_lowrank(args, stream))
+
+
 #: the second-pass operators on torch tensors (``_ops``), loaded on first use: the decoder itself needs no torch
 _OPS = ("QuantMatrix", "pack_quant", "matvec_quant", "norm_rotate", "attend_workspace", "attend_paged",
-        "sample_tokens")
+        "sample_tokens", "attend_prefix_workspace", "attend_prefix", "score_tokens", "add_lowrank")
 
 
 def __getattr__(name):

@@ -1,6 +1,6 @@
 """Compile the CUDA decoder library for GB300 (sm_103a), in tree.
 
-Ten translation units are compiled in parallel and linked into
+Thirteen translation units are compiled in parallel and linked into
 ``wfst_beam_search_gb300/_build/libwfst_gb300.so``.  Where torch with CUDA and
 Python's headers are installed, ``ops_binding.so`` is compiled beside it: the
 second-pass operators' path from torch tensors into that library.
@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "libwfst_gb300.so")
 BINDING = os.path.join(BUILD, "ops_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["wfst_kernel.cu", "wfst_api.cu", "wfst_static.cu", "wfst_preslice.cu", "wfst_vmm.cu", "wfst_probe.cu",
-           "wfst_matvec.cu", "wfst_rotate.cu", "wfst_attend.cu", "wfst_sample.cu"]
+           "wfst_matvec.cu", "wfst_rotate.cu", "wfst_attend.cu", "wfst_sample.cu", "wfst_prefix.cu", "wfst_score.cu",
+           "wfst_lowrank.cu"]
 BINDING_SOURCE = "ops_binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -4,7 +4,10 @@ One step of a small language model that reads the first-pass words: products
 with 4-bit weights (``pack_quant``, ``matvec_quant``), the heads' norm and
 rotation with the write into the paged cache (``norm_rotate``), attention of
 one new token per lane over that cache (``attend_workspace``,
-``attend_paged``) and the draw of the next token (``sample_tokens``).
+``attend_paged``) and the draw of the next token (``sample_tokens``).  Where it
+rescores many hypotheses: attention behind a prefix that all lanes share
+(``attend_prefix_workspace``, ``attend_prefix``), low-rank adapters by lane
+(``add_lowrank``) and the scores of given tokens (``score_tokens``).
 
 As in the rest of the binding, the functions check and marshal arguments; the
 work is done by the CUDA library (``include/wfst_gb300.h`` states layouts and
@@ -28,8 +31,8 @@ import struct
 
 import torch
 
-from . import (WFST_ATTEND_ZEROED, WFST_BF16, WFST_F16, WFST_F32, _build, _check, load, wfst_attend_size,
-               wfst_quant_pack, wfst_quant_size)
+from . import (WFST_ATTEND_ZEROED, WFST_BF16, WFST_F16, WFST_F32, WFST_SCORE_TOP, _build, _check, load,
+               wfst_attend_size, wfst_prefix_size, wfst_quant_pack, wfst_quant_size)
 
 _HALF = {torch.float16: WFST_F16, torch.bfloat16: WFST_BF16}
 _ANY = {torch.float32: WFST_F32, **_HALF}
@@ -41,6 +44,9 @@ _MATVEC = struct.Struct("4P2q7i4x").pack
 _ROTATE = struct.Struct("11P14q11if").pack
 _ATTEND = struct.Struct("8P12q11if").pack
 _SAMPLE = struct.Struct("9Pq5i3f").pack
+_PREFIX = struct.Struct("10P12q10if4x").pack
+_SCORE = struct.Struct("6Pq5i4x").pack
+_LOWRANK = struct.Struct("7P7q7i4x").pack
 
 
 def _load_binding():
@@ -297,3 +303,117 @@ def sample_tokens(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.
             _contiguous(uniform=uniform, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
         _refused(y, why)
     return y
+
+
+# ------------------------------------------------------------------ attention behind a shared prefix
+
+def attend_prefix_workspace(lanes, q_heads, kv_heads, head_dim, device=None):
+    """The workspace of ``attend_prefix`` on a device, for up to ``lanes``
+    lanes.  Calls that share one must follow each other on a stream."""
+    workspace = torch.empty(wfst_prefix_size(lanes, q_heads, kv_heads, head_dim), dtype=_U8,
+                            device="cuda" if device is None else device)
+    workspace[:WFST_ATTEND_ZEROED].zero_()
+    return workspace
+
+
+def attend_prefix(q, k_pages, v_pages, prefix_table, prefix_length, page_table, lengths, scale=None, workspace=None,
+                  with_lse=False, out=None, stream=None):
+    """Attention of one new token per lane, all of which follow one prefix
+    that is in the cache once and is read once for all of them.
+
+    q [lanes, q_heads, d]; pages [pages, page_size, kv_heads, d] in any order
+    of strides; prefix_table int32 [prefix_width] and prefix_length int32 [1]
+    are the prefix' pages and tokens, page_table int32 [lanes, width] and
+    lengths int32 [lanes] each lane's own, the new token among them.
+    ``scale`` is 1/sqrt(d) by default.  ``out`` may be q itself.  Returns o
+    [lanes, q_heads, d], with ``with_lse`` also the float32 [lanes, q_heads]
+    log of the sum of exponentials.  Without ``workspace`` (see
+    ``attend_prefix_workspace``) the call makes one of its own."""
+    if stream is not None:
+        with _on(stream, q=q):
+            return attend_prefix(q, k_pages, v_pages, prefix_table, prefix_length, page_table, lengths, scale, workspace,
+                                 with_lse, out)
+    y = _binding.attend_prefix(q, k_pages, v_pages, prefix_table, prefix_length, page_table, lengths, scale, workspace,
+                               with_lse, out)
+    if y.__class__ is int:
+        def why():
+            _tensors(q=q, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table, prefix_length=prefix_length,
+                     page_table=page_table, lengths=lengths, **({} if workspace is None else {"workspace": workspace}))
+            _half_type("q", q.dtype)
+            if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or prefix_table.dim() != 1:
+                raise ValueError("q must be [lanes, heads, d], pages [pages, page_size, heads, d], prefix_table [width], "
+                                 "page_table [lanes, width]")
+            t, (lanes, heads, d) = q.dtype, q.shape
+            cache = (*k_pages.shape[:3], d)
+            _explain(q.get_device(), [
+                ("q", q, t, q.shape), ("k_pages", k_pages, t, cache), ("v_pages", v_pages, t, cache),
+                ("prefix_table", prefix_table, _I32, prefix_table.shape), ("prefix_length", prefix_length, _I32, (1,)),
+                ("page_table", page_table, _I32, (lanes, page_table.shape[1])), ("lengths", lengths, _I32, (lanes,)),
+                ("out", out, t, q.shape)])
+            if workspace is not None:
+                room = wfst_prefix_size(lanes, heads, k_pages.shape[2], d)
+                _explain(q.get_device(), [("workspace", workspace, _U8, (max(workspace.numel(), room),))])
+            _last_axis(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, out=out)
+            _contiguous(prefix_table=prefix_table, lengths=lengths, workspace=workspace)
+        _refused(y, why)
+    return y
+
+
+# ------------------------------------------------------------------ scores of given tokens
+
+def score_tokens(logits, tokens, top=0, stream=None):
+    """How likely each row's given token is: (logprobs float32 [rows], entropy
+    float32 [rows], top_tokens int32 [rows, top], top_logprobs float32 [rows,
+    top]) from logits [rows, vocab] and tokens int32 [rows].
+
+    The alternatives come in order of descending logit, equal ones by
+    ascending index; -inf logits are none (token -1 where a row has too few).
+    A negative token is not scored: its logprob is 0."""
+    if stream is not None:
+        with _on(stream, logits=logits):
+            return score_tokens(logits, tokens, top)
+    y = _binding.score_tokens(logits, tokens, top)
+    if y.__class__ is int:
+        def why():
+            _tensors(logits=logits, tokens=tokens)
+            if logits.dtype not in _ANY:
+                raise TypeError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
+            if logits.dim() != 2:
+                raise ValueError("logits must be [rows, vocab]")
+            if not 0 <= top <= WFST_SCORE_TOP:
+                raise ValueError(f"top must be between 0 and {WFST_SCORE_TOP}")
+            _explain(logits.get_device(), [("logits", logits, logits.dtype, logits.shape),
+                                           ("tokens", tokens, _I32, logits.shape[:1])])
+            _last_axis(logits=logits)
+            _contiguous(tokens=tokens)
+        _refused(y, why)
+    return y
+
+
+# ------------------------------------------------------------------ low-rank adapters
+
+def add_lowrank(y, x, shrink, expand, adapters, scales=None, out=None, stream=None):
+    """y [rows, n] plus each row's own low-rank adapter's part of it:
+    scales[a] * (x[r] @ shrink[a].T) @ expand[a].T with a = adapters[r], for x
+    [rows, k], shrink [count, rank, k], expand [count, n, rank], adapters int32
+    [rows] (negative, or past the last one: the row is y as it is) and scales
+    float32 [count] (None: one).  ``out`` may be y itself."""
+    if stream is not None:
+        with _on(stream, y=y):
+            return add_lowrank(y, x, shrink, expand, adapters, scales, out)
+    z = _binding.add_lowrank(y, x, shrink, expand, adapters, scales, out)
+    if z.__class__ is int:
+        def why():
+            _tensors(y=y, x=x, shrink=shrink, expand=expand, adapters=adapters)
+            _half_type("y", y.dtype)
+            if y.dim() != 2 or x.dim() != 2 or shrink.dim() != 3:
+                raise ValueError("y must be [rows, n], x [rows, k], shrink [count, rank, k], expand [count, n, rank]")
+            t, (rows, n), k, (count, rank) = y.dtype, y.shape, x.shape[1], shrink.shape[:2]
+            _explain(y.get_device(), [
+                ("y", y, t, y.shape), ("x", x, t, (rows, k)), ("shrink", shrink, t, (count, rank, k)),
+                ("expand", expand, t, (count, n, rank)), ("adapters", adapters, _I32, (rows,)),
+                ("scales", scales, _F32, (count,)), ("out", out, t, y.shape)])
+            _last_axis(y=y, x=x, shrink=shrink, expand=expand, out=out)
+            _contiguous(adapters=adapters, scales=scales)
+        _refused(z, why)
+    return z

@@ -342,6 +342,175 @@ PyObject* sample_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// attend_prefix(q, k_pages, v_pages, prefix_table, prefix_length, page_table, lengths, scale, workspace, with_lse, out)
+PyObject* attend_prefix(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 11) return look();
+  Reader r;
+  const Tensor* q = r.first(arg[0], 3);
+  if (!q || type_code(r.type) <= 0) return look();
+  const Tensor *kp = r.tensor(arg[1], 4, r.type), *vp = r.tensor(arg[2], 4, r.type);
+  const Tensor* shared = r.tensor(arg[3], 1, ScalarType::Int);
+  const Tensor* table = r.tensor(arg[5], 2, ScalarType::Int);
+  const Tensor* ws = arg[8] == Py_None ? nullptr : r.tensor(arg[8], 1, ScalarType::Byte);
+  if (!r.ok) return look();
+  const int64_t lanes = q->size(0), hq = q->size(1), d = q->size(2);
+  if (kp->size(3) != d || vp->sizes() != kp->sizes() || table->size(0) != lanes || !unit(*q) || !unit(*kp) ||
+      !unit(*vp) || !unit(*table) || !shared->is_contiguous() || (ws && !ws->is_contiguous()))
+    return look();
+  wfst_prefix_args a = {};
+  a.prefix_length = (const int32_t*)r.vector(arg[4], 1, ScalarType::Int);
+  a.lengths = (const int32_t*)r.vector(arg[6], lanes, ScalarType::Int);
+  a.scale = arg[7] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)PyFloat_AsDouble(arg[7]);
+  const int with_lse = PyObject_IsTrue(arg[9]);
+  if (PyErr_Occurred()) return nullptr;
+  a.lanes = r.i32(lanes);
+  a.q_heads = r.i32(hq);
+  a.kv_heads = r.i32(kp->size(2));
+  a.head_dim = r.i32(d);
+  a.prefix_width = r.i32(shared->size(0));
+  a.table_width = r.i32(table->size(1));
+  a.num_pages = r.i32(kp->size(0));
+  a.page_size = r.i32(kp->size(1));
+  if (!r.ok) return look();
+  int64_t ws_bytes = 0;
+  if (const int rc = wfst_prefix_size(a.lanes, a.q_heads, a.kv_heads, a.head_dim, &ws_bytes)) return PyLong_FromLong(rc);
+  if (ws && ws->numel() < ws_bytes) return look();
+  Tensor y, lse;
+  if (arg[10] == Py_None) {
+    y = empty({lanes, hq, d}, r.type, r.dev);
+  } else {
+    const Tensor* out = r.tensor(arg[10], 3, r.type);
+    if (!out || out->sizes() != q->sizes() || !unit(*out)) return look();
+    y = *out;
+  }
+  Tensor own;
+  if (!ws) {  // as attend_prefix_workspace makes it
+    own = empty({ws_bytes}, ScalarType::Byte, r.dev);
+    own.narrow(0, 0, WFST_ATTEND_ZEROED).zero_();
+    ws = &own;
+  }
+  if (with_lse) {
+    lse = empty({lanes, hq}, ScalarType::Float, r.dev);
+    a.lse = (float*)lse.data_ptr();
+    a.lse_stride = hq;
+  }
+  a.q = q->data_ptr();
+  a.k_pages = kp->data_ptr();
+  a.v_pages = vp->data_ptr();
+  a.prefix_table = (const int32_t*)shared->data_ptr();
+  a.table = (const int32_t*)table->data_ptr();
+  a.o = y.data_ptr();
+  a.workspace = ws->data_ptr();
+  for (int i = 0; i < 2; i++) {
+    a.q_stride[i] = q->stride(i);
+    a.o_stride[i] = y.stride(i);
+  }
+  for (int i = 0; i < 3; i++) {
+    a.k_page_stride[i] = kp->stride(i);
+    a.v_page_stride[i] = vp->stride(i);
+  }
+  a.table_stride = table->stride(0);
+  a.device = r.dev;
+  a.dtype = type_code(r.type);
+  if (const int rc = call(wfst_attend_prefix, a, r.dev)) return PyLong_FromLong(rc);
+  if (arg[10] != Py_None) written(y);
+  if (!with_lse) return THPVariable_Wrap(std::move(y));
+  PyObject* both = PyTuple_New(2);
+  if (!both) return nullptr;
+  PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(std::move(y)));
+  PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(std::move(lse)));
+  return both;
+  END_HANDLE_TH_ERRORS
+}
+
+// score_tokens(logits, tokens, top)
+PyObject* score_tokens(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 3) return look();
+  Reader r;
+  const Tensor* x = r.first(arg[0], 2);
+  if (!x || type_code(r.type) < 0 || !unit(*x)) return look();
+  const int64_t rows = x->size(0);
+  wfst_score_args a = {};
+  a.tokens = (const int32_t*)r.vector(arg[1], rows, ScalarType::Int);
+  a.top = r.number(arg[2]);
+  if (PyErr_Occurred()) return nullptr;
+  a.logits = x->data_ptr();
+  a.stride = x->stride(0);
+  a.device = r.dev;
+  a.dtype = type_code(r.type);
+  a.rows = r.i32(rows);
+  a.vocab = r.i32(x->size(1));
+  if (!r.ok || a.top < 0 || a.top > WFST_SCORE_TOP) return look();
+  Tensor logprobs = empty({rows}, ScalarType::Float, r.dev), entropy = empty({rows}, ScalarType::Float, r.dev),
+         tokens = empty({rows, a.top}, ScalarType::Int, r.dev), top = empty({rows, a.top}, ScalarType::Float, r.dev);
+  a.logprobs = (float*)logprobs.data_ptr();
+  a.entropy = (float*)entropy.data_ptr();
+  a.top_tokens = (int32_t*)tokens.data_ptr();
+  a.top_logprobs = (float*)top.data_ptr();
+  if (const int rc = call(wfst_score_tokens, a, r.dev)) return PyLong_FromLong(rc);
+  PyObject* all = PyTuple_New(4);
+  if (!all) return nullptr;
+  PyTuple_SET_ITEM(all, 0, THPVariable_Wrap(std::move(logprobs)));
+  PyTuple_SET_ITEM(all, 1, THPVariable_Wrap(std::move(entropy)));
+  PyTuple_SET_ITEM(all, 2, THPVariable_Wrap(std::move(tokens)));
+  PyTuple_SET_ITEM(all, 3, THPVariable_Wrap(std::move(top)));
+  return all;
+  END_HANDLE_TH_ERRORS
+}
+
+// add_lowrank(y, x, shrink, expand, adapters, scales, out)
+PyObject* add_lowrank(PyObject*, PyObject* const* arg, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 7) return look();
+  Reader r;
+  const Tensor* y = r.first(arg[0], 2);
+  if (!y || type_code(r.type) <= 0) return look();
+  const Tensor *x = r.tensor(arg[1], 2, r.type), *s = r.tensor(arg[2], 3, r.type), *e = r.tensor(arg[3], 3, r.type);
+  if (!r.ok) return look();
+  const int64_t rows = y->size(0), n = y->size(1), k = x->size(1), adapters = s->size(0), rank = s->size(1);
+  if (x->size(0) != rows || s->size(2) != k || e->size(0) != adapters || e->size(1) != n || e->size(2) != rank ||
+      !unit(*y) || !unit(*x) || !unit(*s) || !unit(*e))
+    return look();
+  wfst_lowrank_args a = {};
+  a.adapter = (const int32_t*)r.vector(arg[4], rows, ScalarType::Int);
+  a.scales = (const float*)r.vector_or_none(arg[5], adapters, ScalarType::Float);
+  if (!r.ok) return look();
+  Tensor z;
+  if (arg[6] == Py_None) {
+    z = empty({rows, n}, r.type, r.dev);
+  } else {
+    const Tensor* out = r.tensor(arg[6], 2, r.type);
+    if (!out || out->sizes() != y->sizes() || !unit(*out)) return look();
+    z = *out;
+  }
+  a.y = y->data_ptr();
+  a.x = x->data_ptr();
+  a.shrink = s->data_ptr();
+  a.expand = e->data_ptr();
+  a.out = z.data_ptr();
+  a.y_stride = y->stride(0);
+  a.x_stride = x->stride(0);
+  a.out_stride = z.stride(0);
+  for (int i = 0; i < 2; i++) {
+    a.shrink_stride[i] = s->stride(i);
+    a.expand_stride[i] = e->stride(i);
+  }
+  a.device = r.dev;
+  a.dtype = type_code(r.type);
+  a.rows = r.i32(rows);
+  a.n = r.i32(n);
+  a.k = r.i32(k);
+  a.rank = r.i32(rank);
+  a.adapters = r.i32(adapters);
+  if (!r.ok) return look();
+  if (const int rc = call(wfst_add_lowrank, a, r.dev)) return PyLong_FromLong(rc);
+  if (arg[6] != Py_None) written(z);
+  return THPVariable_Wrap(std::move(z));
+  END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, (PyCFunction)(void (*)(void))F, METH_FASTCALL, nullptr};
@@ -349,6 +518,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<matvec_quant>("matvec_quant"), method<norm_rotate>("norm_rotate"),
                          method<attend_paged>("attend_paged"), method<sample_tokens>("sample_tokens"),
+                         method<attend_prefix>("attend_prefix"), method<score_tokens>("score_tokens"),
+                         method<add_lowrank>("add_lowrank"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ops_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
