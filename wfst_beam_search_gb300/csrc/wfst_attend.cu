@@ -69,6 +69,7 @@ struct Args {
   int32_t div_s;
   float scale2;  // scale * log2(e)
   int32_t o_even;  // o's pairs of elements are 4-byte aligned
+  PrefixParts pre;
 };
 
 // What a lane sees: n tokens, the first `first` as they are, the others
@@ -145,15 +146,18 @@ constexpr int kRing = D == 64 ? 8 : D == 128 ? 5 : 3;
 template <int D, int NT>
 constexpr int kSmem = kWarps<D> * kRing<D> * 16 * D * 2 + 2 * D * 8 * NT * 4 + kWarps<D> * 2 * 8 * NT * 4;
 
-// D: elements of a head; NT: runs of 8 * NT query heads.
-template <typename T, int D, int NT>
+// D: elements of a head; NT: runs of 8 * NT query heads.  PRE: a prefix' parts are
+// added to each lane's own before it is written.
+template <typename T, int D, int NT, bool PRE>
 __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   constexpr int W = kWarps<D>, UNIT = 16 * W, S = kRing<D>, kTile = 16 * D * 2, KS = D / 16, DT = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_last[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int runs = a.hkv * a.runs;
-  ops_begin();
+  // The prefix' kernel lets this one start when it has waited itself for what was
+  // before it; this one waits for it where its parts are added.
+  if (!PRE) ops_begin();
   ops_next();
 
   // ---- this CTA's units: all lanes' tiles, numbered through (each warp for itself)
@@ -324,6 +328,50 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
     } else {
       reinterpret_cast<uint16_t*>(out)[0] = (uint16_t)r0, reinterpret_cast<uint16_t*>(out)[1] = (uint16_t)(r0 >> 16);
       reinterpret_cast<uint16_t*>(out)[8] = (uint16_t)r1, reinterpret_cast<uint16_t*>(out)[9] = (uint16_t)(r1 >> 16);
+    }
+  };
+  // adds the prefix' parts to the own one of heads 2t and 2t + 1 of run n: m, l and
+  // the elements g and g + 8 of the E tiles of 16 from d0 on
+  auto add_prefix = [&](int b, int run, int n, int d0, auto& oo, float (&mm)[2], float (&ll)[2]) {
+    constexpr int E = sizeof(oo) / sizeof(oo[0]);
+    ops_begin();
+    const uint32_t tiles = (uint32_t)((max((int64_t)0, min((int64_t)*a.pre.length, a.pre.room)) + a.pre.keys - 1) / a.pre.keys);
+    if (!tiles) return;
+    const uint32_t all = tiles * a.hkv * a.pre.groups, ctas = min((uint32_t)a.pre.grid, all), per = all / ctas,
+                   rest = all - per * ctas;
+    auto owner = [&](uint32_t u) {
+      const uint32_t at = rest * (per + 1);
+      return u < at ? u / (per + 1) : rest + (u - at) / per;
+    };
+    const int64_t slot = (int64_t)a.pre.rows * (2 + D);
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+      const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
+      if (c >= a.share) continue;
+      const uint32_t r = (uint32_t)b * a.share + c, group = (uint32_t)(run / a.runs) * a.pre.groups + r / a.pre.rows;
+      const uint32_t row = r % a.pre.rows, c0 = owner(group * tiles), c1 = owner(group * tiles + tiles - 1);
+      const float* part = a.pre.parts + (c0 + group) * slot + row;
+#pragma unroll 2
+      for (uint32_t i = c0; i <= c1; i++, part += slot) {
+        const float pm = __ldcg(part), pl = __ldcg(part + a.pre.rows);
+        float v[E][2];
+#pragma unroll
+        for (int e = 0; e < E; e++)
+#pragma unroll
+          for (int y = 0; y < 2; y++) {
+            const int el = (d0 + e) * 16 + y * 8 + g;
+            v[e][y] = __ldcg(part - row + 2 * a.pre.rows + ((int64_t)(el >> 2) * a.pre.rows + row) * 4 + (el & 3));
+          }
+        const float now = fmaxf(mm[x], pm), ref = now == -INFINITY ? 0.f : now;
+        const float keep = exp2a(mm[x] - ref), add = exp2a(pm - ref);
+        mm[x] = now;
+        ll[x] = ll[x] * keep + pl * add;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          oo[e][x] = oo[e][x] * keep + v[e][0] * add;
+          oo[e][2 + x] = oo[e][2 + x] * keep + v[e][1] * add;
+        }
+      }
     }
   };
   auto put_lse = [&](int b, int run, const float (&wm)[NT][2], const float (&wl)[NT][2]) {
@@ -517,7 +565,22 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         __syncthreads();
       }
       const bool whole = whole_start && ends;
-      if (warp < 2) {
+      if (PRE && whole && warp < 2) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float w[DT / 2][4];
+#pragma unroll
+          for (int e = 0; e < DT / 2; e++) {
+            const float4 v = reinterpret_cast<float4*>(xo)[(((1 - warp) * NT + n) * DT + e + warp * (DT / 2)) * 32 + lane];
+            w[e][0] = (warp ? o[n][e + DT / 2][0] : o[n][e][0]) + v.x, w[e][1] = (warp ? o[n][e + DT / 2][1] : o[n][e][1]) + v.y;
+            w[e][2] = (warp ? o[n][e + DT / 2][2] : o[n][e][2]) + v.z, w[e][3] = (warp ? o[n][e + DT / 2][3] : o[n][e][3]) + v.w;
+          }
+          add_prefix(at.b, at.run, n, warp * (DT / 2), w, m[n], l[n]);
+#pragma unroll
+          for (int e = 0; e < DT / 2; e++) put_out(at.b, at.run, n, e + warp * (DT / 2), w[e], l[n]);
+        }
+        if (warp == 0 && g == 0) put_lse(at.b, at.run, m, l);
+      } else if (warp < 2) {
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -622,6 +685,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
           oo[e][3] = oo[e][3] * keep[1] + v[e].w * add[1];
         }
       }
+      if (PRE) add_prefix(w.b, w.run, n, warp * E, oo, mm, ll);
 #pragma unroll
       for (int e = 0; e < E; e++) put_out(w.b, w.run, n, warp * E + e, oo[e], ll);
       m[n][0] = mm[0], m[n][1] = mm[1], l[n][0] = ll[0], l[n][1] = ll[1];
@@ -631,9 +695,9 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
 }
 
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool PRE>
 cudaError_t launch(const Args& a, int64_t most_units, cudaStream_t st) {
-  auto* fn = attend_kernel<T, D, NT>;
+  auto* fn = attend_kernel<T, D, NT, PRE>;
   constexpr int smem = kSmem<D, NT>;
   static OpsOnce once;
   static int resident = 1;  // CTAs of a multiprocessor
@@ -656,10 +720,11 @@ template <typename T, int D>
 cudaError_t by_share(Args& a, int64_t tiles, cudaStream_t st) {
   if (a.share <= 8) {
     a.runs = 1;
-    return launch<T, D, 1>(a, tiles * a.hkv, st);
+    return a.pre.parts ? launch<T, D, 1, true>(a, tiles * a.hkv, st) : launch<T, D, 1, false>(a, tiles * a.hkv, st);
   }
   a.runs = (a.share + 15) / 16;
-  return launch<T, D, 2>(a, tiles * a.hkv * a.runs, st);
+  const int64_t units = tiles * a.hkv * a.runs;
+  return a.pre.parts ? launch<T, D, 2, true>(a, units, st) : launch<T, D, 2, false>(a, units, st);
 }
 
 template <typename T>
@@ -674,13 +739,15 @@ cudaError_t by_width(Args& a, int d, int64_t tiles, cudaStream_t st) {
 
 using namespace wfst;
 
+extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) { return attend_behind(r, nullptr, stream); }
+
 extern "C" int wfst_attend_size(int64_t* bytes) {
   if (!bytes) return api_fail(WFST_ERR_INVALID_ARG, "attend_size: NULL argument");
   *bytes = kCounterBytes + (int64_t)kMaxGrid * 2 * kPartFloats * 4;
   return WFST_OK;
 }
 
-extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
+int wfst::attend_behind(const wfst_attend_args* r, const PrefixParts* prefix, void* stream) {
   if (!r) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: NULL argument");
   if (r->dtype != WFST_F16 && r->dtype != WFST_BF16) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: bad dtype");
   if (r->head_dim != 64 && r->head_dim != 128 && r->head_dim != 256)
@@ -728,6 +795,7 @@ extern "C" int wfst_attend_paged(const wfst_attend_args* r, void* stream) {
   a.div_m = (uint32_t)((((uint64_t)1 << (31 + l)) + r->page_size - 1) / r->page_size);
   a.div_s = 31 + l;
   a.scale2 = r->scale * kLog2e;
+  a.pre = prefix ? *prefix : PrefixParts{};
   a.o_even = aligned(r->o, 4) && a.so_b % 2 == 0 && a.so_h % 2 == 0;
   int64_t most = (int64_t)r->table_width * r->page_size;
   if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;

@@ -68,6 +68,24 @@ inline int ops_current() {
   return d;
 }
 
+// What wfst_prefix.cu leaves of the shared prefix for the kernel that attends to
+// each lane's own tokens and adds it: the prefix is cut into tiles of `keys`
+// keys, a key-value head's lanes * share query heads into `groups` groups of `rows`;
+// the tiles of all groups and heads are numbered through and shared evenly among
+// `grid` CTAs (fewer if there are fewer tiles).  CTA c leaves what it has of group s
+// in slot c + s: m [rows], l [rows], then o [head_dim / 4][rows][4], m, l and o
+// as the attention kernels hold them.
+struct PrefixParts {
+  const float* parts;
+  const int32_t* length;
+  int64_t room;  // tokens the prefix' table holds
+  int32_t keys, rows, groups, grid;
+};
+// wfst_attend_paged of checked arguments, behind such a prefix where there is one.
+// The kernel then starts while the prefix' kernel, which has to stand before it in
+// the stream, still runs.
+int attend_behind(const wfst_attend_args* args, const PrefixParts* prefix, void* stream);
+
 #ifdef __CUDACC__
 
 // Launches `fn` so that its CTAs may be set up while the kernel before it in the
