@@ -121,6 +121,16 @@ def test_splits(W, prefix, lens, hq, hkv, d):
     check(*attend(W, a), *a, d ** -0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("share", [1, 50])
+def test_long_runs(W, share, d, dtype):
+    """Many tiles of keys for each CTA, with one tile of rows and with two."""
+    for prefix in (20011, 7100):
+        a = make(prefix + share, prefix, [70, 0, 5], 8 * share, 8, d, 48, dtype)
+        check(*attend(W, a), *a, d ** -0.5)
+
+
 def test_a_workspace_whose_parts_hold_anything(W):
     a = make(3, 3000, [2000, 1, 0, 700], 24, 2, 128, 32, torch.bfloat16)
     ws = W.attend_prefix_workspace(4, 24, 2, 128)

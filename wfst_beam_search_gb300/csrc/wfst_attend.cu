@@ -330,49 +330,61 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
       reinterpret_cast<uint16_t*>(out)[8] = (uint16_t)r1, reinterpret_cast<uint16_t*>(out)[9] = (uint16_t)(r1 >> 16);
     }
   };
-  // adds the prefix' parts to the own one of heads 2t and 2t + 1 of run n: m, l and
-  // the elements g and g + 8 of the E tiles of 16 from d0 on
-  auto add_prefix = [&](int b, int run, int n, int d0, auto& oo, float (&mm)[2], float (&ll)[2]) {
-    constexpr int E = sizeof(oo) / sizeof(oo[0]);
-    ops_begin();
+  // adds the prefix' parts to the own one of a run's heads, which lies in shared
+  // memory (m and l in xm, o in xo [head][D]), and writes the result: a thread takes
+  // four elements of a head at a time
+  auto add_prefix = [&](int b, int run) {
     const uint32_t tiles = (uint32_t)((max((int64_t)0, min((int64_t)*a.pre.length, a.pre.room)) + a.pre.keys - 1) / a.pre.keys);
-    if (!tiles) return;
-    const uint32_t all = tiles * a.hkv * a.pre.groups, ctas = min((uint32_t)a.pre.grid, all), per = all / ctas,
+    const uint32_t all = tiles * a.hkv * a.pre.groups, ctas = max(1u, min((uint32_t)a.pre.grid, all)), per = all / ctas,
                    rest = all - per * ctas;
     auto owner = [&](uint32_t u) {
       const uint32_t at = rest * (per + 1);
       return u < at ? u / (per + 1) : rest + (u - at) / per;
     };
     const int64_t slot = (int64_t)a.pre.rows * (2 + D);
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
-      if (c >= a.share) continue;
-      const uint32_t r = (uint32_t)b * a.share + c, group = (uint32_t)(run / a.runs) * a.pre.groups + r / a.pre.rows;
-      const uint32_t row = r % a.pre.rows, c0 = owner(group * tiles), c1 = owner(group * tiles + tiles - 1);
-      const float* part = a.pre.parts + (c0 + group) * slot + row;
-#pragma unroll 2
-      for (uint32_t i = c0; i <= c1; i++, part += slot) {
-        const float pm = __ldcg(part), pl = __ldcg(part + a.pre.rows);
-        float v[E][2];
-#pragma unroll
-        for (int e = 0; e < E; e++)
-#pragma unroll
-          for (int y = 0; y < 2; y++) {
-            const int el = (d0 + e) * 16 + y * 8 + g;
-            v[e][y] = __ldcg(part - row + 2 * a.pre.rows + ((int64_t)(el >> 2) * a.pre.rows + row) * 4 + (el & 3));
-          }
-        const float now = fmaxf(mm[x], pm), ref = now == -INFINITY ? 0.f : now;
-        const float keep = exp2a(mm[x] - ref), add = exp2a(pm - ref);
-        mm[x] = now;
-        ll[x] = ll[x] * keep + pl * add;
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-          oo[e][x] = oo[e][x] * keep + v[e][0] * add;
-          oo[e][2 + x] = oo[e][2 + x] * keep + v[e][1] * add;
+    const int c0 = (run % a.runs) * (8 * NT), heads = min(8 * NT, a.share - c0);
+    for (int i = tid; i < heads * (D / 4); i += W * 32) {
+      // neighbours take neighbouring heads, which lie side by side
+      const int h = i % heads, d4 = i / heads;
+      float m1 = xm[h], l1 = xm[8 * NT + h];
+      float4 o1 = reinterpret_cast<const float4*>(xo)[h * (D / 4) + d4];
+      if (tiles) {
+        const uint32_t r = (uint32_t)b * a.share + c0 + h, group = (uint32_t)(run / a.runs) * a.pre.groups + r / a.pre.rows;
+        const uint32_t row = r % a.pre.rows, first = owner(group * tiles), last = owner(group * tiles + tiles - 1);
+        const float* part = a.pre.parts + (first + group) * slot;
+#pragma unroll 4
+        for (uint32_t k = first; k <= last; k++, part += slot) {
+          const float pm = __ldcg(part + row), pl = __ldcg(part + a.pre.rows + row);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 2 * a.pre.rows) + (int64_t)d4 * a.pre.rows + row);
+          const float now = fmaxf(m1, pm), ref = now == -INFINITY ? 0.f : now;
+          const float keep = exp2a(m1 - ref), add = exp2a(pm - ref);
+          m1 = now;
+          l1 = l1 * keep + pl * add;
+          o1.x = o1.x * keep + v.x * add, o1.y = o1.y * keep + v.y * add;
+          o1.z = o1.z * keep + v.z * add, o1.w = o1.w * keep + v.w * add;
         }
       }
+      const float inv = l1 > 0.f || l1 != l1 ? 1.f / l1 : 0.f;
+      const int head = (run / a.runs) * a.share + c0 + h;
+      const uint32_t w0 = pack2<T>(o1.x * inv, o1.y * inv), w1 = pack2<T>(o1.z * inv, o1.w * inv);
+      T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + (int64_t)head * a.so_h + d4 * 4;
+      if (a.o_even) {
+        reinterpret_cast<uint32_t*>(out)[0] = w0, reinterpret_cast<uint32_t*>(out)[1] = w1;
+      } else {
+        uint16_t* one = reinterpret_cast<uint16_t*>(out);
+        one[0] = (uint16_t)w0, one[1] = (uint16_t)(w0 >> 16), one[2] = (uint16_t)w1, one[3] = (uint16_t)(w1 >> 16);
+      }
+      if (a.lse && d4 == 0) a.lse[b * a.sl_b + head] = (m1 + (log2f(l1) - kLift<T>)) * kLn2;
     }
+  };
+  // puts 16 elements from 16 * d on of run n's heads where add_prefix wants them
+  auto lay_out = [&](int n, int d, const float (&w)[4]) {
+    float* at = xo + (n * 8 + 2 * t) * D + d * 16 + g;
+    at[0] = w[0], at[D] = w[1], at[8] = w[2], at[D + 8] = w[3];
+  };
+  auto lay_out_ml = [&](int n, const float (&mm)[2], const float (&ll)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; x++) xm[n * 8 + 2 * t + x] = mm[x], xm[8 * NT + n * 8 + 2 * t + x] = ll[x];
   };
   auto put_lse = [&](int b, int run, const float (&wm)[NT][2], const float (&wl)[NT][2]) {
     if (!a.lse) return;
@@ -565,21 +577,31 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         __syncthreads();
       }
       const bool whole = whole_start && ends;
-      if (PRE && whole && warp < 2) {
+      if (PRE && whole) {
+        float w[NT][DT / 2][4];
+        if (warp < 2) {
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-          float w[DT / 2][4];
+          for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int e = 0; e < DT / 2; e++) {
-            const float4 v = reinterpret_cast<float4*>(xo)[(((1 - warp) * NT + n) * DT + e + warp * (DT / 2)) * 32 + lane];
-            w[e][0] = (warp ? o[n][e + DT / 2][0] : o[n][e][0]) + v.x, w[e][1] = (warp ? o[n][e + DT / 2][1] : o[n][e][1]) + v.y;
-            w[e][2] = (warp ? o[n][e + DT / 2][2] : o[n][e][2]) + v.z, w[e][3] = (warp ? o[n][e + DT / 2][3] : o[n][e][3]) + v.w;
-          }
-          add_prefix(at.b, at.run, n, warp * (DT / 2), w, m[n], l[n]);
-#pragma unroll
-          for (int e = 0; e < DT / 2; e++) put_out(at.b, at.run, n, e + warp * (DT / 2), w[e], l[n]);
+            for (int e = 0; e < DT / 2; e++) {
+              const float4 v = reinterpret_cast<float4*>(xo)[(((1 - warp) * NT + n) * DT + e + warp * (DT / 2)) * 32 + lane];
+              w[n][e][0] = (warp ? o[n][e + DT / 2][0] : o[n][e][0]) + v.x, w[n][e][1] = (warp ? o[n][e + DT / 2][1] : o[n][e][1]) + v.y;
+              w[n][e][2] = (warp ? o[n][e + DT / 2][2] : o[n][e][2]) + v.z, w[n][e][3] = (warp ? o[n][e + DT / 2][3] : o[n][e][3]) + v.w;
+            }
         }
-        if (warp == 0 && g == 0) put_lse(at.b, at.run, m, l);
+        ops_begin();
+        __syncthreads();  // xo and xm have been read
+        if (warp < 2) {
+#pragma unroll
+          for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int e = 0; e < DT / 2; e++) lay_out(n, e + warp * (DT / 2), w[n][e]);
+            if (warp == 0 && g == 0) lay_out_ml(n, m[n], l[n]);
+          }
+        }
+        __syncthreads();
+        add_prefix(at.b, at.run);
+        __syncthreads();
       } else if (warp < 2) {
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -685,12 +707,24 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
           oo[e][3] = oo[e][3] * keep[1] + v[e].w * add[1];
         }
       }
-      if (PRE) add_prefix(w.b, w.run, n, warp * E, oo, mm, ll);
 #pragma unroll
-      for (int e = 0; e < E; e++) put_out(w.b, w.run, n, warp * E + e, oo[e], ll);
+      for (int e = 0; e < E; e++) {
+        if (PRE)
+          lay_out(n, warp * E + e, oo[e]);
+        else
+          put_out(w.b, w.run, n, warp * E + e, oo[e], ll);
+      }
+      if (PRE && warp == 0 && g == 0) lay_out_ml(n, mm, ll);
       m[n][0] = mm[0], m[n][1] = mm[1], l[n][0] = ll[0], l[n][1] = ll[1];
     }
-    if (warp == 0 && g == 0) put_lse(w.b, w.run, m, l);
+    if (PRE) {
+      ops_begin();
+      __syncthreads();
+      add_prefix(w.b, w.run);
+      __syncthreads();
+    } else if (warp == 0 && g == 0) {
+      put_lse(w.b, w.run, m, l);
+    }
   }
 }
 

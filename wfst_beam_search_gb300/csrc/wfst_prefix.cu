@@ -32,6 +32,8 @@
 // numbered through, and each CTA takes an equal range.
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "wfst_ops.h"
 
 namespace wfst {
@@ -39,13 +41,15 @@ namespace {
 
 constexpr int kRows = 128;       // of a tile, one to a thread
 constexpr int kMostGrid = 160;   // CTAs the workspace has room for: the multiprocessors of the chip
-constexpr int kMaskRing = 8;     // tiles whose masks are kept, more than are ever in flight
+constexpr int kMaskRing = 16;    // tiles whose masks are kept, more than are ever in flight
 constexpr uint32_t kNap = 20000, kSpins = 1u << 16;  // a wait sleeps so many ns at a time, and gives up after so many times
+constexpr int kLooks = 200;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 4.f;    // how far, in powers of two, a row's largest score may be above its reference
-// fp16 has no exponents below 2^-24: P is held times 2^11, so that with kSlack it stays
+// How far, in powers of two, a row's largest score may be above its reference.  fp16 has no exponents below 2^-24: P is held times 2^11, so that with kSlack it stays
 // within 2^15 and what is lost is below 2^-35 of the largest weight; the parts that are
 // left hold l and o times 2^15, as wfst_attend.cu does.
+template <typename T>
+constexpr float kSlack = std::is_same_v<T, __half> ? 4.f : 8.f;
 template <typename T>
 constexpr float kLift = std::is_same_v<T, __half> ? 11.f : 0.f;
 template <typename T>
@@ -58,9 +62,9 @@ constexpr int kKeys = D == 256 ? 64 : 128;
 template <int D>
 constexpr int kGroups = D == 256 ? 1 : 2;
 template <int D, int NQ>
-constexpr int kSlots = D == 64 ? 8 : D == 256 ? 4 : NQ == 2 ? 4 : 5;
+constexpr int kSlots = D == 64 ? 8 : D == 256 || NQ == 2 ? 4 : 6;
 template <int D>
-constexpr int kThreads = (kGroups<D> * 4 + 5) * 32;
+constexpr int kThreads = (kGroups<D> * 5 + 4) * 32;
 
 struct Args {
   const void *q, *kc, *vc;
@@ -70,16 +74,17 @@ struct Args {
   int32_t lanes, hkv, share, groups, page, num_pages;
   uint32_t div_m, div_s, flip;  // flip: the signs of q, for a negative scale
   float scale2;                 // |scale| * log2(e)
+  int32_t box;                  // keys of a page that one copy takes; 0: the maps are not for use
 };
 
 // What lies behind Q and the ring in shared memory.
 template <int S>
 struct Control {
-  uint64_t full[S], empty[S];          // a slot is filled, is free
-  uint64_t s_full[2], p_full[2], pv[2];  // S is there, P is there, the second product is through
-  uint64_t q_full, done;
-  uint32_t masks[kMaskRing][4];        // keys of a tile that are seen
-  float m[2][kRows], l[2][kRows];
+  uint64_t full[S], empty[S];  // a slot is filled, is free
+  // of each stream's 128 columns S is in halves: S is there, P is there, the second product is through
+  uint64_t s_full[2][2], p_full[2][2], pv[2][2];
+  uint64_t q_full[2], done[2];   // of a stream: Q is there, all its products are through
+  uint32_t masks[kMaskRing][4];  // keys of a tile that are seen, a quarter to a word
   uint32_t tmem;
 };
 template <int D, int NQ>
@@ -96,7 +101,11 @@ __device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
                : "memory");
   return done;
 }
+// (A warp that has gone to sleep wakes some 500 cycles late: it looks a while first.)
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < kLooks; i++)
+    if (test_bar(bar, parity)) return true;
 #pragma unroll 1
   for (uint32_t i = 0; i < kSpins; i++) {
     uint32_t done;
@@ -109,44 +118,77 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-__device__ __forceinline__ void arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ bool elected() {
   uint32_t is;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(is));
   return is != 0;
 }
+// a box of 64 elements by some keys of a page
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int element, int place, int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(element), "r"(place), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+// What the products' warp issues, by the one lane that `one` is not zero in.  The
+// predicate is on the instruction and there is no branch around it: what the matrix
+// instructions take has to be in registers that a warp has in common, and in a branch
+// of one lane it is moved there for each of them, which takes longer than a product.
+// The upper half of what describes an operand in shared memory: groups of eight rows
+// 1024 bytes apart, 16-byte pieces exchanged within that.
+constexpr uint32_t kUpper = 1024 >> 4 | 1u << 14 | 2u << 29;
 // d (+)= a * b; a in shared memory, and in tensor memory
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void product_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %6, 0;\n"
+      "mov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kUpper), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void product_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %6, 0;\n"
+      "mov.b64 y, {%2, %5};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kUpper), "r"(one)
       : "memory");
 }
-// 32 columns of this warp's 32 lanes, when they are there
-__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t at) {
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t one, uint32_t bar) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(one) : "memory");
+}
+// 32 columns of this warp's 32 lanes: asked for, and there (the registers go through
+// the wait, so that nothing that uses them is moved before it)
+__device__ __forceinline__ void tmem_ask(uint32_t (&r)[32], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at)
       : "memory");
+}
+__device__ __forceinline__ void tmem_there(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t at) {
+  tmem_ask(r, at);
+  tmem_there(r);
 }
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
@@ -156,6 +198,14 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 16 columns
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -168,6 +218,39 @@ __device__ __forceinline__ float exp2a(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// Two fp32 numbers at once.
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// Two weights as 16-bit parts: a first one, cut off (bf16, whose bits are the upper ones
+// of fp32) or rounded, and the rest, rounded.
+template <typename T>
+__device__ __forceinline__ uint32_t first_part(float p0, float p1) {
+  if (std::is_same_v<T, __half>) return pack2<T>(p0, p1);
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+}
+
+// A value that all lanes of a warp have, so that the compiler knows it: a reduction's
+// result is in a register that the warp has in common.
+__device__ __forceinline__ uint32_t same(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
 // Waits until all but the `open` youngest groups of this thread's copies have landed.
 __device__ __forceinline__ void landed(int open) {
   switch (open) {
@@ -186,18 +269,24 @@ __device__ __forceinline__ void landed(int open) {
 // pieces are exchanged by row within 1024 bytes.  Q and K are read along the rows
 // (groups of eight rows 1024 bytes apart), V across them (blocks of 64 elements
 // `block` bytes apart, groups of eight keys 1024).
-__device__ __forceinline__ uint64_t describe(uint32_t at, uint32_t block) {
-  return (uint64_t)(at >> 4 & 0x3fffu) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
+__device__ __forceinline__ uint32_t describe(uint32_t at, uint32_t block) { return (at >> 4 & 0x3fffu) | (block >> 4) << 16; }
 
 // NQ: tiles of rows of a CTA.
 template <typename T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads<D>, 1)
+    prefix_kernel(const Args a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ unsigned char raw_smem[];
   constexpr int KT = kKeys<D>, G = kGroups<D>, S = kSlots<D, NQ>, kTile = KT * D * 2, kRowsAll = NQ * kRows;
-  constexpr bool kTurns = NQ == 1;  // tiles of keys go to the two places of S in turn
-  constexpr int kO = 2 * KT;        // tensor memory: two places of S, then o (two of them with G == 2)
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // G streams of scores: of a tile of rows each, or of every other tile of keys (kTurns).
+  // A stream has 128 columns of tensor memory for S, which are exponentiated 64 at a
+  // time: the halves of a tile of keys (H == 2), or two tiles (H == 1).  P takes the place
+  // of S.  o lies behind them.
+  constexpr bool kTurns = NQ == 1 && G == 2;
+  constexpr int H = KT / 64, kO = 256;
+  // Slots of the ring go round for both streams together, or, with kTurns, for either by
+  // itself; a tile's keys are item 2 t of it, its values item 2 t + 1.
+  constexpr int R = kTurns ? S / 2 : S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)same(tid >> 5);
   unsigned char* q_tile = raw_smem + ((1024 - ((uint32_t)__cvta_generic_to_shared(raw_smem) & 1023)) & 1023);
   unsigned char* ring = q_tile + kRowsAll * D * 2;
   auto& sh = *reinterpret_cast<Control<S>*>(ring + S * kTile);
@@ -207,7 +296,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
   ops_begin();
   ops_next();
   // ---- this CTA's tiles
-  const int n = (int)max((int64_t)0, min((int64_t)*a.length, a.room));
+  const int n = (int)same((uint32_t)max((int64_t)0, min((int64_t)*a.length, a.room)));
   const uint32_t tiles = (n + KT - 1) / KT, units = tiles * a.hkv * a.groups;
   const uint32_t ctas = min(gridDim.x, units);
   if (blockIdx.x >= ctas) return;
@@ -218,10 +307,9 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
     auto init = [&](const uint64_t& b, int count) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(b)), "r"(count) : "memory");
     };
-    for (int i = 0; i < S; i++) init(sh.full[i], 4), init(sh.empty[i], 1);
-    for (int i = 0; i < 2; i++) init(sh.s_full[i], 2), init(sh.p_full[i], 4), init(sh.pv[i], 1);
-    init(sh.q_full, 4 * G);
-    init(sh.done, 1);
+    for (int i = 0; i < S; i++) init(sh.full[i], 4), init(sh.empty[i], NQ);
+    for (int i = 0; i < 4; i++) init(sh.s_full[i / 2][i % 2], 2), init(sh.p_full[i / 2][i % 2], 4), init(sh.pv[i / 2][i % 2], 1);
+    for (int i = 0; i < G; i++) init(sh.q_full[i], kTurns ? 8 : 4), init(sh.done[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 4 * G + 4) {
@@ -233,20 +321,22 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
   tmem_before();
   __syncthreads();
   tmem_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = same(sh.tmem);
   bool good = true;
 
   if (warp >= 4 * G && warp < 4 * G + 4) {
     // ---- copies: a warp takes a quarter of each tile's keys, in the order in which the tiles are needed
     constexpr int kMine = KT / 4, kLanes = D / 8, kAtOnce = 32 / kLanes;  // keys; lanes of a key, keys of an instruction
     const int w = warp - 4 * G;
-    uint32_t issued = 0, told = 0;
-    auto tell = [&]() {  // the oldest slot that is filled but not known to be
-      landed((int)(issued - told) - 1);
+    uint32_t pending[4] = {}, count = 0;  // barriers of the slots that are filled but not known to be, oldest first
+    auto tell = [&]() {
+      landed((int)count - 1);
       smem_seen();
       __syncwarp();
-      if (lane == 0) arrive(bar(sh.full[told % S]));
-      told++;
+      if (lane == 0) arrive(1, pending[0]);
+#pragma unroll
+      for (int i = 0; i < 3; i++) pending[i] = pending[i + 1];
+      count--;
     };
     struct Key {
       int id, place;
@@ -261,25 +351,23 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
       }
       return k;
     };
-    auto copy = [&](const Key& k, const void* pool, int64_t s_p, int64_t s_s, int64_t from) {
-      const int slot = issued % S;
-      if (issued >= S) {
-        const uint32_t parity = (issued / S - 1) & 1;
-        while (!__all_sync(0xffffffffu, test_bar(bar(sh.empty[slot]), parity))) {
-          if (issued > told) {
-            tell();
-          } else {
-            good = wait_bar(bar(sh.empty[slot]), parity);
-            break;
-          }
-        }
-        good = __all_sync(0xffffffffu, good);
-        if (!good) return;
-      }
+    // A warp's keys that are all there come in boxes, if pages hold whole ones; the others one by one.
+    auto copy = [&](int ring_no, uint32_t item, const Key& k, const CUtensorMap* map, int head, const void* pool, int64_t s_p,
+                    int64_t s_s, int64_t s_h) {
+      const int slot = ring_no * R + item % R;
       const bool seen = (uint32_t)k.id < (uint32_t)a.num_pages;
-      const int64_t off = seen ? k.id * s_p + k.place * s_s + from : 0;
-      const uint32_t some = __ballot_sync(0xffffffffu, seen);
-      const uint32_t dst = ring_at + slot * kTile;
+      const int64_t off = seen ? k.id * s_p + k.place * s_s + head * s_h : 0;
+      const uint32_t some = __ballot_sync(0xffffffffu, seen), full = bar(sh.full[slot]), dst = ring_at + slot * kTile;
+      if (a.box && some == 0xffffffffu >> (32 - kMine)) {
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "n"(kMine * D * 2) : "memory");
+        __syncwarp();
+        const int from = lane / (D / 64) * a.box, block = lane % (D / 64);
+        const int id = __shfl_sync(0xffffffffu, k.id, from % 32), place = __shfl_sync(0xffffffffu, k.place, from % 32);
+        if (from < kMine)
+          copy_box(dst + block * (KT * 128) + (w * kMine + from) * 128, map, block * 64, place, head, id, full);
+        return;
+      }
 #pragma unroll 8
       for (int i = 0; i < kMine; i += kAtOnce) {
         const int mine = i + lane / kLanes, row = w * kMine + mine, piece = lane % kLanes;
@@ -291,189 +379,193 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
                      : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      issued++;
-      if (issued - told > 3) tell();
+      if (count == 0) pending[0] = full;
+      if (count == 1) pending[1] = full;
+      if (count == 2) pending[2] = full;
+      if (count == 3) pending[3] = full;
+      if (++count == 4) tell();
     };
-    uint32_t count = 0;  // tiles whose keys have been copied
+    // waits for the slot of an item
+    auto room = [&](int ring_no, uint32_t item) {
+      if (item < (uint32_t)R || !good) return;
+      const uint32_t free = bar(sh.empty[ring_no * R + item % R]), parity = (item / R - 1) & 1;
+      while (!__all_sync(0xffffffffu, test_bar(free, parity))) {
+        if (count) {
+          tell();
+        } else {
+          good = wait_bar(free, parity);
+          break;
+        }
+      }
+      good = __all_sync(0xffffffffu, good);
+    };
+    uint32_t items[2] = {0, 0}, tile_no = 0;  // of either ring; all tiles
     for (uint32_t u = u0; u < u1 && good;) {
       const uint32_t group = u / tiles, t0 = u - group * tiles, some = min(tiles - t0, u1 - u);
-      const int64_t head = group / a.groups;
-      Key now[2], ahead = look_up(t0);
-      auto keys = [&](uint32_t i) {
+      const int head = group / a.groups;
+      Key ahead = look_up(t0);
+      for (uint32_t i = 0; i < some && good; i++, tile_no++) {
+        const int r = kTurns ? i % 2 : 0;
+        const uint32_t item = r ? items[1] : items[0];
         const Key k = ahead;
-        if (i % 2)
-          now[1] = k;
-        else
-          now[0] = k;
-        ahead = look_up(t0 + i + 1);
-        const uint32_t ok = __ballot_sync(0xffffffffu, (uint32_t)k.id < (uint32_t)a.num_pages);
-        copy(k, a.kc, a.ck_p, a.ck_s, head * a.ck_h);
-        if (lane == 0) sh.masks[count % kMaskRing][w] = ok;
-        count++;
-      };
-      constexpr uint32_t kLead = kTurns ? 2 : 1;
-      for (uint32_t i = 0; i < kLead && i < some; i++) keys(i);
-      for (uint32_t i = 0; i < some && good; i++) {
-        copy(i % 2 ? now[1] : now[0], a.vc, a.cv_p, a.cv_s, head * a.cv_h);
-        if (i + kLead < some) keys(i + kLead);
+        if (i + 1 < some) ahead = look_up(t0 + i + 1);
+        const uint32_t seen = __ballot_sync(0xffffffffu, (uint32_t)k.id < (uint32_t)a.num_pages);
+        room(r, item);
+        if (!good) break;
+        if (lane == 0) sh.masks[tile_no % kMaskRing][w] = seen;  // (the slot is free, and what went with its tile before it)
+        copy(r, item, k, &k_map, head, a.kc, a.ck_p, a.ck_s, a.ck_h);
+        room(r, item + 1);
+        if (good) copy(r, item + 1, k, &v_map, head, a.vc, a.cv_p, a.cv_s, a.cv_h);
+        (r ? items[1] : items[0]) += good ? 2 : 1;
       }
       u += some;
     }
-    while (good && issued > told) tell();
-    landed(0);
-  } else if (warp == 4 * G + 4) {
-    // ---- products.  kind::f16: fp32 sums, 128 rows; Q K^T with N = KT, P V with N = D and V read across its rows
+    while (count) tell();
+    // no box may be on its way when the CTA ends, nor where a wait gave up
+#pragma unroll
+    for (int r = 0; r < (kTurns ? 2 : 1); r++)
+      for (uint32_t i = items[r] > (uint32_t)R ? items[r] - R : 0; i < items[r]; i++)
+        if (!wait_bar(bar(sh.full[r * R + i % R]), i / R & 1)) break;
+  } else if (warp >= 4 * G + 4) {
+    // ---- products, a warp to each stream.  kind::f16: fp32 sums, 128 rows; Q K^T with N = KT, P V with N = D and V read across its rows
     constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
     constexpr uint32_t kBase = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kRows / 16) << 24;
     constexpr uint32_t kScores = kBase | (uint32_t)(KT / 8) << 17, kValues = kBase | (uint32_t)(D / 8) << 17 | 1u << 16;
-    uint32_t taken = 0;          // slots of the ring, in order
-    uint32_t s_used[2] = {0, 0};  // times either place has been used
-    auto slot_in = [&]() {
-      const int slot = taken % S;
-      good = good && wait_bar(bar(sh.full[slot]), (taken / S) & 1);
-      taken++;
+    const uint32_t one = elected();
+    const int j = G == 2 ? warp - (4 * G + 4) : 0, ring_no = kTurns ? j : 0;
+    uint32_t items = 0, scored = 0, summed = 0;  // items of the ring, and tiles (scores) and halves or tiles (values), before what is next
+    auto slot_in = [&](uint32_t item) {
+      const int slot = ring_no * R + item % R;
+      good = good && wait_bar(bar(sh.full[slot]), item / R & 1);
       return slot;
     };
-    auto scores = [&](int place, int q_tile_no, int slot, bool last) {
-      __syncwarp();
+    // S of a tile, where P of the one before (H == 1: before that) was
+    auto scores = [&](uint32_t item) {
+      const int slot = slot_in(item);
+      const uint32_t k = scored++, place = H == 2 ? 0 : k & 1;
+      if (k >= 3 - H) good = good && wait_bar(bar(sh.pv[j][H == 2 ? 1 : place]), (H == 2 ? k - 1 : (k - 2) >> 1) & 1);
+      good = __all_sync(0xffffffffu, good);
+      if (!good) return;
       tmem_after();
-      if (elected() && good) {
-        const uint64_t q = describe(q_at + q_tile_no * (kRows * D * 2), 16), k = describe(ring_at + slot * kTile, 16);
+      const uint32_t q = same(describe(q_at + (kTurns ? 0 : j) * (kRows * D * 2), 16)), key = same(describe(ring_at + slot * kTile, 16));
+      const uint32_t d = same(tmem + j * 128 + place * 64);
 #pragma unroll
-        for (int s = 0; s < D / 16; s++)
-          product_ss(tmem + place * KT, q + s / 4 * (kRows * 128 >> 4) + s % 4 * 2, k + s / 4 * (KT * 128 >> 4) + s % 4 * 2, kScores,
-                     s != 0);
-        commit(bar(sh.s_full[place]));
-        arrive(bar(sh.s_full[place]));  // (what was seen before it, the tile's mask among it, is seen behind it)
-        if (last) commit(bar(sh.empty[slot]));
-      }
-      __syncwarp();
+      for (int s = 0; s < D / 16; s++)
+        product_ss(one, d, q + s / 4 * (kRows * 128 >> 4) + s % 4 * 2, key + s / 4 * (KT * 128 >> 4) + s % 4 * 2, kScores, s != 0);
+      commit(one, bar(sh.s_full[j][place]));
+      arrive(one, bar(sh.s_full[j][place]));  // (what was seen before it, the tile's mask among it, is seen behind it)
+      commit(one, bar(sh.empty[slot]));
     };
-    auto values = [&](int place, int o_place, int slot, bool begins, bool last) {
-      good = good && wait_bar(bar(sh.p_full[place]), s_used[place] & 1);
-      s_used[place]++;
-      __syncwarp();
-      tmem_after();
-      if (elected() && good) {
-        const uint64_t v = describe(ring_at + slot * kTile, KT * 128);
+    // and its P V
+    auto values = [&](uint32_t item, bool begins) {
+      const int slot = slot_in(item);
+#pragma unroll 1
+      for (int h = 0; h < H; h++) {
+        const uint32_t m = summed++, x = m & 1;
+        good = good && wait_bar(bar(sh.p_full[j][x]), m >> 1 & 1);
+        good = __all_sync(0xffffffffu, good);
+        if (!good) continue;
+        tmem_after();
+        const uint32_t v = same(describe(ring_at + slot * kTile + h * (64 * 128), KT * 128)), p = same(tmem + j * 128 + x * 64);
+        const uint32_t d = same(tmem + kO + j * D);
 #pragma unroll
-        for (int s = 0; s < KT / 16; s++) {
-          const uint32_t p = tmem + place * KT + s / 2 * 32 + s % 2 * 8;
-          product_ts(tmem + kO + o_place * D, p, v + s * (2048 >> 4), kValues, !begins || s != 0);
-          product_ts(tmem + kO + o_place * D, p + 16, v + s * (2048 >> 4), kValues, true);
+        for (int s = 0; s < 4; s++) {
+          product_ts(one, d, p + s * 16, v + s * (2048 >> 4), kValues, !begins || h || s);
+          product_ts(one, d, p + s * 16 + 8, v + s * (2048 >> 4), kValues, true);
         }
-        commit(bar(sh.pv[place]));
-        if (last) commit(bar(sh.empty[slot]));
+        commit(one, bar(sh.pv[j][x]));
+        if (h == H - 1) commit(one, bar(sh.empty[slot]));
       }
-      __syncwarp();
     };
-    // P lies where the next S goes
-    auto through = [&](int place) { good = good && wait_bar(bar(sh.pv[place]), (s_used[place] - 1) & 1); };
-    uint32_t segment = 0;
+    uint32_t segment = 0;  // those that the stream has a part in
     for (uint32_t u = u0; u < u1;) {
-      const uint32_t some = min(tiles - u % tiles, u1 - u);
-      good = good && wait_bar(bar(sh.q_full), segment & 1);
-      if (kTurns) {
-        for (uint32_t i = 0; i < 2 && i < some; i++) scores(i, 0, slot_in(), true);
-        for (uint32_t i = 0; i < some; i++) {
-          const int place = i % 2;
-          values(place, G == 2 ? place : 0, slot_in(), i < (uint32_t)G, true);
-          if (i + 2 < some) {
-            const int slot = slot_in();
-            through(place);
-            scores(place, 0, slot, true);
-          }
-        }
-      } else {
-        int slot = slot_in();
-        scores(0, 0, slot, false);
-        scores(1, 1, slot, true);
-        for (uint32_t i = 0; i < some; i++) {
-          const int v = slot_in();
-          values(0, 0, v, i == 0, false);
-          if (i + 1 < some) {
-            slot = slot_in();
-            through(0);
-            scores(0, 0, slot, false);
-          }
-          values(1, 1, v, i == 0, true);
-          if (i + 1 < some) {
-            through(1);
-            scores(1, 1, slot, true);
-          }
-        }
-      }
+      const uint32_t some = min(tiles - u % tiles, u1 - u), steps = kTurns ? (some + 1 - j) / 2 : some;
       u += some;
-      segment++;
+      if (steps == 0) continue;
+      good = good && wait_bar(bar(sh.q_full[j]), segment++ & 1);
+      constexpr uint32_t kAhead = 3 - H;
+      for (uint32_t i = 0; i < kAhead && i < steps; i++) scores(items + 2 * i);
+      for (uint32_t i = 0; i < steps; i++) {
+        values(items + 2 * i + 1, i == 0);
+        if (i + kAhead < steps) scores(items + 2 * (i + kAhead));
+      }
+      items += 2 * steps;
     }
     // nothing may be on its way when its memory is given back, nor where a wait gave up
-    __syncwarp();
-    if (elected()) commit(bar(sh.done));
-    __syncwarp();
-    good = wait_bar(bar(sh.done), 0) && good;
+    commit(one, bar(sh.done[j]));
+    good = wait_bar(bar(sh.done[j]), 0) && good;
   } else if (warp < 4 * G) {
     // ---- a row to each thread
     const int wg = warp / 4, row = tid % kRows;
     const uint32_t mine = tmem + (uint32_t)((warp % 4) * 32 << 16);  // this warp's lanes
-    uint32_t used[2] = {0, 0}, count = 0;
+    uint32_t used = 0, count = 0;  // tiles of the stream, and of the CTA before this segment's
     for (uint32_t u = u0; u < u1;) {
       const uint32_t group = u / tiles, some = min(tiles - u % tiles, u1 - u);
       const uint32_t head = group / a.groups, row0 = group % a.groups * kRowsAll, rows = (uint32_t)a.lanes * a.share;
       // ---- Q: each warpgroup its own tile of rows, or half of the one
       {
-        constexpr int kPieces = D / 8, kStep = kTurns ? G * 128 : 128;
-        for (int i = kTurns ? tid : tid % 128; i < kRows * kPieces; i += kStep) {
-          const int r = i / kPieces + (kTurns ? 0 : wg * kRows), piece = i % kPieces;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row0 + r < rows) {
+        constexpr int kPieces = D / 8, kStep = NQ == 1 ? G * 128 : 128, kEach = kRows * kPieces / kStep,
+                      kBatch = kEach < 8 ? kEach : 8;
+#pragma unroll 1
+        for (int i0 = NQ == 1 ? tid : tid % 128; i0 < kRows * kPieces; i0 += kBatch * kStep) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; j++) {
+            const int i = i0 + j * kStep, r = i / kPieces + (NQ == 1 ? 0 : wg * kRows);
             const uint32_t b = (row0 + r) / a.share, c = (row0 + r) - b * a.share;
-            v = ops_load(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + b * a.sq_b +
-                                                        ((int64_t)head * a.share + c) * a.sq_h + piece * 8));
-            v.x ^= a.flip, v.y ^= a.flip, v.z ^= a.flip, v.w ^= a.flip;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (row0 + r < rows)
+              v[j] = ops_load(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + b * a.sq_b +
+                                                             ((int64_t)head * a.share + c) * a.sq_h + i % kPieces * 8));
           }
-          *reinterpret_cast<uint4*>(q_tile + r / kRows * (kRows * D * 2) + piece / 8 * (kRows * 128) + r % kRows * 128 +
-                                    ((piece % 8) ^ (r % 8)) * 16) = v;
+#pragma unroll
+          for (int j = 0; j < kBatch; j++) {
+            const int i = i0 + j * kStep, r = i / kPieces + (NQ == 1 ? 0 : wg * kRows), piece = i % kPieces;
+            v[j].x ^= a.flip, v[j].y ^= a.flip, v[j].z ^= a.flip, v[j].w ^= a.flip;
+            *reinterpret_cast<uint4*>(q_tile + r / kRows * (kRows * D * 2) + piece / 8 * (kRows * 128) + r % kRows * 128 +
+                                      ((piece % 8) ^ (r % 8)) * 16) = v[j];
+          }
         }
+        static_assert(kRows * kPieces % (kBatch * kStep) == 0);
       }
       smem_seen();
       tmem_before();  // (the segment before: o has been read)
       __syncwarp();
-      if (lane == 0) arrive(bar(sh.q_full));
+      // (each stream that has something to do is told, by all that have a part in its Q)
+#pragma unroll
+      for (int j = 0; j < G; j++)
+        if (lane == 0 && (kTurns ? some > (uint32_t)j : j == wg)) arrive(1, bar(sh.q_full[j]));
 
       float ref = -INFINITY, l = 0.f;
       bool any = false;  // o holds something
-      for (uint32_t i = kTurns && G == 2 ? wg : 0; i < some; i += kTurns && G == 2 ? 2 : 1) {
-        const int place = kTurns ? i % 2 : wg;
-        const uint32_t s_at = mine + place * KT, o_at = mine + kO + (G == 2 ? wg : 0) * D;
-        good = good && wait_bar(bar(sh.s_full[place]), used[place] & 1);
-        used[place]++;
+      for (uint32_t i = kTurns ? wg : 0; i < some; i += kTurns ? 2 : 1) {
+        const uint32_t k = used++;
+        good = good && wait_bar(bar(sh.s_full[wg][H == 2 ? 0 : k & 1]), (H == 2 ? k : k >> 1) & 1);
+#pragma unroll 1
+        for (int h = 0; h < H; h++) {
+        const uint32_t part = k * H + h, x = part & 1, s_at = mine + wg * 128 + x * 64, o_at = mine + kO + wg * D;
         __syncwarp();
         tmem_after();
-        uint32_t mask[KT / 32];
-        bool whole = true;
-        {
-          const uint32_t* seen = sh.masks[(count + i) % kMaskRing];
+        const uint32_t* seen = sh.masks[(count + i) % kMaskRing];
+        uint32_t r[2][32];  // the scores; -inf where the key is not seen
+        tmem_ask(r[0], s_at);
+        tmem_ask(r[1], s_at + 32);
+        tmem_there(r[0]);
+        tmem_there(r[1]);
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < KT / 32; c++) {
-            mask[c] = KT == 128 ? seen[c] : seen[2 * c] | seen[2 * c + 1] << 16;
-            whole = whole && mask[c] == 0xffffffffu;
-          }
-        }
-        uint32_t r[32];
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < KT / 32; c++) {
-          tmem_load(r, s_at + c * 32);
-          if (whole) {
-#pragma unroll
-            for (int j = 0; j < 32; j++) top = fmaxf(top, __uint_as_float(r[j]));
-          } else {
+        for (int c = 0; c < 2; c++) {
+          const uint32_t mask = H == 2 ? seen[2 * h + c] : seen[2 * c] | seen[2 * c + 1] << 16;
+          if (mask != 0xffffffffu) {
 #pragma unroll
             for (int j = 0; j < 32; j++)
-              if (mask[c] >> j & 1) top = fmaxf(top, __uint_as_float(r[j]));
+              if (!(mask >> j & 1)) r[c][j] = 0xff800000u;
           }
+#pragma unroll
+          for (int j = 0; j < 32; j++) tops[j % 4] = fmaxf(tops[j % 4], __uint_as_float(r[c][j]));
         }
-        const bool grows = top > ref && !((top - ref) * a.scale2 <= kSlack);
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        const bool grows = top > ref && !((top - ref) * a.scale2 <= kSlack<T>);
         if (__any_sync(0xffffffffu, grows)) {
           float keep = 1.f;
           if (grows) {
@@ -482,91 +574,98 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
             l *= keep;
           }
           if (any) {
-            if (G == 1) {  // the product of the tile before may still be adding to o
-              good = good && wait_bar(bar(sh.pv[place ^ 1]), (used[place ^ 1] - 1) & 1);
-              __syncwarp();
-              tmem_after();
-            }
+            // the product of the tile before may still be adding to o
+            good = good && wait_bar(bar(sh.pv[wg][x ^ 1]), (part - 1) >> 1 & 1);
+            __syncwarp();
+            tmem_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; c++) {
-              tmem_load(r, o_at + c * 32);
+              uint32_t v[32];
+              tmem_load(v, o_at + c * 32);
 #pragma unroll
-              for (int j = 0; j < 32; j++) r[j] = __float_as_uint(__uint_as_float(r[j]) * keep);
-              tmem_store(o_at + c * 32, r);
+              for (int j = 0; j < 32; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) * keep);
+              tmem_store(o_at + c * 32, v);
             }
             tmem_stored();
           }
         }
         any = true;
         const float from = ref == -INFINITY ? 0.f : ref;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const Two less(-from, -from), by(a.scale2, a.scale2), lift(kLift<T>, kLift<T>), minus(-1.f, -1.f);
+        Two sum[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < KT / 32; c++) {
-          tmem_load(r, s_at + c * 32);
-          uint32_t p[32];
+        for (int c = 0; c < 4; c++) {  // 16 keys: eight columns of first parts, eight of the rests
+          uint32_t p[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float p0 = exp2a(fmaf(__uint_as_float(r[j]) - from, a.scale2, kLift<T>));
-            float p1 = exp2a(fmaf(__uint_as_float(r[j + 1]) - from, a.scale2, kLift<T>));
-            if (!whole) {
-              p0 = mask[c] >> j & 1 ? p0 : 0.f;
-              p1 = mask[c] >> (j + 1) & 1 ? p1 : 0.f;
-            }
-            sum[j / 2 % 2 * 2] += p0;
-            sum[j / 2 % 2 * 2 + 1] += p1;
-            const uint32_t hi = pack2<T>(p0, p1);
-            const float2 f = unpack2<T>(hi);
-            p[j / 2] = hi;
-            p[16 + j / 2] = pack2<T>(p0 - f.x, p1 - f.y);
+          for (int j = 0; j < 8; j++) {
+            const uint32_t* x = &r[c / 2][c % 2 * 16 + 2 * j];
+            const float2 y = fma2(add2(Two(__uint_as_float(x[0]), __uint_as_float(x[1])), less), by, lift).get();
+            const float p0 = exp2a(y.x), p1 = exp2a(y.y);
+            const Two both(p0, p1);
+            sum[j % 2] = add2(sum[j % 2], both);
+            p[j] = first_part<T>(p0, p1);
+            const float2 f = unpack2<T>(p[j]);
+            const float2 rest = fma2(Two(f.x, f.y), minus, both).get();
+            p[8 + j] = pack2<T>(rest.x, rest.y);
           }
-          tmem_store(s_at + c * 32, p);
+          tmem_store(s_at + c * 16, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 s0 = sum[0].get(), s1 = sum[1].get();
+        l += (s0.x + s0.y) + (s1.x + s1.y);
         tmem_stored();
         tmem_before();
         __syncwarp();
-        if (lane == 0) arrive(bar(sh.p_full[place]));
+        if (lane == 0) arrive(1, bar(sh.p_full[wg][x]));
+        }
       }
-      if (kTurns && G == 2) used[wg ^ 1] += (some + wg) / 2;  // of the other warpgroup's place
 
       // ---- this CTA's part of the group
       float* part = a.parts + ((int64_t)blockIdx.x + group) * (kRowsAll * (2 + D));
-      if (kTurns) {  // all products are through when the last one is
-        good = good && wait_bar(bar(sh.pv[(some - 1) % 2]), (used[(some - 1) % 2] - 1) & 1);
-      } else {
-        good = good && wait_bar(bar(sh.pv[wg]), (used[wg] - 1) & 1);
+      if (used) {  // a stream's products are through when its last one is
+        const uint32_t last = used * H - 1;
+        good = good && wait_bar(bar(sh.pv[wg][last & 1]), last >> 1 & 1);
+      }
+      if (kTurns) {  // here both streams' have to be
+        __syncwarp();
+        tmem_after();
+        tmem_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
       }
       __syncwarp();
       tmem_after();
       float4* out = reinterpret_cast<float4*>(part + 2 * kRowsAll);
-      if (kTurns && G == 2) {
-        sh.m[wg][row] = ref, sh.l[wg][row] = l;
+      if (kTurns) {
+        float* const ml = reinterpret_cast<float*>(q_tile);  // (Q is not needed any more)
+        ml[wg * 256 + row] = ref, ml[wg * 256 + 128 + row] = l;
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const bool both = some > 1;
-        const float m0 = sh.m[0][row], m1 = both ? sh.m[1][row] : -INFINITY, top = fmaxf(m0, m1);
+        const float m0 = ml[row], m1 = both ? ml[256 + row] : -INFINITY, top = fmaxf(m0, m1);
         const float from = top == -INFINITY ? 0.f : top;
         const float f0 = m0 == -INFINITY ? 0.f : exp2a((m0 - from) * a.scale2) * kLeft<T>;
         const float f1 = m1 == -INFINITY ? 0.f : exp2a((m1 - from) * a.scale2) * kLeft<T>;
         if (wg == 0 && row0 + row < rows) {
           part[row] = good ? (top == -INFINITY ? top : top * a.scale2) : INFINITY;  // (makes NaN of what it is added to)
-          part[kRowsAll + row] = sh.l[0][row] * f0 + (both ? sh.l[1][row] * f1 : 0.f);
+          part[kRowsAll + row] = ml[128 + row] * f0 + (both ? ml[384 + row] * f1 : 0.f);
         }
 #pragma unroll 1
         for (int c = wg * (D / 64); c < (wg + 1) * (D / 64); c++) {
-          uint32_t r[32], s[32];
+          uint32_t r[32];
+          float v[32];
           tmem_load(r, mine + kO + c * 32);
-          if (both) tmem_load(s, mine + kO + D + c * 32);
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            r[j] = __float_as_uint(__uint_as_float(r[j]) * f0 + (both ? __uint_as_float(s[j]) * f1 : 0.f));
+          for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]) * f0;
+          if (both) {
+            tmem_load(r, mine + kO + D + c * 32);
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] += __uint_as_float(r[j]) * f1;
+          }
           if (row0 + row < rows) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              out[(c * 8 + j / 4) * kRowsAll + row] = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
-                                                                  __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+              out[(c * 8 + j / 4) * kRowsAll + row] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // m and l may be written again
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // Q may be written again
       } else {
         const int at = wg * kRows + row;
         if (row0 + at < rows) {
@@ -596,7 +695,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) prefix_kernel(const Args a) {
 }
 
 template <typename T, int D, int NQ>
-cudaError_t launch(const Args& a, int grid, cudaStream_t st) {
+cudaError_t launch(const Args& a, const CUtensorMap (&maps)[2], int grid, cudaStream_t st) {
   auto* fn = prefix_kernel<T, D, NQ>;
   constexpr int smem = kSmem<D, NQ>;
   static OpsOnce once;
@@ -605,14 +704,37 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     once.set(dev);
   }
-  return ops_launch(fn, dim3(grid), kThreads<D>, smem, 0, st, a);
+  return ops_launch(fn, dim3(grid), kThreads<D>, smem, 0, st, a, maps[0], maps[1]);
 }
 
 template <typename T>
-cudaError_t by_width(const Args& a, int d, int rows, int grid, cudaStream_t st) {
-  if (d == 256) return launch<T, 256, 1>(a, grid, st);
-  if (d == 128) return rows == kRows ? launch<T, 128, 1>(a, grid, st) : launch<T, 128, 2>(a, grid, st);
-  return rows == kRows ? launch<T, 64, 1>(a, grid, st) : launch<T, 64, 2>(a, grid, st);
+cudaError_t by_width(const Args& a, const CUtensorMap (&maps)[2], int d, int rows, int grid, cudaStream_t st) {
+  if (d == 256) return launch<T, 256, 1>(a, maps, grid, st);
+  if (d == 128) return rows == kRows ? launch<T, 128, 1>(a, maps, grid, st) : launch<T, 128, 2>(a, maps, grid, st);
+  return rows == kRows ? launch<T, 64, 1>(a, maps, grid, st) : launch<T, 64, 2>(a, maps, grid, st);
+}
+
+// The pool as the copies of boxes want it: (element, place, head, page), in any order of strides.
+bool map_pool(CUtensorMap* map, CUtensorMapDataType type, const void* pool, int d, const Args& a, int64_t s_s, int64_t s_h,
+              int64_t s_p) {
+  static const auto encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &how) != cudaSuccess)
+      fn = nullptr;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn);
+  }();
+  const cuuint64_t size[4] = {(cuuint64_t)d, (cuuint64_t)a.page, (cuuint64_t)a.hkv, (cuuint64_t)a.num_pages};
+  cuuint64_t stride[3];
+  const int64_t s[3] = {s_s, s_h, s_p};
+  for (int i = 0; i < 3; i++) {
+    if (size[i + 1] > 1 && (s[i] <= 0 || s[i] >= (int64_t)1 << 38)) return false;
+    stride[i] = size[i + 1] > 1 ? (cuuint64_t)s[i] * 2 : (cuuint64_t)d * 2;  // (along one entry, any)
+  }
+  const cuuint32_t box[4] = {64, (cuuint32_t)a.box, 1, 1}, step[4] = {1, 1, 1, 1};
+  return encode && encode(map, type, 4, const_cast<void*>(pool), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Rows of a group: two tiles where one does not hold all of them, so that a key that
@@ -691,11 +813,22 @@ extern "C" int wfst_attend_prefix(const wfst_prefix_args* r, void* stream) {
     a.div_s = 31 + l;
     a.flip = r->scale < 0.f ? 0x80008000u : 0u;
     a.scale2 = (r->scale < 0.f ? -r->scale : r->scale) * kLog2e;
+    if (a.scale2 < FLT_MIN) a.scale2 = FLT_MIN;  // (what is not seen, at -inf, stays there)
     int64_t grid = ops_sm_count();
     if (grid > kMostGrid) grid = kMostGrid;
     if (grid > units) grid = units;
-    const cudaError_t e = r->dtype == WFST_F16 ? by_width<__half>(a, r->head_dim, rows, (int)grid, (cudaStream_t)stream)
-                                               : by_width<__nv_bfloat16>(a, r->head_dim, rows, (int)grid, (cudaStream_t)stream);
+    // Boxes of as many keys as pages hold whole ones of, up to a warp's share of a tile; rows
+    // of eight at least, in which the 16-byte pieces are exchanged.
+    CUtensorMap maps[2] = {};
+    a.box = keys / 4;
+    while (a.box > 1 && r->page_size % a.box) a.box /= 2;
+    const auto type = r->dtype == WFST_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (a.box < 8 || !map_pool(maps, type, a.kc, r->head_dim, a, ck_s, ck_h, ck_p) ||
+        !map_pool(maps + 1, type, a.vc, r->head_dim, a, cv_s, cv_h, cv_p))
+      a.box = 0;
+    const cudaError_t e = r->dtype == WFST_F16
+                              ? by_width<__half>(a, maps, r->head_dim, rows, (int)grid, (cudaStream_t)stream)
+                              : by_width<__nv_bfloat16>(a, maps, r->head_dim, rows, (int)grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return api_cuda_fail(e, "attend_prefix launch");
     pre = {a.parts, r->prefix_length, room, keys, rows, (int)groups, (int)grid};
   }
