@@ -69,7 +69,8 @@ struct Args {
   int32_t div_s;
   float scale2;  // scale * log2(e)
   int32_t o_even;  // o's pairs of elements are 4-byte aligned
-  PrefixParts pre;
+  float* own;  // PRE: m [own_rows], l [own_rows], o [own_rows][D]; rows by key-value head, lane, head
+  int64_t own_rows;
 };
 
 // What a lane sees: n tokens, the first `first` as they are, the others
@@ -146,8 +147,9 @@ constexpr int kRing = D == 64 ? 8 : D == 128 ? 5 : 3;
 template <int D, int NT>
 constexpr int kSmem = kWarps<D> * kRing<D> * 16 * D * 2 + 2 * D * 8 * NT * 4 + kWarps<D> * 2 * 8 * NT * 4;
 
-// D: elements of a head; NT: runs of 8 * NT query heads.  PRE: a prefix' parts are
-// added to each lane's own before it is written.
+// D: elements of a head; NT: runs of 8 * NT query heads.  PRE: m, l and o are left
+// unscaled for wfst_prefix.cu, whose kernel before this one may still run: this one
+// ends after it.
 template <typename T, int D, int NT, bool PRE>
 __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   constexpr int W = kWarps<D>, UNIT = 16 * W, S = kRing<D>, kTile = 16 * D * 2, KS = D / 16, DT = D / 16;
@@ -155,8 +157,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   __shared__ uint32_t s_last[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int runs = a.hkv * a.runs;
-  // The prefix' kernel lets this one start when it has waited itself for what was
-  // before it; this one waits for it where its parts are added.
+  // (with PRE the kernel before has waited itself for what this one reads)
   if (!PRE) ops_begin();
   ops_next();
 
@@ -167,7 +168,10 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   units = __reduce_add_sync(0xffffffffu, units) * runs;
   // CTAs that share the units; each of them has one at least
   const uint32_t G = min(gridDim.x, units), each = units / G, more = units - each * G;
-  if (blockIdx.x >= G) return;
+  if (blockIdx.x >= G) {
+    if (PRE) ops_begin();
+    return;
+  }
   auto first_of = [&](uint32_t c) { return c * each + min(c, more); };
   auto cta_of = [&](uint32_t u) {
     const uint32_t at = more * (each + 1);
@@ -330,61 +334,24 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
       reinterpret_cast<uint16_t*>(out)[8] = (uint16_t)r1, reinterpret_cast<uint16_t*>(out)[9] = (uint16_t)(r1 >> 16);
     }
   };
-  // adds the prefix' parts to the own one of a run's heads, which lies in shared
-  // memory (m and l in xm, o in xo [head][D]), and writes the result: a thread takes
-  // four elements of a head at a time
-  auto add_prefix = [&](int b, int run) {
-    const uint32_t tiles = (uint32_t)((max((int64_t)0, min((int64_t)*a.pre.length, a.pre.room)) + a.pre.keys - 1) / a.pre.keys);
-    const uint32_t all = tiles * a.hkv * a.pre.groups, ctas = max(1u, min((uint32_t)a.pre.grid, all)), per = all / ctas,
-                   rest = all - per * ctas;
-    auto owner = [&](uint32_t u) {
-      const uint32_t at = rest * (per + 1);
-      return u < at ? u / (per + 1) : rest + (u - at) / per;
-    };
-    const int64_t slot = (int64_t)a.pre.rows * (2 + D);
-    const int c0 = (run % a.runs) * (8 * NT), heads = min(8 * NT, a.share - c0);
-    for (int i = tid; i < heads * (D / 4); i += W * 32) {
-      // neighbours take neighbouring heads, which lie side by side
-      const int h = i % heads, d4 = i / heads;
-      float m1 = xm[h], l1 = xm[8 * NT + h];
-      float4 o1 = reinterpret_cast<const float4*>(xo)[h * (D / 4) + d4];
-      if (tiles) {
-        const uint32_t r = (uint32_t)b * a.share + c0 + h, group = (uint32_t)(run / a.runs) * a.pre.groups + r / a.pre.rows;
-        const uint32_t row = r % a.pre.rows, first = owner(group * tiles), last = owner(group * tiles + tiles - 1);
-        const float* part = a.pre.parts + (first + group) * slot;
-#pragma unroll 4
-        for (uint32_t k = first; k <= last; k++, part += slot) {
-          const float pm = __ldcg(part + row), pl = __ldcg(part + a.pre.rows + row);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 2 * a.pre.rows) + (int64_t)d4 * a.pre.rows + row);
-          const float now = fmaxf(m1, pm), ref = now == -INFINITY ? 0.f : now;
-          const float keep = exp2a(m1 - ref), add = exp2a(pm - ref);
-          m1 = now;
-          l1 = l1 * keep + pl * add;
-          o1.x = o1.x * keep + v.x * add, o1.y = o1.y * keep + v.y * add;
-          o1.z = o1.z * keep + v.z * add, o1.w = o1.w * keep + v.w * add;
-        }
-      }
-      const float inv = l1 > 0.f || l1 != l1 ? 1.f / l1 : 0.f;
-      const int head = (run / a.runs) * a.share + c0 + h;
-      const uint32_t w0 = pack2<T>(o1.x * inv, o1.y * inv), w1 = pack2<T>(o1.z * inv, o1.w * inv);
-      T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + (int64_t)head * a.so_h + d4 * 4;
-      if (a.o_even) {
-        reinterpret_cast<uint32_t*>(out)[0] = w0, reinterpret_cast<uint32_t*>(out)[1] = w1;
-      } else {
-        uint16_t* one = reinterpret_cast<uint16_t*>(out);
-        one[0] = (uint16_t)w0, one[1] = (uint16_t)(w0 >> 16), one[2] = (uint16_t)w1, one[3] = (uint16_t)(w1 >> 16);
-      }
-      if (a.lse && d4 == 0) a.lse[b * a.sl_b + head] = (m1 + (log2f(l1) - kLift<T>)) * kLn2;
+  // PRE: leaves 16 elements from 16 * d on of run n's heads, and m and l, unscaled
+  auto leave_out = [&](int b, int run, int n, int d, const float (&w)[4]) {
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+      const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
+      if (c >= a.share) continue;
+      float* at = a.own + 2 * a.own_rows + (((int64_t)(run / a.runs) * a.lanes + b) * a.share + c) * D + d * 16 + g;
+      at[0] = w[x], at[8] = w[2 + x];
     }
   };
-  // puts 16 elements from 16 * d on of run n's heads where add_prefix wants them
-  auto lay_out = [&](int n, int d, const float (&w)[4]) {
-    float* at = xo + (n * 8 + 2 * t) * D + d * 16 + g;
-    at[0] = w[0], at[D] = w[1], at[8] = w[2], at[D + 8] = w[3];
-  };
-  auto lay_out_ml = [&](int n, const float (&mm)[2], const float (&ll)[2]) {
+  auto leave_ml = [&](int b, int run, int n, const float (&mm)[2], const float (&ll)[2]) {
 #pragma unroll
-    for (int x = 0; x < 2; x++) xm[n * 8 + 2 * t + x] = mm[x], xm[8 * NT + n * 8 + 2 * t + x] = ll[x];
+    for (int x = 0; x < 2; x++) {
+      const int c = (run % a.runs) * (8 * NT) + n * 8 + 2 * t + x;
+      if (c >= a.share) continue;
+      float* at = a.own + ((int64_t)(run / a.runs) * a.lanes + b) * a.share + c;
+      at[0] = mm[x], at[a.own_rows] = ll[x];
+    }
   };
   auto put_lse = [&](int b, int run, const float (&wm)[NT][2], const float (&wl)[NT][2]) {
     if (!a.lse) return;
@@ -577,32 +544,7 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
         __syncthreads();
       }
       const bool whole = whole_start && ends;
-      if (PRE && whole) {
-        float w[NT][DT / 2][4];
-        if (warp < 2) {
-#pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < DT / 2; e++) {
-              const float4 v = reinterpret_cast<float4*>(xo)[(((1 - warp) * NT + n) * DT + e + warp * (DT / 2)) * 32 + lane];
-              w[n][e][0] = (warp ? o[n][e + DT / 2][0] : o[n][e][0]) + v.x, w[n][e][1] = (warp ? o[n][e + DT / 2][1] : o[n][e][1]) + v.y;
-              w[n][e][2] = (warp ? o[n][e + DT / 2][2] : o[n][e][2]) + v.z, w[n][e][3] = (warp ? o[n][e + DT / 2][3] : o[n][e][3]) + v.w;
-            }
-        }
-        ops_begin();
-        __syncthreads();  // xo and xm have been read
-        if (warp < 2) {
-#pragma unroll
-          for (int n = 0; n < NT; n++) {
-#pragma unroll
-            for (int e = 0; e < DT / 2; e++) lay_out(n, e + warp * (DT / 2), w[n][e]);
-            if (warp == 0 && g == 0) lay_out_ml(n, m[n], l[n]);
-          }
-        }
-        __syncthreads();
-        add_prefix(at.b, at.run);
-        __syncthreads();
-      } else if (warp < 2) {
+      if (warp < 2) {
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -613,7 +555,10 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
                           warp ? o[n][e + DT / 2][2] : o[n][e][2], warp ? o[n][e + DT / 2][3] : o[n][e][3]};
             w[0] += v.x, w[1] += v.y, w[2] += v.z, w[3] += v.w;
             if (whole) {
-              put_out(at.b, at.run, n, d, w, l[n]);
+              if (PRE)
+                leave_out(at.b, at.run, n, d, w);
+              else
+                put_out(at.b, at.run, n, d, w, l[n]);
             } else {  // to the workspace; the last CTA adds up, below
               float* part = a.parts + ((int64_t)blockIdx.x * 2 + (from_u0 ? 0 : 1)) * kPartFloats;
               reinterpret_cast<float4*>(part + 2 * kColsMost)[(n * DT + d) * 32 + lane] = make_float4(w[0], w[1], w[2], w[3]);
@@ -621,7 +566,12 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
           }
         if (warp == 0 && g == 0) {
           if (whole) {
-            put_lse(at.b, at.run, m, l);
+            if (PRE) {
+#pragma unroll
+              for (int n = 0; n < NT; n++) leave_ml(at.b, at.run, n, m[n], l[n]);
+            } else {
+              put_lse(at.b, at.run, m, l);
+            }
           } else {
             float* part = a.parts + ((int64_t)blockIdx.x * 2 + (from_u0 ? 0 : 1)) * kPartFloats;
 #pragma unroll
@@ -651,7 +601,10 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
   }
 
   // ---- heads that are shared with other CTAs: the last one of them adds up, in CTA order
-  if (!left0.some && !left1.some) return;
+  if (!left0.some && !left1.some) {
+    if (PRE) ops_begin();
+    return;
+  }
   if (warp < 2) __threadfence();
   __syncthreads();
   if (tid < 2) {
@@ -710,22 +663,16 @@ __global__ void __launch_bounds__(kWarps<D> * 32) attend_kernel(const Args a) {
 #pragma unroll
       for (int e = 0; e < E; e++) {
         if (PRE)
-          lay_out(n, warp * E + e, oo[e]);
+          leave_out(w.b, w.run, n, warp * E + e, oo[e]);
         else
           put_out(w.b, w.run, n, warp * E + e, oo[e], ll);
       }
-      if (PRE && warp == 0 && g == 0) lay_out_ml(n, mm, ll);
+      if (PRE && warp == 0 && g == 0) leave_ml(w.b, w.run, n, mm, ll);
       m[n][0] = mm[0], m[n][1] = mm[1], l[n][0] = ll[0], l[n][1] = ll[1];
     }
-    if (PRE) {
-      ops_begin();
-      __syncthreads();
-      add_prefix(w.b, w.run);
-      __syncthreads();
-    } else if (warp == 0 && g == 0) {
-      put_lse(w.b, w.run, m, l);
-    }
+    if (!PRE && warp == 0 && g == 0) put_lse(w.b, w.run, m, l);
   }
+  if (PRE) ops_begin();
 }
 
 
@@ -754,11 +701,11 @@ template <typename T, int D>
 cudaError_t by_share(Args& a, int64_t tiles, cudaStream_t st) {
   if (a.share <= 8) {
     a.runs = 1;
-    return a.pre.parts ? launch<T, D, 1, true>(a, tiles * a.hkv, st) : launch<T, D, 1, false>(a, tiles * a.hkv, st);
+    return a.own ? launch<T, D, 1, true>(a, tiles * a.hkv, st) : launch<T, D, 1, false>(a, tiles * a.hkv, st);
   }
   a.runs = (a.share + 15) / 16;
   const int64_t units = tiles * a.hkv * a.runs;
-  return a.pre.parts ? launch<T, D, 2, true>(a, units, st) : launch<T, D, 2, false>(a, units, st);
+  return a.own ? launch<T, D, 2, true>(a, units, st) : launch<T, D, 2, false>(a, units, st);
 }
 
 template <typename T>
@@ -781,7 +728,7 @@ extern "C" int wfst_attend_size(int64_t* bytes) {
   return WFST_OK;
 }
 
-int wfst::attend_behind(const wfst_attend_args* r, const PrefixParts* prefix, void* stream) {
+int wfst::attend_behind(const wfst_attend_args* r, float* own, void* stream) {
   if (!r) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: NULL argument");
   if (r->dtype != WFST_F16 && r->dtype != WFST_BF16) return api_fail(WFST_ERR_INVALID_ARG, "attend_paged: bad dtype");
   if (r->head_dim != 64 && r->head_dim != 128 && r->head_dim != 256)
@@ -829,7 +776,8 @@ int wfst::attend_behind(const wfst_attend_args* r, const PrefixParts* prefix, vo
   a.div_m = (uint32_t)((((uint64_t)1 << (31 + l)) + r->page_size - 1) / r->page_size);
   a.div_s = 31 + l;
   a.scale2 = r->scale * kLog2e;
-  a.pre = prefix ? *prefix : PrefixParts{};
+  a.own = own;
+  a.own_rows = ((int64_t)r->lanes * r->q_heads + 3) / 4 * 4;
   a.o_even = aligned(r->o, 4) && a.so_b % 2 == 0 && a.so_h % 2 == 0;
   int64_t most = (int64_t)r->table_width * r->page_size;
   if (a.window && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;

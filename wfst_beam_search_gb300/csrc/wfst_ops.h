@@ -68,23 +68,12 @@ inline int ops_current() {
   return d;
 }
 
-// What wfst_prefix.cu leaves of the shared prefix for the kernel that attends to
-// each lane's own tokens and adds it: the prefix is cut into tiles of `keys`
-// keys, a key-value head's lanes * share query heads into `groups` groups of `rows`;
-// the tiles of all groups and heads are numbered through and shared evenly among
-// `grid` CTAs (fewer if there are fewer tiles).  CTA c leaves what it has of group s
-// in slot c + s: m [rows], l [rows], then o [head_dim / 4][rows][4], m, l and o
-// as the attention kernels hold them.
-struct PrefixParts {
-  const float* parts;
-  const int32_t* length;
-  int64_t room;  // tokens the prefix' table holds
-  int32_t keys, rows, groups, grid;
-};
-// wfst_attend_paged of checked arguments, behind such a prefix where there is one.
-// The kernel then starts while the prefix' kernel, which has to stand before it in
-// the stream, still runs.
-int attend_behind(const wfst_attend_args* args, const PrefixParts* prefix, void* stream);
+// wfst_attend_paged of checked arguments.  With `own` m, l and o are left there
+// unscaled, as the attention kernels hold them (m [rows], l [rows], o
+// [rows][head_dim]; rows: lanes * q_heads up to a multiple of 4, by key-value head,
+// lane, head of it), and o and lse are not written; the kernel then starts while the one before it in
+// the stream, which has to be ops_launch's, still runs, and ends after it.
+int attend_behind(const wfst_attend_args* args, float* own, void* stream);
 
 #ifdef __CUDACC__
 

@@ -57,12 +57,12 @@ constexpr float kLeft = std::is_same_v<T, __half> ? 16.f : 1.f;
 
 // Keys of a tile; warpgroups that exponentiate; slots of the ring (keys or values of
 // one tile each), as many as fit beside Q.
-template <int D>
-constexpr int kKeys = D == 256 ? 64 : 128;
+template <int D, int NQ>
+constexpr int kKeys = D == 256 || NQ == 2 ? 64 : 128;
 template <int D>
 constexpr int kGroups = D == 256 ? 1 : 2;
 template <int D, int NQ>
-constexpr int kSlots = D == 64 ? 8 : D == 256 || NQ == 2 ? 4 : 6;
+constexpr int kSlots = D == 256 ? 4 : NQ == 2 ? 8 : 6;
 template <int D>
 constexpr int kThreads = (kGroups<D> * 5 + 4) * 32;
 
@@ -88,7 +88,7 @@ struct Control {
   uint32_t tmem;
 };
 template <int D, int NQ>
-constexpr int kSmem = 1024 + NQ * kRows * D * 2 + kSlots<D, NQ> * kKeys<D> * D * 2 + (int)sizeof(Control<kSlots<D, NQ>>);
+constexpr int kSmem = 1024 + NQ * kRows * D * 2 + kSlots<D, NQ> * kKeys<D, NQ> * D * 2 + (int)sizeof(Control<kSlots<D, NQ>>);
 static_assert(kSmem<64, 2> <= 232448 && kSmem<128, 1> <= 232448 && kSmem<128, 2> <= 232448 && kSmem<256, 1> <= 232448);
 
 // ---- instructions
@@ -276,7 +276,7 @@ template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads<D>, 1)
     prefix_kernel(const Args a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ unsigned char raw_smem[];
-  constexpr int KT = kKeys<D>, G = kGroups<D>, S = kSlots<D, NQ>, kTile = KT * D * 2, kRowsAll = NQ * kRows;
+  constexpr int KT = kKeys<D, NQ>, G = kGroups<D>, S = kSlots<D, NQ>, kTile = KT * D * 2, kRowsAll = NQ * kRows;
   // G streams of scores: of a tile of rows each, or of every other tile of keys (kTurns).
   // A stream has 128 columns of tensor memory for S, which are exponentiated 64 at a
   // time: the halves of a tile of keys (H == 2), or two tiles (H == 1).  P takes the place
@@ -505,28 +505,30 @@ __global__ void __launch_bounds__(kThreads<D>, 1)
       // ---- Q: each warpgroup its own tile of rows, or half of the one
       {
         constexpr int kPieces = D / 8, kStep = NQ == 1 ? G * 128 : 128, kEach = kRows * kPieces / kStep,
-                      kBatch = kEach < 8 ? kEach : 8;
+                      kBatch = kEach < 16 ? kEach : 16, kDown = kStep / kPieces;  // a thread's next piece is kDown rows below
+        static_assert(kStep % kPieces == 0 && kEach % kBatch == 0);
+        const int t0 = NQ == 1 ? tid : tid % 128, piece = t0 % kPieces;
+        int r = t0 / kPieces;
+        const uint32_t first = row0 + r + (NQ == 1 ? 0 : wg * kRows), down_b = kDown / a.share, down_c = kDown - down_b * a.share;
+        uint32_t b = first / a.share, c = first - b * a.share;
+        const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)head * a.share * a.sq_h + piece * 8;
+        unsigned char* to = q_tile + (NQ == 1 ? 0 : wg) * (kRows * D * 2) + piece / 8 * (kRows * 128);
 #pragma unroll 1
-        for (int i0 = NQ == 1 ? tid : tid % 128; i0 < kRows * kPieces; i0 += kBatch * kStep) {
+        for (int n = 0; n < kEach; n += kBatch) {
           uint4 v[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; j++) {
-            const int i = i0 + j * kStep, r = i / kPieces + (NQ == 1 ? 0 : wg * kRows);
-            const uint32_t b = (row0 + r) / a.share, c = (row0 + r) - b * a.share;
             v[j] = make_uint4(0, 0, 0, 0);
-            if (row0 + r < rows)
-              v[j] = ops_load(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + b * a.sq_b +
-                                                             ((int64_t)head * a.share + c) * a.sq_h + i % kPieces * 8));
+            if (b < (uint32_t)a.lanes) v[j] = ops_load(reinterpret_cast<const uint4*>(q + b * a.sq_b + c * a.sq_h));
+            b += down_b, c += down_c;
+            if (c >= (uint32_t)a.share) c -= a.share, b++;
           }
 #pragma unroll
-          for (int j = 0; j < kBatch; j++) {
-            const int i = i0 + j * kStep, r = i / kPieces + (NQ == 1 ? 0 : wg * kRows), piece = i % kPieces;
+          for (int j = 0; j < kBatch; j++, r += kDown) {
             v[j].x ^= a.flip, v[j].y ^= a.flip, v[j].z ^= a.flip, v[j].w ^= a.flip;
-            *reinterpret_cast<uint4*>(q_tile + r / kRows * (kRows * D * 2) + piece / 8 * (kRows * 128) + r % kRows * 128 +
-                                      ((piece % 8) ^ (r % 8)) * 16) = v[j];
+            *reinterpret_cast<uint4*>(to + r * 128 + ((piece % 8) ^ (r % 8)) * 16) = v[j];
           }
         }
-        static_assert(kRows * kPieces % (kBatch * kStep) == 0);
       }
       smem_seen();
       tmem_before();  // (the segment before: o has been read)
@@ -737,6 +739,86 @@ bool map_pool(CUtensorMap* map, CUtensorMapDataType type, const void* pool, int 
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ---- the parts put together
+//
+// A CTA takes eight rows of a key-value head, a thread four elements of one: with
+// eight neighbours of a group the parts' 128 bytes.
+constexpr int kJoinRows = 8, kJoinThreads = 256;
+struct Join {
+  const float *parts, *own;
+  const int32_t* length;
+  void* o;
+  float* lse;
+  int64_t so_b, so_h, sl_b, room, own_rows;
+  int32_t hkv, share, rows, keys, group, groups, grid, o_even;  // rows: of a key-value head; group: rows of one
+};
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Join a) {
+  __shared__ float ms[kMostGrid + 1][kJoinRows], ls[kMostGrid + 1][kJoinRows];
+  constexpr int kSide = kJoinThreads / kJoinRows;
+  const int head = blockIdx.y, side = threadIdx.x / kJoinRows, r = threadIdx.x % kJoinRows;
+  const int row = min(blockIdx.x * kJoinRows + r, (uint32_t)a.rows - 1);  // (one past the end does the last one's work again)
+  // (the length was there before the kernels that this one waits for)
+  const uint32_t tiles = (uint32_t)((max((int64_t)0, min((int64_t)*a.length, a.room)) + a.keys - 1) / a.keys);
+  const uint32_t units = tiles * a.hkv * a.groups, ctas = min((uint32_t)a.grid, units);
+  const uint32_t group = head * a.groups + row / a.group, at = row % a.group;
+  uint32_t first = 0, count = 0;  // CTAs that have a part of the group
+  if (units) {
+    const uint32_t each = units / ctas, more = units - each * ctas;
+    auto owner = [&](uint32_t u) {
+      const uint32_t big = more * (each + 1);
+      return u < big ? u / (each + 1) : more + (u - big) / each;
+    };
+    first = owner(group * tiles), count = owner(group * tiles + tiles - 1) - first + 1;
+  }
+  const int64_t mine = (int64_t)head * a.rows + row, slot = (int64_t)a.group * (2 + D);
+  const float* part = a.parts + (first + group) * slot;
+  ops_begin();
+  ops_next();
+  // m and l of all parts, the lane's own last, then their weights
+  for (uint32_t i = side; i <= count; i += kSide) {
+    ms[i][r] = __ldcg(i < count ? part + i * slot + at : a.own + mine);
+    ls[i][r] = __ldcg(i < count ? part + i * slot + a.group + at : a.own + a.own_rows + mine);
+  }
+  float4 v = __ldcg(reinterpret_cast<const float4*>(a.own + 2 * a.own_rows + mine * D) + min(side, D / 4 - 1));
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f;
+  for (uint32_t i = 0; i <= count; i++) top = fmaxf(top, ms[i][r]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  for (uint32_t i = 0; i <= count; i++) sum += ls[i][r] * exp2a(ms[i][r] - ref);
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  const int b = row / a.share, c = row - b * a.share, h = head * a.share + c;
+  if (a.lse && side == 0) {
+    constexpr float kLn2 = 0.6931471805599453f, kLifted = std::is_same_v<T, __half> ? 15.f : 0.f;
+    a.lse[b * a.sl_b + h] = (top + (log2f(sum) - kLifted)) * kLn2;
+  }
+#pragma unroll 1
+  for (int d4 = side; d4 < D / 4; d4 += kSide) {
+    if (d4 != side) v = __ldcg(reinterpret_cast<const float4*>(a.own + 2 * a.own_rows + mine * D) + d4);
+    const float f0 = exp2a(ms[count][r] - ref);
+    v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll 8
+    for (uint32_t i = 0; i < count; i++) {
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(part + i * slot + 2 * a.group) + (int64_t)d4 * a.group + at);
+      const float f = exp2a(ms[i][r] - ref);
+      v.x += w.x * f, v.y += w.y * f, v.z += w.z * f, v.w += w.w * f;
+    }
+    const uint32_t w0 = pack2<T>(v.x * inv, v.y * inv), w1 = pack2<T>(v.z * inv, v.w * inv);
+    T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + h * a.so_h + d4 * 4;
+    if (a.o_even) {
+      reinterpret_cast<uint32_t*>(out)[0] = w0, reinterpret_cast<uint32_t*>(out)[1] = w1;
+    } else {
+      uint16_t* one = reinterpret_cast<uint16_t*>(out);
+      one[0] = (uint16_t)w0, one[1] = (uint16_t)(w0 >> 16), one[2] = (uint16_t)w1, one[3] = (uint16_t)(w1 >> 16);
+    }
+  }
+}
+template <typename T>
+cudaError_t join(const Join& a, int d, cudaStream_t st) {
+  auto* fn = d == 64 ? join_kernel<T, 64> : d == 128 ? join_kernel<T, 128> : join_kernel<T, 256>;
+  return ops_launch(fn, dim3((a.rows + kJoinRows - 1) / kJoinRows, a.hkv), kJoinThreads, 0, 0, st, a);
+}
+
 // Rows of a group: two tiles where one does not hold all of them, so that a key that
 // has been copied is used twice.
 int rows_of_group(int64_t rows, int d) { return d == 256 || rows <= kRows ? kRows : 2 * kRows; }
@@ -753,12 +835,12 @@ extern "C" int wfst_prefix_size(int32_t lanes, int32_t q_heads, int32_t kv_heads
   if (lanes < 0 || q_heads < 0) return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: counts must be >= 0");
   if (kv_heads < 1 || q_heads % kv_heads)
     return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: q_heads must be a multiple of kv_heads");
-  if ((int64_t)lanes * q_heads > INT32_MAX) return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: too many heads");
+  if ((int64_t)lanes * q_heads > INT32_MAX || kv_heads > 65535) return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: too many heads");
   int64_t own;
   if (const int rc = wfst_attend_size(&own)) return rc;
   const int64_t rows = (int64_t)lanes * (q_heads / kv_heads), group = rows_of_group(rows, head_dim);
   const int64_t groups = (rows + group - 1) / group * kv_heads;
-  *bytes = own + (kMostGrid + groups) * group * (2 + head_dim) * 4;
+  *bytes = own + ((kMostGrid + groups) * group + (rows * kv_heads + 3) / 4 * 4) * (2 + head_dim) * 4;
   return WFST_OK;
 }
 
@@ -790,14 +872,14 @@ extern "C" int wfst_attend_prefix(const wfst_prefix_args* r, void* stream) {
   if (dev < 0) return api_fail(WFST_ERR_INVALID_ARG, "attend_prefix: every array must be device memory of one device");
   const int share = r->q_heads / r->kv_heads, rows = rows_of_group((int64_t)r->lanes * share, r->head_dim);
   const int64_t groups = ((int64_t)r->lanes * share + rows - 1) / rows, room = (int64_t)r->prefix_width * r->page_size;
-  const int keys = r->head_dim == 256 ? kKeys<256> : kKeys<128>;
+  const int keys = r->head_dim == 256 ? kKeys<256, 1> : rows == kRows ? kKeys<128, 1> : kKeys<128, 2>;
   const int64_t units = (room + keys - 1) / keys * groups * r->kv_heads;
   if (units > INT32_MAX) return api_fail(WFST_ERR_INVALID_ARG, "attend_prefix: lanes * heads * tokens is too large");
   int64_t own;
   if (const int rc = wfst_attend_size(&own)) return rc;
   OpsDevice guard(dev);
   if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "attend_prefix: device");
-  PrefixParts pre = {};
+  Join j = {};
   if (units) {
     Args a;
     a.q = r->q, a.kc = r->k_pages, a.vc = r->v_pages;
@@ -830,7 +912,9 @@ extern "C" int wfst_attend_prefix(const wfst_prefix_args* r, void* stream) {
                               ? by_width<__half>(a, maps, r->head_dim, rows, (int)grid, (cudaStream_t)stream)
                               : by_width<__nv_bfloat16>(a, maps, r->head_dim, rows, (int)grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return api_cuda_fail(e, "attend_prefix launch");
-    pre = {a.parts, r->prefix_length, room, keys, rows, (int)groups, (int)grid};
+    j.parts = a.parts, j.length = r->prefix_length, j.room = room, j.keys = keys, j.group = rows, j.groups = (int)groups;
+    j.grid = (int)grid;
+    j.own = a.parts + (kMostGrid + groups * r->kv_heads) * rows * (2 + r->head_dim);
   }
   wfst_attend_args b = {};
   b.q = r->q, b.k_pages = r->k_pages, b.v_pages = r->v_pages, b.table = r->table, b.lengths = r->lengths;
@@ -841,5 +925,13 @@ extern "C" int wfst_attend_prefix(const wfst_prefix_args* r, void* stream) {
   b.device = dev, b.dtype = r->dtype, b.lanes = r->lanes, b.q_heads = r->q_heads, b.kv_heads = r->kv_heads;
   b.head_dim = r->head_dim, b.table_width = r->table_width, b.num_pages = r->num_pages, b.page_size = r->page_size;
   b.scale = r->scale;
-  return attend_behind(&b, units ? &pre : nullptr, stream);
+  if (const int rc = attend_behind(&b, const_cast<float*>(j.own), stream)) return rc;
+  if (!units) return WFST_OK;
+  j.o = r->o, j.lse = r->lse;
+  j.so_b = stride(r->o_stride[0], r->lanes), j.so_h = stride(r->o_stride[1], r->q_heads), j.sl_b = r->lse_stride;
+  j.own_rows = ((int64_t)r->lanes * r->q_heads + 3) / 4 * 4, j.hkv = r->kv_heads, j.share = share, j.rows = r->lanes * share;
+  j.o_even = aligned(r->o, 4) && j.so_b % 2 == 0 && j.so_h % 2 == 0;
+  const cudaError_t e = r->dtype == WFST_F16 ? join<__half>(j, r->head_dim, (cudaStream_t)stream)
+                                             : join<__nv_bfloat16>(j, r->head_dim, (cudaStream_t)stream);
+  return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "attend_prefix join launch");
 }
