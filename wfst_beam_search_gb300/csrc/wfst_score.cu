@@ -10,15 +10,16 @@
 // at a time, four of them ahead, and keeps the running maximum with Z and U against it;
 // rows end with the CTA's (and the cluster's) threads putting theirs together.
 //
-// The alternatives cost no second pass.  A thread has its own largest logit: the k
-// largest of those are k logits, so the k largest of all are among those not below the
-// k-th of them, which only the threads that have one so large can hold.  What bound lets
-// between k and some more threads through is found by halving; what they hold above it,
-// read again (from the L2 cache), is usually a few more than k, and is ordered by
-// counting.  Where it does not fit the list (many equal logits), the list is cut to its
-// k first whenever it is full, and from then on only what is before the last of those
-// goes in.
+// The alternatives cost no second pass.  A thread keeps the largest logit of each
+// eighth of what it reads.  The k largest of the threads' largest logits are k logits,
+// so the k largest of all are among those not below the k-th of them.  A bound that k
+// threads reach, and not many more, is found by halving; the eighths that reach it, read
+// again, hold a few more than k logits above it, usually, which are ordered by counting.
+// Where they do not fit the list (many equal logits), the list is cut to its k first
+// whenever it is full, and from then on only what is before the last of those goes in.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "wfst_ops.h"
 
@@ -27,12 +28,11 @@ namespace cg = cooperative_groups;
 namespace wfst {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 64 + kThreads * 8;  // candidates: what is kept, and what all threads' 16 bytes can add
+template <int N>
+constexpr int kAhead = N == 256 ? 8 : 4;  // granules of 16 bytes that a thread loads at once
+constexpr int kParts = 8;   // of what a thread reads, each with its largest logit
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args {
   const void* logits;
@@ -65,25 +65,26 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
   return r;
 }
 
-// Z and U (in powers of two) against the largest logit m.
+// Z and U against the largest logit m.
 struct Sums {
   float m = -INFINITY, z = 0.f, u = 0.f;
   // moves the reference up; what lies at -inf stays nothing
   __device__ __forceinline__ void raise(float to) {
     if (!(to > m)) return;
     if (m > -INFINITY) {
-      const float down = (m - to) * kLog2e, f = exp2a(down);
-      u = f > 0.f ? f * (u + down * z) : 0.f * u;  // (NaN stays)
+      const float down = fmaxf(m - to, -1000.f), f = exp2a(down * kLog2e);
+      u = f * (u + down * z);
       z *= f;
     }
     m = to;
   }
-  __device__ __forceinline__ void add(const Sums& o) {
-    Sums b = o;
-    raise(b.m);
-    b.raise(m);
-    z += b.z;
-    u += b.u;
+  // all lanes get the sum over the warp
+  __device__ __forceinline__ void over_warp() {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key_of(m));
+    if (top) raise(of_key(top));
+#pragma unroll
+    for (int x = 16; x; x /= 2) z += __shfl_xor_sync(0xffffffffu, z, x), u += __shfl_xor_sync(0xffffffffu, u, x);
+    m = top ? of_key(top) : -INFINITY;
   }
 };
 
@@ -115,124 +116,262 @@ __device__ __forceinline__ void widen(uint4 raw, float (&v)[16 / sizeof(T)]) {
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
+template <int N>  // threads
 struct Shared {
-  Sums part[kWarps];
-  uint32_t least[kWarps], most[kWarps];
-  Sums box[kMaxCluster];                       // the cluster's CTAs' sums
+  static constexpr int kList = WFST_SCORE_TOP + N * 8;  // candidates: what is kept, and what all threads' 16 bytes can add
+  Sums sums[N / 32];
+  Sums box[kMaxCluster];                         // the cluster's CTAs' sums
   uint64_t first[kMaxCluster * WFST_SCORE_TOP];  // and their first ones
   uint64_t list[kList], kept[WFST_SCORE_TOP];
-  uint32_t best[kThreads];                     // each thread's largest logit
-  uint16_t winner[kThreads];                   // threads that hold candidates
-  uint32_t count, winners;
+  uint32_t best[N], best_of[kParts][N];          // each thread's largest logit, and that of its parts
+  uint16_t cell[kParts * N];                     // parts that hold candidates
+  uint32_t cells, count, low;
 };
 
 // The `top` first of list[0 .. n) in order, to `to` (0 where there are no more).
+template <int N>
 __device__ void order_list(const uint64_t* list, uint32_t n, uint64_t* to, int top) {
-  for (int i = threadIdx.x; i < top; i += kThreads) to[i] = 0;
+  for (int i = threadIdx.x; i < top; i += N) to[i] = 0;
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+  for (uint32_t i = threadIdx.x; i < n; i += N) {
     const uint64_t v = list[i];
     int before = 0;
-    for (uint32_t j = 0; j < n && before < top; j++) before += list[j] > v;
+#pragma unroll 8
+    for (uint32_t j = 0; j < n; j++) before += list[j] > v;
     if (before < top) to[before] = v;
   }
   __syncthreads();
 }
 
-// The `top` first logits among the granules [lo, hi) that this CTA has read, in order, to sh->kept.
-template <typename T>
-__device__ void alternatives(const Row<T>& row, int lo, int hi, int top, Shared* sh) {
-  constexpr int VEC = Row<T>::VEC;
+// The `top` first logits among the granules [lo, hi) that this CTA has read in parts of 2^steps
+// granules a thread, in order, to sh->kept.
+template <typename T, int N>
+__device__ void alternatives(const Row<T>& row, int lo, int hi, int steps, int top, Shared<N>* sh) {
+  constexpr int VEC = Row<T>::VEC, W = N / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t mine = sh->best[tid];
   // ---- a bound that at least `top` threads' largest logits reach, and not many more if it can be
-  uint32_t least = mine ? mine : ~0u, most = mine;
-  least = __reduce_min_sync(0xffffffffu, least);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) sh->least[warp] = least, sh->most[warp] = most;
-  if (tid == 0) sh->count = sh->winners = 0;
-  __syncthreads();
+  if (warp == 0) {
+    uint32_t k[W], least = ~0u, most = 0, with = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) least = min(least, sh->least[w]), most = max(most, sh->most[w]);
-  // at least `top` reach low, fewer reach high
-  uint32_t low = least, high = most + 1;
-  const int enough = top + top / 2 + 4;
-  int n = __syncthreads_count(mine != 0);
-  if (n < top) low = 1, n = 0;  // fewer threads have a logit: all logits are candidates
-  while (n > enough && high - low > 1) {
-    const uint32_t mid = low + (high - low) / 2;
-    const int c = __syncthreads_count(mine >= mid);
-    if (c >= top)
-      low = mid, n = c;
-    else
-      high = mid;
+    for (int w = 0; w < W; w++) {
+      k[w] = sh->best[w * 32 + lane];
+      least = min(least, k[w] ? k[w] : ~0u), most = max(most, k[w]);
+      with += k[w] != 0;
+    }
+    least = __reduce_min_sync(0xffffffffu, least), most = __reduce_max_sync(0xffffffffu, most);
+    int n = (int)__reduce_add_sync(0xffffffffu, with);
+    uint32_t low = least, high = most + 1;  // at least `top` reach low, fewer reach high
+    if (n < top) low = 1, n = 0;            // fewer threads have a logit: all logits are candidates
+    const int enough = top + top / 2 + 4;
+    constexpr uint32_t kUnit = sizeof(T) == 4 ? 1u : std::is_same_v<T, __half> ? 1u << 13 : 1u << 16;  // between two values of T
+    while (n > enough && high - low > kUnit) {
+      const uint32_t mid = low + (high - low) / 2;
+      uint32_t c = 0;
+#pragma unroll
+      for (int w = 0; w < W; w++) c += k[w] >= mid;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if ((int)c >= top)
+        low = mid, n = (int)c;
+      else
+        high = mid;
+    }
+    if (lane == 0) sh->low = low, sh->count = sh->cells = 0;
   }
-  // ---- the threads that reach it, in order
-  const bool wins = mine != 0 && mine >= low;
-  const uint32_t votes = __ballot_sync(0xffffffffu, wins);
-  if (lane == 0) sh->least[warp] = __popc(votes);
   __syncthreads();
-  uint32_t before = 0, winners = 0;
+  const uint32_t low = sh->low;
+  // ---- the parts that reach it
+  if (sh->best[tid] >= low) {
+    uint32_t reach = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) before += w < warp ? sh->least[w] : 0, winners += sh->least[w];
-  if (wins) sh->winner[before + __popc(votes & ((1u << lane) - 1))] = (uint16_t)tid;
+    for (int g = 0; g < kParts; g++) reach |= (sh->best_of[g][tid] >= low ? 1u : 0u) << g;
+    for (uint32_t at = atomicAdd(&sh->cells, __popc(reach)); reach; reach &= reach - 1, at++)
+      sh->cell[at] = (uint16_t)((__ffs(reach) - 1) * N + tid);
+  }
   __syncthreads();
-  // ---- what they have read, from the first granule on, again
-  const int each = (hi - lo + kThreads - 1) / kThreads;
-  const int items = each * (int)winners;
-  auto visit = [&](int i, uint64_t after, auto push) {
-    const int g = lo + i / (int)winners * kThreads + sh->winner[i % (int)winners];
-    if (g >= hi) return;
-    float v[VEC];
-    widen<T>(row.load(g), v);
+  // ---- what they hold: bits of a granule's logits that count, and one of them
+  auto those = [&](const float (&v)[VEC], int g, uint64_t after) {
+    uint32_t is = 0;
 #pragma unroll
     for (int j = 0; j < VEC; j++) {
       const uint32_t key = key_of(v[j]);
-      if (key && key >= low) {
-        const uint64_t o = order_of(key, g * VEC - row.pad + j);
-        if (o > after) push(o);
-      }
+      is |= (key && key >= low && order_of(key, g * VEC - row.pad + j) > after ? 1u : 0u) << j;
     }
+    return is;
   };
-  for (int i = tid; i < items; i += kThreads)
-    visit(i, 0, [&](uint64_t o) {
-      const uint32_t at = atomicAdd(&sh->count, 1u);
-      if (at < (uint32_t)kList) sh->list[at] = o;
-    });
+  constexpr uint32_t kList = Shared<N>::kList;
+  auto push = [&](const float (&v)[VEC], int g, uint32_t is) {
+    uint32_t at = is ? atomicAdd(&sh->count, __popc(is)) : 0;
+#pragma unroll
+    for (int j = 0; j < VEC; j++)
+      if (is >> j & 1) {
+        if (at < kList) sh->list[at] = order_of(key_of(v[j]), g * VEC - row.pad + j);
+        at++;
+      }
+  };
+  for (int i = tid; i < (int)sh->cells << steps; i += N) {
+    const int c = sh->cell[i >> steps], g = lo + c % N + ((c / N << steps) + (i & ((1 << steps) - 1))) * N;
+    if (g >= hi) continue;
+    float v[VEC];
+    widen<T>(row.load(g), v);
+    push(v, g, those(v, g, 0));
+  }
   __syncthreads();
   uint32_t found = sh->count;
-  if (found > (uint32_t)kList / 2) {  // equal logits, mostly: in steps, the list cut to the first ones in between
-    uint64_t after = 0;
-    uint32_t have = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-      if (tid == 0) sh->count = have;
-      __syncthreads();
-      if (i0 + tid < items) visit(i0 + tid, after, [&](uint64_t o) { sh->list[atomicAdd(&sh->count, 1u)] = o; });
-      __syncthreads();
-      found = have = sh->count;
-      __syncthreads();
-      if (found > (uint32_t)WFST_SCORE_TOP || i0 + kThreads >= items) {
-        order_list(sh->list, found, sh->kept, top);
-        if (tid < top) sh->list[tid] = sh->kept[tid];
-        have = min(found, (uint32_t)top);
-        if (have == (uint32_t)top) after = sh->kept[top - 1];
-        __syncthreads();
-      }
-    }
+  if (found <= kList / 2) {
+    order_list<N>(sh->list, found, sh->kept, top);
     return;
   }
-  order_list(sh->list, found, sh->kept, top);
+  // equal logits, mostly: everything again in order, the list cut to the first ones in between
+  uint64_t after = 0;
+  uint32_t have = 0;
+  for (int i0 = lo; i0 < hi; i0 += N) {
+    __syncthreads();
+    if (tid == 0) sh->count = have;
+    __syncthreads();
+    if (i0 + tid < hi) {
+      float v[VEC];
+      widen<T>(row.load(i0 + tid), v);
+      push(v, i0 + tid, those(v, i0 + tid, after));
+    }
+    __syncthreads();
+    found = have = sh->count;
+    if (found > (uint32_t)WFST_SCORE_TOP || i0 + N >= hi) {
+      order_list<N>(sh->list, found, sh->kept, top);
+      if (tid < top) sh->list[tid] = sh->kept[tid];
+      have = min(found, (uint32_t)top);
+      if (have == (uint32_t)top) after = sh->kept[top - 1];
+    }
+  }
+  __syncthreads();
 }
 
+// ---- 16-bit logits two by two
 template <typename T>
-__global__ void __launch_bounds__(kThreads) score_kernel(const Args a) {
-  constexpr int VEC = Row<T>::VEC, kAhead = 4;
-  extern __shared__ __align__(16) unsigned char raw[];
-  Shared* sh = reinterpret_cast<Shared*>(raw);
+struct Pairs;
+template <>
+struct Pairs<__half> {
+  using V = __half2;
+  static constexpr uint32_t kNone = 0xfc00fc00u, kBound = 0xfbfffbffu;  // -inf; -65504
+  static constexpr float kFrom = -32000.f;
+};
+template <>
+struct Pairs<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static constexpr uint32_t kNone = 0xff80ff80u, kBound = 0xf14af14au;  // -inf; -1e30
+  static constexpr float kFrom = -1e29f;
+};
+template <typename V>
+__device__ __forceinline__ V as(uint32_t w) {
+  return *reinterpret_cast<const V*>(&w);
+}
+template <typename V>
+__device__ __forceinline__ uint32_t bits(V v) {
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The largest of some granules' logits; NaN is passed over.
+template <typename T, int A>
+__device__ __forceinline__ float largest(const uint4 (&raw)[A]) {
+  if constexpr (sizeof(T) == 4) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < A; j++)
+      top = fmaxf(fmaxf(fmaxf(top, __uint_as_float(raw[j].x)), fmaxf(__uint_as_float(raw[j].y), __uint_as_float(raw[j].z))),
+                  __uint_as_float(raw[j].w));
+    return top;
+  } else {
+    using V = typename Pairs<T>::V;
+    V top = as<V>(Pairs<T>::kNone);
+#pragma unroll
+    for (int j = 0; j < A; j++)
+      top = __hmax2(__hmax2(top, __hmax2(as<V>(raw[j].x), as<V>(raw[j].y))), __hmax2(as<V>(raw[j].z), as<V>(raw[j].w)));
+    const float2 t = unpack2<T>(bits(top));
+    return fmaxf(t.x, t.y);
+  }
+}
+
+// Adds some granules' logits, none of which is above s.m.
+template <typename T, int A>
+__device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[A]) {
+  constexpr int VEC = Row<T>::VEC;
+  // -inf weighs nothing, and must not be multiplied by that: it is brought up to a bound far below
+  // the largest logit, where the weight is zero all the same
+  if (constexpr float from = sizeof(T) == 4 ? -1e29f : Pairs<std::conditional_t<sizeof(T) == 4, __half, T>>::kFrom; s.m > from) {
+    const uint64_t less = two(-s.m, -s.m), by = two(kLog2e, kLog2e);
+    uint64_t z = two(0.f, 0.f), u = z;
+#pragma unroll
+    for (int j = 0; j < A; j++) {
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int e = 0; e < VEC / 2; e++) {
+        float2 x;
+        if constexpr (sizeof(T) == 4) {
+          x = make_float2(max_or_nan(__uint_as_float(w[2 * e]), -1e30f), max_or_nan(__uint_as_float(w[2 * e + 1]), -1e30f));
+        } else {
+          using V = typename Pairs<T>::V;
+          x = unpack2<T>(bits(__hmax2_nan(as<V>(w[e]), as<V>(Pairs<T>::kBound))));
+        }
+        const uint64_t y = add2(two(x.x, x.y), less);
+        const float2 p = parts(mul2(y, by));
+        const uint64_t f = two(exp2a(p.x), exp2a(p.y));
+        z = add2(z, f);
+        u = fma2(f, y, u);
+      }
+    }
+    const float2 zz = parts(z), uu = parts(u);
+    s.z += zz.x + zz.y;
+    s.u += uu.x + uu.y;
+  } else {  // a row of such logits alone, so far
+    const float ref = s.m > -INFINITY ? s.m : 0.f;
+#pragma unroll
+    for (int j = 0; j < A; j++) {
+      float v[VEC];
+      widen<T>(raw[j], v);
+#pragma unroll
+      for (int e = 0; e < VEC; e++) {
+        const float y = max_or_nan(v[e] - ref, -1000.f), f = exp2a(y * kLog2e);
+        s.z += f;
+        s.u += f * y;
+      }
+    }
+  }
+}
+
+// N threads; 256 for few rows, 128 for many (2000 x 20000, fp16, %FIG%).
+template <typename T, int N>
+__global__ void __launch_bounds__(N, N == 256 ? 4 : 12) score_kernel(const Args a) {
+  constexpr int VEC = Row<T>::VEC, W = N / 32, A = kAhead<N>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared<N>* sh = reinterpret_cast<Shared<N>*>(smem);
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), r = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (C > 1) cl.barrier_arrive();  // (waited for where another CTA's memory is written)
   ops_begin();
   ops_next();
   Row<T> row;
@@ -244,94 +383,84 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const Args a) {
   const int t = tid == 0 && rank == 0 ? ops_load(a.tokens + r) : 0;
   const float x_t = tid == 0 && rank == 0 && t >= 0 && t < a.vocab ? to_f32(ops_load(row.p + t)) : 0.f;
 
-  // ---- one pass
+  // ---- one pass, in parts of 2^rounds rounds of A granules
+  int rounds = 0;
+  while ((A * N * kParts) << rounds < hi - lo) rounds++;
   Sums s;
-  for (int i0 = lo + tid; i0 < hi; i0 += kAhead * kThreads) {
-    uint4 raw[kAhead];
-    float top = -INFINITY;
+  uint32_t best = 0;
+#pragma unroll 1
+  for (int g = 0; g < kParts; g++) {
+    float top_of = -INFINITY;
+    for (int k = 0; k < 1 << rounds; k++) {
+      const int i0 = lo + tid + ((g << rounds) + k) * (A * N);
+      if (i0 >= hi) break;
+      uint4 raw[A];
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      const int i = i0 + j * kThreads;
-      raw[j] = make_uint4(0, 0, 0, 0);
-      if (i < hi) raw[j] = row.load(i);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      if (i0 + j * kThreads >= hi) break;
-      float v[VEC];
-      widen<T>(raw[j], v);
-#pragma unroll
-      for (int e = 0; e < VEC; e++) top = fmaxf(top, v[e]);
-    }
-    s.raise(top);
-    const float ref = s.m > -INFINITY ? s.m : 0.f;
-#pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      if (i0 + j * kThreads >= hi) break;
-      float v[VEC];
-      widen<T>(raw[j], v);
-#pragma unroll
-      for (int e = 0; e < VEC; e++) {
-        // (from 2^-1000 on it weighs nothing, and must not be -inf: 0 times that is NaN)
-        const float y = max_or_nan((v[e] - ref) * kLog2e, -1000.f), w = exp2a(y);
-        s.z += w;
-        s.u += w * y;
+      for (int j = 0; j < A; j++) {
+        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : Pairs<std::conditional_t<sizeof(T) == 4, __half, T>>::kNone;
+        raw[j] = make_uint4(kNone, kNone, kNone, kNone);
+        if (i0 + j * N < hi) raw[j] = row.load(i0 + j * N);
       }
+      const float top = largest<T, A>(raw);
+      top_of = fmaxf(top_of, top);
+      s.raise(top);
+      add_granules<T, A>(s, raw);
     }
+    const uint32_t key = key_of(top_of);
+    sh->best_of[g][tid] = key;
+    best = max(best, key);
   }
-  sh->best[tid] = key_of(s.m);
-#pragma unroll
-  for (int x = 16; x; x /= 2) {
-    Sums o;
-    o.m = __shfl_xor_sync(0xffffffffu, s.m, x);
-    o.z = __shfl_xor_sync(0xffffffffu, s.z, x);
-    o.u = __shfl_xor_sync(0xffffffffu, s.u, x);
-    s.add(o);
-  }
-  if (lane == 0) sh->part[warp] = s;
+  sh->best[tid] = best;
+  s.over_warp();
+  if (lane == 0) sh->sums[warp] = s;
   __syncthreads();
-  if (a.top) alternatives(row, lo, hi, a.top, sh);
-  const uint64_t* first = sh->kept;
-  Sums all = sh->part[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; w++) all.add(sh->part[w]);
+  if (a.top) alternatives<T, N>(row, lo, hi, rounds + (A == 8 ? 3 : 2), a.top, sh);
+  s = lane < W ? sh->sums[lane] : Sums();
+  s.over_warp();
   if (C > 1) {
-    cl.sync();  // every CTA runs
-    Shared* to = cl.map_shared_rank(sh, 0);
-    if (tid == 0) to->box[rank] = all;
+    cl.barrier_wait();  // every CTA runs
+    Shared<N>* to = cl.map_shared_rank(sh, 0);
+    if (tid == 0) to->box[rank] = s;
     if (tid < a.top) to->first[rank * a.top + tid] = sh->kept[tid];
     cl.sync();
     if (rank) return;
-    all = sh->box[0];
-    for (int w = 1; w < C; w++) all.add(sh->box[w]);
-    if (a.top) order_list(sh->first, C * a.top, sh->kept, a.top);
+    s = lane < C ? sh->box[lane] : Sums();
+    s.over_warp();
+    if (a.top) order_list<N>(sh->first, C * a.top, sh->kept, a.top);
   }
   // (NaN and +inf: Z is NaN; no logit: Z is 0)
-  const float log_z = logf(all.z), ref = all.m > -INFINITY ? all.m : 0.f;
+  const float log_z = logf(s.z), ref = s.m > -INFINITY ? s.m : 0.f;
   if (tid == 0) {
     float v = 0.f;
     if (t >= a.vocab)
       v = NAN;
     else if (t >= 0)
-      v = all.z == 0.f ? -INFINITY : x_t - ref - log_z;
+      v = s.z == 0.f ? -INFINITY : x_t - ref - log_z;
     a.logprobs[r] = v;
-    a.entropy[r] = all.z == 0.f ? 0.f : log_z - all.u / all.z * kLn2;
+    a.entropy[r] = s.z == 0.f ? 0.f : log_z - s.u / s.z;
   }
-  for (int i = tid; i < a.top; i += kThreads) {
-    const uint64_t o = first[i];
-    a.top_tokens[(int64_t)r * a.top + i] = o ? (int)(0xffffffffu - (uint32_t)o) : -1;
-    a.top_logprobs[(int64_t)r * a.top + i] = o ? of_key((uint32_t)(o >> 32)) - ref - log_z : -INFINITY;
+  if (tid < a.top) {
+    const uint64_t o = sh->kept[tid];
+    a.top_tokens[(int64_t)r * a.top + tid] = o ? (int)(0xffffffffu - (uint32_t)o) : -1;
+    a.top_logprobs[(int64_t)r * a.top + tid] = o ? of_key((uint32_t)(o >> 32)) - ref - log_z : -INFINITY;
   }
+}
+
+template <typename T, int N>
+cudaError_t launch_as(const Args& a, int cluster, cudaStream_t st) {
+  static_assert(sizeof(Shared<N>) <= 48 * 1024);
+  return ops_launch(score_kernel<T, N>, dim3((unsigned)a.rows * cluster), N, (int)sizeof(Shared<N>), cluster, st, a);
 }
 
 template <typename T>
 cudaError_t launch(const Args& a, cudaStream_t st) {
-  // A row is shared among as many CTAs as leave each of them a few rounds and all of them a
-  // place: some four to a multiprocessor are resident.
-  const int granules = (int)(((int64_t)a.vocab * sizeof(T) + 15) / 16);
+  const int granules = (int)(((int64_t)a.vocab * sizeof(T) + 15) / 16), places = 4 * ops_sm_count();
+  if (a.rows > places) return launch_as<T, 128>(a, 1, st);
+  // A row is shared among as many CTAs as leave each thread some granules and all CTAs a
+  // place: four to a multiprocessor are resident.
   int C = 1;
-  while (C < kMaxCluster && granules / C > 2 * kThreads && (int64_t)a.rows * C * 2 <= 4 * ops_sm_count()) C *= 2;
-  return ops_launch(score_kernel<T>, dim3((unsigned)a.rows * C), kThreads, (int)sizeof(Shared), C, st, a);
+  while (C < kMaxCluster && granules / C > 512 && (int64_t)a.rows * C * 2 <= places) C *= 2;
+  return launch_as<T, 256>(a, C, st);
 }
 
 }  // namespace
