@@ -1,12 +1,38 @@
-// wfst_lowrank.cu — low-rank adapters of many requests beside a shared
-// projection: first form, one CTA per row.
+// wfst_lowrank.cu — low-rank adapters of many requests beside a shared projection.
+//
+//   a = adapter[r],  t_j = scale[a] * sum_k x[r, k] * shrink[a, j, k]
+//   out[r, n] = y[r, n] + sum_j t_j * expand[a, n, j]
+//
+// A pass has to read the adapters that some row uses, rank * (k + n) values each, and
+// x and y, and write out: HBM bounds it, with few rows by the adapters, with many by x, y
+// and out.
+//
+// A cluster of CTAs takes the rows of one adapter among 64 neighbouring rows: there
+// are never more adapters than rows, a lane's rows lie side by side, and nothing has to be
+// sorted.  Its CTAs share k for the first product and n for the second one; in between
+// they exchange t through each other's shared memory, so that one launch does both.
+// Which rows and adapter are its own a CTA finds by itself from the 64 numbers.
+//
+// Both products run on mma.sync, 16 rows at a time, with the adapters' values straight
+// from memory (k is permuted within a step, alike on both sides, so that a lane loads 16
+// or 8 bytes).  t is held in fp32 and goes into the second one in two 16-bit parts.  fp16
+// has few exponents: there a row's t is multiplied by the power of two that brings
+// its largest element to 2^14.
+#include <cooperative_groups.h>
+
 #include "wfst_ops.h"
+
+namespace cg = cooperative_groups;
 
 namespace wfst {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRank = 128;
+constexpr int kMaxCluster = 8;
+constexpr int kTile = 64;   // neighbouring rows
+constexpr int kChunk = 64;  // ranks that the first product has sums for at a time
 
 struct Args {
   const void *y, *x, *shrink, *expand;
@@ -14,38 +40,286 @@ struct Args {
   const float* scales;
   void* out;
   int64_t sy, sx, so, ss_a, ss_j, se_a, se_n;
-  int32_t rows, n, k, rank, adapters;
+  int32_t rows, n, k, rank, adapters, ranks;  // ranks: rank up to a multiple of 16
+  int32_t same, wide;  // out is y; y's and out's rows begin at 16 bytes
 };
 
-template <typename T>
+// Shared memory, in floats, of a pass of P rows: sums of the warps; t, this CTA's part and
+// all of it; t's parts, rows of 16-bit values with 8 more.
+__host__ __device__ constexpr int red_floats(int P, int ranks) { return 4 * P * (ranks < kChunk ? ranks : kChunk); }
+__host__ __device__ constexpr int smem_floats(int P, int ranks) { return red_floats(P, ranks) + 2 * P * ranks + P * (ranks + 8); }
+
+// Loads that nothing else is read with.
+__device__ __forceinline__ uint4 load16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint2 load8(const void* p) { return *reinterpret_cast<const uint2*>(p); }
+
+// P rows to a pass, 16 or 32.
+template <typename T, int P>
 __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
-  __shared__ float t[kMaxRank];
-  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int MT = P / 16;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int ids[kTile], mine[kTile];
+  __shared__ float lift[P];  // fp16: the powers of two to be taken off again
+  __shared__ uint64_t s_leaders;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  float* red = smem;
+  float* part = red + red_floats(P, a.ranks);
+  float* full = part + P * a.ranks;
+  T* split = reinterpret_cast<T*>(full + P * a.ranks);  // [2][P][ranks + 8]
+  const int row0 = blockIdx.z * kTile;
   ops_begin();
   ops_next();
-  const int which = ops_load(a.adapter + r);
-  const bool some = (uint32_t)which < (uint32_t)a.adapters;
-  if (some) {
-    const T* x = reinterpret_cast<const T*>(a.x) + r * a.sx;
-    for (int j = warp; j < a.rank; j += kThreads / 32) {
-      const T* s = reinterpret_cast<const T*>(a.shrink) + which * a.ss_a + j * a.ss_j;
-      float v = 0.f;
-      for (int k = lane; k < a.k; k += 32) v += to_f32(x[k]) * to_f32(s[k]);
-      for (int i = 16; i; i /= 2) v += __shfl_xor_sync(0xffffffffu, v, i);
-      if (lane == 0) t[j] = v * (a.scales ? a.scales[which] : 1.f);
-    }
+  // ---- the tile's adapters, each at the first row that has it
+  if (tid < kTile) {
+    const int id = row0 + tid < a.rows ? ops_load(a.adapter + row0 + tid) : -1;
+    ids[tid] = (uint32_t)id < (uint32_t)a.adapters ? id : -1;
+    if (tid == 0) s_leaders = 0;
   }
   __syncthreads();
-  for (int n = threadIdx.x; n < a.n; n += kThreads) {
-    T v = reinterpret_cast<const T*>(a.y)[r * a.sy + n];
-    if (some) {
-      const T* e = reinterpret_cast<const T*>(a.expand) + which * a.se_a + n * a.se_n;
-      float more = 0.f;
-      for (int j = 0; j < a.rank; j++) more += t[j] * to_f32(e[j]);
-      v = from_f32<T>(to_f32(v) + more);
-    }
-    reinterpret_cast<T*>(a.out)[r * a.so + n] = v;
+  if (tid < kTile) {
+    const int id = ids[tid];
+    bool first = id >= 0;
+    for (int i = 0; i < kTile; i++)
+      if (i < tid && ids[i] == id) first = false;
+    const uint32_t votes = __ballot_sync(0xffffffffu, first);
+    if (lane == 0 && votes) atomicOr((unsigned long long*)&s_leaders, (unsigned long long)votes << (warp * 32));
   }
+  __syncthreads();
+  uint64_t leaders = s_leaders;
+  const int blocks_n = (a.n + 31) / 32, n_lo = (int)((int64_t)blocks_n * rank_c / C), n_hi = (int)((int64_t)blocks_n * (rank_c + 1) / C);
+  // ---- rows without an adapter stay as they are
+  if (blockIdx.y == 0 && !a.same)
+    for (int i = warp; i < kTile && row0 + i < a.rows; i += kWarps)
+      if (ids[i] < 0)
+        for (int n = n_lo * 32 + lane; n < min(n_hi * 32, a.n); n += 32)
+          reinterpret_cast<uint16_t*>(a.out)[(row0 + i) * a.so + n] = reinterpret_cast<const uint16_t*>(a.y)[(row0 + i) * a.sy + n];
+  const int blocks_k = (a.k + 31) / 32, k_lo = (int)((int64_t)blocks_k * rank_c / C), k_hi = (int)((int64_t)blocks_k * (rank_c + 1) / C);
+
+  for (int which = 0; leaders; which++, leaders &= leaders - 1) {
+    if (which % gridDim.y != blockIdx.y) continue;
+    const int id = ids[__ffsll((long long)leaders) - 1];
+    // its rows
+    __syncthreads();
+    int count = 0;
+    for (int h = 0; h < 2; h++) {
+      const uint32_t is = __ballot_sync(0xffffffffu, ids[h * 32 + lane] == id);
+      if (warp == 0 && (is >> lane & 1)) mine[count + __popc(is & ((1u << lane) - 1))] = row0 + h * 32 + lane;
+      count += __popc(is);
+    }
+    __syncthreads();
+    const T* shrink = reinterpret_cast<const T*>(a.shrink) + id * a.ss_a;
+    const T* expand = reinterpret_cast<const T*>(a.expand) + id * a.se_a;
+    // the second product's values, on their way to the L2 cache meanwhile
+    for (int n = n_lo * 32 + tid; n < min(n_hi * 32, a.n); n += kThreads)
+      for (int j = 0; j < a.rank; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(expand + n * a.se_n + j));
+    const float scale = a.scales ? ops_load(a.scales + id) : 1.f;
+
+    for (int p0 = 0; p0 < count; p0 += P) {
+      const int rows = min(P, count - p0);
+      // ---- t, this CTA's share of k
+      const T* xp[2 * MT];
+#pragma unroll
+      for (int m = 0; m < 2 * MT; m++) xp[m] = reinterpret_cast<const T*>(a.x) + mine[p0 + min(m * 8 + g, rows - 1)] * a.sx + t * 8;
+      for (int r0 = 0; r0 < a.ranks; r0 += kChunk) {
+        const int nt = min(kChunk, a.ranks - r0) / 8;  // runs of eight ranks
+        float acc[MT][kChunk / 8][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int j = 0; j < kChunk / 8; j++) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
+        for (int blk = k_lo + warp; blk < k_hi; blk += kWarps) {
+          const int k = blk * 32;
+          const bool in = k + t * 8 < a.k;
+          uint4 xv[2 * MT], sv[kChunk / 8];
+#pragma unroll
+          for (int m = 0; m < 2 * MT; m++) xv[m] = in && m * 8 < rows ? load16(xp[m] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < kChunk / 8; j++)
+            if (j < nt) {
+              const int rank = r0 + j * 8 + g;
+              sv[j] = in && rank < a.rank ? load16(shrink + rank * a.ss_j + k + t * 8) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+          for (int j = 0; j < kChunk / 8; j++)
+            if (j < nt) {
+#pragma unroll
+              for (int m = 0; m < MT; m++) {
+                mma16816<T>(acc[m][j], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, sv[j].x, sv[j].y);
+                mma16816<T>(acc[m][j], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, sv[j].z, sv[j].w);
+              }
+            }
+        }
+        // the warps' sums: four to four, then all of those, in order
+        const int width = nt * 8;
+        auto at = [&](int w, int m, int j, int half) { return red + ((w * P + m * 16 + half * 8 + g) * width + j * 8 + 2 * t); };
+        __syncthreads();
+        if (warp >= 4) {
+#pragma unroll
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int j = 0; j < kChunk / 8; j++)
+              if (j < nt) {
+                *reinterpret_cast<float2*>(at(warp - 4, m, j, 0)) = make_float2(acc[m][j][0], acc[m][j][1]);
+                *reinterpret_cast<float2*>(at(warp - 4, m, j, 1)) = make_float2(acc[m][j][2], acc[m][j][3]);
+              }
+        }
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int j = 0; j < kChunk / 8; j++)
+              if (j < nt)
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                  float2* p = reinterpret_cast<float2*>(at(warp, m, j, half));
+                  const float2 v = *p;
+                  *p = make_float2(v.x + acc[m][j][2 * half], v.y + acc[m][j][2 * half + 1]);
+                }
+        }
+        __syncthreads();
+        for (int i = tid; i < P * width; i += kThreads) {
+          const int r = i / width, j = i % width;
+          part[r * a.ranks + r0 + j] = (red[i] + red[P * width + i]) + (red[2 * P * width + i] + red[3 * P * width + i]);
+        }
+      }
+      // ---- the cluster's: each CTA adds up its share of t, in order, and gives it to all
+      if (C > 1) {
+        cl.sync();
+        const float* from[kMaxCluster];
+        float* to[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; c++) {
+          from[c] = cl.map_shared_rank(part, c < C ? c : 0);
+          to[c] = cl.map_shared_rank(full, c < C ? c : 0);
+        }
+        for (int i = rank_c * kThreads + tid; i < rows * a.ranks; i += C * kThreads) {
+          float v[kMaxCluster];
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; c++) v[c] = c < C ? from[c][i] : 0.f;
+          float sum = v[0];
+#pragma unroll
+          for (int c = 1; c < kMaxCluster; c++) sum += v[c];
+          sum *= scale;
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; c++)
+            if (c < C) to[c][i] = sum;
+        }
+        cl.sync();
+      } else {
+        __syncthreads();
+        for (int i = tid; i < rows * a.ranks; i += kThreads) full[i] = part[i] * scale;
+        __syncthreads();
+      }
+      // ---- in two parts; a warp takes a row at a time
+      for (int r = warp; r < P; r += kWarps) {
+        float up = 1.f;
+        if (std::is_same_v<T, __half>) {
+          float top = 0.f;
+          if (r < rows)
+            for (int j = lane; j < a.ranks; j += 32) top = fmaxf(top, fabsf(full[r * a.ranks + j]));
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+          // 2^14 / 2^exponent, and its inverse, both within fp32's exponents
+          const int e = min(max((int)(most >> 23) - 127, -112), 126);
+          if (most && most < 0x7f800000u) up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          if (lane == 0) lift[r] = most && most < 0x7f800000u ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.f;
+        }
+        for (int j = lane; j < a.ranks; j += 32) {
+          const float v = r < rows ? full[r * a.ranks + j] * up : 0.f;
+          const T hi = from_f32<T>(v);
+          split[r * (a.ranks + 8) + j] = hi;
+          split[(P + r) * (a.ranks + 8) + j] = from_f32<T>(v - to_f32(hi));
+        }
+      }
+      __syncthreads();
+      // ---- y plus t times expand: 32 outputs to a warp at a time, of which a lane has eight
+      // neighbours in the end (run q of eight holds outputs 8 i + 2 q and 8 i + 2 q + 1)
+      for (int blk = n_lo + warp; blk < n_hi; blk += kWarps) {
+        const int n0 = blk * 32;
+        float acc[MT][4][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
+        const T* ep[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) ep[q] = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + t * 4;
+#pragma unroll 4
+        for (int s = 0; s < a.ranks; s += 16) {
+          uint2 e[4];
+#pragma unroll
+          for (int q = 0; q < 4; q++) e[q] = s + t * 4 < a.rank ? load8(ep[q] + s) : make_uint2(0, 0);
+#pragma unroll
+          for (int m = 0; m < MT; m++) {
+            if (m * 16 >= rows) continue;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const T* tp = split + (h * P + m * 16 + g) * (a.ranks + 8) + s + t * 4;
+              const uint2 lo = load8(tp), hi = load8(tp + 8 * (a.ranks + 8));
+#pragma unroll
+              for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, e[q].x, e[q].y);
+            }
+          }
+        }
+        const int n = n0 + t * 8;
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const int r = m * 16 + half * 8 + g;
+            if (r >= rows || n >= a.n) continue;
+            const float down = std::is_same_v<T, __half> ? lift[r] : 1.f;
+            const int row = mine[p0 + r];
+            const T* y = reinterpret_cast<const T*>(a.y) + row * a.sy + n;
+            T* out = reinterpret_cast<T*>(a.out) + row * a.so + n;
+            if (a.wide && n + 8 <= a.n) {
+              const uint4 v = load16(y);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                const float2 f = unpack2<T>(w[q]);
+                o[q] = pack2<T>(f.x + acc[m][q][2 * half] * down, f.y + acc[m][q][2 * half + 1] * down);
+              }
+              *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q++)
+#pragma unroll
+                for (int z = 0; z < 2; z++)
+                  if (n + 2 * q + z < a.n)
+                    out[2 * q + z] = from_f32<T>(to_f32(y[2 * q + z]) + acc[m][q][2 * half + z] * down);
+            }
+          }
+      }
+      __syncthreads();  // t's parts have been read
+    }
+  }
+  if (C > 1) cl.sync();  // no CTA leaves while another may read its shared memory
+}
+
+template <typename T, int P>
+cudaError_t launch(const Args& a, cudaStream_t st) {
+  auto* fn = lowrank_kernel<T, P>;
+  constexpr int most = smem_floats(P, kMaxRank) * 4;
+  static OpsOnce once;
+  if (const int dev = ops_current(); !once(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    once.set(dev);
+  }
+  // A CTA has 256 of k or n at least.  A tile's adapters are shared among clusters while
+  // there are places for them.
+  int C = 1;
+  while (C < kMaxCluster && C * 512 <= (a.k > a.n ? a.k : a.n)) C *= 2;
+  const int tiles = (a.rows + kTile - 1) / kTile;
+  int among = a.rows < kTile ? a.rows : kTile;
+  if (among > a.adapters) among = a.adapters > 0 ? a.adapters : 1;
+  const int64_t room = 4ll * ops_sm_count() / ((int64_t)tiles * C);
+  if (among > room && tiles > 1) among = room > 1 ? (int)room : 1;
+  return ops_launch(fn, dim3(C, among, tiles), kThreads, smem_floats(P, a.ranks) * 4, C, st, a);
 }
 
 }  // namespace
@@ -62,6 +336,7 @@ extern "C" int wfst_add_lowrank(const wfst_lowrank_args* r, void* stream) {
   if (r->rank < 8 || r->rank % 8 || r->rank > kMaxRank)
     return api_fail(WFST_ERR_INVALID_ARG, "add_lowrank: rank must be a multiple of 8 up to 128");
   if (r->n > INT32_MAX - 4096) return api_fail(WFST_ERR_INVALID_ARG, "add_lowrank: n is too large");
+  if (r->rows > 65535 * kTile) return api_fail(WFST_ERR_INVALID_ARG, "add_lowrank: too many rows");
   if (r->rows == 0 || r->n == 0) return WFST_OK;
   if (!r->y || !r->x || !r->adapter || !r->out || (r->adapters && (!r->shrink || !r->expand)))
     return api_fail(WFST_ERR_INVALID_ARG, "add_lowrank: NULL argument");
@@ -80,7 +355,12 @@ extern "C" int wfst_add_lowrank(const wfst_lowrank_args* r, void* stream) {
   if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "add_lowrank: device");
   a.y = r->y, a.x = r->x, a.shrink = r->shrink, a.expand = r->expand, a.adapter = r->adapter, a.scales = r->scales;
   a.out = r->out, a.rows = r->rows, a.n = r->n, a.k = r->k, a.rank = r->rank, a.adapters = r->adapters;
-  auto* fn = r->dtype == WFST_F16 ? lowrank_kernel<__half> : lowrank_kernel<__nv_bfloat16>;
-  const cudaError_t e = ops_launch(fn, dim3(a.rows), kThreads, 0, 0, (cudaStream_t)stream, a);
+  a.ranks = (a.rank + 15) / 16 * 16;
+  a.same = a.out == a.y && a.so == a.sy;
+  a.wide = aligned(a.y, 16) && aligned(a.out, 16) && a.sy % 8 == 0 && a.so % 8 == 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = r->dtype == WFST_F16 ? a.rows <= 16 ? launch<__half, 16>(a, st) : launch<__half, 32>(a, st)
+                        : a.rows <= 16       ? launch<__nv_bfloat16, 16>(a, st)
+                                             : launch<__nv_bfloat16, 32>(a, st);
   return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "add_lowrank launch");
 }

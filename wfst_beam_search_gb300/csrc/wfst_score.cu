@@ -29,8 +29,7 @@ namespace wfst {
 namespace {
 
 constexpr int kMaxCluster = 8;
-template <int N>
-constexpr int kAhead = N == 256 ? 8 : 4;  // granules of 16 bytes that a thread loads at once
+constexpr int kAhead = 8;   // granules of 16 bytes that a thread loads at once (four: 2048 x 131072 95 us, eight 83)
 constexpr int kParts = 8;   // of what a thread reads, each with its largest logit
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -295,12 +294,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // The largest of some granules' logits; NaN is passed over.
-template <typename T, int A>
-__device__ __forceinline__ float largest(const uint4 (&raw)[A]) {
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 (&raw)[kAhead]) {
   if constexpr (sizeof(T) == 4) {
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < A; j++)
+    for (int j = 0; j < kAhead; j++)
       top = fmaxf(fmaxf(fmaxf(top, __uint_as_float(raw[j].x)), fmaxf(__uint_as_float(raw[j].y), __uint_as_float(raw[j].z))),
                   __uint_as_float(raw[j].w));
     return top;
@@ -308,7 +307,7 @@ __device__ __forceinline__ float largest(const uint4 (&raw)[A]) {
     using V = typename Pairs<T>::V;
     V top = as<V>(Pairs<T>::kNone);
 #pragma unroll
-    for (int j = 0; j < A; j++)
+    for (int j = 0; j < kAhead; j++)
       top = __hmax2(__hmax2(top, __hmax2(as<V>(raw[j].x), as<V>(raw[j].y))), __hmax2(as<V>(raw[j].z), as<V>(raw[j].w)));
     const float2 t = unpack2<T>(bits(top));
     return fmaxf(t.x, t.y);
@@ -316,8 +315,8 @@ __device__ __forceinline__ float largest(const uint4 (&raw)[A]) {
 }
 
 // Adds some granules' logits, none of which is above s.m.
-template <typename T, int A>
-__device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[A]) {
+template <typename T>
+__device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[kAhead]) {
   constexpr int VEC = Row<T>::VEC;
   // -inf weighs nothing, and must not be multiplied by that: it is brought up to a bound far below
   // the largest logit, where the weight is zero all the same
@@ -325,7 +324,7 @@ __device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[A]) {
     const uint64_t less = two(-s.m, -s.m), by = two(kLog2e, kLog2e);
     uint64_t z = two(0.f, 0.f), u = z;
 #pragma unroll
-    for (int j = 0; j < A; j++) {
+    for (int j = 0; j < kAhead; j++) {
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
       for (int e = 0; e < VEC / 2; e++) {
@@ -349,7 +348,7 @@ __device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[A]) {
   } else {  // a row of such logits alone, so far
     const float ref = s.m > -INFINITY ? s.m : 0.f;
 #pragma unroll
-    for (int j = 0; j < A; j++) {
+    for (int j = 0; j < kAhead; j++) {
       float v[VEC];
       widen<T>(raw[j], v);
 #pragma unroll
@@ -362,10 +361,10 @@ __device__ __forceinline__ void add_granules(Sums& s, const uint4 (&raw)[A]) {
   }
 }
 
-// N threads; 256 for few rows, 128 for many (2000 x 20000, fp16, %FIG%).
+// N threads: 128 for many short rows.
 template <typename T, int N>
-__global__ void __launch_bounds__(N, N == 256 ? 4 : 12) score_kernel(const Args a) {
-  constexpr int VEC = Row<T>::VEC, W = N / 32, A = kAhead<N>;
+__global__ void __launch_bounds__(N, 1024 / N) score_kernel(const Args a) {
+  constexpr int VEC = Row<T>::VEC, W = N / 32, A = kAhead;
   extern __shared__ __align__(16) unsigned char smem[];
   Shared<N>* sh = reinterpret_cast<Shared<N>*>(smem);
   cg::cluster_group cl = cg::this_cluster();
@@ -396,15 +395,15 @@ __global__ void __launch_bounds__(N, N == 256 ? 4 : 12) score_kernel(const Args 
       if (i0 >= hi) break;
       uint4 raw[A];
 #pragma unroll
-      for (int j = 0; j < A; j++) {
+      for (int j = 0; j < kAhead; j++) {
         constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : Pairs<std::conditional_t<sizeof(T) == 4, __half, T>>::kNone;
         raw[j] = make_uint4(kNone, kNone, kNone, kNone);
         if (i0 + j * N < hi) raw[j] = row.load(i0 + j * N);
       }
-      const float top = largest<T, A>(raw);
+      const float top = largest<T>(raw);
       top_of = fmaxf(top_of, top);
       s.raise(top);
-      add_granules<T, A>(s, raw);
+      add_granules<T>(s, raw);
     }
     const uint32_t key = key_of(top_of);
     sh->best_of[g][tid] = key;
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(N, N == 256 ? 4 : 12) score_kernel(const Args 
   s.over_warp();
   if (lane == 0) sh->sums[warp] = s;
   __syncthreads();
-  if (a.top) alternatives<T, N>(row, lo, hi, rounds + (A == 8 ? 3 : 2), a.top, sh);
+  if (a.top) alternatives<T, N>(row, lo, hi, rounds + 3, a.top, sh);
   s = lane < W ? sh->sums[lane] : Sums();
   s.over_warp();
   if (C > 1) {
@@ -455,7 +454,10 @@ cudaError_t launch_as(const Args& a, int cluster, cudaStream_t st) {
 template <typename T>
 cudaError_t launch(const Args& a, cudaStream_t st) {
   const int granules = (int)(((int64_t)a.vocab * sizeof(T) + 15) / 16), places = 4 * ops_sm_count();
-  if (a.rows > places) return launch_as<T, 128>(a, 1, st);
+  // Many rows: with 64 KB or more 256 threads to a row, and the fewest of them have nothing to
+  // do with 128 below (2048 x 131072, 20 alternatives, 93 us, with 128 threads 102; 2000 x
+  // 20000 21, with 256 28).
+  if (a.rows > places) return granules >= 4096 ? launch_as<T, 256>(a, 1, st) : launch_as<T, 128>(a, 1, st);
   // A row is shared among as many CTAs as leave each thread some granules and all CTAs a
   // place: four to a multiprocessor are resident.
   int C = 1;
