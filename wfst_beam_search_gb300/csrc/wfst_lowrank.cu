@@ -32,7 +32,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRank = 128;
 constexpr int kMaxCluster = 8;
 constexpr int kTile = 64;   // neighbouring rows
-constexpr int kChunk = 64;  // ranks that the first product has sums for at a time
 
 struct Args {
   const void *y, *x, *shrink, *expand;
@@ -46,26 +45,28 @@ struct Args {
 
 // Shared memory, in floats, of a pass of P rows: sums of the warps; t, this CTA's part and
 // all of it; t's parts, rows of 16-bit values with 8 more.
-__host__ __device__ constexpr int red_floats(int P, int ranks) { return 4 * P * (ranks < kChunk ? ranks : kChunk); }
-__host__ __device__ constexpr int smem_floats(int P, int ranks) { return red_floats(P, ranks) + 2 * P * ranks + P * (ranks + 8); }
+__host__ __device__ constexpr int red_floats(int P, int R, int ranks) { return 4 * P * (ranks < R ? ranks : R); }
+__host__ __device__ constexpr int smem_floats(int P, int R, int ranks) {
+  return red_floats(P, R, ranks) + 2 * P * ranks + P * (ranks + 8);
+}
 
 // Loads that nothing else is read with.
 __device__ __forceinline__ uint4 load16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 load8(const void* p) { return *reinterpret_cast<const uint2*>(p); }
 
-// P rows to a pass, 16 or 32.
-template <typename T, int P>
+// P rows to a pass; the first product has sums for R ranks at a time.
+template <typename T, int P, int R>
 __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
   constexpr int MT = P / 16;
   extern __shared__ __align__(16) float smem[];
-  __shared__ int ids[kTile], mine[kTile];
+  __shared__ int ids[kTile], mine[kTile], none[kTile];
   __shared__ float lift[P];  // fp16: the powers of two to be taken off again
   __shared__ uint64_t s_leaders;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   float* red = smem;
-  float* part = red + red_floats(P, a.ranks);
+  float* part = red + red_floats(P, R, a.ranks);
   float* full = part + P * a.ranks;
   T* split = reinterpret_cast<T*>(full + P * a.ranks);  // [2][P][ranks + 8]
   const int row0 = blockIdx.z * kTile;
@@ -89,12 +90,33 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
   __syncthreads();
   uint64_t leaders = s_leaders;
   const int blocks_n = (a.n + 31) / 32, n_lo = (int)((int64_t)blocks_n * rank_c / C), n_hi = (int)((int64_t)blocks_n * (rank_c + 1) / C);
-  // ---- rows without an adapter stay as they are
-  if (blockIdx.y == 0 && !a.same)
-    for (int i = warp; i < kTile && row0 + i < a.rows; i += kWarps)
-      if (ids[i] < 0)
-        for (int n = n_lo * 32 + lane; n < min(n_hi * 32, a.n); n += 32)
-          reinterpret_cast<uint16_t*>(a.out)[(row0 + i) * a.so + n] = reinterpret_cast<const uint16_t*>(a.y)[(row0 + i) * a.sy + n];
+  // ---- rows without an adapter stay as they are: all clusters of the tile share them
+  if (!a.same) {
+    int count = 0;
+    for (int h = 0; h < 2; h++) {
+      const bool is_none = ids[h * 32 + lane] < 0 && row0 + h * 32 + lane < a.rows;
+      const uint32_t is = __ballot_sync(0xffffffffu, is_none);
+      if (warp == 0 && is_none) none[count + __popc(is & ((1u << lane) - 1))] = row0 + h * 32 + lane;
+      count += __popc(is);
+    }
+    __syncthreads();
+    const int each = (n_hi - n_lo) * 4;  // runs of eight values
+    for (int i = blockIdx.y * kThreads + tid; i < count * each; i += gridDim.y * kThreads) {
+      const int row = none[i / each], n = n_lo * 32 + i % each * 8;
+      const uint16_t* y = reinterpret_cast<const uint16_t*>(a.y) + row * a.sy + n;
+      uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + row * a.so + n;
+      if (a.wide && n + 8 <= a.n) {
+        *reinterpret_cast<uint4*>(out) = load16(y);
+      } else {
+        uint16_t v[8];
+#pragma unroll
+        for (int z = 0; z < 8; z++) v[z] = n + z < a.n ? y[z] : 0;
+#pragma unroll
+        for (int z = 0; z < 8; z++)
+          if (n + z < a.n) out[z] = v[z];
+      }
+    }
+  }
   const int blocks_k = (a.k + 31) / 32, k_lo = (int)((int64_t)blocks_k * rank_c / C), k_hi = (int)((int64_t)blocks_k * (rank_c + 1) / C);
 
   for (int which = 0; leaders; which++, leaders &= leaders - 1) {
@@ -114,6 +136,9 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
     // the second product's values, on their way to the L2 cache meanwhile
     for (int n = n_lo * 32 + tid; n < min(n_hi * 32, a.n); n += kThreads)
       for (int j = 0; j < a.rank; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(expand + n * a.se_n + j));
+    const int lines = ((min(n_hi * 32, a.n) - n_lo * 32) * (int)sizeof(T) + 127) / 128;
+    for (int i = tid; i < count * lines; i += kThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const T*>(a.y) + mine[i / lines] * a.sy + n_lo * 32 + i % lines * (128 / (int)sizeof(T))));
     const float scale = a.scales ? ops_load(a.scales + id) : 1.f;
 
     for (int p0 = 0; p0 < count; p0 += P) {
@@ -122,27 +147,27 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
       const T* xp[2 * MT];
 #pragma unroll
       for (int m = 0; m < 2 * MT; m++) xp[m] = reinterpret_cast<const T*>(a.x) + mine[p0 + min(m * 8 + g, rows - 1)] * a.sx + t * 8;
-      for (int r0 = 0; r0 < a.ranks; r0 += kChunk) {
-        const int nt = min(kChunk, a.ranks - r0) / 8;  // runs of eight ranks
-        float acc[MT][kChunk / 8][4];
+      for (int r0 = 0; r0 < a.ranks; r0 += R) {
+        const int nt = min(R, a.ranks - r0) / 8;  // runs of eight ranks
+        float acc[MT][R / 8][4];
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
-          for (int j = 0; j < kChunk / 8; j++) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
+          for (int j = 0; j < R / 8; j++) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
         for (int blk = k_lo + warp; blk < k_hi; blk += kWarps) {
           const int k = blk * 32;
           const bool in = k + t * 8 < a.k;
-          uint4 xv[2 * MT], sv[kChunk / 8];
+          uint4 xv[2 * MT], sv[R / 8];
 #pragma unroll
           for (int m = 0; m < 2 * MT; m++) xv[m] = in && m * 8 < rows ? load16(xp[m] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < kChunk / 8; j++)
+          for (int j = 0; j < R / 8; j++)
             if (j < nt) {
               const int rank = r0 + j * 8 + g;
               sv[j] = in && rank < a.rank ? load16(shrink + rank * a.ss_j + k + t * 8) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-          for (int j = 0; j < kChunk / 8; j++)
+          for (int j = 0; j < R / 8; j++)
             if (j < nt) {
 #pragma unroll
               for (int m = 0; m < MT; m++) {
@@ -159,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
 #pragma unroll
           for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int j = 0; j < kChunk / 8; j++)
+            for (int j = 0; j < R / 8; j++)
               if (j < nt) {
                 *reinterpret_cast<float2*>(at(warp - 4, m, j, 0)) = make_float2(acc[m][j][0], acc[m][j][1]);
                 *reinterpret_cast<float2*>(at(warp - 4, m, j, 1)) = make_float2(acc[m][j][2], acc[m][j][3]);
@@ -170,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
 #pragma unroll
           for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int j = 0; j < kChunk / 8; j++)
+            for (int j = 0; j < R / 8; j++)
               if (j < nt)
 #pragma unroll
                 for (int half = 0; half < 2; half++) {
@@ -236,8 +261,30 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
       __syncthreads();
       // ---- y plus t times expand: 32 outputs to a warp at a time, of which a lane has eight
       // neighbours in the end (run q of eight holds outputs 8 i + 2 q and 8 i + 2 q + 1)
+#pragma unroll 1
       for (int blk = n_lo + warp; blk < n_hi; blk += kWarps) {
-        const int n0 = blk * 32;
+        const int n0 = blk * 32, n = n0 + t * 8;
+        const bool wide = a.wide && n + 8 <= a.n;
+        // y first: it takes the longest, and out may be y
+        uint4 yv[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const int r = m * 16 + half * 8 + g;
+            yv[m][half] = make_uint4(0, 0, 0, 0);
+            if (r >= rows || n >= a.n) continue;
+            const uint16_t* y = reinterpret_cast<const uint16_t*>(a.y) + mine[p0 + r] * a.sy + n;
+            if (wide) {
+              yv[m][half] = load16(y);
+            } else {
+              uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int z = 0; z < 8; z++)
+                if (n + z < a.n) w[z / 2] |= (uint32_t)y[z] << z % 2 * 16;
+              yv[m][half] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
         float acc[MT][4][4];
 #pragma unroll
         for (int m = 0; m < MT; m++)
@@ -246,24 +293,31 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
         const T* ep[4];
 #pragma unroll
         for (int q = 0; q < 4; q++) ep[q] = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + t * 4;
-#pragma unroll 4
-        for (int s = 0; s < a.ranks; s += 16) {
-          uint2 e[4];
+        constexpr int U = R / 16;  // steps whose values are asked for at once
+        for (int s0 = 0; s0 < a.ranks; s0 += 16 * U) {
+          uint2 e[U][4];
 #pragma unroll
-          for (int q = 0; q < 4; q++) e[q] = s + t * 4 < a.rank ? load8(ep[q] + s) : make_uint2(0, 0);
+          for (int u = 0; u < U; u++)
 #pragma unroll
-          for (int m = 0; m < MT; m++) {
-            if (m * 16 >= rows) continue;
+            for (int q = 0; q < 4; q++)
+              e[u][q] = s0 + u * 16 + t * 4 < a.rank ? load8(ep[q] + s0 + u * 16) : make_uint2(0, 0);
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const T* tp = split + (h * P + m * 16 + g) * (a.ranks + 8) + s + t * 4;
-              const uint2 lo = load8(tp), hi = load8(tp + 8 * (a.ranks + 8));
+          for (int u = 0; u < U; u++) {
+            const int s = s0 + u * 16;
+            if (s >= a.ranks) break;
 #pragma unroll
-              for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, e[q].x, e[q].y);
+            for (int m = 0; m < MT; m++) {
+              if (m * 16 >= rows) break;
+#pragma unroll
+              for (int h = 0; h < 2; h++) {
+                const T* tp = split + (h * P + m * 16 + g) * (a.ranks + 8) + s + t * 4;
+                const uint2 lo = load8(tp), hi = load8(tp + 8 * (a.ranks + 8));
+#pragma unroll
+                for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, e[u][q].x, e[u][q].y);
+              }
             }
           }
         }
-        const int n = n0 + t * 8;
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -271,26 +325,20 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
             const int r = m * 16 + half * 8 + g;
             if (r >= rows || n >= a.n) continue;
             const float down = std::is_same_v<T, __half> ? lift[r] : 1.f;
-            const int row = mine[p0 + r];
-            const T* y = reinterpret_cast<const T*>(a.y) + row * a.sy + n;
-            T* out = reinterpret_cast<T*>(a.out) + row * a.so + n;
-            if (a.wide && n + 8 <= a.n) {
-              const uint4 v = load16(y);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              uint32_t o[4];
+            const uint32_t w[4] = {yv[m][half].x, yv[m][half].y, yv[m][half].z, yv[m][half].w};
+            uint32_t o[4];
 #pragma unroll
-              for (int q = 0; q < 4; q++) {
-                const float2 f = unpack2<T>(w[q]);
-                o[q] = pack2<T>(f.x + acc[m][q][2 * half] * down, f.y + acc[m][q][2 * half + 1] * down);
-              }
+            for (int q = 0; q < 4; q++) {
+              const float2 f = unpack2<T>(w[q]);
+              o[q] = pack2<T>(f.x + acc[m][q][2 * half] * down, f.y + acc[m][q][2 * half + 1] * down);
+            }
+            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + mine[p0 + r] * a.so + n;
+            if (wide) {
               *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; q++)
-#pragma unroll
-                for (int z = 0; z < 2; z++)
-                  if (n + 2 * q + z < a.n)
-                    out[2 * q + z] = from_f32<T>(to_f32(y[2 * q + z]) + acc[m][q][2 * half + z] * down);
+              for (int z = 0; z < 8; z++)
+                if (n + z < a.n) out[z] = (uint16_t)(o[z / 2] >> z % 2 * 16);
             }
           }
       }
@@ -300,10 +348,10 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
   if (C > 1) cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
-template <typename T, int P>
+template <typename T, int P, int R>
 cudaError_t launch(const Args& a, cudaStream_t st) {
-  auto* fn = lowrank_kernel<T, P>;
-  constexpr int most = smem_floats(P, kMaxRank) * 4;
+  auto* fn = lowrank_kernel<T, P, R>;
+  constexpr int most = smem_floats(P, R, R == 16 ? 16 : kMaxRank) * 4;
   static OpsOnce once;
   if (const int dev = ops_current(); !once(dev)) {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -319,7 +367,16 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   if (among > a.adapters) among = a.adapters > 0 ? a.adapters : 1;
   const int64_t room = 4ll * ops_sm_count() / ((int64_t)tiles * C);
   if (among > room && tiles > 1) among = room > 1 ? (int)room : 1;
-  return ops_launch(fn, dim3(C, among, tiles), kThreads, smem_floats(P, a.ranks) * 4, C, st, a);
+  return ops_launch(fn, dim3(C, among, tiles), kThreads, smem_floats(P, R, a.ranks) * 4, C, st, a);
+}
+
+// Rows to a pass: 16 where an adapter will hardly have more of a tile's, as in a batch of
+// one token per lane; otherwise as many as the registers hold sums for.
+template <typename T>
+cudaError_t by_rows(const Args& a, cudaStream_t st) {
+  const bool few = a.rows <= 16 || (a.rows <= kTile && a.rows <= (int64_t)a.adapters * 12);
+  if (a.ranks == 16) return few ? launch<T, 16, 16>(a, st) : launch<T, 64, 16>(a, st);
+  return few ? launch<T, 16, 64>(a, st) : launch<T, 32, 64>(a, st);
 }
 
 }  // namespace
@@ -359,8 +416,6 @@ extern "C" int wfst_add_lowrank(const wfst_lowrank_args* r, void* stream) {
   a.same = a.out == a.y && a.so == a.sy;
   a.wide = aligned(a.y, 16) && aligned(a.out, 16) && a.sy % 8 == 0 && a.so % 8 == 0;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = r->dtype == WFST_F16 ? a.rows <= 16 ? launch<__half, 16>(a, st) : launch<__half, 32>(a, st)
-                        : a.rows <= 16       ? launch<__nv_bfloat16, 16>(a, st)
-                                             : launch<__nv_bfloat16, 32>(a, st);
+  const cudaError_t e = r->dtype == WFST_F16 ? by_rows<__half>(a, st) : by_rows<__nv_bfloat16>(a, st);
   return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "add_lowrank launch");
 }
