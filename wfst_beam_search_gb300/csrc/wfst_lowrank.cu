@@ -56,7 +56,7 @@ __device__ __forceinline__ uint2 load8(const void* p) { return *reinterpret_cast
 
 // P rows to a pass; the first product has sums for R ranks at a time.
 template <typename T, int P, int R>
-__global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   constexpr int MT = P / 16;
   extern __shared__ __align__(16) float smem[];
   __shared__ int ids[kTile], mine[kTile], none[kTile];
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
   // ---- rows without an adapter stay as they are: all clusters of the tile share them
   if (!a.same) {
     int count = 0;
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < kTile / 32; h++) {
       const bool is_none = ids[h * 32 + lane] < 0 && row0 + h * 32 + lane < a.rows;
       const uint32_t is = __ballot_sync(0xffffffffu, is_none);
       if (warp == 0 && is_none) none[count + __popc(is & ((1u << lane) - 1))] = row0 + h * 32 + lane;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) lowrank_kernel(const Args a) {
     // its rows
     __syncthreads();
     int count = 0;
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < kTile / 32; h++) {
       const uint32_t is = __ballot_sync(0xffffffffu, ids[h * 32 + lane] == id);
       if (warp == 0 && (is >> lane & 1)) mine[count + __popc(is & ((1u << lane) - 1))] = row0 + h * 32 + lane;
       count += __popc(is);
@@ -375,7 +375,7 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
 template <typename T>
 cudaError_t by_rows(const Args& a, cudaStream_t st) {
   const bool few = a.rows <= 16 || (a.rows <= kTile && a.rows <= (int64_t)a.adapters * 12);
-  if (a.ranks == 16) return few ? launch<T, 16, 16>(a, st) : launch<T, 64, 16>(a, st);
+  if (a.ranks == 16) return few ? launch<T, 16, 16>(a, st) : launch<T, 32, 16>(a, st);
   return few ? launch<T, 16, 64>(a, st) : launch<T, 32, 64>(a, st);
 }
 
