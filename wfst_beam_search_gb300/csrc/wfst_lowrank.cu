@@ -133,12 +133,15 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
     __syncthreads();
     const T* shrink = reinterpret_cast<const T*>(a.shrink) + id * a.ss_a;
     const T* expand = reinterpret_cast<const T*>(a.expand) + id * a.se_a;
-    // the second product's values, on their way to the L2 cache meanwhile
-    for (int n = n_lo * 32 + tid; n < min(n_hi * 32, a.n); n += kThreads)
-      for (int j = 0; j < a.rank; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(expand + n * a.se_n + j));
+    // the second product's values and y, on their way to the L2 cache meanwhile
     const int lines = ((min(n_hi * 32, a.n) - n_lo * 32) * (int)sizeof(T) + 127) / 128;
-    for (int i = tid; i < count * lines; i += kThreads)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const T*>(a.y) + mine[i / lines] * a.sy + n_lo * 32 + i % lines * (128 / (int)sizeof(T))));
+    auto fetch = [&]() {
+      for (int n = n_lo * 32 + tid; n < min(n_hi * 32, a.n); n += kThreads)
+        for (int j = 0; j < a.rank; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(expand + n * a.se_n + j));
+      for (int i = warp; i < count; i += kWarps)
+        for (int l = lane; l < lines; l += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const T*>(a.y) + mine[i] * a.sy + n_lo * 32 + l * (128 / (int)sizeof(T))));
+    };
     const float scale = a.scales ? ops_load(a.scales + id) : 1.f;
 
     for (int p0 = 0; p0 < count; p0 += P) {
@@ -154,27 +157,35 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
         for (int m = 0; m < MT; m++)
 #pragma unroll
           for (int j = 0; j < R / 8; j++) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
-        for (int blk = k_lo + warp; blk < k_hi; blk += kWarps) {
-          const int k = blk * 32;
-          const bool in = k + t * 8 < a.k;
-          uint4 xv[2 * MT], sv[R / 8];
+        constexpr int B = R == 16 ? 2 : 1;  // blocks whose values are asked for at once, as many as registers hold
+        for (int blk = k_lo + warp; blk < k_hi; blk += B * kWarps) {
+          uint4 xv[B][2 * MT], sv[B][R / 8];
 #pragma unroll
-          for (int m = 0; m < 2 * MT; m++) xv[m] = in && m * 8 < rows ? load16(xp[m] + k) : make_uint4(0, 0, 0, 0);
+          for (int b = 0; b < B; b++) {
+            const int k = (blk + b * kWarps) * 32;
+            const bool in = blk + b * kWarps < k_hi && k + t * 8 < a.k;
 #pragma unroll
-          for (int j = 0; j < R / 8; j++)
-            if (j < nt) {
-              const int rank = r0 + j * 8 + g;
-              sv[j] = in && rank < a.rank ? load16(shrink + rank * a.ss_j + k + t * 8) : make_uint4(0, 0, 0, 0);
-            }
+            for (int m = 0; m < 2 * MT; m++) xv[b][m] = in && m * 8 < rows ? load16(xp[m] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < R / 8; j++)
-            if (j < nt) {
-#pragma unroll
-              for (int m = 0; m < MT; m++) {
-                mma16816<T>(acc[m][j], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, sv[j].x, sv[j].y);
-                mma16816<T>(acc[m][j], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, sv[j].z, sv[j].w);
+            for (int j = 0; j < R / 8; j++)
+              if (j < nt) {
+                const int rank = r0 + j * 8 + g;
+                sv[b][j] = in && rank < a.rank ? load16(shrink + rank * a.ss_j + k + t * 8) : make_uint4(0, 0, 0, 0);
               }
-            }
+          }
+          if (p0 == 0 && r0 == 0 && blk < k_lo + kWarps) fetch();
+#pragma unroll
+          for (int b = 0; b < B; b++)
+#pragma unroll
+            for (int j = 0; j < R / 8; j++)
+              if (j < nt) {
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                  const uint4 lo = xv[b][2 * m], hi = xv[b][2 * m + 1];
+                  mma16816<T>(acc[m][j], lo.x, hi.x, lo.y, hi.y, sv[b][j].x, sv[b][j].y);
+                  mma16816<T>(acc[m][j], lo.z, hi.z, lo.w, hi.w, sv[b][j].z, sv[b][j].w);
+                }
+              }
         }
         // the warps' sums: four to four, then all of those, in order
         const int width = nt * 8;
@@ -261,46 +272,51 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
       __syncthreads();
       // ---- y plus t times expand: 32 outputs to a warp at a time, of which a lane has eight
       // neighbours in the end (run q of eight holds outputs 8 i + 2 q and 8 i + 2 q + 1)
-#pragma unroll 1
-      for (int blk = n_lo + warp; blk < n_hi; blk += kWarps) {
+      constexpr int U = R / 16;  // steps of 16 ranks that are asked for at once
+      struct Block {
+        uint4 y[MT][2];
+        uint2 e[U][4];
+      };
+      auto wide = [&](int n) { return a.wide && n + 8 <= a.n; };
+      auto ask_e = [&](Block& v, int n0, int s0) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const T* ep = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + s0 + t * 4;
+#pragma unroll
+          for (int u = 0; u < U; u++) v.e[u][q] = s0 + u * 16 + t * 4 < a.rank ? load8(ep + u * 16) : make_uint2(0, 0);
+        }
+      };
+      auto ask = [&](Block& v, int blk) {
         const int n0 = blk * 32, n = n0 + t * 8;
-        const bool wide = a.wide && n + 8 <= a.n;
-        // y first: it takes the longest, and out may be y
-        uint4 yv[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
           for (int half = 0; half < 2; half++) {
             const int r = m * 16 + half * 8 + g;
-            yv[m][half] = make_uint4(0, 0, 0, 0);
+            v.y[m][half] = make_uint4(0, 0, 0, 0);
             if (r >= rows || n >= a.n) continue;
             const uint16_t* y = reinterpret_cast<const uint16_t*>(a.y) + mine[p0 + r] * a.sy + n;
-            if (wide) {
-              yv[m][half] = load16(y);
+            if (wide(n)) {
+              v.y[m][half] = load16(y);
             } else {
               uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
               for (int z = 0; z < 8; z++)
                 if (n + z < a.n) w[z / 2] |= (uint32_t)y[z] << z % 2 * 16;
-              yv[m][half] = make_uint4(w[0], w[1], w[2], w[3]);
+              v.y[m][half] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+        ask_e(v, n0, 0);
+      };
+      auto finish = [&](Block& v, int blk) {
+        const int n0 = blk * 32, n = n0 + t * 8;
         float acc[MT][4][4];
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
           for (int q = 0; q < 4; q++) acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
-        const T* ep[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) ep[q] = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + t * 4;
-        constexpr int U = R / 16;  // steps whose values are asked for at once
         for (int s0 = 0; s0 < a.ranks; s0 += 16 * U) {
-          uint2 e[U][4];
-#pragma unroll
-          for (int u = 0; u < U; u++)
-#pragma unroll
-            for (int q = 0; q < 4; q++)
-              e[u][q] = s0 + u * 16 + t * 4 < a.rank ? load8(ep[q] + s0 + u * 16) : make_uint2(0, 0);
+          if (s0) ask_e(v, n0, s0);
 #pragma unroll
           for (int u = 0; u < U; u++) {
             const int s = s0 + u * 16;
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
                 const T* tp = split + (h * P + m * 16 + g) * (a.ranks + 8) + s + t * 4;
                 const uint2 lo = load8(tp), hi = load8(tp + 8 * (a.ranks + 8));
 #pragma unroll
-                for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, e[u][q].x, e[u][q].y);
+                for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, v.e[u][q].x, v.e[u][q].y);
               }
             }
           }
@@ -325,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
             const int r = m * 16 + half * 8 + g;
             if (r >= rows || n >= a.n) continue;
             const float down = std::is_same_v<T, __half> ? lift[r] : 1.f;
-            const uint32_t w[4] = {yv[m][half].x, yv[m][half].y, yv[m][half].z, yv[m][half].w};
+            const uint32_t w[4] = {v.y[m][half].x, v.y[m][half].y, v.y[m][half].z, v.y[m][half].w};
             uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; q++) {
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
               o[q] = pack2<T>(f.x + acc[m][q][2 * half] * down, f.y + acc[m][q][2 * half + 1] * down);
             }
             uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + mine[p0 + r] * a.so + n;
-            if (wide) {
+            if (wide(n)) {
               *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
 #pragma unroll
@@ -341,6 +357,12 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
                 if (n + z < a.n) out[z] = (uint16_t)(o[z / 2] >> z % 2 * 16);
             }
           }
+      };
+#pragma unroll 1
+      for (int blk = n_lo + warp; blk < n_hi; blk += kWarps) {
+        Block v;
+        ask(v, blk);  // (y among it: it takes the longest, and out may be y)
+        finish(v, blk);
       }
       __syncthreads();  // t's parts have been read
     }
