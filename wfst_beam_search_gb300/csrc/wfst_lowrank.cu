@@ -20,6 +20,8 @@
 // its largest element to 2^14.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "wfst_ops.h"
 
 namespace cg = cooperative_groups;
@@ -39,7 +41,7 @@ struct Args {
   const float* scales;
   void* out;
   int64_t sy, sx, so, ss_a, ss_j, se_a, se_n;
-  int32_t rows, n, k, rank, adapters, ranks;  // ranks: rank up to a multiple of 16
+  int32_t rows, n, k, rank, adapters, ranks;  // ranks: rank up to a multiple of 16 (32, where it is more)
   int32_t same, wide;  // out is y; y's and out's rows begin at 16 bytes
 };
 
@@ -52,14 +54,13 @@ __host__ __device__ constexpr int smem_floats(int P, int R, int ranks) {
 
 // Loads that nothing else is read with.
 __device__ __forceinline__ uint4 load16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ uint2 load8(const void* p) { return *reinterpret_cast<const uint2*>(p); }
 
 // P rows to a pass; the first product has sums for R ranks at a time.
 template <typename T, int P, int R>
 __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   constexpr int MT = P / 16;
   extern __shared__ __align__(16) float smem[];
-  __shared__ int ids[kTile], mine[kTile], none[kTile];
+  __shared__ __align__(16) int ids[kTile], mine[kTile], none[kTile];
   __shared__ float lift[P];  // fp16: the powers of two to be taken off again
   __shared__ uint64_t s_leaders;
   cg::cluster_group cl = cg::this_cluster();
@@ -81,9 +82,12 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   __syncthreads();
   if (tid < kTile) {
     const int id = ids[tid];
-    bool first = id >= 0;
-    for (int i = 0; i < kTile; i++)
-      if (i < tid && ids[i] == id) first = false;
+    const uint32_t alike = __match_any_sync(0xffffffffu, id);  // (by all lanes, whatever they have)
+    bool first = id >= 0 && (alike & ((1u << lane) - 1)) == 0;
+    for (int i = 0; i < warp * 32; i += 4) {  // nor among the warps before
+      const int4 v = *reinterpret_cast<const int4*>(ids + i);
+      if (v.x == id || v.y == id || v.z == id || v.w == id) first = false;
+    }
     const uint32_t votes = __ballot_sync(0xffffffffu, first);
     if (lane == 0 && votes) atomicOr((unsigned long long*)&s_leaders, (unsigned long long)votes << (warp * 32));
   }
@@ -119,16 +123,30 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   }
   const int blocks_k = (a.k + 31) / 32, k_lo = (int)((int64_t)blocks_k * rank_c / C), k_hi = (int)((int64_t)blocks_k * (rank_c + 1) / C);
 
-  for (int which = 0; leaders; which++, leaders &= leaders - 1) {
-    if (which % gridDim.y != blockIdx.y) continue;
+  // the tile's passes, of all its adapters, are dealt out to its clusters
+  uint32_t until = blockIdx.y;  // passes until this cluster's next one
+  for (; leaders; leaders &= leaders - 1) {
     const int id = ids[__ffsll((long long)leaders) - 1];
+    int count = 0;
+    uint32_t is[kTile / 32];
+#pragma unroll
+    for (int h = 0; h < kTile / 32; h++) {
+      is[h] = __ballot_sync(0xffffffffu, ids[h * 32 + lane] == id);
+      count += __popc(is[h]);
+    }
+    const uint32_t passes = (count + P - 1) / P, to_mine = until;
+    while (until < passes) until += gridDim.y;
+    until -= passes;
+    if (to_mine >= passes) continue;
     // its rows
     __syncthreads();
-    int count = 0;
-    for (int h = 0; h < kTile / 32; h++) {
-      const uint32_t is = __ballot_sync(0xffffffffu, ids[h * 32 + lane] == id);
-      if (warp == 0 && (is >> lane & 1)) mine[count + __popc(is & ((1u << lane) - 1))] = row0 + h * 32 + lane;
-      count += __popc(is);
+    if (warp == 0) {
+      int at = 0;
+#pragma unroll
+      for (int h = 0; h < kTile / 32; h++) {
+        if (is[h] >> lane & 1) mine[at + __popc(is[h] & ((1u << lane) - 1))] = row0 + h * 32 + lane;
+        at += __popc(is[h]);
+      }
     }
     __syncthreads();
     const T* shrink = reinterpret_cast<const T*>(a.shrink) + id * a.ss_a;
@@ -144,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
     };
     const float scale = a.scales ? ops_load(a.scales + id) : 1.f;
 
-    for (int p0 = 0; p0 < count; p0 += P) {
+    for (int p0 = (int)to_mine * P; p0 < count; p0 += (int)gridDim.y * P) {
       const int rows = min(P, count - p0);
       // ---- t, this CTA's share of k
       const T* xp[2 * MT];
@@ -173,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
                 sv[b][j] = in && rank < a.rank ? load16(shrink + rank * a.ss_j + k + t * 8) : make_uint4(0, 0, 0, 0);
               }
           }
-          if (p0 == 0 && r0 == 0 && blk < k_lo + kWarps) fetch();
+          if (p0 == (int)to_mine * P && r0 == 0 && blk < k_lo + kWarps) fetch();
 #pragma unroll
           for (int b = 0; b < B; b++)
 #pragma unroll
@@ -272,18 +290,23 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
       __syncthreads();
       // ---- y plus t times expand: 32 outputs to a warp at a time, of which a lane has eight
       // neighbours in the end (run q of eight holds outputs 8 i + 2 q and 8 i + 2 q + 1)
-      constexpr int U = R / 16;  // steps of 16 ranks that are asked for at once
+      // steps of S ranks, of which a lane has S / 4 neighbours on either side; U of them are asked for at once
+      constexpr int S = R == 16 ? 16 : 32, U = R / S;
+      using Run = std::conditional_t<S == 16, uint2, uint4>;
       struct Block {
         uint4 y[MT][2];
-        uint2 e[U][4];
+        Run e[U][4];
       };
+      // up to eight rows: the upper eight of the product's 16 are the same rows' second parts
+      const bool beside = P == 16 && rows <= 8;
       auto wide = [&](int n) { return a.wide && n + 8 <= a.n; };
       auto ask_e = [&](Block& v, int n0, int s0) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-          const T* ep = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + s0 + t * 4;
+          const T* ep = expand + (int64_t)min(n0 + g / 2 * 8 + 2 * q + g % 2, a.n - 1) * a.se_n + s0 + t * (S / 4);
 #pragma unroll
-          for (int u = 0; u < U; u++) v.e[u][q] = s0 + u * 16 + t * 4 < a.rank ? load8(ep + u * 16) : make_uint2(0, 0);
+          for (int u = 0; u < U; u++)
+            v.e[u][q] = s0 + u * S + t * (S / 4) < a.rank ? *reinterpret_cast<const Run*>(ep + u * S) : Run{};
         }
       };
       auto ask = [&](Block& v, int blk) {
@@ -315,24 +338,35 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
         for (int m = 0; m < MT; m++)
 #pragma unroll
           for (int q = 0; q < 4; q++) acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
-        for (int s0 = 0; s0 < a.ranks; s0 += 16 * U) {
+        for (int s0 = 0; s0 < a.ranks; s0 += S * U) {
           if (s0) ask_e(v, n0, s0);
 #pragma unroll
           for (int u = 0; u < U; u++) {
-            const int s = s0 + u * 16;
+            const int s = s0 + u * S;
             if (s >= a.ranks) break;
+            auto multiply = [&](int m, const Run& lo, const Run& hi) {
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, v.e[u][q].x, v.e[u][q].y);
+                if constexpr (S == 32) mma16816<T>(acc[m][q], lo.z, hi.z, lo.w, hi.w, v.e[u][q].z, v.e[u][q].w);
+              }
+            };
+            auto row = [&](int r) { return *reinterpret_cast<const Run*>(split + r * (a.ranks + 8) + s + t * (S / 4)); };
+            if (beside) {
+              multiply(0, row(g), row(P + g));
+              continue;
+            }
 #pragma unroll
             for (int m = 0; m < MT; m++) {
               if (m * 16 >= rows) break;
 #pragma unroll
-              for (int h = 0; h < 2; h++) {
-                const T* tp = split + (h * P + m * 16 + g) * (a.ranks + 8) + s + t * 4;
-                const uint2 lo = load8(tp), hi = load8(tp + 8 * (a.ranks + 8));
-#pragma unroll
-                for (int q = 0; q < 4; q++) mma16816<T>(acc[m][q], lo.x, hi.x, lo.y, hi.y, v.e[u][q].x, v.e[u][q].y);
-              }
+              for (int h = 0; h < 2; h++) multiply(m, row(h * P + m * 16 + g), row(h * P + m * 16 + 8 + g));
             }
           }
+        }
+        if (beside) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[0][q][0] += acc[0][q][2], acc[0][q][1] += acc[0][q][3];
         }
 #pragma unroll
         for (int m = 0; m < MT; m++)
@@ -385,8 +419,9 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
   int C = 1;
   while (C < kMaxCluster && C * 512 <= (a.k > a.n ? a.k : a.n)) C *= 2;
   const int tiles = (a.rows + kTile - 1) / kTile;
-  int among = a.rows < kTile ? a.rows : kTile;
-  if (among > a.adapters) among = a.adapters > 0 ? a.adapters : 1;
+  const int most_rows = a.rows < kTile ? a.rows : kTile;
+  int among = a.adapters > (most_rows + P - 1) / P ? a.adapters : (most_rows + P - 1) / P;  // passes of a tile, or hardly more
+  if (among > most_rows) among = most_rows;
   const int64_t room = 4ll * ops_sm_count() / ((int64_t)tiles * C);
   if (among > room && tiles > 1) among = room > 1 ? (int)room : 1;
   return ops_launch(fn, dim3(C, among, tiles), kThreads, smem_floats(P, R, a.ranks) * 4, C, st, a);
@@ -396,9 +431,9 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
 // one token per lane; otherwise as many as the registers hold sums for.
 template <typename T>
 cudaError_t by_rows(const Args& a, cudaStream_t st) {
-  const bool few = a.rows <= 16 || (a.rows <= kTile && a.rows <= (int64_t)a.adapters * 12);
+  const bool few = a.rows <= 16 || a.rows <= (int64_t)a.adapters * 12;
   if (a.ranks == 16) return few ? launch<T, 16, 16>(a, st) : launch<T, 32, 16>(a, st);
-  return few ? launch<T, 16, 64>(a, st) : launch<T, 32, 64>(a, st);
+  return few ? launch<T, 16, 64>(a, st) : launch<T, 32, 32>(a, st);
 }
 
 }  // namespace
@@ -434,7 +469,7 @@ extern "C" int wfst_add_lowrank(const wfst_lowrank_args* r, void* stream) {
   if (guard.err != cudaSuccess) return api_cuda_fail(guard.err, "add_lowrank: device");
   a.y = r->y, a.x = r->x, a.shrink = r->shrink, a.expand = r->expand, a.adapter = r->adapter, a.scales = r->scales;
   a.out = r->out, a.rows = r->rows, a.n = r->n, a.k = r->k, a.rank = r->rank, a.adapters = r->adapters;
-  a.ranks = (a.rank + 15) / 16 * 16;
+  a.ranks = a.rank <= 16 ? 16 : (a.rank + 31) / 32 * 32;
   a.same = a.out == a.y && a.so == a.sy;
   a.wide = aligned(a.y, 16) && aligned(a.out, 16) && a.sy % 8 == 0 && a.so % 8 == 0;
   cudaStream_t st = (cudaStream_t)stream;
