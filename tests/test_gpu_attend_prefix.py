@@ -391,3 +391,35 @@ def test_refusals(W):
         W.attend_prefix(**{**ok, "q": asks})
     with torch.no_grad():
         W.attend_prefix(**{**ok, "q": asks})
+
+
+def test_two_streams_at_once(W):
+    """Calls on two streams with workspaces of their own, beside each other and
+    beside products that use tensor memory too."""
+    a = make(15, 3000, [100, 1, 0, 40] * 10, 8, 2, 64, 16, torch.bfloat16)
+    b = make(16, 900, [30] * 64, 16, 4, 128, 48, torch.bfloat16)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w = W.pack_quant(torch.randint(0, 256, (4096, 512), generator=g, device="cuda", dtype=torch.uint8),
+                     torch.full((4096, 8), 0.01, device="cuda").bfloat16())
+    x = torch.randn(64, 1024, generator=g, device="cuda").bfloat16()
+    want = [attend(W, a)[0], attend(W, b)[0], W.matvec_quant(x, w)]
+    ws = [W.attend_prefix_workspace(40, 8, 2, 64), W.attend_prefix_workspace(64, 16, 4, 128)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], [], []]
+    for _ in range(20):
+        for i, call in enumerate((lambda: W.attend_prefix(*a, workspace=ws[0]), lambda: W.attend_prefix(*b, workspace=ws[1]),
+                                  lambda: W.matvec_quant(x, w))):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    for mine, one in zip(got, want):
+        assert all(torch.equal(m, one) for m in mine)
+
+
+def test_a_pool_without_pages(W):
+    """Tables that point into a pool that has none: nothing is seen."""
+    q, kc, vc, ptable, plen, table, n = make(17, 300, [40, 5], 4, 2, 64, 16, torch.float16)
+    o, lse = attend(W, (q, kc[:0], vc[:0], ptable, plen, table, n))
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())

@@ -205,3 +205,30 @@ def test_refusals(W):
             (W.WfstError, dict(logits=torch.zeros(1, 1, device="cuda").expand(4, 2 ** 20 + 1).half()))]:
         with pytest.raises(error):
             W.score_tokens(**{**dict(logits=x, tokens=t, top=2), **change})
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(5, 3001), (700, 3001), (700, 70001)])
+def test_what_16_bits_hold(W, rows, vocab, dtype):
+    """NaN and +inf among 16-bit logits, and rows whose logits are all near the
+    type's lowest number, masked and not: two by two they are treated otherwise
+    than in fp32."""
+    low = -65504.0 if dtype == torch.float16 else -3.3895313892515355e38
+    x, t = logits(rows + vocab, rows, vocab, dtype, masked=0.3)
+    x[0, 1::2], x[0, ::2] = low, -math.inf
+    x[1] = low
+    x[2, :] = low
+    x[2, vocab // 2] = low * 0.5
+    x[3, 5:] = low
+    check(W.score_tokens(x, t, top=20), x, t, 20)
+    for bad in (math.nan, math.inf):
+        for at in (0, 1, vocab - 1):
+            y = x.clone()
+            y[4, at] = bad
+            got, clean = W.score_tokens(y, t, top=4), W.score_tokens(x, t, top=4)
+            assert all(bool(g[4].isnan().all()) for g in (got[0], got[1], got[3]))
+            want = torch.sort(torch.where(y[4].isnan(), -math.inf, y[4].float()), descending=True, stable=True).indices[:4]
+            assert torch.equal(got[2][4].long(), want)
+            for g, c in zip(got, clean):
+                g[4] = c[4] = 0
+                assert torch.equal(g, c)
