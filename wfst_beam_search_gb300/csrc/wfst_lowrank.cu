@@ -18,6 +18,14 @@
 // or 8 bytes).  t is held in fp32 and goes into the second one in two 16-bit parts.  fp16
 // has few exponents: there a row's t is multiplied by the power of two that brings
 // its largest element to 2^14.
+//
+// What bounds it is the chain of one cluster: find the rows, first product, the warps' and
+// the cluster's sums, second product, each some 2 to 5 us.  So what can be asked for early is
+// (expand and y into the L2 cache during the first product, y before the second one), and
+// two CTAs share a multiprocessor (with more registers for passes of 64 rows and one
+// CTA, 4096 x 6144 x 4096 90 us instead of 50).  1 x 4096 x 4096 of rank 16 takes 6.5 us, 64 x
+// 8192 x 8192 of 40 adapters of rank 64 27 (2.6 TB/s), 4096 x 6144 x 4096 of 16 of rank 16
+// 50 (2.7 TB/s).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -93,7 +101,8 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   }
   __syncthreads();
   uint64_t leaders = s_leaders;
-  const int blocks_n = (a.n + 31) / 32, n_lo = (int)((int64_t)blocks_n * rank_c / C), n_hi = (int)((int64_t)blocks_n * (rank_c + 1) / C);
+  auto share = [&](int blocks, int c) { return (int)((int64_t)blocks * c / C); };
+  const int blocks_n = (a.n + 31) / 32, n_lo = share(blocks_n, rank_c), n_hi = share(blocks_n, rank_c + 1);
   // ---- rows without an adapter stay as they are: all clusters of the tile share them
   if (!a.same) {
     int count = 0;
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
       }
     }
   }
-  const int blocks_k = (a.k + 31) / 32, k_lo = (int)((int64_t)blocks_k * rank_c / C), k_hi = (int)((int64_t)blocks_k * (rank_c + 1) / C);
+  const int blocks_k = (a.k + 31) / 32, k_lo = share(blocks_k, rank_c), k_hi = share(blocks_k, rank_c + 1);
 
   // the tile's passes, of all its adapters, are dealt out to its clusters
   uint32_t until = blockIdx.y;  // passes until this cluster's next one
@@ -158,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
         for (int j = 0; j < a.rank; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(expand + n * a.se_n + j));
       for (int i = warp; i < count; i += kWarps)
         for (int l = lane; l < lines; l += 32)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const T*>(a.y) + mine[i] * a.sy + n_lo * 32 + l * (128 / (int)sizeof(T))));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const T*>(a.y) + mine[i] * a.sy + n_lo * 32 +
+                                                        l * (128 / (int)sizeof(T))));
     };
     const float scale = a.scales ? ops_load(a.scales + id) : 1.f;
 
@@ -428,7 +438,7 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
 }
 
 // Rows to a pass: 16 where an adapter will hardly have more of a tile's, as in a batch of
-// one token per lane; otherwise as many as the registers hold sums for.
+// one token per lane; otherwise 32 (4096 x 6144 x 4096 50 us, with 16 76).
 template <typename T>
 cudaError_t by_rows(const Args& a, cudaStream_t st) {
   const bool few = a.rows <= 16 || a.rows <= (int64_t)a.adapters * 12;

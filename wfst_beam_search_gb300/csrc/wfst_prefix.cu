@@ -8,28 +8,42 @@
 // key-value head, for 4 * D flops per query head and lane: with R = lanes * (query
 // heads to a key-value head) rows HBM bounds it up to some 200 rows, the tensor
 // cores above.  So the prefix is a matrix product here: the R rows of a key-value
-// head are the rows of S = Q K^T and O = P V on tcgen05.  Each CTA leaves the m, l
-// and unscaled o of its share of the keys; the kernel of wfst_attend.cu attends to
-// each lane's own tokens meanwhile and adds these parts to its own.
+// head are the rows of S = Q K^T and O = P V on tcgen05.  Three kernels: this one
+// leaves m, l and the unscaled o of each CTA's share of the keys; that of
+// wfst_attend.cu does so for each lane's own tokens, and starts as this one's CTAs end;
+// the last one puts them together.  (Put together at the end of the second one, whose
+// CTAs take a lane and head after the other: 128 x 32767 241 us instead of 180.)
 //
-// A CTA takes 128 keys by 128 or 256 rows at a time (heads of 256: 64 by 128).  Four
-// warps copy keys and values ahead into a ring (16 bytes a lane, since pages may end
-// anywhere and lie in any order of strides), one issues the products, and a
-// thread of four or eight more owns a row: it takes its row of S from tensor memory,
-// where a row's maximum and sum need no exchange between threads, and puts P back
-// in the same place as the operand of the second product.  There are two places for
-// S, so that one is computed while the other one is exponentiated: two tiles of
-// rows, or with up to 128 rows every other tile of keys (each with its own o, added
-// up at the end), or, with heads of 256, whose o fills half of the tensor memory,
-// the next tile of keys.
+// A CTA takes tiles of keys by 128 or 256 rows.  Four warps copy keys and values ahead
+// into a ring: in boxes of up to 32 keys by 64 elements where pages hold whole ones and
+// all keys are there, otherwise 16 bytes a lane.  Two streams of tiles are under way at
+// once, so that one's scores are exponentiated while the tensor cores work for the other:
+// with more than 128 rows two tiles of rows, which share the keys that were copied, with
+// up to 128 every other tile of keys, each with its own o.  A warp issues each stream's
+// products, and a thread of four or eight warps owns a row: it takes its row of S from
+// tensor memory, where the maximum and sum need no exchange between threads, 64
+// scores at a time, and puts P in their place, as the operand of the second product.
+// Heads of 256, whose o fills half of the tensor memory, have one stream.
+//
+// Tiles are of 128 keys where the copies bound it (up to 128 rows): S is computed once
+// for either half's P.  With two tiles of rows they are of 64, and S is computed a tile
+// ahead: 147 us became 130 with 64 x 16 rows of 32767 keys, but 16 x 4 of 131072 took 114
+// instead of 101.
 //
 // o is rescaled only where a row's maximum has grown by more than 2^kSlack: the sum
 // is the same with any reference.  P is held in two 16-bit parts, whose sum is off
 // by at most 2^-16 of it (bf16; fp16: 2^-22), by two products into the same fp32
-// sum.
+// sum.  (One part would be off by as much as o's own rounding; with a first part that is
+// cut off instead of rounded, 2^-15, 128 x 32767 takes 180 us instead of 185.)
 //
 // Work is split evenly whatever the sizes: the tiles of all heads and groups of rows are
 // numbered through, and each CTA takes an equal range.
+//
+// Heads of 128, bf16: 16 lanes with 32 query and 8 key-value heads behind 131072 tokens
+// (0.54 GB) take 103 us, 5.3 TB/s; 128 lanes with 64 and 8 heads behind 32767, and their own
+// 500 at most (0.27 GB), 185: this kernel 135, of which the tensor cores are busy for 108 at
+// their measured rate, the lanes' own tokens 42, the joining 6; 64 lanes with 32 and 8
+// heads behind 8192 45; 8 lanes with 16 and 16 heads of 64, fp16, behind 500 9.
 #include <cuda.h>
 
 #include <cfloat>
@@ -43,11 +57,12 @@ constexpr int kRows = 128;       // of a tile, one to a thread
 constexpr int kMostGrid = 160;   // CTAs the workspace has room for: the multiprocessors of the chip
 constexpr int kMaskRing = 16;    // tiles whose masks are kept, more than are ever in flight
 constexpr uint32_t kNap = 20000, kSpins = 1u << 16;  // a wait sleeps so many ns at a time, and gives up after so many times
-constexpr int kLooks = 200;
+constexpr int kLooks = 200;      // before it sleeps at all: a warp that has gone to sleep wakes some 500 cycles late
 constexpr float kLog2e = 1.4426950408889634f;
-// How far, in powers of two, a row's largest score may be above its reference.  fp16 has no exponents below 2^-24: P is held times 2^11, so that with kSlack it stays
-// within 2^15 and what is lost is below 2^-35 of the largest weight; the parts that are
-// left hold l and o times 2^15, as wfst_attend.cu does.
+// How far, in powers of two, a row's largest score may be above its reference.  fp16
+// has no exponents below 2^-24: P is held times 2^11, so that with kSlack it stays within
+// 2^15 and what is lost is below 2^-35 of the largest weight; the parts that are left
+// hold l and o times 2^15, as wfst_attend.cu does.
 template <typename T>
 constexpr float kSlack = std::is_same_v<T, __half> ? 4.f : 8.f;
 template <typename T>
@@ -101,7 +116,6 @@ __device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
                : "memory");
   return done;
 }
-// (A warp that has gone to sleep wakes some 500 cycles late: it looks a while first.)
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < kLooks; i++)
@@ -124,10 +138,11 @@ __device__ __forceinline__ bool elected() {
   return is != 0;
 }
 // a box of 64 elements by some keys of a page
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int element, int place, int head, int page, uint32_t bar) {
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int element, int place, int head, int page,
+                                         uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(element), "r"(place), "r"(head), "r"(page), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(element), "r"(place), "r"(head), "r"(page), "r"(bar)
       : "memory");
 }
 // What the products' warp issues, by the one lane that `one` is not zero in.  The
@@ -162,7 +177,8 @@ __device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
       : "memory");
 }
 __device__ __forceinline__ void arrive(uint32_t one, uint32_t bar) {
-  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(one) : "memory");
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(one)
+               : "memory");
 }
 // 32 columns of this warp's 32 lanes: asked for, and there (the registers go through
 // the wait, so that nothing that uses them is moved before it)
@@ -239,14 +255,6 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
-// Two weights as 16-bit parts: a first one, cut off (bf16, whose bits are the upper ones
-// of fp32) or rounded, and the rest, rounded.
-template <typename T>
-__device__ __forceinline__ uint32_t first_part(float p0, float p1) {
-  if (std::is_same_v<T, __half>) return pack2<T>(p0, p1);
-  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-}
-
 // A value that all lanes of a warp have, so that the compiler knows it: a reduction's
 // result is in a register that the warp has in common.
 __device__ __forceinline__ uint32_t same(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
@@ -427,13 +435,15 @@ __global__ void __launch_bounds__(kThreads<D>, 1)
       for (uint32_t i = items[r] > (uint32_t)R ? items[r] - R : 0; i < items[r]; i++)
         if (!wait_bar(bar(sh.full[r * R + i % R]), i / R & 1)) break;
   } else if (warp >= 4 * G + 4) {
-    // ---- products, a warp to each stream.  kind::f16: fp32 sums, 128 rows; Q K^T with N = KT, P V with N = D and V read across its rows
+    // ---- products, a warp to each stream.  kind::f16: fp32 sums, 128 rows; Q K^T with N = KT, P V with N = D and
+    // V read across its rows
     constexpr uint32_t kType = std::is_same_v<T, __half> ? 0u : 1u;
     constexpr uint32_t kBase = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kRows / 16) << 24;
     constexpr uint32_t kScores = kBase | (uint32_t)(KT / 8) << 17, kValues = kBase | (uint32_t)(D / 8) << 17 | 1u << 16;
     const uint32_t one = elected();
     const int j = G == 2 ? warp - (4 * G + 4) : 0, ring_no = kTurns ? j : 0;
-    uint32_t items = 0, scored = 0, summed = 0;  // items of the ring, and tiles (scores) and halves or tiles (values), before what is next
+    // items of the ring, tiles that have been through the first product, halves (H == 2) or tiles through the second one
+    uint32_t items = 0, scored = 0, summed = 0;
     auto slot_in = [&](uint32_t item) {
       const int slot = ring_no * R + item % R;
       good = good && wait_bar(bar(sh.full[slot]), item / R & 1);
@@ -447,7 +457,8 @@ __global__ void __launch_bounds__(kThreads<D>, 1)
       good = __all_sync(0xffffffffu, good);
       if (!good) return;
       tmem_after();
-      const uint32_t q = same(describe(q_at + (kTurns ? 0 : j) * (kRows * D * 2), 16)), key = same(describe(ring_at + slot * kTile, 16));
+      const uint32_t q = same(describe(q_at + (kTurns ? 0 : j) * (kRows * D * 2), 16));
+      const uint32_t key = same(describe(ring_at + slot * kTile, 16));
       const uint32_t d = same(tmem + j * 128 + place * 64);
 #pragma unroll
       for (int s = 0; s < D / 16; s++)
@@ -545,79 +556,79 @@ __global__ void __launch_bounds__(kThreads<D>, 1)
         good = good && wait_bar(bar(sh.s_full[wg][H == 2 ? 0 : k & 1]), (H == 2 ? k : k >> 1) & 1);
 #pragma unroll 1
         for (int h = 0; h < H; h++) {
-        const uint32_t part = k * H + h, x = part & 1, s_at = mine + wg * 128 + x * 64, o_at = mine + kO + wg * D;
-        __syncwarp();
-        tmem_after();
-        const uint32_t* seen = sh.masks[(count + i) % kMaskRing];
-        uint32_t r[2][32];  // the scores; -inf where the key is not seen
-        tmem_ask(r[0], s_at);
-        tmem_ask(r[1], s_at + 32);
-        tmem_there(r[0]);
-        tmem_there(r[1]);
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const uint32_t part = k * H + h, x = part & 1, s_at = mine + wg * 128 + x * 64, o_at = mine + kO + wg * D;
+          __syncwarp();
+          tmem_after();
+          const uint32_t* seen = sh.masks[(count + i) % kMaskRing];
+          uint32_t r[2][32];  // the scores; -inf where the key is not seen
+          tmem_ask(r[0], s_at);
+          tmem_ask(r[1], s_at + 32);
+          tmem_there(r[0]);
+          tmem_there(r[1]);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-          const uint32_t mask = H == 2 ? seen[2 * h + c] : seen[2 * c] | seen[2 * c + 1] << 16;
-          if (mask != 0xffffffffu) {
+          for (int c = 0; c < 2; c++) {
+            const uint32_t mask = H == 2 ? seen[2 * h + c] : seen[2 * c] | seen[2 * c + 1] << 16;
+            if (mask != 0xffffffffu) {
 #pragma unroll
-            for (int j = 0; j < 32; j++)
-              if (!(mask >> j & 1)) r[c][j] = 0xff800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j++) tops[j % 4] = fmaxf(tops[j % 4], __uint_as_float(r[c][j]));
-        }
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        const bool grows = top > ref && !((top - ref) * a.scale2 <= kSlack<T>);
-        if (__any_sync(0xffffffffu, grows)) {
-          float keep = 1.f;
-          if (grows) {
-            keep = ref == -INFINITY ? 0.f : exp2a((ref - top) * a.scale2);
-            ref = top;
-            l *= keep;
-          }
-          if (any) {
-            // the product of the tile before may still be adding to o
-            good = good && wait_bar(bar(sh.pv[wg][x ^ 1]), (part - 1) >> 1 & 1);
-            __syncwarp();
-            tmem_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 32; c++) {
-              uint32_t v[32];
-              tmem_load(v, o_at + c * 32);
-#pragma unroll
-              for (int j = 0; j < 32; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) * keep);
-              tmem_store(o_at + c * 32, v);
+              for (int j = 0; j < 32; j++)
+                if (!(mask >> j & 1)) r[c][j] = 0xff800000u;
             }
-            tmem_stored();
-          }
-        }
-        any = true;
-        const float from = ref == -INFINITY ? 0.f : ref;
-        const Two less(-from, -from), by(a.scale2, a.scale2), lift(kLift<T>, kLift<T>), minus(-1.f, -1.f);
-        Two sum[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; c++) {  // 16 keys: eight columns of first parts, eight of the rests
-          uint32_t p[16];
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const uint32_t* x = &r[c / 2][c % 2 * 16 + 2 * j];
-            const float2 y = fma2(add2(Two(__uint_as_float(x[0]), __uint_as_float(x[1])), less), by, lift).get();
-            const float p0 = exp2a(y.x), p1 = exp2a(y.y);
-            const Two both(p0, p1);
-            sum[j % 2] = add2(sum[j % 2], both);
-            p[j] = first_part<T>(p0, p1);
-            const float2 f = unpack2<T>(p[j]);
-            const float2 rest = fma2(Two(f.x, f.y), minus, both).get();
-            p[8 + j] = pack2<T>(rest.x, rest.y);
+            for (int j = 0; j < 32; j++) tops[j % 4] = fmaxf(tops[j % 4], __uint_as_float(r[c][j]));
           }
-          tmem_store(s_at + c * 16, p);
-        }
-        const float2 s0 = sum[0].get(), s1 = sum[1].get();
-        l += (s0.x + s0.y) + (s1.x + s1.y);
-        tmem_stored();
-        tmem_before();
-        __syncwarp();
-        if (lane == 0) arrive(1, bar(sh.p_full[wg][x]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          const bool grows = top > ref && !((top - ref) * a.scale2 <= kSlack<T>);
+          if (__any_sync(0xffffffffu, grows)) {
+            float keep = 1.f;
+            if (grows) {
+              keep = ref == -INFINITY ? 0.f : exp2a((ref - top) * a.scale2);
+              ref = top;
+              l *= keep;
+            }
+            if (any) {
+              // the product of the tile before may still be adding to o
+              good = good && wait_bar(bar(sh.pv[wg][x ^ 1]), (part - 1) >> 1 & 1);
+              __syncwarp();
+              tmem_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; c++) {
+                uint32_t v[32];
+                tmem_load(v, o_at + c * 32);
+#pragma unroll
+                for (int j = 0; j < 32; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) * keep);
+                tmem_store(o_at + c * 32, v);
+              }
+              tmem_stored();
+            }
+          }
+          any = true;
+          const float from = ref == -INFINITY ? 0.f : ref;
+          const Two less(-from, -from), by(a.scale2, a.scale2), lift(kLift<T>, kLift<T>), minus(-1.f, -1.f);
+          Two sum[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 4; c++) {  // 16 keys: eight columns of first parts, eight of the rests
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const uint32_t* x = &r[c / 2][c % 2 * 16 + 2 * j];
+              const float2 y = fma2(add2(Two(__uint_as_float(x[0]), __uint_as_float(x[1])), less), by, lift).get();
+              const float p0 = exp2a(y.x), p1 = exp2a(y.y);
+              const Two both(p0, p1);
+              sum[j % 2] = add2(sum[j % 2], both);
+              p[j] = pack2<T>(p0, p1);
+              const float2 f = unpack2<T>(p[j]);
+              const float2 rest = fma2(Two(f.x, f.y), minus, both).get();
+              p[8 + j] = pack2<T>(rest.x, rest.y);
+            }
+            tmem_store(s_at + c * 16, p);
+          }
+          const float2 s0 = sum[0].get(), s1 = sum[1].get();
+          l += (s0.x + s0.y) + (s1.x + s1.y);
+          tmem_stored();
+          tmem_before();
+          __syncwarp();
+          if (lane == 0) arrive(1, bar(sh.p_full[wg][x]));
         }
       }
 
@@ -835,7 +846,8 @@ extern "C" int wfst_prefix_size(int32_t lanes, int32_t q_heads, int32_t kv_heads
   if (lanes < 0 || q_heads < 0) return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: counts must be >= 0");
   if (kv_heads < 1 || q_heads % kv_heads)
     return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: q_heads must be a multiple of kv_heads");
-  if ((int64_t)lanes * q_heads > INT32_MAX || kv_heads > 65535) return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: too many heads");
+  if ((int64_t)lanes * q_heads > INT32_MAX || kv_heads > 65535)
+    return api_fail(WFST_ERR_INVALID_ARG, "prefix_size: too many heads");
   int64_t own;
   if (const int rc = wfst_attend_size(&own)) return rc;
   const int64_t rows = (int64_t)lanes * (q_heads / kv_heads), group = rows_of_group(rows, head_dim);

@@ -17,6 +17,12 @@
 // again, hold a few more than k logits above it, usually, which are ordered by counting.
 // Where they do not fit the list (many equal logits), the list is cut to its k first
 // whenever it is full, and from then on only what is before the last of those goes in.
+//
+// 16-bit logits are compared two by two, and fp32 arithmetic is on two at a time: with one
+// at a time the instructions bound it (2048 x 131072, bf16, 110 us without alternatives,
+// two at a time and eight granules ahead 83).  2048 x 131072, bf16, with 20 alternatives
+// takes 94 us (5.7 TB/s), 2000 x 20000, fp16, 21, 64 x 131071 with 8 10.1, 1 x 5000, fp32,
+// with 5 5.5; the short ones are bound by the chain of steps after the pass.
 #include <cooperative_groups.h>
 
 #include <type_traits>
