@@ -178,6 +178,21 @@ def test_runs_behind_a_prefix(P):
     assert second.score([[], []]) == [{"logprobs": [], "entropy": []}] * 2 and second.score([]) == []
 
 
+def test_other_adapters_after_a_pass(P):
+    """A step that was captured with other adapters, or with none, is not run again."""
+    s = shape(P)
+    words, which = [[1, 2, 3], list(range(20, 50)), [700]], [1, None, 0]
+    lm = P.LanguageModel.random(s)
+    second = P.SecondPass(lm, 3, 64, page_size=16)
+    seen = [second.run(words, 12, top_p=0.9, seed=4)]
+    for seed in (7, 8):
+        lm.adapt(adapters_of(s, 2, seed))
+        seen.append(second.run(words, 12, top_p=0.9, seed=4, adapters=which))
+        assert second.run(words, 12, top_p=0.9, seed=4, adapters=which, graph=False) == seen[-1]
+        assert seen[-1][1] == seen[0][1] and seen[-1][0] != seen[0][0]
+    assert seen[1][0] != seen[2][0]
+
+
 def test_windows_score_too(P):
     s = shape(P, window=7, sinks=2)
     tensors = P.random_tensors(s, 2)

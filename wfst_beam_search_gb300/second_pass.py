@@ -111,7 +111,7 @@ class LanguageModel:
         return cls(shape, random_tensors(shape, seed), dtype, device)
 
     def adapt(self, tensors, scales=None):
-        """Low-rank adapters beside some matrices, for passes made from now on:
+        """Low-rank adapters beside some matrices, in place of those before:
         "i.qkv.shrink" [count, rank, width] and "i.qkv.expand" [count, outputs,
         rank] add scales[a] * expand[a] @ shrink[a] to that matrix for the lanes
         of adapter a, and so do "out", "up" and "down".  One count for all;
@@ -195,7 +195,7 @@ class SecondPass:
         self.last = torch.zeros(max_lanes, dtype=torch.int32, device=dev)
         self.at = torch.zeros(1, dtype=torch.int64, device=dev)
         self.workspace = _ops.attend_workspace(dev)
-        self.graph = None
+        self.graph = self.adapted = None    # the step and the adapters in it
 
     def _rotary(self, contexts):
         s = self.model.shape
@@ -291,7 +291,7 @@ class SecondPass:
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):    # (torch's own capture stream may be another device's)
             self._step()
-        self.graph = graph
+        self.graph, self.adapted = graph, self.model.adapters
 
     def _load(self, plan):
         self.plan[:len(plan)].copy_(torch.from_numpy(np.ascontiguousarray(plan)))
@@ -392,7 +392,8 @@ class SecondPass:
         if not len(plan):
             return []
         with torch.cuda.device(self.model.device):    # streams, capture and replay are of the current device
-            if graph and self.graph is None:
+            # (a graph holds the addresses of the adapters that it was made with)
+            if graph and (self.graph is None or self.adapted is not self.model.adapters):
                 self._capture()
             self._load(plan)
             self.table.copy_(torch.from_numpy(table))
