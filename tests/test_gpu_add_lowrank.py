@@ -85,6 +85,34 @@ def test_larger(W, rows, n, k, rank, adapters):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rank", [16, 64])
+@pytest.mark.parametrize("rows,adapters", [(13, 3), (100, 2)])
+def test_rows_that_begin_anywhere(W, rows, adapters, rank, dtype):
+    """y and out at every place between 16-byte boundaries, rows alike and
+    each its own; the values are those of rows that begin at one, and nothing
+    else is written."""
+    n = 329
+    a = make(rank + rows, rows, n, 264, rank, adapters, dtype)
+    even, want = (torch.empty(rows, 336, device="cuda", dtype=dtype)[:, :n] for _ in range(2))
+    even.copy_(a["y"])
+    W.add_lowrank(**{**a, "y": even}, out=want)
+    check(want, **a)
+    for width in (344, 345, 347, 350):
+        for shift in range(8):
+            room = torch.full((rows, width), 7.0, device="cuda", dtype=dtype)
+            y = room[:, shift:shift + n]
+            y.copy_(a["y"])
+            base = torch.full((rows, 351), 9.0, device="cuda", dtype=dtype)
+            to = shift * 3 % 8
+            out = base[:, to:to + n]
+            W.add_lowrank(**{**a, "y": y}, out=out)
+            assert torch.equal(out, want)
+            assert bool((base[:, :to] == 9).all()) and bool((base[:, to + n:] == 9).all())
+            W.add_lowrank(**{**a, "y": y}, out=y)
+            assert torch.equal(y, want) and bool((room[:, :shift] == 7).all()) and bool((room[:, shift + n:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("rows", [3, 70])
 def test_strides_scales_and_places(W, rows, dtype):
     """Parts of wider tensors, rows that begin anywhere, out in place of y and

@@ -50,7 +50,7 @@ struct Args {
   void* out;
   int64_t sy, sx, so, ss_a, ss_j, se_a, se_n;
   int32_t rows, n, k, rank, adapters, ranks;  // ranks: rank up to a multiple of 16 (32, where it is more)
-  int32_t same, wide;  // out is y; y's and out's rows begin at 16 bytes
+  int32_t same;  // out is y
 };
 
 // Shared memory, in floats, of a pass of P rows: sums of the warps; t, this CTA's part and
@@ -63,8 +63,29 @@ __host__ __device__ constexpr int smem_floats(int P, int R, int ranks) {
 // Loads that nothing else is read with.
 __device__ __forceinline__ uint4 load16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// P rows to a pass; the first product has sums for R ranks at a time.
-template <typename T, int P, int R>
+// Eight neighbours of the 16 16-bit values of a and b, from the one at `first` (0 to 8) on.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t first) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (first & 8) return b;
+#pragma unroll
+  for (int i = 0; i < 6; i++) w[i] = first & 4 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; i++) w[i] = first & 2 ? w[i + 1] : w[i];
+  const uint32_t by = first % 2 * 16;
+  return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by), __funnelshift_r(w[2], w[3], by),
+                    __funnelshift_r(w[3], w[4], by));
+}
+// v of another lane, by all lanes of the warp.
+__device__ __forceinline__ uint4 from_lane(const uint4& v, int lane) {
+  return make_uint4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                    __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+}
+// How many 16-bit values p is behind a 16-byte boundary.
+__device__ __forceinline__ uint32_t behind(const uint16_t* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) >> 1) & 7; }
+
+// P rows to a pass; the first product has sums for R ranks at a time.  WIDE: y's and out's
+// rows begin at 16 bytes.
+template <typename T, int P, int R, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   constexpr int MT = P / 16;
   extern __shared__ __align__(16) float smem[];
@@ -113,20 +134,22 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
       count += __popc(is);
     }
     __syncthreads();
-    const int each = (n_hi - n_lo) * 4;  // runs of eight values
-    for (int i = blockIdx.y * kThreads + tid; i < count * each; i += gridDim.y * kThreads) {
-      const int row = none[i / each], n = n_lo * 32 + i % each * 8;
+    // runs of eight values to a thread; where rows begin anywhere, of 256 to a warp, lane by lane
+    const int each = WIDE ? (n_hi - n_lo) * 4 : (n_hi - n_lo + 7) / 8, end = min(n_hi * 32, a.n);
+    const int by = WIDE ? 1 : 32, takes = kThreads / by;
+    for (int i = blockIdx.y * takes + tid / by; i < count * each; i += gridDim.y * takes) {
+      const int row = none[i / each], n = n_lo * 32 + i % each * (8 * by) + tid % by;
       const uint16_t* y = reinterpret_cast<const uint16_t*>(a.y) + row * a.sy + n;
       uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + row * a.so + n;
-      if (a.wide && n + 8 <= a.n) {
+      if (WIDE && n + 8 <= a.n) {
         *reinterpret_cast<uint4*>(out) = load16(y);
       } else {
         uint16_t v[8];
 #pragma unroll
-        for (int z = 0; z < 8; z++) v[z] = n + z < a.n ? y[z] : 0;
+        for (int z = 0; z < 8; z++) v[z] = n + z * by < end ? y[z * by] : 0;
 #pragma unroll
         for (int z = 0; z < 8; z++)
-          if (n + z < a.n) out[z] = v[z];
+          if (n + z * by < end) out[z * by] = v[z];
       }
     }
   }
@@ -303,13 +326,18 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
       // steps of S ranks, of which a lane has S / 4 neighbours on either side; U of them are asked for at once
       constexpr int S = R == 16 ? 16 : 32, U = R / S;
       using Run = std::conditional_t<S == 16, uint2, uint4>;
+      // Rows that do not begin at 16 bytes: of a block inside the row, four neighbouring lanes load the
+      // aligned pieces that hold a row's values, and shift them.  A fifth piece is needed for the last
+      // values: lane t has that of its rows' t-th.  (What else is in the outer pieces, which another warp
+      // may be writing where out is y, is not used.)  640 x 7517 x 864 of rank 16 takes 27 us so, 47 with
+      // each value loaded and stored by itself; with 7520 it takes 16.
       struct Block {
-        uint4 y[MT][2];
+        uint4 y[MT][2], more;
         Run e[U][4];
       };
       // up to eight rows: the upper eight of the product's 16 are the same rows' second parts
       const bool beside = P == 16 && rows <= 8;
-      auto wide = [&](int n) { return a.wide && n + 8 <= a.n; };
+      auto wide = [&](int n) { return WIDE && n + 8 <= a.n; };
       auto ask_e = [&](Block& v, int n0, int s0) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
@@ -319,8 +347,26 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
             v.e[u][q] = s0 + u * S + t * (S / 4) < a.rank ? *reinterpret_cast<const Run*>(ep + u * S) : Run{};
         }
       };
+      auto inside = [&](int n0) { return !WIDE && n0 >= 8 && n0 + 40 <= a.n; };
       auto ask = [&](Block& v, int blk) {
         const int n0 = blk * 32, n = n0 + t * 8;
+        if (inside(n0)) {
+          v.more = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+              const int r = m * 16 + half * 8 + g;
+              v.y[m][half] = make_uint4(0, 0, 0, 0);
+              if (r >= rows) continue;  // (of that lane)
+              const uint16_t* y = reinterpret_cast<const uint16_t*>(a.y) + mine[p0 + r] * a.sy + n0;
+              const uint32_t d = behind(y);
+              v.y[m][half] = load16(y - d + t * 8);
+              if (t == 2 * m + half && d) v.more = load16(y - d + 32);
+            }
+          ask_e(v, n0, 0);
+          return;
+        }
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -378,6 +424,50 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
 #pragma unroll
           for (int q = 0; q < 4; q++) acc[0][q][0] += acc[0][q][2], acc[0][q][1] += acc[0][q][3];
         }
+        if (inside(n0)) {  // (all lanes take part in the exchange)
+#pragma unroll
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+              if (m * 16 + half * 8 >= rows) break;  // (of all lanes)
+              const int r = m * 16 + half * 8 + g, row = mine[p0 + min(r, rows - 1)];
+              const uint4 next = from_lane(v.y[m][half], lane + 1), last = from_lane(v.more, lane - t + 2 * m + half);
+              const uint4 w = shifted(v.y[m][half], t < 3 ? next : last,
+                                      behind(reinterpret_cast<const uint16_t*>(a.y) + row * a.sy + n0));
+              const float down = std::is_same_v<T, __half> && r < rows ? lift[r] : 1.f;
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                const float2 f = unpack2<T>(u[q]);
+                o[q] = pack2<T>(f.x + acc[m][q][2 * half] * down, f.y + acc[m][q][2 * half + 1] * down);
+              }
+              // a lane stores the piece that its first values are in, from the boundary on; the first one's,
+              // and what lies behind the last boundary, is one piece too, whose ends the outer lanes store
+              const uint4 own = make_uint4(o[0], o[1], o[2], o[3]), before = from_lane(own, lane ^ t ^ ((t + 3) & 3));
+              uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + row * a.so + n0;
+              const uint32_t d = behind(out);
+              const uint4 piece = shifted(before, own, 8 - d), ends = from_lane(piece, lane - t);
+              if (r >= rows) continue;
+              out += t * 8 - (int)d;
+              if (t > 0 || d == 0) *reinterpret_cast<uint4*>(out) = piece;
+              if (d && (t == 0 || t == 3)) {
+                const bool head = t == 0;
+                const uint32_t few = head ? 8 - d : d;
+                if (!head) out += 8;
+                if (few & 4) *reinterpret_cast<uint2*>(out + (head ? 4 : 0)) = head ? make_uint2(ends.z, ends.w) : make_uint2(ends.x, ends.y);
+                if (few & 2) {
+                  const uint32_t low = head ? ends.y : ends.x, high = head ? ends.w : ends.z;
+                  *reinterpret_cast<uint32_t*>(out + (d & 4) + (head ? 2 : 0)) = d & 4 ? high : low;
+                }
+                if (few & 1) {
+                  const uint32_t odd = d & 4 ? (d & 2 ? ends.w : ends.z) : d & 2 ? ends.y : ends.x;
+                  out[head ? d : d - 1] = (uint16_t)(head ? odd >> 16 : odd);
+                }
+              }
+            }
+          return;
+        }
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -414,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 2) lowrank_kernel(const Args a) {
   if (C > 1) cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
-template <typename T, int P, int R>
+template <typename T, int P, int R, bool WIDE>
 cudaError_t launch(const Args& a, cudaStream_t st) {
-  auto* fn = lowrank_kernel<T, P, R>;
+  auto* fn = lowrank_kernel<T, P, R, WIDE>;
   constexpr int most = smem_floats(P, R, R == 16 ? 16 : kMaxRank) * 4;
   static OpsOnce once;
   if (const int dev = ops_current(); !once(dev)) {
@@ -439,11 +529,11 @@ cudaError_t launch(const Args& a, cudaStream_t st) {
 
 // Rows to a pass: 16 where an adapter will hardly have more of a tile's, as in a batch of
 // one token per lane; otherwise 32 (4096 x 6144 x 4096 50 us, with 16 76).
-template <typename T>
+template <typename T, bool WIDE>
 cudaError_t by_rows(const Args& a, cudaStream_t st) {
   const bool few = a.rows <= 16 || a.rows <= (int64_t)a.adapters * 12;
-  if (a.ranks == 16) return few ? launch<T, 16, 16>(a, st) : launch<T, 32, 16>(a, st);
-  return few ? launch<T, 16, 64>(a, st) : launch<T, 32, 32>(a, st);
+  if (a.ranks == 16) return few ? launch<T, 16, 16, WIDE>(a, st) : launch<T, 32, 16, WIDE>(a, st);
+  return few ? launch<T, 16, 64, WIDE>(a, st) : launch<T, 32, 32, WIDE>(a, st);
 }
 
 }  // namespace
@@ -481,8 +571,9 @@ extern "C" int wfst_add_lowrank(const wfst_lowrank_args* r, void* stream) {
   a.out = r->out, a.rows = r->rows, a.n = r->n, a.k = r->k, a.rank = r->rank, a.adapters = r->adapters;
   a.ranks = a.rank <= 16 ? 16 : (a.rank + 31) / 32 * 32;
   a.same = a.out == a.y && a.so == a.sy;
-  a.wide = aligned(a.y, 16) && aligned(a.out, 16) && a.sy % 8 == 0 && a.so % 8 == 0;
+  const bool wide = aligned(a.y, 16) && aligned(a.out, 16) && a.sy % 8 == 0 && a.so % 8 == 0;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = r->dtype == WFST_F16 ? by_rows<__half>(a, st) : by_rows<__nv_bfloat16>(a, st);
+  const cudaError_t e = r->dtype == WFST_F16 ? (wide ? by_rows<__half, true>(a, st) : by_rows<__half, false>(a, st))
+                                             : (wide ? by_rows<__nv_bfloat16, true>(a, st) : by_rows<__nv_bfloat16, false>(a, st));
   return e == cudaSuccess ? WFST_OK : api_cuda_fail(e, "add_lowrank launch");
 }
