@@ -40,10 +40,10 @@
 // numbered through, and each CTA takes an equal range.
 //
 // Heads of 128, bf16: 16 lanes with 32 query and 8 key-value heads behind 131072 tokens
-// (0.54 GB) take 103 us, 5.3 TB/s; 128 lanes with 64 and 8 heads behind 32767, and their own
-// 500 at most (0.27 GB), 185: this kernel 135, of which the tensor cores are busy for 108 at
+// (0.54 GB) take 101 us, 5.5 TB/s; 128 lanes with 64 and 8 heads behind 32767, and their own
+// 500 at most (0.27 GB), 186: this kernel 135, of which the tensor cores are busy for 108 at
 // their measured rate, the lanes' own tokens 42, the joining 6; 64 lanes with 32 and 8
-// heads behind 8192 45; 8 lanes with 16 and 16 heads of 64, fp16, behind 500 9.
+// heads behind 8192 43; 8 lanes with 16 and 16 heads of 64, fp16, behind 500 8.
 #include <cuda.h>
 
 #include <cfloat>
@@ -752,9 +752,10 @@ bool map_pool(CUtensorMap* map, CUtensorMapDataType type, const void* pool, int 
 
 // ---- the parts put together
 //
-// A CTA takes eight rows of a key-value head, a thread four elements of one: with
-// eight neighbours of a group the parts' 128 bytes.
-constexpr int kJoinRows = 8, kJoinThreads = 256;
+// A CTA takes eight rows of a key-value head and 4 Q elements of them, a thread four elements
+// of one: with eight neighbours of a group the parts' 128 bytes.  Where that leaves threads, as
+// many share a head's parts, whose sums are added up in order.
+constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 struct Join {
   const float *parts, *own;
   const int32_t* length;
@@ -763,9 +764,12 @@ struct Join {
   int64_t so_b, so_h, sl_b, room, own_rows;
   int32_t hkv, share, rows, keys, group, groups, grid, o_even;  // rows: of a key-value head; group: rows of one
 };
-template <typename T, int D>
+template <typename T, int D, int Q>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Join a) {
+  constexpr int kSplit = kJoinThreads / kJoinRows / Q;
   __shared__ float ms[kMostGrid + 1][kJoinRows], ls[kMostGrid + 1][kJoinRows];
+  __shared__ float tops[kJoinWarps][kJoinRows], sums[kJoinWarps][kJoinRows];
+  __shared__ float4 more[kSplit][kJoinRows * Q];  // (the first of them is not used)
   constexpr int kSide = kJoinThreads / kJoinRows;
   const int head = blockIdx.y, side = threadIdx.x / kJoinRows, r = threadIdx.x % kJoinRows;
   const int row = min(blockIdx.x * kJoinRows + r, (uint32_t)a.rows - 1);  // (one past the end does the last one's work again)
@@ -787,47 +791,89 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Join a) {
   ops_begin();
   ops_next();
   // m and l of all parts, the lane's own last, then their weights
-  for (uint32_t i = side; i <= count; i += kSide) {
-    ms[i][r] = __ldcg(i < count ? part + i * slot + at : a.own + mine);
-    ls[i][r] = __ldcg(i < count ? part + i * slot + a.group + at : a.own + a.own_rows + mine);
-  }
-  float4 v = __ldcg(reinterpret_cast<const float4*>(a.own + 2 * a.own_rows + mine * D) + min(side, D / 4 - 1));
-  __syncthreads();
+  const int warp = threadIdx.x / 32, split = side / Q, d4 = blockIdx.z * Q + side % Q;
   float top = -INFINITY, sum = 0.f;
-  for (uint32_t i = 0; i <= count; i++) top = fmaxf(top, ms[i][r]);
+  for (uint32_t i = side; i <= count; i += kSide) {
+    const float m = __ldcg(i < count ? part + i * slot + at : a.own + mine);
+    ls[i][r] = __ldcg(i < count ? part + i * slot + a.group + at : a.own + a.own_rows + mine);
+    ms[i][r] = m, top = fmaxf(top, m);
+  }
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (split == 0) v = __ldcg(reinterpret_cast<const float4*>(a.own + 2 * a.own_rows + mine * D) + d4);
+  // (a warp's threads of a row are eight apart)
+  auto of_warp = [&](float x, auto both) {
+    x = both(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return both(x, __shfl_xor_sync(0xffffffffu, x, 16));
+  };
+  auto larger = [](float x, float y) { return fmaxf(x, y); };
+  auto plus = [](float x, float y) { return x + y; };
+  top = of_warp(top, larger);
+  tops[warp][r] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; w++) top = fmaxf(top, tops[w][r]);
   const float ref = top == -INFINITY ? 0.f : top;
-  for (uint32_t i = 0; i <= count; i++) sum += ls[i][r] * exp2a(ms[i][r] - ref);
+  for (uint32_t i = side; i <= count; i += kSide) {
+    const float f = exp2a(ms[i][r] - ref);
+    ms[i][r] = f, sum += ls[i][r] * f;
+  }
+  sum = of_warp(sum, plus);
+  sums[warp][r] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; w++) sum += sums[w][r];
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
   const int b = row / a.share, c = row - b * a.share, h = head * a.share + c;
-  if (a.lse && side == 0) {
+  if (a.lse && side == 0 && blockIdx.z == 0) {
     constexpr float kLn2 = 0.6931471805599453f, kLifted = std::is_same_v<T, __half> ? 15.f : 0.f;
     a.lse[b * a.sl_b + h] = (top + (log2f(sum) - kLifted)) * kLn2;
   }
-#pragma unroll 1
-  for (int d4 = side; d4 < D / 4; d4 += kSide) {
-    if (d4 != side) v = __ldcg(reinterpret_cast<const float4*>(a.own + 2 * a.own_rows + mine * D) + d4);
-    const float f0 = exp2a(ms[count][r] - ref);
-    v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+  if (split == 0) {
+    const float f = ms[count][r];
+    v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+  }
 #pragma unroll 8
-    for (uint32_t i = 0; i < count; i++) {
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(part + i * slot + 2 * a.group) + (int64_t)d4 * a.group + at);
-      const float f = exp2a(ms[i][r] - ref);
-      v.x += w.x * f, v.y += w.y * f, v.z += w.z * f, v.w += w.w * f;
-    }
-    const uint32_t w0 = pack2<T>(v.x * inv, v.y * inv), w1 = pack2<T>(v.z * inv, v.w * inv);
-    T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + h * a.so_h + d4 * 4;
-    if (a.o_even) {
-      reinterpret_cast<uint32_t*>(out)[0] = w0, reinterpret_cast<uint32_t*>(out)[1] = w1;
-    } else {
-      uint16_t* one = reinterpret_cast<uint16_t*>(out);
-      one[0] = (uint16_t)w0, one[1] = (uint16_t)(w0 >> 16), one[2] = (uint16_t)w1, one[3] = (uint16_t)(w1 >> 16);
+  for (uint32_t i = split; i < count; i += kSplit) {
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(part + i * slot + 2 * a.group) + (int64_t)d4 * a.group + at);
+    const float f = ms[i][r];
+    v.x += w.x * f, v.y += w.y * f, v.z += w.z * f, v.w += w.w * f;
+  }
+  if (kSplit > 1) {
+    const int place = side % Q * kJoinRows + r;
+    if (split) more[split][place] = v;
+    __syncthreads();
+    if (split) return;
+#pragma unroll
+    for (int i = 1; i < kSplit; i++) {
+      const float4 w = more[i][place];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
   }
+  const uint32_t w0 = pack2<T>(v.x * inv, v.y * inv), w1 = pack2<T>(v.z * inv, v.w * inv);
+  T* out = reinterpret_cast<T*>(a.o) + b * a.so_b + h * a.so_h + d4 * 4;
+  if (a.o_even) {
+    reinterpret_cast<uint32_t*>(out)[0] = w0, reinterpret_cast<uint32_t*>(out)[1] = w1;
+  } else {
+    uint16_t* one = reinterpret_cast<uint16_t*>(out);
+    one[0] = (uint16_t)w0, one[1] = (uint16_t)(w0 >> 16), one[2] = (uint16_t)w1, one[3] = (uint16_t)(w1 >> 16);
+  }
+}
+template <typename T, int D>
+cudaError_t join_by(const Join& a, cudaStream_t st) {
+  // With four of the wide CTAs to a multiprocessor what each finds out by itself counts most
+  // (128 lanes with 64 heads behind 32767 186 us, 193 with the narrow ones), with fewer the chain of
+  // loads (64 lanes with 32 heads behind 8192 43.4 us, 45.3 with the wide ones; 32 lanes with 8 heads to
+  // one key-value head behind 32768 26, 42 where one thread adds up all parts of a row's four elements).
+  constexpr int kWide = D / 4 < 32 ? D / 4 : 32;
+  const dim3 grid((a.rows + kJoinRows - 1) / kJoinRows, a.hkv, D / 4 / kWide);
+  if ((int64_t)grid.x * grid.y * grid.z >= 4 * ops_sm_count())
+    return ops_launch(join_kernel<T, D, kWide>, grid, kJoinThreads, 0, 0, st, a);
+  return ops_launch(join_kernel<T, D, 8>, dim3(grid.x, grid.y, D / 32), kJoinThreads, 0, 0, st, a);
 }
 template <typename T>
 cudaError_t join(const Join& a, int d, cudaStream_t st) {
-  auto* fn = d == 64 ? join_kernel<T, 64> : d == 128 ? join_kernel<T, 128> : join_kernel<T, 256>;
-  return ops_launch(fn, dim3((a.rows + kJoinRows - 1) / kJoinRows, a.hkv), kJoinThreads, 0, 0, st, a);
+  return d == 64 ? join_by<T, 64>(a, st) : d == 128 ? join_by<T, 128>(a, st) : join_by<T, 256>(a, st);
 }
 
 // Rows of a group: two tiles where one does not hold all of them, so that a key that
