@@ -31,6 +31,9 @@
 // to 1.08 GB) 174 to 179, 128 lanes with a window of 2047 (1.07 GB) 173 to 178: 83
 // to 94% of a plain copy's rate.  One lane of 500 tokens takes 7.5 us: finding the units,
 // two round trips to memory (page, keys), the join.
+//
+// wfst_prefix.cu has this kernel leave m, l and o unscaled (PRE), for lanes that follow a
+// shared prefix.
 #include "wfst_ops.h"
 
 namespace wfst {
