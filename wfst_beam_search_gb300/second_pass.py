@@ -173,6 +173,7 @@ class SecondPass:
     model at a time."""
 
     prefix, prefix_table, prefix_length, rows = 0, None, None, 256    # tokens of the prefix, its pages, its length on the device
+    adapted = None    # the adapters in the graph
 
     def __init__(self, model, max_lanes, max_tokens, page_size=64, pages=None, rows=256):
         s, dev = model.shape, model.device
@@ -195,7 +196,7 @@ class SecondPass:
         self.last = torch.zeros(max_lanes, dtype=torch.int32, device=dev)
         self.at = torch.zeros(1, dtype=torch.int64, device=dev)
         self.workspace = _ops.attend_workspace(dev)
-        self.graph = self.adapted = None    # the step and the adapters in it
+        self.graph = None
 
     def _rotary(self, contexts):
         s = self.model.shape
@@ -291,7 +292,7 @@ class SecondPass:
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):    # (torch's own capture stream may be another device's)
             self._step()
-        self.graph, self.adapted = graph, self.model.adapters
+        self.graph, self.adapted = graph, getattr(self.model, "adapters", None)
 
     def _load(self, plan):
         self.plan[:len(plan)].copy_(torch.from_numpy(np.ascontiguousarray(plan)))
@@ -393,7 +394,7 @@ class SecondPass:
             return []
         with torch.cuda.device(self.model.device):    # streams, capture and replay are of the current device
             # (a graph holds the addresses of the adapters that it was made with)
-            if graph and (self.graph is None or self.adapted is not self.model.adapters):
+            if graph and (self.graph is None or self.adapted is not getattr(self.model, "adapters", None)):
                 self._capture()
             self._load(plan)
             self.table.copy_(torch.from_numpy(table))
